@@ -1,0 +1,974 @@
+// cache_attn.cuh -- attention of a few new tokens per sequence (one decoded
+// token, or a tree of drafted ones) over a paged cache, 16-bit or e4m3, for
+// sm_103a.  Reached through gqa_cache_attention.
+//
+// Mathematics.  One pass over the keys with a running reference per row, in
+// the log2 domain.  With s = scale log2(e) <q, k> and, for an e4m3 cache, the
+// key's value scale 2^w (w = 0 otherwise),
+//   M   >= max (s + w) - kSlack             the row's reference, moved lazily
+//   P_j  = 2^(s_j + w_j - M + kBias)        fp32, rounded once to 16 bits
+//   O    = sum P_j V_j,  L = sum P_j 2^-w_j   (fp32; V_j the stored values)
+//   out  = O / (L + 2^(x - M + kBias)),   lse = (M - kBias + log2(L + ..)) ln 2
+// so the value scales cost no pass of their own and L keeps the unrounded
+// probabilities.  kBias uses f16's range upwards: P reaches 2^14, and keys
+// 2^-38 below the reference still count.
+//
+// Layout.  A page holds page_size tokens x Hkv heads x d values: the K of one
+// token's heads is one run of memory, and so is a page's.  A CTA therefore
+// takes HPC heads at once (all of them up to 8), one warp per head (or
+// several warps that share a head's keys when there are fewer heads), and a
+// producer warp copies whole runs of a page into a shared-memory ring with
+// cp.async.bulk: no tensor map, no gather of 64-byte head slices, every DRAM
+// burst read whole.  The G query heads of the tokens are the rows of the
+// products: few (8 for one token of a 64 / 8 head model), so the products are
+// m16n8k16 warp instructions whose operands are converted from e4m3 in
+// registers; a 128-row tensor-memory tile would be 94% padding there.
+//
+// Fragment order.  A contraction may run in any order, so the fragments are
+// laid out by what one wide shared-memory load brings: lane (g, t) = (lane /
+// 4, lane % 4) loads 16 bytes of key 4 (g / 2) + 2 tau + g % 2 for the score
+// tile tau of a 16-key group, which puts keys 4 t .. 4 t + 3 into its
+// accumulators: exactly the keys whose V rows it then loads, 8 values at 8 g.
+// The transposition that the second product needs is the byte interleave of
+// the conversion.
+//
+// Work split.  Every CTA takes an equal share of all (sequence, row tile,
+// head group) key tiles laid end to end (lengths are device data: the split
+// is found on the device), and a unit cut by a share boundary leaves fp32
+// partials (O, M, L) that cache_merge_kernel joins.  When whole units dealt
+// out cost no more than equal shares plus a join, they are dealt whole.
+#pragma once
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "prefill_kernel.cuh"
+#include "ptx.cuh"
+
+namespace gqa {
+
+constexpr int kCaWarps = 8;                        // consumer warps
+constexpr int kCaThreads = 32 * (kCaWarps + 1);    // and one producer warp
+constexpr int kCaMaxSlots = 16;                    // ring slots at most
+constexpr float kCaSlack = 4.f;
+constexpr int kCaWholeSlack = 6;                   // tiles a join is worth
+
+struct CacheAttnParams {
+  const void* q;
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  const int32_t* cu;
+  const int32_t* pre;
+  const int32_t* indptr;
+  const int32_t* indices;
+  const float* sinks;
+  const uint32_t* mask;
+  const int32_t* mask_indptr;
+  const int32_t* depths;
+  void* out;
+  float* lse;
+  unsigned int* status;
+  float* part_o;     // [2 per CTA][HPC * RT rows][D]
+  float* part_ml;    // [2 per CTA][HPC * RT rows][2] (M, L)
+  int32_t* hdr;      // [0] units; [8 + 8 u ..] see hdr_of
+  long long total_mask_words;
+  unsigned long long timeout_ns;
+  int entries, num_pages, page_size;
+  int num_seqs, first_seq, total_q;
+  int Hq, Hkv, G;
+  int HPC, HG;       // heads per CTA, head groups
+  int KW;            // warps that share a head's keys
+  int T;             // keys per tile (16 GK KW)
+  int run;           // tokens per copy: divides T and the page
+  int NS;            // ring slots
+  uint32_t slot_bytes, data_bytes;  // a slot, and its values (scales follow)
+  int window, smooth;
+  int whole;         // units dealt whole whatever the lengths
+  int max_units;
+  float scale_log2;
+  int metadata_ready;
+};
+
+// Rows of a unit: MT tiles of 16.  GK: 16-key groups a warp takes per tile.
+__host__ __device__ constexpr int ca_gk(int D, bool C8, int MT) {
+  return MT == 1 && D * (C8 ? 1 : 2) <= 128 ? 2 : 1;
+}
+constexpr uint32_t kCaScratch = kCaWarps * 16u * 64u * 4u;  // per warp 16 rows x 64 columns fp32
+__host__ __device__ constexpr uint32_t ca_fixed_smem() {
+  return 1024u + 128u + kCaScratch + kCaWarps * 16u * 8u + 2u * kCaMaxSlots * 8u + 32u +
+         8u * (kMaxSeqs + 1) + 4u * (4 * kMaxSeqs + 2) + 8u * 16u;
+}
+
+struct CaTab {
+  const long long* tiles;  // [B + 1] exclusive scan of key tiles
+  const int32_t* units;    // [B + 1] exclusive scan of units
+  const int32_t* cu0;      // [B + 1]
+  const int32_t* pre;      // [B]
+  const int32_t* ipt;      // [B]
+};
+
+// A piece of work: tiles [t0, t1) of the n tiles of one unit.
+struct CaPiece {
+  int b, rt, hg, unit;
+  int P, E, lo, hi;  // keys [lo, hi), lo a multiple of T
+  int n, t0, t1;
+};
+
+// Key range of row tile rt: rows rt * RT .. of the sequence's E * G.
+__device__ __forceinline__ void ca_range(const CacheAttnParams& p, int P, int E, int rt, int RT,
+                                         int& lo, int& hi, int& n) {
+  const int i0 = rt * RT / p.G, i1 = min((rt * RT + RT - 1) / p.G, E - 1);
+  hi = P + i1 + 1;
+  lo = 0;
+  if (p.window > 0) {
+    // The lowest position of the tile's rows: depths may be anything >= 0.
+    const long long a = (long long)P + (p.depths != nullptr ? 0 : i0) - p.window + 1;
+    if (a > 0) lo = (int)(a / p.T) * p.T;
+    if (lo >= hi) lo = (hi - 1) / p.T * p.T;
+  }
+  n = (hi - lo + p.T - 1) / p.T;
+}
+
+struct CaWalk {
+  long long at, end;  // share mode: tiles left
+  int unit, step;     // whole mode: next unit
+  int n_units;
+  bool whole;
+};
+
+__device__ __forceinline__ bool ca_next(const CacheAttnParams& p, const CaTab& T, CaWalk& w, int RT,
+                                        CaPiece& u) {
+  int lo = 0, hi = p.num_seqs;
+  if (w.whole) {
+    if (w.unit >= w.n_units) return false;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (T.units[mid] <= w.unit) lo = mid; else hi = mid;
+    }
+  } else {
+    if (w.at >= w.end) return false;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (T.tiles[mid] <= w.at) lo = mid; else hi = mid;
+    }
+  }
+  u.b = lo;
+  u.P = T.pre[lo];
+  u.E = T.cu0[lo + 1] - T.cu0[lo];
+  if (w.whole) {
+    const int k = w.unit - T.units[lo];
+    u.rt = k / p.HG;
+    u.hg = k - u.rt * p.HG;
+    ca_range(p, u.P, u.E, u.rt, RT, u.lo, u.hi, u.n);
+    u.t0 = 0;
+    u.t1 = u.n;
+    u.unit = w.unit;
+    w.unit += w.step;
+    return true;
+  }
+  long long off = w.at - T.tiles[lo];
+  for (u.rt = 0;; ++u.rt) {  // ends: off lies within the sequence's tiles
+    ca_range(p, u.P, u.E, u.rt, RT, u.lo, u.hi, u.n);
+    const long long all = (long long)u.n * p.HG;
+    if (off < all) break;
+    off -= all;
+  }
+  u.hg = (int)(off / u.n);
+  u.t0 = (int)(off - (long long)u.hg * u.n);
+  const long long left = w.end - w.at;
+  u.t1 = left < u.n - u.t0 ? u.t0 + (int)left : u.n;
+  u.unit = T.units[lo] + u.rt * p.HG + u.hg;
+  w.at += u.t1 - u.t0;
+  return true;
+}
+
+// Share boundaries in 64 bits.
+__device__ __forceinline__ long long ca_lo(long long W, int c, int C) { return W * c / C; }
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// Named barrier over `count` threads that tells whether all of them said yes.
+__device__ __forceinline__ bool named_bar_all(uint32_t id, uint32_t count, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.aligned.pred q, %1, %2, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"((uint32_t)yes)
+      : "memory");
+  return r != 0;
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {  // low 16 bits: two values
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)w));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(a)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
+  return r;
+}
+
+// D: head dim.  BF16: type of q and out.  C8: e4m3 cache (products in f16),
+// else the cache has q's type.  MT: 16-row tiles per warp.
+template <int D, bool BF16, bool C8, int MT>
+__global__ void __launch_bounds__(kCaThreads, 1)
+    cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
+  constexpr int GK = ca_gk(D, C8, MT);
+  constexpr int RT = 16 * MT;
+  constexpr bool MBF = BF16 && !C8;          // product type
+  constexpr float kBias = MBF ? 0.f : 10.f;  // 2^(kCaSlack + kBias) fits f16
+  constexpr int kEsz = C8 ? 1 : 2;
+  constexpr int KS = D / 16;                 // k16 steps of the scores
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float* scratch = reinterpret_cast<float*>(smem);  // [8][16][64]
+  float2* s_ml = reinterpret_cast<float2*>(smem + kCaScratch);  // [8][16]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_ml + kCaWarps * 16);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kCaMaxSlots);  // [0] abort [1] bad
+  long long* tiles = reinterpret_cast<long long*>(misc + 8);
+  long long* wtot = tiles + (kMaxSeqs + 1);
+  int32_t* units = reinterpret_cast<int32_t*>(wtot + 16);
+  int32_t* s_cu = units + (kMaxSeqs + 1);
+  int32_t* s_pre = s_cu + (kMaxSeqs + 1);
+  int32_t* s_ipt = s_pre + kMaxSeqs;
+  const uint32_t ring = (smem_u32(s_ipt + kMaxSeqs) + 127u) & ~127u;
+  const uint32_t sBar = smem_u32(bars);
+  volatile uint32_t* abort_flag = misc;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nact = p.HPC * p.KW;  // consumer warps at work
+  const unsigned long long tmo = p.timeout_ns;
+
+  // ---------------------------------------------------------------- set-up
+  if (tid == 0) {
+    for (int i = 0; i < p.NS; ++i) {
+      mbar_init(sBar + 8u * i, 1u);
+      mbar_init(sBar + 8u * (kCaMaxSlots + i), (uint32_t)nact);
+    }
+    misc[0] = 0u;
+    misc[1] = 0u;
+    misc[2] = 0u;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  grid_dep_launch_dependents();
+  if (!p.metadata_ready) grid_dep_wait();
+
+  const int nseq = p.num_seqs;
+  bool bad = tid == 0 && p.first_seq == 0 && __ldg(p.cu) != 0;
+  long long my_tiles = 0;
+  int my_units = 0, my_max = 0;
+  const int per = (nseq + kCaThreads - 1) / kCaThreads;
+  const int b_lo = min(tid * per, nseq), b_hi = min(b_lo + per, nseq);
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), P = __ldg(p.pre + b);
+    const int i0 = __ldg(p.indptr + b), i1 = __ldg(p.indptr + b + 1);
+    const long long E = (long long)c1 - c0;
+    bool mask_bad = false;
+    if (p.mask != nullptr) {
+      const long long m0 = __ldg(p.mask_indptr + b), m1 = __ldg(p.mask_indptr + b + 1);
+      mask_bad = m0 < 0 || m1 > p.total_mask_words || m1 - m0 != E * ((E + 31) / 32);
+    }
+    const bool b_bad = E < 0 || P < 0 || c0 < 0 || c1 > p.total_q || i0 < 0 || i1 > p.entries ||
+                       P + E > 0x7ffff000ll ||
+                       (long long)i1 - i0 != (P + E + p.page_size - 1) / p.page_size || mask_bad;
+    bad |= b_bad;
+    long long w = 0;
+    int nu = 0;
+    if (!b_bad && E > 0) {
+      const int nrt = (int)((E * p.G + RT - 1) / RT);
+      for (int rt = 0; rt < nrt; ++rt) {
+        int lo, hi, n;
+        ca_range(p, P, (int)E, rt, RT, lo, hi, n);
+        w += n;
+        my_max = max(my_max, n);
+      }
+      w *= p.HG;
+      nu = nrt * p.HG;
+    }
+    s_cu[b] = c0;
+    s_pre[b] = P;
+    s_ipt[b] = i0;
+    tiles[b] = w;
+    units[b] = nu;
+    if (b == nseq - 1) s_cu[nseq] = c1;
+    my_tiles += w;
+    my_units += nu;
+  }
+  if (bad) misc[1] = 1u;
+  my_max = __reduce_max_sync(0xffffffffu, my_max);
+  if (lane == 0 && my_max > 0) atomicMax(reinterpret_cast<int*>(misc + 2), my_max);
+  // Exclusive scans of the tiles and units: warp scans, then warp totals.
+  long long it = my_tiles;
+  int iu = my_units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long a = __shfl_up_sync(0xffffffffu, it, o);
+    const int b = __shfl_up_sync(0xffffffffu, iu, o);
+    if (lane >= o) {
+      it += a;
+      iu += b;
+    }
+  }
+  int* utot = reinterpret_cast<int*>(s_ml);
+  if (lane == 31) {
+    wtot[warp] = it;
+    utot[warp] = iu;
+  }
+  __syncthreads();
+  {
+    long long at = it - my_tiles;
+    int au = iu - my_units;
+    for (int w = 0; w < warp; ++w) {
+      at += wtot[w];
+      au += utot[w];
+    }
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long w = tiles[b];
+      const int nu = units[b];
+      tiles[b] = at;
+      units[b] = au;
+      at += w;
+      au += nu;
+      if (b == nseq - 1) {
+        tiles[nseq] = at;
+        units[nseq] = au;
+      }
+    }
+  }
+  __syncthreads();
+  const bool bad_meta = misc[1] != 0u;
+  if (p.metadata_ready) grid_dep_wait();  // before any global write or other read
+  if (bad_meta) {
+    if (tid == 0) {
+      atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
+      if (blockIdx.x == 0) p.hdr[0] = 0;
+    }
+    return;
+  }
+  const CaTab T{tiles, units, s_cu, s_pre, s_ipt};
+  const long long W = tiles[nseq];
+  // No more shares than tiles: every share holds a tile, so the pieces of a
+  // cut unit lie on consecutive CTAs.
+  const int C = W < (long long)gridDim.x ? (int)W : (int)gridDim.x;
+  const int n_units = units[nseq], c = blockIdx.x;
+  if (c == 0 && tid == 0 && W == 0) p.hdr[0] = 0;
+  if (c >= C) return;
+  CaWalk walk;
+  walk.n_units = n_units;
+  // Whole units when the deepest deal costs no more than an equal share and
+  // the join that cut units need.
+  walk.whole = p.whole != 0 ||
+               (long long)((n_units + C - 1) / C) * (int)misc[2] <= W / C + kCaWholeSlack;
+  walk.unit = c;
+  walk.step = C;
+  walk.at = ca_lo(W, c, C);
+  walk.end = ca_lo(W, c + 1, C);
+  if (c == 0 && tid == 0) p.hdr[0] = walk.whole ? 0 : n_units;  // W > 0 here
+
+  const uint32_t row_bytes = (uint32_t)p.HPC * D * kEsz;        // a token's values in the ring
+  const long long tok_bytes = (long long)p.Hkv * D * kEsz;      // in the pool
+
+  if (warp == kCaWarps) {
+    // -------------------------------------------------------------- producer
+    // The tile's runs are spread over the lanes; slots alternate K and V.
+    uint32_t slot = 0, ph = 0, issued = 0;
+    bool ok = true;
+    CaPiece u;
+    const int nrun = p.T / p.run;
+    while (ok && ca_next(p, T, walk, RT, u)) {
+      const int npg = (u.P + u.E + p.page_size - 1) / p.page_size;
+      const int32_t* table = p.indices + T.ipt[u.b];
+      for (int t = u.t0; ok && t < u.t1; ++t) {
+        const int n0 = u.lo + t * p.T;
+        const int ntok = min(p.T, u.hi - n0);
+        for (int kv = 0; kv < 2; ++kv) {
+          if (lane == 0) {
+            ok = wait_bounded(sBar + 8u * (kCaMaxSlots + slot), ph ^ 1u, abort_flag, p.status, tmo);
+            if (ok) {
+              uint32_t bytes = (uint32_t)ntok * row_bytes;
+              if (C8) bytes += (uint32_t)((ntok + p.run - 1) / p.run * p.run) * (uint32_t)p.Hkv;
+              mbar_arrive_expect_tx(sBar + 8u * slot, bytes);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+          if (!ok) break;
+          const uint32_t dst = ring + slot * p.slot_bytes, bar = sBar + 8u * slot;
+          const uint8_t* pages = kv ? p.v_pages : p.k_pages;
+          for (int r = lane; r < nrun && r * p.run < ntok; r += 32) {
+            const int key = n0 + r * p.run, cnt = min(p.run, ntok - r * p.run);
+            int pg = __ldg(table + min(key / p.page_size, npg - 1));
+            if (pg < 0 || pg >= p.num_pages) {
+              atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
+              pg = 0;
+            }
+            const long long row = (long long)pg * p.page_size + key % p.page_size;
+            const uint8_t* src = pages + row * tok_bytes + (long long)u.hg * row_bytes;
+            const uint32_t to = dst + (uint32_t)(r * p.run) * row_bytes;
+            if (p.HG == 1)
+              bulk_load(to, src, (uint32_t)cnt * row_bytes, bar);
+            else
+              for (int i = 0; i < cnt; ++i)
+                bulk_load(to + i * row_bytes, src + i * tok_bytes, row_bytes, bar);
+            if (C8)  // the scales of all heads, whole runs: within the page
+              bulk_load(dst + p.data_bytes + (uint32_t)(r * p.run * p.Hkv),
+                        (kv ? p.v_scales : p.k_scales) + row * p.Hkv, (uint32_t)(p.run * p.Hkv),
+                        bar);
+          }
+          ++issued;
+          if (++slot == (uint32_t)p.NS) {
+            slot = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+    // Let every copy issued land before the CTA can exit.
+    __syncwarp();
+    if (lane < p.NS) {
+      const uint32_t loads = issued / p.NS + ((uint32_t)lane < issued % p.NS ? 1u : 0u);
+      if (loads > 0) wait_drain(sBar + 8u * lane, (loads - 1u) & 1u, tmo);
+    }
+    return;
+  }
+  if (warp >= nact) return;  // more warps than heads can use
+
+  // ---------------------------------------------------------------- consumers
+  const int hl = warp % p.HPC, kw = warp / p.HPC;
+  const int g = lane >> 2, t = lane & 3;
+  // Every lane of a warp goes on or none.
+  auto wait_full = [&](uint32_t sl, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_bounded(sBar + 8u * sl, parity, abort_flag, p.status, tmo)) != 0;
+  };
+  uint32_t slot = 0, ph = 0;
+  CaPiece u;
+  bool ok = true;
+  while (ok && ca_next(p, T, walk, RT, u)) {
+    const int head = u.hg * p.HPC + hl;  // KV head
+    const int cu0 = T.cu0[u.b];
+    // The thread's rows: g and g + 8 of every 16-row tile.
+    int ri[MT][2], rdep[MT][2];  // token index (-1: none) and depth
+    float rs[MT][2];             // scale to the log2 domain
+    uint32_t qf[MT][KS][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = u.rt * RT + m * 16 + g + 8 * h;
+        const int i = r / p.G;
+        const bool on = i < u.E;
+        ri[m][h] = on ? i : -1;
+        rdep[m][h] = i;
+        if (on && p.depths != nullptr) rdep[m][h] = __ldg(p.depths + cu0 + i);
+        const uint16_t* qr = static_cast<const uint16_t*>(p.q) +
+                             ((long long)(cu0 + (on ? i : 0)) * p.Hq + head * p.G + r % p.G) * D;
+        rs[m][h] = p.scale_log2;
+        if constexpr (C8) {
+          // f16 operands: the row scaled by the power of two that brings its
+          // largest magnitude into [1, 2); smaller values round at 2^-25.
+          float x[KS][4], amax = 0.f;
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            const uint2 w = on ? __ldg(reinterpret_cast<const uint2*>(
+                                     qr + 64 * (s >> 2) + 16 * t + 4 * (s & 3)))
+                               : make_uint2(0u, 0u);
+            x[s][0] = unpack_lo<BF16>(w.x), x[s][1] = unpack_hi<BF16>(w.x);
+            x[s][2] = unpack_lo<BF16>(w.y), x[s][3] = unpack_hi<BF16>(w.y);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fabsf(x[s][j]));
+          }
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
+          const float f = __int_as_float((127 - e) << 23);
+          rs[m][h] = p.scale_log2 * __int_as_float((127 + e) << 23);
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            qf[m][s][h] = pack2<false>(x[s][0] * f, x[s][1] * f);
+            qf[m][s][2 + h] = pack2<false>(x[s][2] * f, x[s][3] * f);
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            const uint2 w = on ? __ldg(reinterpret_cast<const uint2*>(
+                                     qr + 32 * (s >> 1) + 8 * t + 4 * (s & 1)))
+                               : make_uint2(0u, 0u);
+            qf[m][s][h] = w.x;
+            qf[m][s][2 + h] = w.y;
+          }
+        }
+      }
+    float o[MT][D / 8][4];
+    float M[MT][2], L[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      M[m][0] = M[m][1] = -1e30f;
+      L[m][0] = L[m][1] = 0.f;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
+    }
+
+    for (int tl = u.t0; tl < u.t1; ++tl) {
+      const int n0 = u.lo + tl * p.T + kw * 16 * GK;  // this warp's first key
+      // ---- scores of 16 GK keys
+      if (!(ok = wait_full(slot, ph))) break;
+      float s[MT][2 * GK][4];
+      float ks[GK][4];
+      {
+        const uint32_t base = ring + slot * p.slot_bytes;
+        const uint32_t kb = base + (uint32_t)(kw * 16 * GK) * row_bytes + (uint32_t)(hl * D * kEsz);
+#pragma unroll
+        for (int n = 0; n < 2 * GK; ++n) {
+#pragma unroll
+          for (int m = 0; m < MT; ++m) s[m][n][0] = s[m][n][1] = s[m][n][2] = s[m][n][3] = 0.f;
+          const int kr = 16 * (n >> 1) + 4 * (g >> 1) + 2 * (n & 1) + (g & 1);
+          const uint32_t ka = kb + (uint32_t)kr * row_bytes + 16u * t;
+#pragma unroll
+          for (int c4 = 0; c4 < D * kEsz / 64; ++c4) {
+            const uint4 w = lds128(ka + 64u * c4);
+            if constexpr (C8) {
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t b0 = e4m3x2_f16x2(ww[j]), b1 = e4m3x2_f16x2(ww[j] >> 16);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) mma16816<MBF>(s[m][n], qf[m][4 * c4 + j], b0, b1);
+              }
+            } else {
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                mma16816<MBF>(s[m][n], qf[m][2 * c4], w.x, w.y);
+                mma16816<MBF>(s[m][n], qf[m][2 * c4 + 1], w.z, w.w);
+              }
+            }
+          }
+        }
+        if constexpr (C8) {
+          const uint32_t sa = base + p.data_bytes + (uint32_t)((kw * 16 * GK + 4 * t) * p.Hkv + head);
+#pragma unroll
+          for (int k = 0; k < GK; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              ks[k][j] = __int_as_float((int)lds8(sa + (uint32_t)((16 * k + j) * p.Hkv)) << 23);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sBar + 8u * (kCaMaxSlots + slot));
+        if (++slot == (uint32_t)p.NS) {
+          slot = 0;
+          ph ^= 1u;
+        }
+      }
+      // ---- V of the tile: its scales join the exponents
+      if (!(ok = wait_full(slot, ph))) break;
+      const uint32_t vbase = ring + slot * p.slot_bytes;
+      float we[GK][4], wi[GK][4];  // the value scale's exponent, and 2^-exponent
+      if constexpr (C8) {
+        const uint32_t sa = vbase + p.data_bytes + (uint32_t)((kw * 16 * GK + 4 * t) * p.Hkv + head);
+#pragma unroll
+        for (int k = 0; k < GK; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = (int)lds8(sa + (uint32_t)((16 * k + j) * p.Hkv));
+            we[k][j] = (float)(e - 127);
+            wi[k][j] = __int_as_float(max(254 - e, 0) << 23);
+          }
+      }
+      // Which keys need a look at the mask: any at or past the prefix's end
+      // (causal, tree, end of the sequence) or below some row's window.
+      const bool edge = n0 + 16 * GK > u.P || p.window > 0;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float sc = rs[m][h];
+#pragma unroll
+          for (int n = 0; n < 2 * GK; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& x = s[m][n][2 * h + e];
+              const int j = 2 * (n & 1) + e;
+              if constexpr (C8)
+                x = fmaf(x * sc, ks[n >> 1][j], we[n >> 1][j]);
+              else
+                x *= sc;
+            }
+          if (edge) {
+            const int i = ri[m][h], dep = rdep[m][h];
+#pragma unroll
+            for (int n = 0; n < 2 * GK; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int key = n0 + 16 * (n >> 1) + 4 * t + 2 * (n & 1) + e;
+                const int x = key - u.P;  // index among the new tokens
+                bool keep = i >= 0 && x <= i;
+                if (keep && x >= 0 && p.mask != nullptr)
+                  keep = (__ldg(p.mask + __ldg(p.mask_indptr + u.b) +
+                                (long long)i * ((u.E + 31) >> 5) + (x >> 5)) >>
+                          (x & 31)) & 1u;
+                if (keep && p.window > 0) {
+                  const int place = x >= 0 && p.depths != nullptr ? __ldg(p.depths + cu0 + x) : x;
+                  keep = place > dep - p.window;
+                }
+                if (!keep) s[m][n][2 * h + e] = -INFINITY;
+              }
+          }
+        }
+      // ---- the references: moved when some score exceeds one by kCaSlack
+      bool raise = false;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float mx = s[m][0][2 * h];
+#pragma unroll
+          for (int n = 0; n < 2 * GK; ++n) mx = max3(mx, s[m][n][2 * h], s[m][n][2 * h + 1]);
+          raise |= mx > M[m][h] + kCaSlack;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float mx = M[m][h];
+#pragma unroll
+            for (int n = 0; n < 2 * GK; ++n) mx = max3(mx, s[m][n][2 * h], s[m][n][2 * h + 1]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float f = ex2(M[m][h] - mx);
+            M[m][h] = mx;
+            L[m][h] *= f;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+              o[m][n][2 * h] *= f;
+              o[m][n][2 * h + 1] *= f;
+            }
+          }
+      }
+      uint32_t pf[MT][GK][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float ref = M[m][h] - kBias;
+#pragma unroll
+          for (int n = 0; n < 2 * GK; ++n) {
+            const float a = ex2(s[m][n][2 * h] - ref), b = ex2(s[m][n][2 * h + 1] - ref);
+            if constexpr (C8)
+              L[m][h] += a * wi[n >> 1][2 * (n & 1)] + b * wi[n >> 1][2 * (n & 1) + 1];
+            else
+              L[m][h] += a + b;
+            pf[m][n >> 1][2 * (n & 1) + h] = pack2<MBF>(a, b);
+          }
+        }
+      // ---- O += P V
+      const uint32_t va = vbase + (uint32_t)(kw * 16 * GK) * row_bytes + (uint32_t)(hl * D * kEsz) +
+                          (uint32_t)(8 * kEsz * g);
+#pragma unroll
+      for (int k = 0; k < GK; ++k) {
+        const uint32_t vk = va + (uint32_t)(16 * k + 4 * t) * row_bytes;
+        // Keys that no row sees may hold anything: zeros in their place.
+        uint32_t live = 15u;
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = n0 + 16 * k + 4 * t + j;
+            if (key >= u.hi || (p.window > 0 && key <= u.P - p.window))
+              live &= ~(1u << j);
+          }
+        }
+#pragma unroll
+        for (int c64 = 0; c64 < D / 64; ++c64) {
+          if constexpr (C8) {
+            uint2 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              w[j] = lds64(vk + (uint32_t)j * row_bytes + 64u * c64);
+              if (!(live >> j & 1u)) w[j] = make_uint2(0u, 0u);
+            }
+#pragma unroll
+            for (int n = 0; n < 8; n += 2) {
+              const uint32_t sel = (n & 2) ? 0x7362u : 0x5140u;
+              const uint32_t a = __byte_perm(n < 4 ? w[0].x : w[0].y, n < 4 ? w[1].x : w[1].y, sel);
+              const uint32_t b = __byte_perm(n < 4 ? w[2].x : w[2].y, n < 4 ? w[3].x : w[3].y, sel);
+              const uint32_t a0 = e4m3x2_f16x2(a), a1 = e4m3x2_f16x2(a >> 16);
+              const uint32_t b0 = e4m3x2_f16x2(b), b1 = e4m3x2_f16x2(b >> 16);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                mma16816<MBF>(o[m][8 * c64 + n], pf[m][k], a0, b0);
+                mma16816<MBF>(o[m][8 * c64 + n + 1], pf[m][k], a1, b1);
+              }
+            }
+          } else {
+            uint4 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              w[j] = lds128(vk + (uint32_t)j * row_bytes + 128u * c64);
+              if (!(live >> j & 1u)) w[j] = make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const uint32_t x0 = n == 0 ? w[0].x : n == 1 ? w[0].y : n == 2 ? w[0].z : w[0].w;
+              const uint32_t x1 = n == 0 ? w[1].x : n == 1 ? w[1].y : n == 2 ? w[1].z : w[1].w;
+              const uint32_t x2 = n == 0 ? w[2].x : n == 1 ? w[2].y : n == 2 ? w[2].z : w[2].w;
+              const uint32_t x3 = n == 0 ? w[3].x : n == 1 ? w[3].y : n == 2 ? w[3].z : w[3].w;
+              const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
+              const uint32_t b0 = __byte_perm(x2, x3, 0x5410), b1 = __byte_perm(x2, x3, 0x7632);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                mma16816<MBF>(o[m][8 * c64 + 2 * n], pf[m][k], a0, b0);
+                mma16816<MBF>(o[m][8 * c64 + 2 * n + 1], pf[m][k], a1, b1);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sBar + 8u * (kCaMaxSlots + slot));
+      if (++slot == (uint32_t)p.NS) {
+        slot = 0;
+        ph ^= 1u;
+      }
+    }
+    // A wait that ran out in one warp ends the piece for all that join rows
+    // with it: nothing more is written.
+    if (p.KW > 1) ok = named_bar_all(1u, 32u * (uint32_t)nact, ok);
+
+    // ---- the unit's (or piece's) rows: join the warps of a head, write.
+    // Warp area [16 rows][64 columns] in shared memory, a tile and 64 columns
+    // at a time; with one warp per head only that warp takes part.
+    const bool cut = u.t0 > 0 || u.t1 < u.n;
+    const long long pslot = 2ll * c + (u.t0 > 0 ? 0 : 1);
+    if (cut && u.t0 == 0 && hl == 0 && kw == 0 && lane == 0) {
+      int32_t* hd = p.hdr + 8 + 8ll * u.unit;
+      const long long gend = walk.at - u.t1 + u.n;  // tile after the unit's last
+      // CTA of the unit's last tile: the share that holds tile gend - 1.
+      int a = c, b = C;
+      while (b - a > 1) {
+        const int mid = (a + b) >> 1;
+        if (ca_lo(W, mid, C) <= gend - 1) a = mid; else b = mid;
+      }
+      hd[0] = a - c;  // pieces after the first
+      hd[1] = c;
+      hd[2] = u.rt * RT;
+      hd[3] = u.hg * p.HPC;
+      hd[4] = cu0;
+      hd[5] = u.E;
+    } else if (!walk.whole && !cut && hl == 0 && kw == 0 && lane == 0) {
+      p.hdr[8 + 8ll * u.unit] = 0;
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        L[m][h] += __shfl_xor_sync(0xffffffffu, L[m][h], 1);
+        L[m][h] += __shfl_xor_sync(0xffffffffu, L[m][h], 2);
+      }
+    auto join = [&]() {
+      if (p.KW == 1) __syncwarp();
+      else named_bar_sync(1u, 32u * (uint32_t)nact);
+    };
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (t == 0) {
+        s_ml[warp * 16 + g] = make_float2(M[m][0], L[m][0]);
+        s_ml[warp * 16 + g + 8] = make_float2(M[m][1], L[m][1]);
+      }
+#pragma unroll
+      for (int c64 = 0; c64 < D / 64; ++c64) {
+        // Value (row, column 8 (2 t + e) + j) of the chunk; columns rotated by
+        // the row so that neither side meets bank conflicts beyond two ways.
+        float* area = scratch + warp * 16 * 64;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+              const int col = (8 * (2 * t + e) + j + 8 * g) & 63;
+              *reinterpret_cast<float4*>(area + (g + 8 * h) * 64 + col) =
+                  make_float4(o[m][8 * c64 + j][2 * h + e], o[m][8 * c64 + j + 1][2 * h + e],
+                              o[m][8 * c64 + j + 2][2 * h + e], o[m][8 * c64 + j + 3][2 * h + e]);
+            }
+        join();
+        // Rows kw, kw + KW, .. of the head, two columns a lane.
+        for (int r = kw; r < 16; r += p.KW) {
+          const int gr = u.rt * RT + m * 16 + r;  // row of the sequence
+          const int i = gr / p.G;
+          if (i >= u.E) continue;
+          const int col = (2 * lane + 8 * (r & 7)) & 63;
+          float mf = -1e30f;
+          for (int w = 0; w < p.KW; ++w) mf = fmaxf(mf, s_ml[(w * p.HPC + hl) * 16 + r].x);
+          float x = 0.f, y = 0.f, l = 0.f;
+          for (int w = 0; w < p.KW; ++w) {
+            const int wa = w * p.HPC + hl;
+            const float2 ml = s_ml[wa * 16 + r];
+            const float f = ex2(ml.x - mf);
+            const float2 v = *reinterpret_cast<const float2*>(scratch + (wa * 16 + r) * 64 + col);
+            x = fmaf(v.x, f, x);
+            y = fmaf(v.y, f, y);
+            l = fmaf(ml.y, f, l);
+          }
+          if (!ok) continue;
+          const int qh = head * p.G + gr % p.G;
+          if (cut) {
+            const long long pr = pslot * (p.HPC * RT) + hl * RT + m * 16 + r;
+            *reinterpret_cast<float2*>(p.part_o + pr * D + 64 * c64 + 2 * lane) = make_float2(x, y);
+            if (c64 == 0 && lane == 0)
+              *reinterpret_cast<float2*>(p.part_ml + pr * 2) = make_float2(mf, l);
+          } else {
+            float xs = -INFINITY;
+            if (p.sinks != nullptr) xs = __ldg(p.sinks + qh) * kLog2e;
+            else if (p.smooth) xs = 0.f;
+            // With the sink above the keys the reference moves to it.
+            const bool any = l > 0.f;
+            const float mm = fmaxf(mf - kBias, xs), f = ex2(mf - kBias - mm);
+            const float den = fmaf(l, f, ex2(xs - mm));
+            const float inv = any ? f / den : 0.f;
+            const long long row = (long long)(cu0 + i) * p.Hq + qh;
+            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + 64 * c64 +
+                                         2 * lane) = pack2<BF16>(x * inv, y * inv);
+            if (c64 == 0 && lane == 0 && p.lse != nullptr)
+              p.lse[row] = any ? (mm + log2f(den)) * kLn2 : -INFINITY;
+          }
+        }
+        join();
+      }
+    }
+  }
+}
+
+// Joins the partials of the units that share boundaries cut: with mf the
+// largest reference (the sink's included),
+//   out = sum O_s 2^(M_s - mf) / (sum L_s 2^(M_s - mf) + 2^(x - mf)).
+// blockIdx.x walks the units, blockIdx.y a unit's rows.  A unit of few pieces
+// takes a warp per row; one of many (a long sequence over all CTAs) the whole
+// block per row, its warps sharing the pieces.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant__ CacheAttnParams p,
+                                                          int RT, float bias) {
+  __shared__ float s_o[8][D];
+  __shared__ float2 s_ml[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  const int n_units = __ldcg(p.hdr);
+  const int rows = p.HPC * RT;
+  for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
+    const int32_t* hd = p.hdr + 8 + 8ll * u;
+    const int4 h4 = __ldcg(reinterpret_cast<const int4*>(hd));
+    const int np = h4.x + 1;
+    if (np == 1) continue;
+    const int c0 = h4.y, r0 = h4.z, h0 = h4.w, cu0 = __ldcg(hd + 4), E = __ldcg(hd + 5);
+    const bool wide = np > 8;  // the whole block per row
+    const int step = wide ? gridDim.y : gridDim.y * 8;
+    for (int r = wide ? blockIdx.y : blockIdx.y * 8 + warp; r < rows; r += step) {
+      const int hl = r / RT, gr = r0 + r % RT, i = gr / p.G;
+      if (i >= E) continue;
+      const int qh = (h0 + hl) * p.G + gr % p.G;
+      const int s0 = wide ? warp : 0, ds = wide ? 8 : 1;
+      // Piece s of the unit: slot 2 c + 1 of its first CTA, slot 2 (c + s) after.
+      auto at = [&](int s) { return (2ll * (c0 + s) + (s == 0 ? 1 : 0)) * rows + r; };
+      float mf = -1e30f;
+      for (int s = s0 + lane * ds; s < np; s += 32 * ds)
+        mf = fmaxf(mf, __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(s)).x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xffffffffu, mf, o));
+      float acc[D / 32], l = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
+#pragma unroll 4
+      for (int s = s0; s < np; s += ds) {
+        const long long a = at(s);
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + a);
+        const float f = ex2(ml.x - mf);
+        l = fmaf(ml.y, f, l);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part_o + a * D) + 32 * k + lane);
+          acc[2 * k] = fmaf(v.x, f, acc[2 * k]);
+          acc[2 * k + 1] = fmaf(v.y, f, acc[2 * k + 1]);
+        }
+      }
+      if (wide) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+          *reinterpret_cast<float2*>(&s_o[warp][64 * k + 2 * lane]) =
+              make_float2(acc[2 * k], acc[2 * k + 1]);
+        if (lane == 0) s_ml[warp] = make_float2(mf, l);
+        __syncthreads();
+        if (warp != 0) continue;
+        mf = -1e30f;
+        for (int w = 0; w < 8; ++w) mf = fmaxf(mf, s_ml[w].x);
+        l = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
+        for (int w = 0; w < 8; ++w) {
+          const float f = ex2(s_ml[w].x - mf);
+          l = fmaf(s_ml[w].y, f, l);
+#pragma unroll
+          for (int k = 0; k < D / 64; ++k) {
+            acc[2 * k] = fmaf(s_o[w][64 * k + 2 * lane], f, acc[2 * k]);
+            acc[2 * k + 1] = fmaf(s_o[w][64 * k + 2 * lane + 1], f, acc[2 * k + 1]);
+          }
+        }
+      }
+      float xs = -INFINITY;
+      if (p.sinks != nullptr) xs = __ldg(p.sinks + qh) * kLog2e;
+      else if (p.smooth) xs = 0.f;
+      const bool any = l > 0.f;
+      const float mm = fmaxf(mf - bias, xs), f = ex2(mf - bias - mm);
+      const float den = fmaf(l, f, ex2(xs - mm));
+      const float inv = any ? f / den : 0.f;
+      const long long row = (long long)(cu0 + i) * p.Hq + qh;
+#pragma unroll
+      for (int k = 0; k < D / 64; ++k)
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + 64 * k + 2 * lane) =
+            pack2<BF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+      if (lane == 0 && p.lse != nullptr) p.lse[row] = any ? (mm + log2f(den)) * kLn2 : -INFINITY;
+    }
+  }
+}
+
+}  // namespace gqa

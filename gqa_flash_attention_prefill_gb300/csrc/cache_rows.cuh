@@ -1,0 +1,106 @@
+// cache_rows.cuh -- what the row operators around the paged cache share: the
+// lookup of a row's sequence and page, the e4m3 rows with one power-of-two
+// scale, and the rotation angles.
+//
+// An e4m3 row of a cache (one token, one KV head, d values x_0 .. x_{d-1}) is
+// held as d bytes and one byte e + 127 of scale 2^e:
+//   e = the least integer with max |x_i| <= 448 * 2^e, at least -60 and 0 for
+//       a row of zeros;   value i = e4m3(x_i * 2^-e), rounded to nearest even.
+// A power of two keeps the products exact: x_i * 2^-e rounds once, to e4m3,
+// and value * 2^e is exact again in bf16 (4 significant bits), so a cache
+// read back to bf16 holds what the attention over the e4m3 cache sees.
+// e4m3 has the same relative precision over 2^-6 .. 448, so a scale of
+// amax / 448 instead would gain at most one bit at its lower end.
+#pragma once
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace gqa {
+
+// The page table of a call (device arrays but for the counts).
+struct PageTable {
+  const int32_t* indptr;   // [num_seqs + 1]
+  const int32_t* indices;  // [entries]
+  int entries, page_size, num_pages, num_seqs;
+};
+
+// Scale exponent of an e4m3 row from the bits of its largest magnitude:
+// 448 = 1.75 * 2^8, so amax = m 2^E needs 2^(E - 8) when m <= 1.75, else
+// 2^(E - 7).
+__device__ __forceinline__ int e4m3_scale_exponent(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  if (u == 0u) return 0;
+  const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return min(max(e, -60), 127);
+}
+// 2^e as fp32, -126 <= e <= 127.
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+// First index i in [0, n) with a[i] > x (n when there is none) for a
+// non-decreasing a, found by a converged warp: 32 probes a step, so 1024
+// sequences take two dependent loads.  Any array gives an index in [0, n].
+__device__ __forceinline__ int warp_upper_bound(const int32_t* a, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;  // the answer lies in [lo, lo + len]
+  while (len > 0) {
+    const int step = (len + 31) >> 5;
+    const int i = lo + (lane + 1) * step - 1;  // last index of this lane's block
+    const bool le = i < lo + len && __ldg(a + i) <= x;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));  // blocks wholly <= x
+    const int at = c * step;
+    if (step == 1) return lo + at;
+    lo += at;
+    len = min(step, len - at);
+  }
+  return lo;
+}
+
+// Where a row lives: its sequence's key index, and the pool row (page *
+// page_size + slot); slot < 0 when the row belongs to no sequence or its
+// metadata is bad (then *bad is set).
+struct RowPlace {
+  int key;
+  long long slot;
+};
+
+// Lookup of key `key` of sequence b by one lane.
+__device__ __forceinline__ long long key_slot(const PageTable& pt, int b, long long key, bool* bad) {
+  const int i0 = __ldg(pt.indptr + b), i1 = __ldg(pt.indptr + b + 1);
+  const long long at = (long long)i0 + key / pt.page_size;
+  if (key < 0 || i0 < 0 || at >= i1 || at >= pt.entries) {
+    *bad = true;
+    return -1;
+  }
+  const int page = __ldg(pt.indices + at);
+  if (page < 0 || page >= pt.num_pages) {
+    *bad = true;
+    return -1;
+  }
+  return (long long)page * pt.page_size + key % pt.page_size;
+}
+
+// cos and sin of position * frequency.  `step` is the angle per position in
+// units of 2^-64 turns, so position * step modulo 2^64 is the phase within
+// one turn, exact for every position: a product in fp32 would be off by 0.06
+// radians at a million positions, one in fp64 costs the slow units.  The
+// phase is rounded once to fp32 (a signed half turn, 2^-25 of it at most).
+__device__ __forceinline__ float2 phase_cos_sin(int pos, unsigned long long step) {
+  const unsigned long long ph = (unsigned long long)(long long)pos * step;
+  const float half_turns = (float)(int)(ph >> 32) * 4.656612873077393e-10f;  // 2^-31
+  float2 cs;
+  sincospif(half_turns, &cs.y, &cs.x);
+  return cs;
+}
+// The step of a frequency in radians per position (|f| < 2^20, say): turns
+// modulo one, in 2^-64.
+__device__ __forceinline__ unsigned long long phase_step(double f) {
+  const double turns = f * 0.15915494309189533577;  // 1 / (2 pi)
+  const double frac = turns - floor(turns);           // [0, 1]
+  return (unsigned long long)__double2ull_rn(frac * 9223372036854775808.0) << 1;  // 2^63, then * 2
+}
+
+}  // namespace gqa

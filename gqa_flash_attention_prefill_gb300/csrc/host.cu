@@ -871,6 +871,18 @@ int run_splitkv_scratch(const void* q, const void* k, const void* v, const int32
              stream, nullptr, num_splits, nullptr, 0, scratch);
 }
 
+int call_device(int* sms, unsigned int** status) {
+  DeviceInfo di;
+  if (device_info(&di) != GQA_OK) return GQA_ERR_CUDA;
+  *sms = di.sms;
+  *status = di.status;
+  return GQA_OK;
+}
+
+unsigned long long wait_limit_ns() { return timeout_ns(); }
+
+bool metadata_ready_flag() { return (t_call_flags & GQA_FLAG_METADATA_READY) != 0u; }
+
 bool kernel_shape(int d, int block_n, int q_tiles, KernelShape* out) {
   KernelShape s;
   s.block_n = block_n;

@@ -1,0 +1,11 @@
+// inst_cache_d256.cu -- gqa_cache_attention's kernels for head dim 256.
+#include "cache_attn.h"
+
+namespace gqa {
+
+cudaError_t launch_cache_attn_d256(const CacheAttnParams& p, bool bf16, bool c8, int, int grid,
+                                  unsigned smem, int merge_x, int merge_y, cudaStream_t st) {
+  return launch_cache_attn_types<256, 1>(p, bf16, c8, grid, smem, merge_x, merge_y, st);
+}
+
+}  // namespace gqa

@@ -1,0 +1,12 @@
+// inst_cache_d64.cu -- gqa_cache_attention's kernels for head dim 64.
+#include "cache_attn.h"
+
+namespace gqa {
+
+cudaError_t launch_cache_attn_d64(const CacheAttnParams& p, bool bf16, bool c8, int mt, int grid,
+                                  unsigned smem, int merge_x, int merge_y, cudaStream_t st) {
+  if (mt == 2) return launch_cache_attn_types<64, 2>(p, bf16, c8, grid, smem, merge_x, merge_y, st);
+  return launch_cache_attn_types<64, 1>(p, bf16, c8, grid, smem, merge_x, merge_y, st);
+}
+
+}  // namespace gqa

@@ -61,6 +61,13 @@ cudaError_t launch_merge(const PrefillParams& p, int d, bool bf16, int part_rows
 // since a device reset makes a new context that may load the module elsewhere.
 void* current_context();
 
+// What a launch takes from the host code (host.cu): the current device's SM
+// count and status word (GQA_OK or GQA_ERR_CUDA), the limit of a bounded wait
+// inside a kernel, and whether the calling thread declared its metadata ready.
+int call_device(int* sms, unsigned int** status);
+unsigned long long wait_limit_ns();
+bool metadata_ready_flag();
+
 // Scratch provider of a split-KV call without a caller workspace: given the
 // bytes the call's plan needs, stores the scratch address and its capacity,
 // or returns GQA_ERR_UNSUPPORTED when the need exceeds the capacity.

@@ -383,3 +383,69 @@ def paged(batch: Batch, page_size: int, spare_pages: int = 3, seed: int = 0,
         indptr.append(len(indices))
     return PagedBatch(batch, k_pages, v_pages, torch.tensor(indptr, dtype=torch.int32),
                       torch.tensor(indices, dtype=torch.int32), page_size)
+
+
+@dataclass
+class Cache:
+    """A page pool for a batch of sequences and their page table.  kind "16":
+    pages of the batch's type; "e4m3": bytes with one scale byte per token and
+    head (value = e4m3 * 2^(byte - 127))."""
+    k_pages: torch.Tensor    # [num_pages, page_size, Hkv, d]
+    v_pages: torch.Tensor
+    k_scales: Optional[torch.Tensor]  # uint8 [num_pages, page_size, Hkv] or None
+    v_scales: Optional[torch.Tensor]
+    page_indptr: torch.Tensor   # int32 [B+1]
+    page_indices: torch.Tensor  # int32 [entries]
+    kind: str
+
+
+def empty_cache(lengths, hkv, d, page_size, dtype="bf16", kind="16", spare_pages=2, seed=0,
+                device="cpu") -> Cache:
+    """A cache with room for sequences of the given lengths: their pages in a
+    seeded random order over the pool, contents zero (scale bytes zero too)."""
+    counts = [-(-int(n) // page_size) for n in lengths]
+    used = sum(counts)
+    gen = torch.Generator().manual_seed(int(seed) * 7243 + page_size)
+    order = torch.randperm(used + spare_pages, generator=gen)[:used].to(torch.int32)
+    indptr = [0]
+    for c in counts:
+        indptr.append(indptr[-1] + c)
+    dt = torch.float8_e4m3fn if kind == "e4m3" else (DTYPES[dtype] if isinstance(dtype, str) else dtype)
+    shape = (used + spare_pages, page_size, hkv, d)
+    pages = [torch.zeros(shape, dtype=torch.uint8, device=device).view(dt) if kind == "e4m3"
+             else torch.zeros(shape, dtype=dt, device=device) for _ in range(2)]
+    scales = [torch.zeros(shape[:3], dtype=torch.uint8, device=device) if kind == "e4m3" else None
+              for _ in range(2)]
+    return Cache(pages[0], pages[1], scales[0], scales[1],
+                 torch.tensor(indptr, dtype=torch.int32, device=device), order.to(device), kind)
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original=4096,
+                     fast_turns=32.0, slow_turns=1.0):
+    """(inv_freq fp64 [rot_dim / 2], attn_factor) of rotary positions: pair i
+    turns base^(-2 i / rot_dim) radians per position.  scaling for contexts
+    `factor` times the `original` length: "linear" divides every frequency by
+    the factor; "base" stretches the base so that the slowest pair is divided
+    by it; "blend" divides the pairs that turn less than slow_turns times over
+    the original length, keeps those that turn more than fast_turns times,
+    blends linearly in the pair's index between, and scales the rotated
+    values by 0.1 ln(factor) + 1."""
+    import math
+    if rot_dim <= 0 or rot_dim % 2 or base <= 1 or factor < 1:
+        raise ValueError("rot_dim must be even and positive, base > 1, factor >= 1")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    if scaling == "none":
+        return base ** (-i / rot_dim), 1.0
+    if scaling == "linear":
+        return base ** (-i / rot_dim) / factor, 1.0
+    if scaling == "base":
+        if rot_dim < 4:
+            raise ValueError("scaling the base needs rot_dim of 4 or more")
+        return (base * factor ** (rot_dim / (rot_dim - 2))) ** (-i / rot_dim), 1.0
+    if scaling != "blend":
+        raise ValueError('scaling must be "none", "linear", "base" or "blend"')
+    inv = base ** (-i / rot_dim)
+    lo, hi = (rot_dim * math.log(original / (t * 2 * math.pi)) / (2 * math.log(base))
+              for t in (fast_turns, slow_turns))
+    ramp = ((i / 2 - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+    return inv / factor * ramp + inv * (1 - ramp), 0.1 * math.log(factor) + 1.0

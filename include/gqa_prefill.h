@@ -198,6 +198,163 @@ GQA_API int gqa_flash_prefill_paged(const void* q, const void* k_pages,
                                     const float* sinks, int smooth_softmax,
                                     void* out, float* lse, void* stream);
 
+/* Element type of a page pool: q's 16-bit type, or e4m3 with scales. */
+enum { GQA_CACHE_16 = 0, GQA_CACHE_E4M3 = 1 };
+
+/*
+ * Rotary positions: the first rot_dim values of a head rotate in pairs, pair
+ * i by the angle t = position * inv_freq[i]:
+ *     (a, b) -> attn_factor * (a cos t - b sin t, b cos t + a sin t).
+ * Pairs are (x[i], x[i + rot_dim / 2]), or neighbours (x[2 i], x[2 i + 1])
+ * when interleaved; values from rot_dim on pass unchanged.  The angle is
+ * exact modulo a turn for every int32 position; long-context scalings are
+ * the caller's choice of inv_freq and attn_factor.  Arithmetic is fp32,
+ * rounded once.
+ *
+ *   positions    device int32 [rows].  gqa_cache_write: NULL for
+ *                prefix_lens[b] + i.
+ *   inv_freq     device fp64 [rot_dim / 2], radians per position.
+ *   rot_dim      even, 2 .. d
+ *   interleaved  0 or 1
+ *   inverse      0 or 1: rotate by -t (attn_factor unchanged), which is the
+ *                gradient of the forward rotation with respect to its input;
+ *                0 in gqa_cache_write.
+ *   q, q_out     [rows] of Hq * d values, rows q_stride / q_out_stride
+ *                elements apart (multiples of 8, at least Hq * d), bases
+ *                16-byte aligned.  Hq = 0: no q.
+ * Output rows must not share memory with their input rows (the range from the
+ * first row to the last).
+ */
+typedef struct {
+    const int32_t* positions;
+    const double* inv_freq;
+    int rot_dim;
+    int interleaved;
+    int inverse;
+    float attn_factor;
+    int Hq;
+    const void* q;
+    long long q_stride;
+    void* q_out;
+    long long q_out_stride;
+} gqa_rope_t;
+
+/*
+ * gqa_rope -- rotates the query rows of `rope` and the key rows k into
+ * rope->q_out and k_out (Hkv = 0: no k).  d is any multiple of 8 up to 1024
+ * with rot_dim <= 512, else GQA_ERR_UNSUPPORTED; f16 or bf16; k and k_out as
+ * q and q_out.  Returns GQA_OK or a negative GQA_ERR_* code.
+ */
+GQA_API int gqa_rope(const gqa_rope_t* rope, const void* k, long long k_stride, void* k_out,
+                     long long k_out_stride, int rows, int Hkv, int d, int dtype, void* stream);
+
+/*
+ * gqa_cache_write -- writes the new tokens' K and V into their pages, before
+ * the attention that reads them.  Row i of sequence b (rows cu_seqlens_q[b]
+ * .. cu_seqlens_q[b + 1] - 1 of k and v) becomes key prefix_lens[b] + i: slot
+ * key % page_size of page kv_page_indices[kv_page_indptr[b] + key /
+ * page_size].  With `rope` (NULL: none) k is rotated on its way, and
+ * rope->q into rope->q_out in the same kernel.
+ *
+ *   k, v          [total_q] rows of Hkv * d values (f16 or bf16), k_stride and
+ *                 v_stride elements apart, as gqa_rope_t.q: slices of a packed
+ *                 projection will do
+ *   cache_type    GQA_CACHE_16: pages of k's type; GQA_CACHE_E4M3: see below
+ *   k_pages, v_pages  [num_pages, page_size, Hkv, d], 16-byte aligned;
+ *                 page_size a multiple of 8
+ *   k_scales, v_scales  GQA_CACHE_E4M3: bytes [num_pages, page_size, Hkv];
+ *                 else ignored
+ *   d             64, 128 or 256
+ *
+ * An e4m3 row (one token, one head) has the scale 2^e, stored as the byte
+ * e + 127, with e the least integer for which the row's largest magnitude is
+ * at most 448 * 2^e (e >= -60; e = 0 for a row of zeros); a value is x * 2^-e
+ * rounded to the nearest e4m3, ties to even.  An infinity becomes +-448 times
+ * its row's scale, NaN stays NaN and does not count in the row's magnitude.
+ *
+ * Rows that belong to no sequence are not read; pages and slots that no row
+ * maps to are left as they were.  A row whose metadata is inconsistent (a key
+ * past the sequence's pages, a page outside the pool) is not written and
+ * raises GQA_DEV_BAD_METADATA.  Rows that share a slot (two sequences with
+ * the same page) race.  Returns as gqa_flash_prefill.
+ */
+GQA_API int gqa_cache_write(const void* k, long long k_stride, const void* v, long long v_stride,
+                            const int32_t* cu_seqlens_q, const int32_t* prefix_lens,
+                            const int32_t* kv_page_indptr, const int32_t* kv_page_indices,
+                            int num_page_entries, int page_size, int num_pages, int num_seqs,
+                            int total_q, int Hkv, int d, int dtype, int cache_type, void* k_pages,
+                            void* v_pages, void* k_scales, void* v_scales, const gqa_rope_t* rope,
+                            void* stream);
+
+/*
+ * gqa_cache_read -- gathers keys and values out of the pages into contiguous
+ * 16-bit rows, the layout gqa_flash_prefill reads.  Sequence b fills rows
+ * kv_indptr[b] .. kv_indptr[b + 1] - 1 of k_out and v_out [total_kv, Hkv, d]
+ * with its keys first_keys[b] .. (first_keys NULL: from key 0; a
+ * window-bounded prefix starts at max(0, length - window)).  An e4m3 value
+ * times its scale is rounded once to dtype; in bf16 the result is exact.
+ * Rows outside every sequence are left as they were; bad metadata as
+ * gqa_cache_write.  Returns as gqa_flash_prefill.
+ */
+GQA_API int gqa_cache_read(const void* k_pages, const void* v_pages, const void* k_scales,
+                           const void* v_scales, int cache_type, const int32_t* kv_page_indptr,
+                           const int32_t* kv_page_indices, int num_page_entries, int page_size,
+                           int num_pages, const int32_t* kv_indptr, const int32_t* first_keys,
+                           int num_seqs, int total_kv, int Hkv, int d, int dtype, void* k_out,
+                           void* v_out, void* stream);
+
+/*
+ * gqa_cache_attention -- attention of a few new tokens per sequence over a
+ * paged cache: one decoded token each, or a tree of drafted tokens.  The
+ * operation is gqa_flash_prefill_paged's (whose keys of the new tokens are in
+ * the pages already, see gqa_cache_write), with
+ *   - an e4m3 pool (cache_type GQA_CACHE_E4M3, k_scales and v_scales, 16-byte
+ *     aligned; page_size * Hkv must be a multiple of 16) besides the 16-bit
+ *     one: the attention over the values times their scales;
+ *   - any page_size that is a multiple of 8;
+ *   - custom_mask and mask_indptr (both or neither) as in
+ *     gqa_flash_prefill_masked: per sequence a bitmap over its new tokens,
+ *     row i keeping new token j <= i only if bit j is set: the ancestors of a
+ *     drafted token;
+ *   - depths, device int32 [total_q] or NULL: token i's position is
+ *     prefix_lens[b] + depths[i], with depths[i] in 0 .. i, where the window
+ *     counts positions (tokens of one depth are alternatives for one
+ *     position).  NULL: position prefix_lens[b] + i.  Causality stays with
+ *     the order of the rows.
+ *   - G = Hq / Hkv of any size.
+ * The key range of every unit is split over the CTAs in equal shares found on
+ * the device, and cut units are joined by a second kernel, so one long
+ * sequence fills the GPU as a large batch does.
+ *
+ *   workspace     device memory of the caller, 256-byte aligned, at least
+ *                 what gqa_cache_attention_workspace() reports for the same
+ *                 shapes; its contents before and after the call mean nothing.
+ *                 Calls that may run at the same time, captured graphs
+ *                 included, need one each.
+ *   max_seqlen_q  as gqa_flash_prefill; with 0 the launch is shaped for one
+ *                 sequence of total_q tokens.
+ *
+ * Keys that no row of a sequence sees (the rest of its last page, keys below
+ * the window) may hold anything; keys that some row sees must hold finite
+ * values.  A row with no key gets out = 0 and lse = -inf.  The result is the
+ * same run to run.  Errors as gqa_flash_prefill_paged; a missing or small
+ * workspace is GQA_ERR_INVALID.
+ */
+GQA_API int gqa_cache_attention(const void* q, const void* k_pages, const void* v_pages,
+                                const void* k_scales, const void* v_scales, int cache_type,
+                                const int32_t* cu_seqlens_q, const int32_t* prefix_lens,
+                                const int32_t* kv_page_indptr, const int32_t* kv_page_indices,
+                                int num_page_entries, int page_size, int num_pages, int num_seqs,
+                                int total_q, int max_seqlen_q, int Hq, int Hkv, int d, int dtype,
+                                float scale, int window, const float* sinks, int smooth_softmax,
+                                const uint32_t* custom_mask, const int32_t* mask_indptr,
+                                long long total_mask_words, const int32_t* depths, void* out,
+                                float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of a gqa_cache_attention call with these shapes (host only). */
+GQA_API int gqa_cache_attention_workspace(int num_seqs, int total_q, int max_seqlen_q, int Hq,
+                                          int Hkv, int d, int dtype, int cache_type, size_t* bytes);
+
 /* num_splits value selecting the balanced split (see below). */
 #define GQA_SPLITS_BALANCED (-1)
 
