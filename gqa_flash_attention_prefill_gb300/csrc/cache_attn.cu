@@ -15,7 +15,7 @@ namespace {
 constexpr unsigned kSmemMax = 227u * 1024u;
 
 struct CachePlan {
-  int G, HPC, HG, KW, MT, T, NS;
+  int G, HPC, HG, KW, NT, T, NS;
   uint32_t data_bytes, slot_bytes;
   int ctas, max_units;  // per launch of at most kMaxSeqs sequences
   size_t ml_off, hdr_off, bytes;
@@ -33,24 +33,25 @@ int cache_plan(int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hkv, int
   pl->G = Hq / Hkv;
   if (Hkv > 4096 || (long long)total_q * pl->G >= (1ll << 30)) return GQA_ERR_UNSUPPORTED;
   // Rows of the longest sequence (all of them, without the hint) decide how
-  // many 16-row tiles share each key a warp loads.
+  // many 8-row tiles share each key a warp loads.
   const long long rows = (long long)(max_seqlen_q > 0 ? max_seqlen_q : total_q) * pl->G;
-  const int mt = cache_attn_max_mt(d);
-  pl->MT = rows > 16 ? mt : 1;
-  const int gk = ca_gk(d, c8, pl->MT), esz = c8 ? 1 : 2;
-  // Heads per CTA: the largest divisor of Hkv up to the warps; the warps left
+  pl->NT = 1;
+  while (pl->NT < cache_attn_max_nt(d) && rows > 8 * pl->NT) pl->NT *= 2;
+  const int gk = ca_gk(d, c8, pl->NT), esz = c8 ? 1 : 2;
+  const int warps = ca_warps(d, c8, pl->NT);
+  // Heads per CTA: the largest divisor of Hkv up to 8; the warps left
   // over share the heads' keys.  A tile that would leave the ring fewer than
   // four slots (two tiles) takes fewer warps per head, then fewer heads.
-  int hpc = Hkv < kCaWarps ? Hkv : kCaWarps;
+  int hpc = Hkv < 8 ? Hkv : 8;
   while (Hkv % hpc != 0) --hpc;
-  int kw = kCaWarps / hpc;
+  int kw = warps / hpc;
   for (;;) {
     pl->HPC = hpc;
     pl->KW = kw;
     pl->T = 16 * gk * kw;
     pl->data_bytes = (uint32_t)pl->T * hpc * d * esz;
     pl->slot_bytes = pl->data_bytes + (c8 ? ((uint32_t)pl->T * Hkv + 127u) / 128u * 128u : 0u);
-    pl->NS = (int)((kSmemMax - ca_fixed_smem()) / pl->slot_bytes);
+    pl->NS = (int)((kSmemMax - ca_fixed_smem(warps)) / pl->slot_bytes);
     if (pl->NS > kCaMaxSlots) pl->NS = kCaMaxSlots;
     if (pl->NS >= 4) break;
     if (kw > 1) {
@@ -69,7 +70,7 @@ int cache_plan(int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hkv, int
   if (call_device(&sms, &status) != GQA_OK) sms = 152;
   pl->ctas = sms;
   const int seqs = num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs;
-  const int rt = 16 * pl->MT;
+  const int rt = 8 * pl->NT;
   const long long units =
       (long long)pl->HG * (((long long)total_q * pl->G + rt - 1) / rt + (long long)seqs);
   if (units > (1ll << 26)) return GQA_ERR_UNSUPPORTED;
@@ -174,11 +175,11 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
       merge_x = 0;
     }
   }
-  const int rows = pl.HPC * 16 * pl.MT;
+  const int rows = pl.HPC * 8 * pl.NT;
   int merge_y = merge_x > 0 ? 8 * pl.ctas / merge_x : 1;
   if (merge_y > rows) merge_y = rows;
   if (merge_y < 1) merge_y = 1;
-  const unsigned smem = ca_fixed_smem() + (unsigned)pl.NS * pl.slot_bytes;
+  const unsigned smem = ca_fixed_smem(ca_warps(d, c8, pl.NT)) + (unsigned)pl.NS * pl.slot_bytes;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   for (int b0 = 0; b0 < num_seqs; b0 += kMaxSeqs) {
     p.cu = cu + b0;
@@ -189,9 +190,9 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
     p.num_seqs = num_seqs - b0 < kMaxSeqs ? num_seqs - b0 : kMaxSeqs;
     const bool bf16 = dtype == GQA_BF16;
     const cudaError_t e =
-        d == 64    ? launch_cache_attn_d64(p, bf16, c8, pl.MT, pl.ctas, smem, merge_x, merge_y, st)
-        : d == 128 ? launch_cache_attn_d128(p, bf16, c8, pl.MT, pl.ctas, smem, merge_x, merge_y, st)
-                   : launch_cache_attn_d256(p, bf16, c8, pl.MT, pl.ctas, smem, merge_x, merge_y, st);
+        d == 64    ? launch_cache_attn_d64(p, bf16, c8, pl.NT, pl.ctas, smem, merge_x, merge_y, st)
+        : d == 128 ? launch_cache_attn_d128(p, bf16, c8, pl.NT, pl.ctas, smem, merge_x, merge_y, st)
+                   : launch_cache_attn_d256(p, bf16, c8, pl.NT, pl.ctas, smem, merge_x, merge_y, st);
     if (e != cudaSuccess) return GQA_ERR_CUDA;
   }
   return GQA_OK;

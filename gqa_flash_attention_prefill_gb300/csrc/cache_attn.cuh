@@ -22,15 +22,19 @@
 // burst read whole.  The G query heads of the tokens are the rows of the
 // products: few (8 for one token of a 64 / 8 head model), so the products are
 // m16n8k16 warp instructions whose operands are converted from e4m3 in
-// registers; a 128-row tensor-memory tile would be 94% padding there.
+// registers; a 128-row tensor-memory tile would be 94% padding there.  They
+// are taken transposed, S^T = K Q^T and O^T = V^T P^T: the keys (the head's
+// values) fill the 16-row side and the queries the 8-column side, so 8 rows
+// waste nothing.  (With the rows on the 16-row side half of every product and
+// of the softmax was padding: 256 sequences of 1k..16k e4m3 keys 689 us.)
 //
 // Fragment order.  A contraction may run in any order, so the fragments are
-// laid out by what one wide shared-memory load brings: lane (g, t) = (lane /
-// 4, lane % 4) loads 16 bytes of key 4 (g / 2) + 2 tau + g % 2 for the score
-// tile tau of a 16-key group, which puts keys 4 t .. 4 t + 3 into its
-// accumulators: exactly the keys whose V rows it then loads, 8 values at 8 g.
-// The transposition that the second product needs is the byte interleave of
-// the conversion.
+// laid out by what one wide shared-memory load brings.  Lane (g, t) = (lane /
+// 4, lane % 4).  Row m of a 16-key score tile is key ca_key(m); lane (g, t)
+// loads 16 bytes of keys ca_key(g) and ca_key(g + 8) and later, for the second
+// product, 8 values at 8 g of the keys 4 t .. 4 t + 3, which are the keys that
+// an 8x8 transpose of P hands it.  The transposition of V is the byte
+// interleave of its conversion.
 //
 // Work split.  Every CTA takes an equal share of all (sequence, row tile,
 // head group) key tiles laid end to end (lengths are device data: the split
@@ -48,8 +52,11 @@
 
 namespace gqa {
 
-constexpr int kCaWarps = 8;                        // consumer warps
-constexpr int kCaThreads = 32 * (kCaWarps + 1);    // and one producer warp
+// Consumer warps; one producer warp follows them.  16 where the accumulators
+// leave room for them (96 registers a thread), else 8 (168 registers).
+__host__ __device__ constexpr int ca_warps(int D, bool C8, int NT) {
+  return NT == 1 && (D == 64 || (D == 128 && C8)) ? 16 : 8;
+}
 constexpr int kCaMaxSlots = 16;                    // ring slots at most
 constexpr float kCaSlack = 4.f;
 constexpr int kCaWholeSlack = 6;                   // tiles a join is worth
@@ -92,14 +99,20 @@ struct CacheAttnParams {
   int metadata_ready;
 };
 
-// Rows of a unit: MT tiles of 16.  GK: 16-key groups a warp takes per tile.
-__host__ __device__ constexpr int ca_gk(int D, bool C8, int MT) {
-  return MT == 1 && D * (C8 ? 1 : 2) <= 128 ? 2 : 1;
+// Rows of a unit: NT tiles of 8.  GK: 16-key groups a warp takes per tile.
+__host__ __device__ constexpr int ca_gk(int D, bool C8, int NT) {
+  return NT == 1 && D == 64 && C8 ? 2 : 1;
 }
-constexpr uint32_t kCaScratch = kCaWarps * 16u * 64u * 4u;  // per warp 16 rows x 64 columns fp32
-__host__ __device__ constexpr uint32_t ca_fixed_smem() {
-  return 1024u + 128u + kCaScratch + kCaWarps * 16u * 8u + 2u * kCaMaxSlots * 8u + 32u +
-         8u * (kMaxSeqs + 1) + 4u * (4 * kMaxSeqs + 2) + 8u * 16u;
+// Key of row m of a 16-key score tile: the transposed P gives lane t the rows
+// 2 t, 2 t + 1, 2 t + 8, 2 t + 9, which are keys 4 t .. 4 t + 3.
+__device__ __forceinline__ int ca_key(int m) {
+  return 4 * ((m & 7) >> 1) + (m & 1) + 2 * (m >> 3);
+}
+// Shared memory besides the ring: per warp an area of 8 rows x 64 columns
+// fp32 and its rows' (M, L), the barriers, the tables of the sequences.
+__host__ __device__ constexpr uint32_t ca_fixed_smem(int warps) {
+  return 1024u + 128u + (uint32_t)warps * (8u * 64u * 4u + 8u * 8u) + 2u * kCaMaxSlots * 8u + 32u +
+         8u * (kMaxSeqs + 1) + 4u * (4 * kMaxSeqs + 2) + 8u * 20u + 4u * 20u;
 }
 
 struct CaTab {
@@ -243,6 +256,13 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
   return r;
 }
+// 8x8 transpose of 16-bit pairs over the warp: lane (g, t) gives (row g,
+// columns 2 t, 2 t + 1) and receives (column g, rows 2 t, 2 t + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   uint32_t r;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
@@ -250,12 +270,14 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
 }
 
 // D: head dim.  BF16: type of q and out.  C8: e4m3 cache (products in f16),
-// else the cache has q's type.  MT: 16-row tiles per warp.
-template <int D, bool BF16, bool C8, int MT>
-__global__ void __launch_bounds__(kCaThreads, 1)
+// else the cache has q's type.  NT: 8-row tiles per warp.
+template <int D, bool BF16, bool C8, int NT>
+__global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
-  constexpr int GK = ca_gk(D, C8, MT);
-  constexpr int RT = 16 * MT;
+  constexpr int NW = ca_warps(D, C8, NT);
+  constexpr int kThreads = 32 * (NW + 1);
+  constexpr int GK = ca_gk(D, C8, NT);
+  constexpr int RT = 8 * NT;
   constexpr bool MBF = BF16 && !C8;          // product type
   constexpr float kBias = MBF ? 0.f : 10.f;  // 2^(kCaSlack + kBias) fits f16
   constexpr int kEsz = C8 ? 1 : 2;
@@ -263,13 +285,14 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* scratch = reinterpret_cast<float*>(smem);  // [8][16][64]
-  float2* s_ml = reinterpret_cast<float2*>(smem + kCaScratch);  // [8][16]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_ml + kCaWarps * 16);
+  float* scratch = reinterpret_cast<float*>(smem);                 // [NW][8][64]
+  float2* s_ml = reinterpret_cast<float2*>(scratch + NW * 8 * 64);  // [NW][8]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_ml + NW * 8);
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kCaMaxSlots);  // [0] abort [1] bad
   long long* tiles = reinterpret_cast<long long*>(misc + 8);
   long long* wtot = tiles + (kMaxSeqs + 1);
-  int32_t* units = reinterpret_cast<int32_t*>(wtot + 16);
+  int32_t* utot = reinterpret_cast<int32_t*>(wtot + 20);
+  int32_t* units = utot + 20;
   int32_t* s_cu = units + (kMaxSeqs + 1);
   int32_t* s_pre = s_cu + (kMaxSeqs + 1);
   int32_t* s_ipt = s_pre + kMaxSeqs;
@@ -299,7 +322,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   bool bad = tid == 0 && p.first_seq == 0 && __ldg(p.cu) != 0;
   long long my_tiles = 0;
   int my_units = 0, my_max = 0;
-  const int per = (nseq + kCaThreads - 1) / kCaThreads;
+  const int per = (nseq + kThreads - 1) / kThreads;
   const int b_lo = min(tid * per, nseq), b_hi = min(b_lo + per, nseq);
   for (int b = b_lo; b < b_hi; ++b) {
     const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), P = __ldg(p.pre + b);
@@ -351,7 +374,6 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       iu += b;
     }
   }
-  int* utot = reinterpret_cast<int*>(s_ml);
   if (lane == 31) {
     wtot[warp] = it;
     utot[warp] = iu;
@@ -410,7 +432,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   const uint32_t row_bytes = (uint32_t)p.HPC * D * kEsz;        // a token's values in the ring
   const long long tok_bytes = (long long)p.Hkv * D * kEsz;      // in the pool
 
-  if (warp == kCaWarps) {
+  if (warp == NW) {
     // -------------------------------------------------------------- producer
     // The tile's runs are spread over the lanes; slots alternate K and V.
     uint32_t slot = 0, ph = 0, issued = 0;
@@ -487,110 +509,119 @@ __global__ void __launch_bounds__(kCaThreads, 1)
   while (ok && ca_next(p, T, walk, RT, u)) {
     const int head = u.hg * p.HPC + hl;  // KV head
     const int cu0 = T.cu0[u.b];
-    // The thread's rows: g and g + 8 of every 16-row tile.
-    int ri[MT][2], rdep[MT][2];  // token index (-1: none) and depth
-    float rs[MT][2];             // scale to the log2 domain
-    uint32_t qf[MT][KS][4];
+    // Softmax rows of the thread: 2 t and 2 t + 1 of every 8-row tile.
+    int ri[NT][2], rdep[NT][2];  // token index (-1: none) and depth
+    float rs[NT][2];             // scale to the log2 domain
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < NT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = u.rt * RT + m * 16 + g + 8 * h;
-        const int i = r / p.G;
+        const int i = (u.rt * RT + m * 8 + 2 * t + h) / p.G;
         const bool on = i < u.E;
         ri[m][h] = on ? i : -1;
         rdep[m][h] = i;
         if (on && p.depths != nullptr) rdep[m][h] = __ldg(p.depths + cu0 + i);
-        const uint16_t* qr = static_cast<const uint16_t*>(p.q) +
-                             ((long long)(cu0 + (on ? i : 0)) * p.Hq + head * p.G + r % p.G) * D;
         rs[m][h] = p.scale_log2;
-        if constexpr (C8) {
-          // f16 operands: the row scaled by the power of two that brings its
-          // largest magnitude into [1, 2); smaller values round at 2^-25.
-          float x[KS][4], amax = 0.f;
+      }
+    // Query fragments: row g of every tile.
+    uint32_t qf[NT][KS][2];
 #pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            const uint2 w = on ? __ldg(reinterpret_cast<const uint2*>(
-                                     qr + 64 * (s >> 2) + 16 * t + 4 * (s & 3)))
-                               : make_uint2(0u, 0u);
-            x[s][0] = unpack_lo<BF16>(w.x), x[s][1] = unpack_hi<BF16>(w.x);
-            x[s][2] = unpack_lo<BF16>(w.y), x[s][3] = unpack_hi<BF16>(w.y);
+    for (int m = 0; m < NT; ++m) {
+      const int r = u.rt * RT + m * 8 + g;
+      const int i = r / p.G;
+      const bool on = i < u.E;
+      const uint16_t* qr = static_cast<const uint16_t*>(p.q) +
+                           ((long long)(cu0 + (on ? i : 0)) * p.Hq + head * p.G + r % p.G) * D;
+      if constexpr (C8) {
+        // f16 operands: the row scaled by the power of two that brings its
+        // largest magnitude into [1, 2); smaller values round at 2^-25.
+        uint2 w[KS];
+        float amax = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fabsf(x[s][j]));
-          }
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
-          const float f = __int_as_float((127 - e) << 23);
-          rs[m][h] = p.scale_log2 * __int_as_float((127 + e) << 23);
+        for (int s = 0; s < KS; ++s) {
+          w[s] = on ? __ldg(reinterpret_cast<const uint2*>(qr + 64 * (s >> 2) + 16 * t + 4 * (s & 3)))
+                    : make_uint2(0u, 0u);
+          amax = max3(amax, fabsf(unpack_lo<BF16>(w[s].x)), fabsf(unpack_hi<BF16>(w[s].x)));
+          amax = max3(amax, fabsf(unpack_lo<BF16>(w[s].y)), fabsf(unpack_hi<BF16>(w[s].y)));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -100), 126);
+        const float f = __int_as_float((127 - e) << 23);
 #pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            qf[m][s][h] = pack2<false>(x[s][0] * f, x[s][1] * f);
-            qf[m][s][2 + h] = pack2<false>(x[s][2] * f, x[s][3] * f);
-          }
-        } else {
+        for (int s = 0; s < KS; ++s) {
+          qf[m][s][0] = pack2<false>(unpack_lo<BF16>(w[s].x) * f, unpack_hi<BF16>(w[s].x) * f);
+          qf[m][s][1] = pack2<false>(unpack_lo<BF16>(w[s].y) * f, unpack_hi<BF16>(w[s].y) * f);
+        }
 #pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            const uint2 w = on ? __ldg(reinterpret_cast<const uint2*>(
-                                     qr + 32 * (s >> 1) + 8 * t + 4 * (s & 1)))
-                               : make_uint2(0u, 0u);
-            qf[m][s][h] = w.x;
-            qf[m][s][2 + h] = w.y;
-          }
+        for (int h = 0; h < 2; ++h)  // lane 4 r holds row r's exponent
+          rs[m][h] *= __int_as_float((127 + __shfl_sync(0xffffffffu, e, 4 * (2 * t + h))) << 23);
+      } else {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const uint2 w = on ? __ldg(reinterpret_cast<const uint2*>(
+                                   qr + 32 * (s >> 1) + 8 * t + 4 * (s & 1)))
+                             : make_uint2(0u, 0u);
+          qf[m][s][0] = w.x;
+          qf[m][s][1] = w.y;
         }
       }
-    float o[MT][D / 8][4];
-    float M[MT][2], L[MT][2];
+    }
+    float o[NT][D / 16][4];  // [tile][16 values][(value g, g + 8) x (row 2 t, 2 t + 1)]
+    float M[NT][2], L[NT][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int m = 0; m < NT; ++m) {
       M[m][0] = M[m][1] = -1e30f;
       L[m][0] = L[m][1] = 0.f;
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
+      for (int n = 0; n < D / 16; ++n) o[m][n][0] = o[m][n][1] = o[m][n][2] = o[m][n][3] = 0.f;
     }
+    const uint32_t koff = (uint32_t)(kw * 16 * GK + ca_key(g)) * row_bytes +
+                          (uint32_t)(hl * D * kEsz) + 16u * t;
+    const uint32_t voff = (uint32_t)(kw * 16 * GK + 4 * t) * row_bytes +
+                          (uint32_t)(hl * D * kEsz + 8 * kEsz * g);
+    const uint32_t soff = p.data_bytes + (uint32_t)((kw * 16 * GK + ca_key(g)) * p.Hkv + head);
 
     for (int tl = u.t0; tl < u.t1; ++tl) {
       const int n0 = u.lo + tl * p.T + kw * 16 * GK;  // this warp's first key
       // ---- scores of 16 GK keys
       if (!(ok = wait_full(slot, ph))) break;
-      float s[MT][2 * GK][4];
-      float ks[GK][4];
+      float s[NT][GK][4];  // [(key g, g + 8) x (row 2 t, 2 t + 1)]
+      float ks[GK][2];
       {
         const uint32_t base = ring + slot * p.slot_bytes;
-        const uint32_t kb = base + (uint32_t)(kw * 16 * GK) * row_bytes + (uint32_t)(hl * D * kEsz);
 #pragma unroll
-        for (int n = 0; n < 2 * GK; ++n) {
+        for (int k = 0; k < GK; ++k) {
 #pragma unroll
-          for (int m = 0; m < MT; ++m) s[m][n][0] = s[m][n][1] = s[m][n][2] = s[m][n][3] = 0.f;
-          const int kr = 16 * (n >> 1) + 4 * (g >> 1) + 2 * (n & 1) + (g & 1);
-          const uint32_t ka = kb + (uint32_t)kr * row_bytes + 16u * t;
+          for (int m = 0; m < NT; ++m) s[m][k][0] = s[m][k][1] = s[m][k][2] = s[m][k][3] = 0.f;
+          const uint32_t ka = base + koff + (uint32_t)(16 * k) * row_bytes;
 #pragma unroll
           for (int c4 = 0; c4 < D * kEsz / 64; ++c4) {
-            const uint4 w = lds128(ka + 64u * c4);
+            const uint4 x = lds128(ka + 64u * c4), y = lds128(ka + 2u * row_bytes + 64u * c4);
             if constexpr (C8) {
-              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+              const uint32_t xx[4] = {x.x, x.y, x.z, x.w}, yy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const uint32_t b0 = e4m3x2_f16x2(ww[j]), b1 = e4m3x2_f16x2(ww[j] >> 16);
+                const uint32_t a[4] = {e4m3x2_f16x2(xx[j]), e4m3x2_f16x2(yy[j]),
+                                       e4m3x2_f16x2(xx[j] >> 16), e4m3x2_f16x2(yy[j] >> 16)};
 #pragma unroll
-                for (int m = 0; m < MT; ++m) mma16816<MBF>(s[m][n], qf[m][4 * c4 + j], b0, b1);
+                for (int m = 0; m < NT; ++m)
+                  mma16816<MBF>(s[m][k], a, qf[m][4 * c4 + j][0], qf[m][4 * c4 + j][1]);
               }
             } else {
+              const uint32_t a[4] = {x.x, y.x, x.y, y.y}, b[4] = {x.z, y.z, x.w, y.w};
 #pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                mma16816<MBF>(s[m][n], qf[m][2 * c4], w.x, w.y);
-                mma16816<MBF>(s[m][n], qf[m][2 * c4 + 1], w.z, w.w);
+              for (int m = 0; m < NT; ++m) {
+                mma16816<MBF>(s[m][k], a, qf[m][2 * c4][0], qf[m][2 * c4][1]);
+                mma16816<MBF>(s[m][k], b, qf[m][2 * c4 + 1][0], qf[m][2 * c4 + 1][1]);
               }
             }
           }
-        }
-        if constexpr (C8) {
-          const uint32_t sa = base + p.data_bytes + (uint32_t)((kw * 16 * GK + 4 * t) * p.Hkv + head);
-#pragma unroll
-          for (int k = 0; k < GK; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              ks[k][j] = __int_as_float((int)lds8(sa + (uint32_t)((16 * k + j) * p.Hkv)) << 23);
+          if constexpr (C8) {
+            const uint32_t sa = base + soff + (uint32_t)(16 * k * p.Hkv);
+            ks[k][0] = __int_as_float((int)lds8(sa) << 23);
+            ks[k][1] = __int_as_float((int)lds8(sa + 2u * p.Hkv) << 23);
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(sBar + 8u * (kCaMaxSlots + slot));
@@ -602,45 +633,43 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       // ---- V of the tile: its scales join the exponents
       if (!(ok = wait_full(slot, ph))) break;
       const uint32_t vbase = ring + slot * p.slot_bytes;
-      float we[GK][4], wi[GK][4];  // the value scale's exponent, and 2^-exponent
+      float we[GK][2], wi[GK][2];  // the value scale's exponent, and 2^-exponent
       if constexpr (C8) {
-        const uint32_t sa = vbase + p.data_bytes + (uint32_t)((kw * 16 * GK + 4 * t) * p.Hkv + head);
 #pragma unroll
         for (int k = 0; k < GK; ++k)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int e = (int)lds8(sa + (uint32_t)((16 * k + j) * p.Hkv));
+          for (int j = 0; j < 2; ++j) {
+            const int e = (int)lds8(vbase + soff + (uint32_t)((16 * k + 2 * j) * p.Hkv));
             we[k][j] = (float)(e - 127);
             wi[k][j] = __int_as_float(max(254 - e, 0) << 23);
           }
       }
+#pragma unroll
+      for (int m = 0; m < NT; ++m)
+#pragma unroll
+        for (int k = 0; k < GK; ++k)
+#pragma unroll
+          for (int c2 = 0; c2 < 4; ++c2) {
+            float& x = s[m][k][c2];
+            if constexpr (C8)
+              x = fmaf(x, rs[m][c2 & 1] * ks[k][c2 >> 1], we[k][c2 >> 1]);
+            else
+              x *= rs[m][c2 & 1];
+          }
       // Which keys need a look at the mask: any at or past the prefix's end
       // (causal, tree, end of the sequence) or below some row's window.
       const bool edge = n0 + 16 * GK > u.P || p.window > 0;
+      if (edge) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+        for (int k = 0; k < GK; ++k)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float sc = rs[m][h];
+          for (int j = 0; j < 2; ++j) {
+            const int x = n0 + 16 * k + ca_key(g + 8 * j) - u.P;  // index among the new tokens
 #pragma unroll
-          for (int n = 0; n < 2 * GK; ++n)
+            for (int m = 0; m < NT; ++m)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& x = s[m][n][2 * h + e];
-              const int j = 2 * (n & 1) + e;
-              if constexpr (C8)
-                x = fmaf(x * sc, ks[n >> 1][j], we[n >> 1][j]);
-              else
-                x *= sc;
-            }
-          if (edge) {
-            const int i = ri[m][h], dep = rdep[m][h];
-#pragma unroll
-            for (int n = 0; n < 2 * GK; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int key = n0 + 16 * (n >> 1) + 4 * t + 2 * (n & 1) + e;
-                const int x = key - u.P;  // index among the new tokens
+              for (int h = 0; h < 2; ++h) {
+                const int i = ri[m][h];
                 bool keep = i >= 0 && x <= i;
                 if (keep && x >= 0 && p.mask != nullptr)
                   keep = (__ldg(p.mask + __ldg(p.mask_indptr + u.b) +
@@ -648,73 +677,73 @@ __global__ void __launch_bounds__(kCaThreads, 1)
                           (x & 31)) & 1u;
                 if (keep && p.window > 0) {
                   const int place = x >= 0 && p.depths != nullptr ? __ldg(p.depths + cu0 + x) : x;
-                  keep = place > dep - p.window;
+                  keep = place > rdep[m][h] - p.window;
                 }
-                if (!keep) s[m][n][2 * h + e] = -INFINITY;
+                if (!keep) s[m][k][2 * j + h] = -INFINITY;
               }
           }
-        }
+      }
       // ---- the references: moved when some score exceeds one by kCaSlack
       bool raise = false;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < NT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float mx = s[m][0][2 * h];
+          float mx = s[m][0][h];
 #pragma unroll
-          for (int n = 0; n < 2 * GK; ++n) mx = max3(mx, s[m][n][2 * h], s[m][n][2 * h + 1]);
+          for (int k = 0; k < GK; ++k) mx = max3(mx, s[m][k][h], s[m][k][2 + h]);
           raise |= mx > M[m][h] + kCaSlack;
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < NT; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float mx = M[m][h];
 #pragma unroll
-            for (int n = 0; n < 2 * GK; ++n) mx = max3(mx, s[m][n][2 * h], s[m][n][2 * h + 1]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            for (int k = 0; k < GK; ++k) mx = max3(mx, s[m][k][h], s[m][k][2 + h]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
             const float f = ex2(M[m][h] - mx);
             M[m][h] = mx;
             L[m][h] *= f;
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              o[m][n][2 * h] *= f;
-              o[m][n][2 * h + 1] *= f;
+            for (int n = 0; n < D / 16; ++n) {
+              o[m][n][h] *= f;
+              o[m][n][2 + h] *= f;
             }
           }
       }
-      uint32_t pf[MT][GK][4];
+      uint32_t pf[NT][GK][2];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < NT; ++m) {
+        const float r0 = M[m][0] - kBias, r1 = M[m][1] - kBias;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float ref = M[m][h] - kBias;
+        for (int k = 0; k < GK; ++k)
 #pragma unroll
-          for (int n = 0; n < 2 * GK; ++n) {
-            const float a = ex2(s[m][n][2 * h] - ref), b = ex2(s[m][n][2 * h + 1] - ref);
-            if constexpr (C8)
-              L[m][h] += a * wi[n >> 1][2 * (n & 1)] + b * wi[n >> 1][2 * (n & 1) + 1];
-            else
-              L[m][h] += a + b;
-            pf[m][n >> 1][2 * (n & 1) + h] = pack2<MBF>(a, b);
+          for (int j = 0; j < 2; ++j) {
+            const float a = ex2(s[m][k][2 * j] - r0), b = ex2(s[m][k][2 * j + 1] - r1);
+            if constexpr (C8) {
+              L[m][0] = fmaf(a, wi[k][j], L[m][0]);
+              L[m][1] = fmaf(b, wi[k][j], L[m][1]);
+            } else {
+              L[m][0] += a;
+              L[m][1] += b;
+            }
+            pf[m][k][j] = transpose8(pack2<MBF>(a, b));
           }
-        }
-      // ---- O += P V
-      const uint32_t va = vbase + (uint32_t)(kw * 16 * GK) * row_bytes + (uint32_t)(hl * D * kEsz) +
-                          (uint32_t)(8 * kEsz * g);
+      }
+      // ---- O^T += V^T P^T
 #pragma unroll
       for (int k = 0; k < GK; ++k) {
-        const uint32_t vk = va + (uint32_t)(16 * k + 4 * t) * row_bytes;
+        const uint32_t vk = vbase + voff + (uint32_t)(16 * k) * row_bytes;
         // Keys that no row sees may hold anything: zeros in their place.
         uint32_t live = 15u;
         if (edge) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int key = n0 + 16 * k + 4 * t + j;
-            if (key >= u.hi || (p.window > 0 && key <= u.P - p.window))
-              live &= ~(1u << j);
+            if (key >= u.hi || (p.window > 0 && key <= u.P - p.window)) live &= ~(1u << j);
           }
         }
 #pragma unroll
@@ -722,29 +751,31 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           if constexpr (C8) {
             uint2 w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              w[j] = lds64(vk + (uint32_t)j * row_bytes + 64u * c64);
-              if (!(live >> j & 1u)) w[j] = make_uint2(0u, 0u);
+            for (int j = 0; j < 4; ++j) w[j] = lds64(vk + (uint32_t)j * row_bytes + 64u * c64);
+            if (edge) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (!(live >> j & 1u)) w[j] = make_uint2(0u, 0u);
             }
 #pragma unroll
-            for (int n = 0; n < 8; n += 2) {
-              const uint32_t sel = (n & 2) ? 0x7362u : 0x5140u;
-              const uint32_t a = __byte_perm(n < 4 ? w[0].x : w[0].y, n < 4 ? w[1].x : w[1].y, sel);
-              const uint32_t b = __byte_perm(n < 4 ? w[2].x : w[2].y, n < 4 ? w[3].x : w[3].y, sel);
-              const uint32_t a0 = e4m3x2_f16x2(a), a1 = e4m3x2_f16x2(a >> 16);
-              const uint32_t b0 = e4m3x2_f16x2(b), b1 = e4m3x2_f16x2(b >> 16);
+            for (int n = 0; n < 4; ++n) {  // values 2 n and 2 n + 1 of the lane's 8
+              const uint32_t sel = (n & 1) ? 0x7362u : 0x5140u;
+              const uint32_t x = __byte_perm(n < 2 ? w[0].x : w[0].y, n < 2 ? w[1].x : w[1].y, sel);
+              const uint32_t y = __byte_perm(n < 2 ? w[2].x : w[2].y, n < 2 ? w[3].x : w[3].y, sel);
+              const uint32_t a[4] = {e4m3x2_f16x2(x), e4m3x2_f16x2(x >> 16), e4m3x2_f16x2(y),
+                                     e4m3x2_f16x2(y >> 16)};
 #pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                mma16816<MBF>(o[m][8 * c64 + n], pf[m][k], a0, b0);
-                mma16816<MBF>(o[m][8 * c64 + n + 1], pf[m][k], a1, b1);
-              }
+              for (int m = 0; m < NT; ++m)
+                mma16816<MBF>(o[m][4 * c64 + n], a, pf[m][k][0], pf[m][k][1]);
             }
           } else {
             uint4 w[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              w[j] = lds128(vk + (uint32_t)j * row_bytes + 128u * c64);
-              if (!(live >> j & 1u)) w[j] = make_uint4(0u, 0u, 0u, 0u);
+            for (int j = 0; j < 4; ++j) w[j] = lds128(vk + (uint32_t)j * row_bytes + 128u * c64);
+            if (edge) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (!(live >> j & 1u)) w[j] = make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -752,13 +783,11 @@ __global__ void __launch_bounds__(kCaThreads, 1)
               const uint32_t x1 = n == 0 ? w[1].x : n == 1 ? w[1].y : n == 2 ? w[1].z : w[1].w;
               const uint32_t x2 = n == 0 ? w[2].x : n == 1 ? w[2].y : n == 2 ? w[2].z : w[2].w;
               const uint32_t x3 = n == 0 ? w[3].x : n == 1 ? w[3].y : n == 2 ? w[3].z : w[3].w;
-              const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
-              const uint32_t b0 = __byte_perm(x2, x3, 0x5410), b1 = __byte_perm(x2, x3, 0x7632);
+              const uint32_t a[4] = {__byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632),
+                                     __byte_perm(x2, x3, 0x5410), __byte_perm(x2, x3, 0x7632)};
 #pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                mma16816<MBF>(o[m][8 * c64 + 2 * n], pf[m][k], a0, b0);
-                mma16816<MBF>(o[m][8 * c64 + 2 * n + 1], pf[m][k], a1, b1);
-              }
+              for (int m = 0; m < NT; ++m)
+                mma16816<MBF>(o[m][4 * c64 + n], a, pf[m][k][0], pf[m][k][1]);
             }
           }
         }
@@ -775,7 +804,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
     if (p.KW > 1) ok = named_bar_all(1u, 32u * (uint32_t)nact, ok);
 
     // ---- the unit's (or piece's) rows: join the warps of a head, write.
-    // Warp area [16 rows][64 columns] in shared memory, a tile and 64 columns
+    // Warp area [8 rows][64 columns] in shared memory, a tile and 64 columns
     // at a time; with one warp per head only that warp takes part.
     const bool cut = u.t0 > 0 || u.t1 < u.n;
     const long long pslot = 2ll * c + (u.t0 > 0 ? 0 : 1);
@@ -798,53 +827,50 @@ __global__ void __launch_bounds__(kCaThreads, 1)
       p.hdr[8 + 8ll * u.unit] = 0;
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < NT; ++m)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        L[m][h] += __shfl_xor_sync(0xffffffffu, L[m][h], 1);
-        L[m][h] += __shfl_xor_sync(0xffffffffu, L[m][h], 2);
-      }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) L[m][h] += __shfl_xor_sync(0xffffffffu, L[m][h], x);
     auto join = [&]() {
       if (p.KW == 1) __syncwarp();
       else named_bar_sync(1u, 32u * (uint32_t)nact);
     };
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if (t == 0) {
-        s_ml[warp * 16 + g] = make_float2(M[m][0], L[m][0]);
-        s_ml[warp * 16 + g + 8] = make_float2(M[m][1], L[m][1]);
+    for (int m = 0; m < NT; ++m) {
+      if (g == 0) {
+        s_ml[warp * 8 + 2 * t] = make_float2(M[m][0], L[m][0]);
+        s_ml[warp * 8 + 2 * t + 1] = make_float2(M[m][1], L[m][1]);
       }
 #pragma unroll
       for (int c64 = 0; c64 < D / 64; ++c64) {
-        // Value (row, column 8 (2 t + e) + j) of the chunk; columns rotated by
-        // the row so that neither side meets bank conflicts beyond two ways.
-        float* area = scratch + warp * 16 * 64;
+        // Rows 2 t and 2 t + 1, columns 8 g .. 8 g + 7 of the chunk, turned by
+        // the row so that the 16-byte stores of 8 lanes fall into all banks.
+        float* area = scratch + warp * 8 * 64;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-              const int col = (8 * (2 * t + e) + j + 8 * g) & 63;
-              *reinterpret_cast<float4*>(area + (g + 8 * h) * 64 + col) =
-                  make_float4(o[m][8 * c64 + j][2 * h + e], o[m][8 * c64 + j + 1][2 * h + e],
-                              o[m][8 * c64 + j + 2][2 * h + e], o[m][8 * c64 + j + 3][2 * h + e]);
-            }
+          for (int j = 0; j < 2; ++j) {
+            const int col = (8 * g + 4 * j + 16 * (t & 1) + 4 * (t >> 1)) & 63;
+            const float(&x)[4] = o[m][4 * c64 + 2 * j], (&y)[4] = o[m][4 * c64 + 2 * j + 1];
+            *reinterpret_cast<float4*>(area + (2 * t + h) * 64 + col) =
+                make_float4(x[h], x[2 + h], y[h], y[2 + h]);
+          }
         join();
         // Rows kw, kw + KW, .. of the head, two columns a lane.
-        for (int r = kw; r < 16; r += p.KW) {
-          const int gr = u.rt * RT + m * 16 + r;  // row of the sequence
+        for (int r = kw; r < 8; r += p.KW) {
+          const int gr = u.rt * RT + m * 8 + r;  // row of the sequence
           const int i = gr / p.G;
           if (i >= u.E) continue;
-          const int col = (2 * lane + 8 * (r & 7)) & 63;
+          const int col = (2 * lane + 16 * ((r >> 1) & 1) + 4 * (r >> 2)) & 63;
           float mf = -1e30f;
-          for (int w = 0; w < p.KW; ++w) mf = fmaxf(mf, s_ml[(w * p.HPC + hl) * 16 + r].x);
+          for (int w = 0; w < p.KW; ++w) mf = fmaxf(mf, s_ml[(w * p.HPC + hl) * 8 + r].x);
           float x = 0.f, y = 0.f, l = 0.f;
           for (int w = 0; w < p.KW; ++w) {
             const int wa = w * p.HPC + hl;
-            const float2 ml = s_ml[wa * 16 + r];
+            const float2 ml = s_ml[wa * 8 + r];
             const float f = ex2(ml.x - mf);
-            const float2 v = *reinterpret_cast<const float2*>(scratch + (wa * 16 + r) * 64 + col);
+            const float2 v = *reinterpret_cast<const float2*>(scratch + (wa * 8 + r) * 64 + col);
             x = fmaf(v.x, f, x);
             y = fmaf(v.y, f, y);
             l = fmaf(ml.y, f, l);
@@ -852,7 +878,7 @@ __global__ void __launch_bounds__(kCaThreads, 1)
           if (!ok) continue;
           const int qh = head * p.G + gr % p.G;
           if (cut) {
-            const long long pr = pslot * (p.HPC * RT) + hl * RT + m * 16 + r;
+            const long long pr = pslot * (p.HPC * RT) + hl * RT + m * 8 + r;
             *reinterpret_cast<float2*>(p.part_o + pr * D + 64 * c64 + 2 * lane) = make_float2(x, y);
             if (c64 == 0 && lane == 0)
               *reinterpret_cast<float2*>(p.part_ml + pr * 2) = make_float2(mf, l);

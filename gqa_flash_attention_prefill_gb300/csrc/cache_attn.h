@@ -6,24 +6,24 @@
 
 namespace gqa {
 
-// 16-row tiles a warp takes at most for head dim d: the accumulators and the
+// 8-row tiles a warp takes at most for head dim d: the accumulators and the
 // query fragments stay in registers.
-constexpr int cache_attn_max_mt(int d) { return d == 64 ? 2 : 1; }
+constexpr int cache_attn_max_nt(int d) { return d == 64 ? 4 : d == 128 ? 2 : 1; }
 
-cudaError_t launch_cache_attn_d64(const CacheAttnParams& p, bool bf16, bool c8, int mt, int grid,
+cudaError_t launch_cache_attn_d64(const CacheAttnParams& p, bool bf16, bool c8, int nt, int grid,
                                   unsigned smem, int merge_x, int merge_y, cudaStream_t st);
-cudaError_t launch_cache_attn_d128(const CacheAttnParams& p, bool bf16, bool c8, int mt, int grid,
+cudaError_t launch_cache_attn_d128(const CacheAttnParams& p, bool bf16, bool c8, int nt, int grid,
                                    unsigned smem, int merge_x, int merge_y, cudaStream_t st);
-cudaError_t launch_cache_attn_d256(const CacheAttnParams& p, bool bf16, bool c8, int mt, int grid,
+cudaError_t launch_cache_attn_d256(const CacheAttnParams& p, bool bf16, bool c8, int nt, int grid,
                                    unsigned smem, int merge_x, int merge_y, cudaStream_t st);
 
 namespace {
 
 // The kernel, and its join when merge_x > 0.
-template <int D, bool BF16, bool C8, int MT>
+template <int D, bool BF16, bool C8, int NT>
 cudaError_t launch_cache_attn(const CacheAttnParams& p, int grid, unsigned smem, int merge_x,
                               int merge_y, cudaStream_t st) {
-  auto kern = cache_attn_kernel<D, BF16, C8, MT>;
+  auto kern = cache_attn_kernel<D, BF16, C8, NT>;
   static SmemAttr attr{};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -34,7 +34,7 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, int grid, unsigned smem,
     if (e != cudaSuccess) return e;
     attr.allowed[dev].store(smem, std::memory_order_release);
   }
-  e = launch_pdl(kern, p, grid, kCaThreads, smem, st);
+  e = launch_pdl(kern, p, grid, 32 * (ca_warps(D, C8, NT) + 1), smem, st);
   if (e != cudaSuccess || merge_x == 0) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)merge_x, (unsigned)merge_y, 1);
@@ -45,18 +45,18 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, int grid, unsigned smem,
   la[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = la;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, BF16>, p, 16 * MT,
+  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, BF16>, p, 8 * NT,
                             BF16 && !C8 ? 0.f : 10.f);
 }
 
-template <int D, int MT>
+template <int D, int NT>
 cudaError_t launch_cache_attn_types(const CacheAttnParams& p, bool bf16, bool c8, int grid,
                                     unsigned smem, int mx, int my, cudaStream_t st) {
   if (bf16)
-    return c8 ? launch_cache_attn<D, true, true, MT>(p, grid, smem, mx, my, st)
-              : launch_cache_attn<D, true, false, MT>(p, grid, smem, mx, my, st);
-  return c8 ? launch_cache_attn<D, false, true, MT>(p, grid, smem, mx, my, st)
-            : launch_cache_attn<D, false, false, MT>(p, grid, smem, mx, my, st);
+    return c8 ? launch_cache_attn<D, true, true, NT>(p, grid, smem, mx, my, st)
+              : launch_cache_attn<D, true, false, NT>(p, grid, smem, mx, my, st);
+  return c8 ? launch_cache_attn<D, false, true, NT>(p, grid, smem, mx, my, st)
+            : launch_cache_attn<D, false, false, NT>(p, grid, smem, mx, my, st);
 }
 
 }  // namespace
