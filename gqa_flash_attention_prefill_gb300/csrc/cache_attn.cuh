@@ -238,10 +238,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {  // low 16 bits: two values
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)w));
-  return r;
+// Four e4m3 values as two f16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 r;
@@ -271,7 +275,8 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
 
 // D: head dim.  BF16: type of q and out.  C8: e4m3 cache (products in f16),
 // else the cache has q's type.  NT: 8-row tiles per warp.
-template <int D, bool BF16, bool C8, int NT>
+// H8: 8 heads per CTA, which makes the ring's strides constants.
+template <int D, bool BF16, bool C8, int NT, bool H8>
 __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     cache_attn_kernel(const __grid_constant__ CacheAttnParams p) {
   constexpr int NW = ca_warps(D, C8, NT);
@@ -429,7 +434,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
   walk.end = ca_lo(W, c + 1, C);
   if (c == 0 && tid == 0) p.hdr[0] = walk.whole ? 0 : n_units;  // W > 0 here
 
-  const uint32_t row_bytes = (uint32_t)p.HPC * D * kEsz;        // a token's values in the ring
+  const uint32_t row_bytes = H8 ? 8u * D * kEsz : (uint32_t)p.HPC * D * kEsz;  // a token in the ring
   const long long tok_bytes = (long long)p.Hkv * D * kEsz;      // in the pool
 
   if (warp == NW) {
@@ -602,8 +607,9 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
               const uint32_t xx[4] = {x.x, x.y, x.z, x.w}, yy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const uint32_t a[4] = {e4m3x2_f16x2(xx[j]), e4m3x2_f16x2(yy[j]),
-                                       e4m3x2_f16x2(xx[j] >> 16), e4m3x2_f16x2(yy[j] >> 16)};
+                uint32_t a[4];
+                e4m3x4_f16(xx[j], a[0], a[2]);
+                e4m3x4_f16(yy[j], a[1], a[3]);
 #pragma unroll
                 for (int m = 0; m < NT; ++m)
                   mma16816<MBF>(s[m][k], a, qf[m][4 * c4 + j][0], qf[m][4 * c4 + j][1]);
@@ -762,8 +768,9 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
               const uint32_t sel = (n & 1) ? 0x7362u : 0x5140u;
               const uint32_t x = __byte_perm(n < 2 ? w[0].x : w[0].y, n < 2 ? w[1].x : w[1].y, sel);
               const uint32_t y = __byte_perm(n < 2 ? w[2].x : w[2].y, n < 2 ? w[3].x : w[3].y, sel);
-              const uint32_t a[4] = {e4m3x2_f16x2(x), e4m3x2_f16x2(x >> 16), e4m3x2_f16x2(y),
-                                     e4m3x2_f16x2(y >> 16)};
+              uint32_t a[4];
+              e4m3x4_f16(x, a[0], a[1]);
+              e4m3x4_f16(y, a[2], a[3]);
 #pragma unroll
               for (int m = 0; m < NT; ++m)
                 mma16816<MBF>(o[m][4 * c64 + n], a, pf[m][k][0], pf[m][k][1]);

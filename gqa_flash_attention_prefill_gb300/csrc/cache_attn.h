@@ -20,10 +20,10 @@ cudaError_t launch_cache_attn_d256(const CacheAttnParams& p, bool bf16, bool c8,
 namespace {
 
 // The kernel, and its join when merge_x > 0.
-template <int D, bool BF16, bool C8, int NT>
+template <int D, bool BF16, bool C8, int NT, bool H8>
 cudaError_t launch_cache_attn(const CacheAttnParams& p, int grid, unsigned smem, int merge_x,
                               int merge_y, cudaStream_t st) {
-  auto kern = cache_attn_kernel<D, BF16, C8, NT>;
+  auto kern = cache_attn_kernel<D, BF16, C8, NT, H8>;
   static SmemAttr attr{};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -49,14 +49,14 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, int grid, unsigned smem,
                             BF16 && !C8 ? 0.f : 10.f);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool H8>
 cudaError_t launch_cache_attn_types(const CacheAttnParams& p, bool bf16, bool c8, int grid,
                                     unsigned smem, int mx, int my, cudaStream_t st) {
   if (bf16)
-    return c8 ? launch_cache_attn<D, true, true, NT>(p, grid, smem, mx, my, st)
-              : launch_cache_attn<D, true, false, NT>(p, grid, smem, mx, my, st);
-  return c8 ? launch_cache_attn<D, false, true, NT>(p, grid, smem, mx, my, st)
-            : launch_cache_attn<D, false, false, NT>(p, grid, smem, mx, my, st);
+    return c8 ? launch_cache_attn<D, true, true, NT, H8>(p, grid, smem, mx, my, st)
+              : launch_cache_attn<D, true, false, NT, H8>(p, grid, smem, mx, my, st);
+  return c8 ? launch_cache_attn<D, false, true, NT, H8>(p, grid, smem, mx, my, st)
+            : launch_cache_attn<D, false, false, NT, H8>(p, grid, smem, mx, my, st);
 }
 
 }  // namespace
