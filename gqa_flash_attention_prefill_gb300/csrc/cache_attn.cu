@@ -44,7 +44,8 @@ int cache_plan(int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hkv, int
   // four slots (two tiles) takes fewer warps per head, then fewer heads.
   int hpc = Hkv < 8 ? Hkv : 8;
   while (Hkv % hpc != 0) --hpc;
-  int kw = warps / hpc;
+  int kw = 1;
+  while (2 * kw * hpc <= warps) kw *= 2;  // a power of two, and so the keys per tile
   for (;;) {
     pl->HPC = hpc;
     pl->KW = kw;
@@ -155,6 +156,9 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
   p.HG = pl.HG;
   p.KW = pl.KW;
   p.T = pl.T;
+  while ((1 << p.log_T) < pl.T) ++p.log_T;
+  p.div_g.set((uint32_t)pl.G);
+  p.div_page.set((uint32_t)page_size);
   p.run = run;
   p.NS = pl.NS;
   p.slot_bytes = pl.slot_bytes;

@@ -61,6 +61,23 @@ constexpr int kCaMaxSlots = 16;                    // ring slots at most
 constexpr float kCaSlack = 4.f;
 constexpr int kCaWholeSlack = 6;                   // tiles a join is worth
 
+// Division of 0 <= n < 2^31 by a divisor fixed for the launch: with l =
+// ceil(log2 d) and m = ceil(2^(32 + l) / d) - 2^32, n / d = (hi(n m) + n) >> l
+// exactly (the rounding of m adds less than n / 2^(32 + l) <= 1 / 2^(l + 1) to
+// the quotient, less than the gap below the next multiple of 1 / d).
+struct FastDiv {
+  uint32_t m;
+  int l;
+  __host__ void set(uint32_t d) {
+    l = 0;
+    while ((1ull << l) < d) ++l;
+    m = (uint32_t)(((1ull << (32 + l)) + d - 1) / d - (1ull << 32));
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> l);
+  }
+};
+
 struct CacheAttnParams {
   const void* q;
   const uint8_t* k_pages;
@@ -88,7 +105,8 @@ struct CacheAttnParams {
   int Hq, Hkv, G;
   int HPC, HG;       // heads per CTA, head groups
   int KW;            // warps that share a head's keys
-  int T;             // keys per tile (16 GK KW)
+  int T, log_T;      // keys per tile (16 GK KW, a power of two)
+  FastDiv div_g, div_page;
   int run;           // tokens per copy: divides T and the page
   int NS;            // ring slots
   uint32_t slot_bytes, data_bytes;  // a slot, and its values (scales follow)
@@ -112,15 +130,15 @@ __device__ __forceinline__ int ca_key(int m) {
 // fp32 and its rows' (M, L), the barriers, the tables of the sequences.
 __host__ __device__ constexpr uint32_t ca_fixed_smem(int warps) {
   return 1024u + 128u + (uint32_t)warps * (8u * 64u * 4u + 8u * 8u) + 2u * kCaMaxSlots * 8u + 32u +
-         8u * (kMaxSeqs + 1) + 4u * (4 * kMaxSeqs + 2) + 8u * 20u + 4u * 20u;
+         4u * (5 * kMaxSeqs + 3) + 8u * 20u + 4u * 20u;
 }
 
 struct CaTab {
-  const long long* tiles;  // [B + 1] exclusive scan of key tiles
-  const int32_t* units;    // [B + 1] exclusive scan of units
-  const int32_t* cu0;      // [B + 1]
-  const int32_t* pre;      // [B]
-  const int32_t* ipt;      // [B]
+  const int32_t* tiles;  // [B + 1] exclusive scan of key tiles
+  const int32_t* units;  // [B + 1] exclusive scan of units
+  const int32_t* cu0;    // [B + 1]
+  const int32_t* pre;    // [B]
+  const int32_t* ipt;    // [B]
 };
 
 // A piece of work: tiles [t0, t1) of the n tiles of one unit.
@@ -133,73 +151,71 @@ struct CaPiece {
 // Key range of row tile rt: rows rt * RT .. of the sequence's E * G.
 __device__ __forceinline__ void ca_range(const CacheAttnParams& p, int P, int E, int rt, int RT,
                                          int& lo, int& hi, int& n) {
-  const int i0 = rt * RT / p.G, i1 = min((rt * RT + RT - 1) / p.G, E - 1);
+  const int i1 = min(p.div_g.div(rt * RT + RT - 1), E - 1);
   hi = P + i1 + 1;
   lo = 0;
   if (p.window > 0) {
     // The lowest position of the tile's rows: depths may be anything >= 0.
-    const long long a = (long long)P + (p.depths != nullptr ? 0 : i0) - p.window + 1;
-    if (a > 0) lo = (int)(a / p.T) * p.T;
-    if (lo >= hi) lo = (hi - 1) / p.T * p.T;
+    const int a = P - p.window + 1 + (p.depths != nullptr ? 0 : p.div_g.div(rt * RT));
+    if (a > 0) lo = a >> p.log_T << p.log_T;
   }
-  n = (hi - lo + p.T - 1) / p.T;
+  n = (hi - lo + p.T - 1) >> p.log_T;
 }
 
+// Equal shares of W tiles over C <= W CTAs: the first W % C hold one more.
+struct CaShares {
+  int q, r;
+  __device__ __forceinline__ CaShares(int W, int C) : q(W / C), r(W - W / C * C) {}
+  __device__ __forceinline__ int lo(int c) const { return c * q + min(c, r); }
+  __device__ __forceinline__ int owner(int x) const {  // CTA of tile x
+    const int big = r * (q + 1);
+    return x < big ? x / (q + 1) : r + (x - big) / q;
+  }
+};
+
 struct CaWalk {
-  long long at, end;  // share mode: tiles left
-  int unit, step;     // whole mode: next unit
-  int n_units;
+  int at, end;  // share mode: tiles left
+  int unit;     // whole mode: next unit, every gridDim.x-th
   bool whole;
 };
 
 __device__ __forceinline__ bool ca_next(const CacheAttnParams& p, const CaTab& T, CaWalk& w, int RT,
                                         CaPiece& u) {
+  const int32_t* key = w.whole ? T.units : T.tiles;
+  const int x = w.whole ? w.unit : w.at;
+  if (x >= (w.whole ? T.units[p.num_seqs] : w.end)) return false;
   int lo = 0, hi = p.num_seqs;
-  if (w.whole) {
-    if (w.unit >= w.n_units) return false;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (T.units[mid] <= w.unit) lo = mid; else hi = mid;
-    }
-  } else {
-    if (w.at >= w.end) return false;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (T.tiles[mid] <= w.at) lo = mid; else hi = mid;
-    }
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (key[mid] <= x) lo = mid; else hi = mid;
   }
   u.b = lo;
   u.P = T.pre[lo];
   u.E = T.cu0[lo + 1] - T.cu0[lo];
+  int off = x - key[lo];
   if (w.whole) {
-    const int k = w.unit - T.units[lo];
-    u.rt = k / p.HG;
-    u.hg = k - u.rt * p.HG;
+    u.rt = p.HG == 1 ? off : off / p.HG;
+    u.hg = off - u.rt * p.HG;
     ca_range(p, u.P, u.E, u.rt, RT, u.lo, u.hi, u.n);
     u.t0 = 0;
     u.t1 = u.n;
-    u.unit = w.unit;
-    w.unit += w.step;
+    u.unit = x;
+    w.unit += gridDim.x;
     return true;
   }
-  long long off = w.at - T.tiles[lo];
   for (u.rt = 0;; ++u.rt) {  // ends: off lies within the sequence's tiles
     ca_range(p, u.P, u.E, u.rt, RT, u.lo, u.hi, u.n);
-    const long long all = (long long)u.n * p.HG;
+    const int all = u.n * p.HG;
     if (off < all) break;
     off -= all;
   }
-  u.hg = (int)(off / u.n);
-  u.t0 = (int)(off - (long long)u.hg * u.n);
-  const long long left = w.end - w.at;
-  u.t1 = left < u.n - u.t0 ? u.t0 + (int)left : u.n;
+  u.hg = p.HG == 1 ? 0 : off / u.n;
+  u.t0 = off - u.hg * u.n;
+  u.t1 = min(u.n, u.t0 + w.end - w.at);
   u.unit = T.units[lo] + u.rt * p.HG + u.hg;
   w.at += u.t1 - u.t0;
   return true;
 }
-
-// Share boundaries in 64 bits.
-__device__ __forceinline__ long long ca_lo(long long W, int c, int C) { return W * c / C; }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -294,10 +310,10 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
   float2* s_ml = reinterpret_cast<float2*>(scratch + NW * 8 * 64);  // [NW][8]
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_ml + NW * 8);
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kCaMaxSlots);  // [0] abort [1] bad
-  long long* tiles = reinterpret_cast<long long*>(misc + 8);
-  long long* wtot = tiles + (kMaxSeqs + 1);
+  long long* wtot = reinterpret_cast<long long*>(misc + 8);  // [NW + 1]
   int32_t* utot = reinterpret_cast<int32_t*>(wtot + 20);
-  int32_t* units = utot + 20;
+  int32_t* tiles = utot + 20;
+  int32_t* units = tiles + (kMaxSeqs + 1);
   int32_t* s_cu = units + (kMaxSeqs + 1);
   int32_t* s_pre = s_cu + (kMaxSeqs + 1);
   int32_t* s_ipt = s_pre + kMaxSeqs;
@@ -327,38 +343,37 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
   bool bad = tid == 0 && p.first_seq == 0 && __ldg(p.cu) != 0;
   long long my_tiles = 0;
   int my_units = 0, my_max = 0;
-  const int per = (nseq + kThreads - 1) / kThreads;
+  const int per = (nseq + kThreads - 1) / kThreads;  // 1 up to 288 sequences
   const int b_lo = min(tid * per, nseq), b_hi = min(b_lo + per, nseq);
   for (int b = b_lo; b < b_hi; ++b) {
     const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), P = __ldg(p.pre + b);
     const int i0 = __ldg(p.indptr + b), i1 = __ldg(p.indptr + b + 1);
-    const long long E = (long long)c1 - c0;
-    bool mask_bad = false;
+    const int E = c1 - c0;
+    bool b_bad = c0 < 0 || c1 < c0 || c1 > p.total_q || P < 0 || P > 0x7fff0000 - E || i0 < 0 ||
+                 i1 > p.entries;
+    if (!b_bad) b_bad = i1 - i0 != (P + E > 0 ? p.div_page.div(P + E - 1) + 1 : 0);
     if (p.mask != nullptr) {
       const long long m0 = __ldg(p.mask_indptr + b), m1 = __ldg(p.mask_indptr + b + 1);
-      mask_bad = m0 < 0 || m1 > p.total_mask_words || m1 - m0 != E * ((E + 31) / 32);
+      b_bad |= m0 < 0 || m1 > p.total_mask_words || m1 - m0 != (long long)E * ((E + 31) / 32);
     }
-    const bool b_bad = E < 0 || P < 0 || c0 < 0 || c1 > p.total_q || i0 < 0 || i1 > p.entries ||
-                       P + E > 0x7ffff000ll ||
-                       (long long)i1 - i0 != (P + E + p.page_size - 1) / p.page_size || mask_bad;
     bad |= b_bad;
     long long w = 0;
     int nu = 0;
     if (!b_bad && E > 0) {
-      const int nrt = (int)((E * p.G + RT - 1) / RT);
-      for (int rt = 0; rt < nrt; ++rt) {
+      nu = (E * p.G + RT - 1) / RT;
+      for (int rt = 0; rt < nu; ++rt) {
         int lo, hi, n;
-        ca_range(p, P, (int)E, rt, RT, lo, hi, n);
+        ca_range(p, P, E, rt, RT, lo, hi, n);
         w += n;
         my_max = max(my_max, n);
       }
       w *= p.HG;
-      nu = nrt * p.HG;
+      nu *= p.HG;
     }
     s_cu[b] = c0;
     s_pre[b] = P;
     s_ipt[b] = i0;
-    tiles[b] = w;
+    tiles[b] = (int)w;
     units[b] = nu;
     if (b == nseq - 1) s_cu[nseq] = c1;
     my_tiles += w;
@@ -392,14 +407,14 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
       au += utot[w];
     }
     for (int b = b_lo; b < b_hi; ++b) {
-      const long long w = tiles[b];
-      const int nu = units[b];
-      tiles[b] = at;
+      const int w = tiles[b], nu = units[b];
+      tiles[b] = (int)at;
       units[b] = au;
       at += w;
       au += nu;
       if (b == nseq - 1) {
-        tiles[nseq] = at;
+        if (at > 0x7fffffffll) misc[1] = 1u;  // more key tiles than the shares count
+        tiles[nseq] = (int)at;
         units[nseq] = au;
       }
     }
@@ -415,24 +430,22 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     return;
   }
   const CaTab T{tiles, units, s_cu, s_pre, s_ipt};
-  const long long W = tiles[nseq];
+  const int W = tiles[nseq], n_units = units[nseq], c = blockIdx.x;
   // No more shares than tiles: every share holds a tile, so the pieces of a
   // cut unit lie on consecutive CTAs.
-  const int C = W < (long long)gridDim.x ? (int)W : (int)gridDim.x;
-  const int n_units = units[nseq], c = blockIdx.x;
-  if (c == 0 && tid == 0 && W == 0) p.hdr[0] = 0;
-  if (c >= C) return;
-  CaWalk walk;
-  walk.n_units = n_units;
+  const int C = min(W, (int)gridDim.x);
   // Whole units when the deepest deal costs no more than an equal share and
   // the join that cut units need.
+  CaWalk walk;
   walk.whole = p.whole != 0 ||
-               (long long)((n_units + C - 1) / C) * (int)misc[2] <= W / C + kCaWholeSlack;
+               (long long)((n_units + (int)gridDim.x - 1) / (int)gridDim.x) * (int)misc[2] <=
+                   W / max(C, 1) + kCaWholeSlack;
+  if (c == 0 && tid == 0) p.hdr[0] = walk.whole ? 0 : n_units;
+  if (c >= C) return;
+  const CaShares shares(W, C);
   walk.unit = c;
-  walk.step = C;
-  walk.at = ca_lo(W, c, C);
-  walk.end = ca_lo(W, c + 1, C);
-  if (c == 0 && tid == 0) p.hdr[0] = walk.whole ? 0 : n_units;  // W > 0 here
+  walk.at = shares.lo(c);
+  walk.end = shares.lo(c + 1);
 
   const uint32_t row_bytes = H8 ? 8u * D * kEsz : (uint32_t)p.HPC * D * kEsz;  // a token in the ring
   const long long tok_bytes = (long long)p.Hkv * D * kEsz;      // in the pool
@@ -443,9 +456,9 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     uint32_t slot = 0, ph = 0, issued = 0;
     bool ok = true;
     CaPiece u;
-    const int nrun = p.T / p.run;
+    const int nrun = p.T / p.run;  // the tile's copies, one a lane
     while (ok && ca_next(p, T, walk, RT, u)) {
-      const int npg = (u.P + u.E + p.page_size - 1) / p.page_size;
+      const int npg = p.div_page.div(u.P + u.E - 1) + 1;
       const int32_t* table = p.indices + T.ipt[u.b];
       for (int t = u.t0; ok && t < u.t1; ++t) {
         const int n0 = u.lo + t * p.T;
@@ -465,12 +478,13 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
           const uint8_t* pages = kv ? p.v_pages : p.k_pages;
           for (int r = lane; r < nrun && r * p.run < ntok; r += 32) {
             const int key = n0 + r * p.run, cnt = min(p.run, ntok - r * p.run);
-            int pg = __ldg(table + min(key / p.page_size, npg - 1));
+            const int kp = p.div_page.div(key);
+            int pg = __ldg(table + min(kp, npg - 1));
             if (pg < 0 || pg >= p.num_pages) {
               atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
               pg = 0;
             }
-            const long long row = (long long)pg * p.page_size + key % p.page_size;
+            const long long row = (long long)pg * p.page_size + (key - kp * p.page_size);
             const uint8_t* src = pages + row * tok_bytes + (long long)u.hg * row_bytes;
             const uint32_t to = dst + (uint32_t)(r * p.run) * row_bytes;
             if (p.HG == 1)
@@ -521,7 +535,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     for (int m = 0; m < NT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int i = (u.rt * RT + m * 8 + 2 * t + h) / p.G;
+        const int i = p.div_g.div(u.rt * RT + m * 8 + 2 * t + h);
         const bool on = i < u.E;
         ri[m][h] = on ? i : -1;
         rdep[m][h] = i;
@@ -533,10 +547,10 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
       const int r = u.rt * RT + m * 8 + g;
-      const int i = r / p.G;
+      const int i = p.div_g.div(r);
       const bool on = i < u.E;
       const uint16_t* qr = static_cast<const uint16_t*>(p.q) +
-                           ((long long)(cu0 + (on ? i : 0)) * p.Hq + head * p.G + r % p.G) * D;
+                           ((long long)(cu0 + (on ? i : 0)) * p.Hq + head * p.G + (r - i * p.G)) * D;
       if constexpr (C8) {
         // f16 operands: the row scaled by the power of two that brings its
         // largest magnitude into [1, 2); smaller values round at 2^-25.
@@ -645,9 +659,9 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
         for (int k = 0; k < GK; ++k)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int e = (int)lds8(vbase + soff + (uint32_t)((16 * k + 2 * j) * p.Hkv));
-            we[k][j] = (float)(e - 127);
-            wi[k][j] = __int_as_float(max(254 - e, 0) << 23);
+            const uint32_t e = lds8(vbase + soff + (uint32_t)((16 * k + 2 * j) * p.Hkv));
+            we[k][j] = __uint_as_float(0x4B000000u | e) - 8388735.f;  // 2^23 + e - (2^23 + 127)
+            wi[k][j] = __uint_as_float((254u << 23) - e * (1u << 23));
           }
       }
 #pragma unroll
@@ -665,7 +679,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
       // Which keys need a look at the mask: any at or past the prefix's end
       // (causal, tree, end of the sequence) or below some row's window.
       const bool edge = n0 + 16 * GK > u.P || p.window > 0;
-      if (edge) {
+      if (__builtin_expect(edge, 0)) {
 #pragma unroll
         for (int k = 0; k < GK; ++k)
 #pragma unroll
@@ -687,6 +701,8 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
                 }
                 if (!keep) s[m][k][2 * j + h] = -INFINITY;
               }
+            if constexpr (C8)  // keys that no row sees may have any scale
+              if (x + u.P >= u.hi || (p.window > 0 && x <= -p.window)) wi[k][j] = 0.f;
           }
       }
       // ---- the references: moved when some score exceeds one by kCaSlack
@@ -700,7 +716,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
           for (int k = 0; k < GK; ++k) mx = max3(mx, s[m][k][h], s[m][k][2 + h]);
           raise |= mx > M[m][h] + kCaSlack;
         }
-      if (__any_sync(0xffffffffu, raise)) {
+      if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
 #pragma unroll
         for (int m = 0; m < NT; ++m)
 #pragma unroll
@@ -745,7 +761,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
         const uint32_t vk = vbase + voff + (uint32_t)(16 * k) * row_bytes;
         // Keys that no row sees may hold anything: zeros in their place.
         uint32_t live = 15u;
-        if (edge) {
+        if (__builtin_expect(edge, 0)) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int key = n0 + 16 * k + 4 * t + j;
@@ -758,7 +774,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
             uint2 w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = lds64(vk + (uint32_t)j * row_bytes + 64u * c64);
-            if (edge) {
+            if (__builtin_expect(edge, 0)) {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 if (!(live >> j & 1u)) w[j] = make_uint2(0u, 0u);
@@ -779,7 +795,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
             uint4 w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = lds128(vk + (uint32_t)j * row_bytes + 128u * c64);
-            if (edge) {
+            if (__builtin_expect(edge, 0)) {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 if (!(live >> j & 1u)) w[j] = make_uint4(0u, 0u, 0u, 0u);
@@ -808,7 +824,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     }
     // A wait that ran out in one warp ends the piece for all that join rows
     // with it: nothing more is written.
-    if (p.KW > 1) ok = named_bar_all(1u, 32u * (uint32_t)nact, ok);
+    if (p.KW > 1) ok = named_bar_all(1u + (uint32_t)hl, 32u * (uint32_t)p.KW, ok);
 
     // ---- the unit's (or piece's) rows: join the warps of a head, write.
     // Warp area [8 rows][64 columns] in shared memory, a tile and 64 columns
@@ -817,14 +833,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     const long long pslot = 2ll * c + (u.t0 > 0 ? 0 : 1);
     if (cut && u.t0 == 0 && hl == 0 && kw == 0 && lane == 0) {
       int32_t* hd = p.hdr + 8 + 8ll * u.unit;
-      const long long gend = walk.at - u.t1 + u.n;  // tile after the unit's last
-      // CTA of the unit's last tile: the share that holds tile gend - 1.
-      int a = c, b = C;
-      while (b - a > 1) {
-        const int mid = (a + b) >> 1;
-        if (ca_lo(W, mid, C) <= gend - 1) a = mid; else b = mid;
-      }
-      hd[0] = a - c;  // pieces after the first
+      hd[0] = shares.owner(walk.at - u.t1 + u.n - 1) - c;  // pieces after the first
       hd[1] = c;
       hd[2] = u.rt * RT;
       hd[3] = u.hg * p.HPC;
@@ -841,7 +850,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
         for (int x = 4; x < 32; x <<= 1) L[m][h] += __shfl_xor_sync(0xffffffffu, L[m][h], x);
     auto join = [&]() {
       if (p.KW == 1) __syncwarp();
-      else named_bar_sync(1u, 32u * (uint32_t)nact);
+      else named_bar_sync(1u + (uint32_t)hl, 32u * (uint32_t)p.KW);
     };
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
@@ -864,44 +873,51 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
                 make_float4(x[h], x[2 + h], y[h], y[2 + h]);
           }
         join();
-        // Rows kw, kw + KW, .. of the head, two columns a lane.
-        for (int r = kw; r < 8; r += p.KW) {
+        // Four rows a warp at a time, 8 columns a lane.
+        for (int r = 4 * kw + (lane >> 3); r < 8; r += 4 * p.KW) {
           const int gr = u.rt * RT + m * 8 + r;  // row of the sequence
-          const int i = gr / p.G;
-          if (i >= u.E) continue;
-          const int col = (2 * lane + 16 * ((r >> 1) & 1) + 4 * (r >> 2)) & 63;
+          const int i = p.div_g.div(gr);
+          if (i >= u.E || !ok) continue;
+          const int qh = head * p.G + (gr - i * p.G);
+          float xs = -INFINITY;
+          if (!cut && p.sinks != nullptr) xs = __ldg(p.sinks + qh) * kLog2e;
+          else if (!cut && p.smooth) xs = 0.f;
+          const int turn = 16 * ((r >> 1) & 1) + 4 * (r >> 2);
+          const int col0 = (8 * (lane & 7) + turn) & 63, col1 = (8 * (lane & 7) + 4 + turn) & 63;
           float mf = -1e30f;
           for (int w = 0; w < p.KW; ++w) mf = fmaxf(mf, s_ml[(w * p.HPC + hl) * 8 + r].x);
-          float x = 0.f, y = 0.f, l = 0.f;
+          float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, l = 0.f;
           for (int w = 0; w < p.KW; ++w) {
-            const int wa = w * p.HPC + hl;
-            const float2 ml = s_ml[wa * 8 + r];
+            const int wr = (w * p.HPC + hl) * 8 + r;
+            const float2 ml = s_ml[wr];
             const float f = ex2(ml.x - mf);
-            const float2 v = *reinterpret_cast<const float2*>(scratch + (wa * 8 + r) * 64 + col);
-            x = fmaf(v.x, f, x);
-            y = fmaf(v.y, f, y);
+            const float4 x = *reinterpret_cast<const float4*>(scratch + wr * 64 + col0);
+            const float4 y = *reinterpret_cast<const float4*>(scratch + wr * 64 + col1);
+            v[0] = fmaf(x.x, f, v[0]), v[1] = fmaf(x.y, f, v[1]);
+            v[2] = fmaf(x.z, f, v[2]), v[3] = fmaf(x.w, f, v[3]);
+            v[4] = fmaf(y.x, f, v[4]), v[5] = fmaf(y.y, f, v[5]);
+            v[6] = fmaf(y.z, f, v[6]), v[7] = fmaf(y.w, f, v[7]);
             l = fmaf(ml.y, f, l);
           }
-          if (!ok) continue;
-          const int qh = head * p.G + gr % p.G;
+          const int col = 64 * c64 + 8 * (lane & 7);
           if (cut) {
             const long long pr = pslot * (p.HPC * RT) + hl * RT + m * 8 + r;
-            *reinterpret_cast<float2*>(p.part_o + pr * D + 64 * c64 + 2 * lane) = make_float2(x, y);
-            if (c64 == 0 && lane == 0)
+            float4* dst = reinterpret_cast<float4*>(p.part_o + pr * D + col);
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            if (c64 == 0 && (lane & 7) == 0)
               *reinterpret_cast<float2*>(p.part_ml + pr * 2) = make_float2(mf, l);
           } else {
-            float xs = -INFINITY;
-            if (p.sinks != nullptr) xs = __ldg(p.sinks + qh) * kLog2e;
-            else if (p.smooth) xs = 0.f;
             // With the sink above the keys the reference moves to it.
             const bool any = l > 0.f;
             const float mm = fmaxf(mf - kBias, xs), f = ex2(mf - kBias - mm);
             const float den = fmaf(l, f, ex2(xs - mm));
             const float inv = any ? f / den : 0.f;
             const long long row = (long long)(cu0 + i) * p.Hq + qh;
-            *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + 64 * c64 +
-                                         2 * lane) = pack2<BF16>(x * inv, y * inv);
-            if (c64 == 0 && lane == 0 && p.lse != nullptr)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + col) = make_uint4(
+                pack2<BF16>(v[0] * inv, v[1] * inv), pack2<BF16>(v[2] * inv, v[3] * inv),
+                pack2<BF16>(v[4] * inv, v[5] * inv), pack2<BF16>(v[6] * inv, v[7] * inv));
+            if (c64 == 0 && (lane & 7) == 0 && p.lse != nullptr)
               p.lse[row] = any ? (mm + log2f(den)) * kLn2 : -INFINITY;
           }
         }
@@ -936,9 +952,9 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant_
     const bool wide = np > 8;  // the whole block per row
     const int step = wide ? gridDim.y : gridDim.y * 8;
     for (int r = wide ? blockIdx.y : blockIdx.y * 8 + warp; r < rows; r += step) {
-      const int hl = r / RT, gr = r0 + r % RT, i = gr / p.G;
+      const int hl = r / RT, gr = r0 + (r - hl * RT), i = p.div_g.div(gr);
       if (i >= E) continue;
-      const int qh = (h0 + hl) * p.G + gr % p.G;
+      const int qh = (h0 + hl) * p.G + (gr - i * p.G);
       const int s0 = wide ? warp : 0, ds = wide ? 8 : 1;
       // Piece s of the unit: slot 2 c + 1 of its first CTA, slot 2 (c + s) after.
       auto at = [&](int s) { return (2ll * (c0 + s) + (s == 0 ? 1 : 0)) * rows + r; };
