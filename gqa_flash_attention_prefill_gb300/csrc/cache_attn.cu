@@ -118,10 +118,10 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
   if (workspace == nullptr || workspace_bytes < pl.bytes ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return GQA_ERR_INVALID;
-  // Tokens per copy: runs that neither a tile nor a page cuts.
-  const int run = page_size % pl.T == 0   ? pl.T
-                  : pl.T % page_size == 0 ? page_size
-                  : page_size % 16 == 0   ? 16 : 8;
+  // Tokens per copy: the largest power of two (8 at least) that divides the
+  // tile and the page.
+  int run = pl.T;
+  while (page_size % run != 0) run >>= 1;
   if (c8 && run * Hkv % 16 != 0) return GQA_ERR_UNSUPPORTED;
 
   CacheAttnParams p;
@@ -159,6 +159,8 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
   while ((1 << p.log_T) < pl.T) ++p.log_T;
   p.div_g.set((uint32_t)pl.G);
   p.div_page.set((uint32_t)page_size);
+  p.div_ctas.set((uint32_t)pl.ctas);
+  while ((1 << p.log_run) < run) ++p.log_run;
   p.run = run;
   p.NS = pl.NS;
   p.slot_bytes = pl.slot_bytes;

@@ -58,6 +58,7 @@ __host__ __device__ constexpr int ca_warps(int D, bool C8, int NT) {
   return NT == 1 && (D == 64 || (D == 128 && C8)) ? 16 : 8;
 }
 constexpr int kCaMaxSlots = 16;                    // ring slots at most
+constexpr int kCaPieces = 4;                       // pieces the producer may be ahead
 constexpr float kCaSlack = 4.f;
 constexpr int kCaWholeSlack = 6;                   // tiles a join is worth
 
@@ -97,7 +98,8 @@ struct CacheAttnParams {
   unsigned int* status;
   float* part_o;     // [2 per CTA][HPC * RT rows][D]
   float* part_ml;    // [2 per CTA][HPC * RT rows][2] (M, L)
-  int32_t* hdr;      // [0] units; [8 + 8 u ..] see hdr_of
+  int32_t* hdr;      // [0] units to look at; [8 + 8 u ..] unit u: pieces after its first, the
+                     // first's CTA, first row, first head, first token, tokens
   long long total_mask_words;
   unsigned long long timeout_ns;
   int entries, num_pages, page_size;
@@ -106,8 +108,8 @@ struct CacheAttnParams {
   int HPC, HG;       // heads per CTA, head groups
   int KW;            // warps that share a head's keys
   int T, log_T;      // keys per tile (16 GK KW, a power of two)
-  FastDiv div_g, div_page;
-  int run;           // tokens per copy: divides T and the page
+  FastDiv div_g, div_page, div_ctas;
+  int run, log_run;  // tokens per copy, a power of two that divides T and the page
   int NS;            // ring slots
   uint32_t slot_bytes, data_bytes;  // a slot, and its values (scales follow)
   int window, smooth;
@@ -130,7 +132,7 @@ __device__ __forceinline__ int ca_key(int m) {
 // fp32 and its rows' (M, L), the barriers, the tables of the sequences.
 __host__ __device__ constexpr uint32_t ca_fixed_smem(int warps) {
   return 1024u + 128u + (uint32_t)warps * (8u * 64u * 4u + 8u * 8u) + 2u * kCaMaxSlots * 8u + 32u +
-         4u * (5 * kMaxSeqs + 3) + 8u * 20u + 4u * 20u;
+         4u * (5 * kMaxSeqs + 3) + kCaPieces * (16u * 4u + 2u * 8u);
 }
 
 struct CaTab {
@@ -164,8 +166,7 @@ __device__ __forceinline__ void ca_range(const CacheAttnParams& p, int P, int E,
 
 // Equal shares of W tiles over C <= W CTAs: the first W % C hold one more.
 struct CaShares {
-  int q, r;
-  __device__ __forceinline__ CaShares(int W, int C) : q(W / C), r(W - W / C * C) {}
+  int q, r;  // W / C, W % C
   __device__ __forceinline__ int lo(int c) const { return c * q + min(c, r); }
   __device__ __forceinline__ int owner(int x) const {  // CTA of tile x
     const int big = r * (q + 1);
@@ -174,21 +175,33 @@ struct CaShares {
 };
 
 struct CaWalk {
-  int at, end;  // share mode: tiles left
+  int at, end;  // share mode: tiles left; whole mode: end is the unit count
   int unit;     // whole mode: next unit, every gridDim.x-th
   bool whole;
 };
 
+// Largest i in [0, n) with a[i] <= x (a[0] = 0 <= x) for a non-decreasing
+// shared-memory array, by a converged warp: 32 probes a step.
+__device__ __forceinline__ int warp_find(const int32_t* a, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const int i = lo + lane * step;
+    const int c = __popc(__ballot_sync(0xffffffffu, lane * step < n && a[i] <= x)) - 1;
+    lo += c * step;
+    n = min(step, n - c * step);
+  }
+  return lo;
+}
+
+// The next piece; called by a converged warp.
 __device__ __forceinline__ bool ca_next(const CacheAttnParams& p, const CaTab& T, CaWalk& w, int RT,
                                         CaPiece& u) {
   const int32_t* key = w.whole ? T.units : T.tiles;
   const int x = w.whole ? w.unit : w.at;
-  if (x >= (w.whole ? T.units[p.num_seqs] : w.end)) return false;
-  int lo = 0, hi = p.num_seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (key[mid] <= x) lo = mid; else hi = mid;
-  }
+  if (x >= w.end) return false;
+  const int lo = warp_find(key, p.num_seqs, x);
   u.b = lo;
   u.P = T.pre[lo];
   u.E = T.cu0[lo + 1] - T.cu0[lo];
@@ -310,15 +323,15 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
   float2* s_ml = reinterpret_cast<float2*>(scratch + NW * 8 * 64);  // [NW][8]
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_ml + NW * 8);
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 2 * kCaMaxSlots);  // [0] abort [1] bad
-  long long* wtot = reinterpret_cast<long long*>(misc + 8);  // [NW + 1]
-  int32_t* utot = reinterpret_cast<int32_t*>(wtot + 20);
-  int32_t* tiles = utot + 20;
+  uint64_t* pbars = reinterpret_cast<uint64_t*>(misc + 8);  // pieces: full, empty
+  int4* s_piece = reinterpret_cast<int4*>(pbars + 2 * kCaPieces);  // [kCaPieces][4]
+  int32_t* tiles = reinterpret_cast<int32_t*>(s_piece + 4 * kCaPieces);
   int32_t* units = tiles + (kMaxSeqs + 1);
   int32_t* s_cu = units + (kMaxSeqs + 1);
   int32_t* s_pre = s_cu + (kMaxSeqs + 1);
   int32_t* s_ipt = s_pre + kMaxSeqs;
   const uint32_t ring = (smem_u32(s_ipt + kMaxSeqs) + 127u) & ~127u;
-  const uint32_t sBar = smem_u32(bars);
+  const uint32_t sBar = smem_u32(bars), sPiece = smem_u32(pbars);
   volatile uint32_t* abort_flag = misc;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nact = p.HPC * p.KW;  // consumer warps at work
@@ -329,6 +342,10 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     for (int i = 0; i < p.NS; ++i) {
       mbar_init(sBar + 8u * i, 1u);
       mbar_init(sBar + 8u * (kCaMaxSlots + i), (uint32_t)nact);
+    }
+    for (int i = 0; i < kCaPieces; ++i) {
+      mbar_init(sPiece + 8u * i, 1u);
+      mbar_init(sPiece + 8u * (kCaPieces + i), (uint32_t)nact);
     }
     misc[0] = 0u;
     misc[1] = 0u;
@@ -341,11 +358,8 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
 
   const int nseq = p.num_seqs;
   bool bad = tid == 0 && p.first_seq == 0 && __ldg(p.cu) != 0;
-  long long my_tiles = 0;
-  int my_units = 0, my_max = 0;
-  const int per = (nseq + kThreads - 1) / kThreads;  // 1 up to 288 sequences
-  const int b_lo = min(tid * per, nseq), b_hi = min(b_lo + per, nseq);
-  for (int b = b_lo; b < b_hi; ++b) {
+  int my_max = 0;
+  for (int b = tid; b < nseq; b += kThreads) {
     const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), P = __ldg(p.pre + b);
     const int i0 = __ldg(p.indptr + b), i1 = __ldg(p.indptr + b + 1);
     const int E = c1 - c0;
@@ -373,52 +387,14 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     s_cu[b] = c0;
     s_pre[b] = P;
     s_ipt[b] = i0;
+    if (w > 0x7fffffffll) bad = true;  // more key tiles than the shares count
     tiles[b] = (int)w;
     units[b] = nu;
     if (b == nseq - 1) s_cu[nseq] = c1;
-    my_tiles += w;
-    my_units += nu;
   }
   if (bad) misc[1] = 1u;
   my_max = __reduce_max_sync(0xffffffffu, my_max);
   if (lane == 0 && my_max > 0) atomicMax(reinterpret_cast<int*>(misc + 2), my_max);
-  // Exclusive scans of the tiles and units: warp scans, then warp totals.
-  long long it = my_tiles;
-  int iu = my_units;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, it, o);
-    const int b = __shfl_up_sync(0xffffffffu, iu, o);
-    if (lane >= o) {
-      it += a;
-      iu += b;
-    }
-  }
-  if (lane == 31) {
-    wtot[warp] = it;
-    utot[warp] = iu;
-  }
-  __syncthreads();
-  {
-    long long at = it - my_tiles;
-    int au = iu - my_units;
-    for (int w = 0; w < warp; ++w) {
-      at += wtot[w];
-      au += utot[w];
-    }
-    for (int b = b_lo; b < b_hi; ++b) {
-      const int w = tiles[b], nu = units[b];
-      tiles[b] = (int)at;
-      units[b] = au;
-      at += w;
-      au += nu;
-      if (b == nseq - 1) {
-        if (at > 0x7fffffffll) misc[1] = 1u;  // more key tiles than the shares count
-        tiles[nseq] = (int)at;
-        units[nseq] = au;
-      }
-    }
-  }
   __syncthreads();
   const bool bad_meta = misc[1] != 0u;
   if (p.metadata_ready) grid_dep_wait();  // before any global write or other read
@@ -429,46 +405,117 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     }
     return;
   }
-  const CaTab T{tiles, units, s_cu, s_pre, s_ipt};
-  const int W = tiles[nseq], n_units = units[nseq], c = blockIdx.x;
-  // No more shares than tiles: every share holds a tile, so the pieces of a
-  // cut unit lie on consecutive CTAs.
-  const int C = min(W, (int)gridDim.x);
-  // Whole units when the deepest deal costs no more than an equal share and
-  // the join that cut units need.
-  CaWalk walk;
-  walk.whole = p.whole != 0 ||
-               (long long)((n_units + (int)gridDim.x - 1) / (int)gridDim.x) * (int)misc[2] <=
-                   W / max(C, 1) + kCaWholeSlack;
-  if (c == 0 && tid == 0) p.hdr[0] = walk.whole ? 0 : n_units;
-  if (c >= C) return;
-  const CaShares shares(W, C);
-  walk.unit = c;
-  walk.at = shares.lo(c);
-  walk.end = shares.lo(c + 1);
-
   const uint32_t row_bytes = H8 ? 8u * D * kEsz : (uint32_t)p.HPC * D * kEsz;  // a token in the ring
   const long long tok_bytes = (long long)p.Hkv * D * kEsz;      // in the pool
 
   if (warp == NW) {
     // -------------------------------------------------------------- producer
+    // Plans the CTA's work, tells the consumers piece by piece, and fills the
+    // ring; the other warps would only repeat the planning (17 warps doing so
+    // cost 3000 clocks before the first load).
+    // Exclusive scans of the tiles and units, a run of sequences a lane.
+    {
+      const int per = (nseq + 31) >> 5, b0 = min(lane * per, nseq), b1 = min(b0 + per, nseq);
+      long long st = 0;
+      int su = 0;
+      for (int b = b0; b < b1; ++b) {
+        st += tiles[b];
+        su += units[b];
+      }
+      long long at = st;
+      int au = su;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, at, o);
+        const int y = __shfl_up_sync(0xffffffffu, au, o);
+        if (lane >= o) {
+          at += x;
+          au += y;
+        }
+      }
+      const long long total = __shfl_sync(0xffffffffu, at, 31);
+      if (lane == 31) {
+        units[nseq] = au;
+        tiles[nseq] = total > 0x7fffffffll ? -1 : (int)total;
+      }
+      at -= st;
+      au -= su;
+      for (int b = b0; b < b1; ++b) {
+        const int w = tiles[b], nu = units[b];
+        tiles[b] = (int)at;
+        units[b] = au;
+        at += w;
+        au += nu;
+      }
+      __syncwarp();
+    }
+    const CaTab T{tiles, units, s_cu, s_pre, s_ipt};
+    int W = tiles[nseq];
+    if (W < 0) {  // more key tiles than the shares count: nothing is done
+      if (lane == 0) atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
+      W = 0;
+    }
+    const int n_units = W > 0 ? units[nseq] : 0, grid = gridDim.x, c = blockIdx.x;
+    // No more shares than tiles: every share holds a tile, so the pieces of a
+    // cut unit lie on consecutive CTAs.
+    const int C = min(W, grid);
+    const int per = W < grid ? 1 : p.div_ctas.div(W);  // tiles of the smaller shares
+    const CaShares shares{per, W < grid ? 0 : W - per * grid};
+    // Whole units when the deepest deal costs no more than an equal share and
+    // the join that cut units need.
+    CaWalk walk;
+    walk.whole = p.whole != 0 || (long long)p.div_ctas.div(n_units + grid - 1) * (int)misc[2] <=
+                                     per + kCaWholeSlack;
+    walk.unit = c;
+    walk.at = c < C ? shares.lo(c) : 0;
+    walk.end = walk.whole ? n_units : c < C ? shares.lo(c + 1) : 0;
+    if (c == 0 && lane == 0) p.hdr[0] = walk.whole ? 0 : n_units;
     // The tile's runs are spread over the lanes; slots alternate K and V.
-    uint32_t slot = 0, ph = 0, issued = 0;
+    uint32_t slot = 0, ph = 0, issued = 0, pi = 0;
     bool ok = true;
-    CaPiece u;
+    CaPiece u = {};
     const int nrun = p.T / p.run;  // the tile's copies, one a lane
-    while (ok && ca_next(p, T, walk, RT, u)) {
+    for (;; ++pi) {
+      const bool more = ca_next(p, T, walk, RT, u);
+      // ---- tell the consumers
+      const uint32_t ps = pi % kCaPieces;
+      if (lane == 0)
+        ok = wait_bounded(sPiece + 8u * (kCaPieces + ps), ((pi / kCaPieces) & 1u) ^ 1u, abort_flag,
+                          p.status, tmo);
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      if (!ok) break;
+      const bool cut = more && (u.t0 > 0 || u.t1 < u.n);
+      if (lane == 0) {
+        int4* d = s_piece + 4 * ps;
+        const int m0 = more && p.mask != nullptr ? __ldg(p.mask_indptr + u.b) : 0;
+        d[0] = make_int4(more ? u.t1 - u.t0 : 0, (cut ? 1 : 0) | (cut && u.t0 == 0 ? 2 : 0),
+                         u.lo + (u.t0 << p.log_T), u.P);
+        d[1] = make_int4(u.E, u.hi, u.rt * RT, u.hg * p.HPC);
+        d[2] = make_int4(more ? T.cu0[u.b] : 0, m0, 0, 0);
+        mbar_arrive(sPiece + 8u * ps);
+        if (more && !walk.whole && u.t0 == 0) {  // the unit's first piece: its entry for the join
+          int4* hd = reinterpret_cast<int4*>(p.hdr + 8 + 8ll * u.unit);
+          hd[0] = make_int4(cut ? shares.owner(walk.at - u.t1 + u.n - 1) - c : 0, c, u.rt * RT,
+                            u.hg * p.HPC);
+          hd[1] = make_int4(T.cu0[u.b], u.E, 0, 0);
+        }
+      }
+      if (!more) break;
       const int npg = p.div_page.div(u.P + u.E - 1) + 1;
       const int32_t* table = p.indices + T.ipt[u.b];
       for (int t = u.t0; ok && t < u.t1; ++t) {
         const int n0 = u.lo + t * p.T;
+        // Tokens [skip, ntok) of the tile: keys below the window are not read.
         const int ntok = min(p.T, u.hi - n0);
+        const int skip = p.window > 0 ? max(u.P - p.window + 1 - n0, 0) : 0;
         for (int kv = 0; kv < 2; ++kv) {
           if (lane == 0) {
             ok = wait_bounded(sBar + 8u * (kCaMaxSlots + slot), ph ^ 1u, abort_flag, p.status, tmo);
             if (ok) {
-              uint32_t bytes = (uint32_t)ntok * row_bytes;
-              if (C8) bytes += (uint32_t)((ntok + p.run - 1) / p.run * p.run) * (uint32_t)p.Hkv;
+              uint32_t bytes = (uint32_t)(ntok - skip) * row_bytes;
+              if (C8)
+                bytes += (uint32_t)(((ntok + p.run - 1) >> p.log_run) - (skip >> p.log_run)) *
+                         (uint32_t)(p.run * p.Hkv);
               mbar_arrive_expect_tx(sBar + 8u * slot, bytes);
             }
           }
@@ -477,7 +524,9 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
           const uint32_t dst = ring + slot * p.slot_bytes, bar = sBar + 8u * slot;
           const uint8_t* pages = kv ? p.v_pages : p.k_pages;
           for (int r = lane; r < nrun && r * p.run < ntok; r += 32) {
-            const int key = n0 + r * p.run, cnt = min(p.run, ntok - r * p.run);
+            const int first = max(skip - r * p.run, 0);  // the run's first live token
+            const int key = n0 + r * p.run, cnt = min(p.run, ntok - r * p.run) - first;
+            if (cnt <= 0) continue;
             const int kp = p.div_page.div(key);
             int pg = __ldg(table + min(kp, npg - 1));
             if (pg < 0 || pg >= p.num_pages) {
@@ -485,8 +534,8 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
               pg = 0;
             }
             const long long row = (long long)pg * p.page_size + (key - kp * p.page_size);
-            const uint8_t* src = pages + row * tok_bytes + (long long)u.hg * row_bytes;
-            const uint32_t to = dst + (uint32_t)(r * p.run) * row_bytes;
+            const uint8_t* src = pages + (row + first) * tok_bytes + (long long)u.hg * row_bytes;
+            const uint32_t to = dst + (uint32_t)(r * p.run + first) * row_bytes;
             if (p.HG == 1)
               bulk_load(to, src, (uint32_t)cnt * row_bytes, bar);
             else
@@ -504,6 +553,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
           }
         }
       }
+      if (!ok) break;
     }
     // Let every copy issued land before the CTA can exit.
     __syncwarp();
@@ -523,11 +573,21 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     return __all_sync(0xffffffffu, wait_bounded(sBar + 8u * sl, parity, abort_flag, p.status, tmo)) != 0;
   };
   uint32_t slot = 0, ph = 0;
-  CaPiece u;
   bool ok = true;
-  while (ok && ca_next(p, T, walk, RT, u)) {
-    const int head = u.hg * p.HPC + hl;  // KV head
-    const int cu0 = T.cu0[u.b];
+  for (uint32_t pi = 0; ok; ++pi) {
+    // ---- the next piece
+    const uint32_t ps = pi % kCaPieces;
+    ok = __all_sync(0xffffffffu, wait_bounded(sPiece + 8u * ps, (pi / kCaPieces) & 1u, abort_flag,
+                                              p.status, tmo)) != 0;
+    if (!ok) break;
+    const int4 d0 = s_piece[4 * ps], d1 = s_piece[4 * ps + 1], d2 = s_piece[4 * ps + 2];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sPiece + 8u * (kCaPieces + ps));
+    const int n_tiles = d0.x, P = d0.w, E = d1.x, hi = d1.y, row0 = d1.z;
+    const bool cut = (d0.y & 1) != 0;
+    if (n_tiles == 0) break;
+    const int head = d1.w + hl;  // KV head
+    const int cu0 = d2.x;
     // Softmax rows of the thread: 2 t and 2 t + 1 of every 8-row tile.
     int ri[NT][2], rdep[NT][2];  // token index (-1: none) and depth
     float rs[NT][2];             // scale to the log2 domain
@@ -535,8 +595,8 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     for (int m = 0; m < NT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int i = p.div_g.div(u.rt * RT + m * 8 + 2 * t + h);
-        const bool on = i < u.E;
+        const int i = p.div_g.div(row0 + m * 8 + 2 * t + h);
+        const bool on = i < E;
         ri[m][h] = on ? i : -1;
         rdep[m][h] = i;
         if (on && p.depths != nullptr) rdep[m][h] = __ldg(p.depths + cu0 + i);
@@ -546,9 +606,9 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     uint32_t qf[NT][KS][2];
 #pragma unroll
     for (int m = 0; m < NT; ++m) {
-      const int r = u.rt * RT + m * 8 + g;
+      const int r = row0 + m * 8 + g;
       const int i = p.div_g.div(r);
-      const bool on = i < u.E;
+      const bool on = i < E;
       const uint16_t* qr = static_cast<const uint16_t*>(p.q) +
                            ((long long)(cu0 + (on ? i : 0)) * p.Hq + head * p.G + (r - i * p.G)) * D;
       if constexpr (C8) {
@@ -601,8 +661,8 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
                           (uint32_t)(hl * D * kEsz + 8 * kEsz * g);
     const uint32_t soff = p.data_bytes + (uint32_t)((kw * 16 * GK + ca_key(g)) * p.Hkv + head);
 
-    for (int tl = u.t0; tl < u.t1; ++tl) {
-      const int n0 = u.lo + tl * p.T + kw * 16 * GK;  // this warp's first key
+    int n0 = d0.z + kw * 16 * GK;  // this warp's first key
+    for (int tl = 0; tl < n_tiles; ++tl, n0 += p.T) {
       // ---- scores of 16 GK keys
       if (!(ok = wait_full(slot, ph))) break;
       float s[NT][GK][4];  // [(key g, g + 8) x (row 2 t, 2 t + 1)]
@@ -678,13 +738,13 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
           }
       // Which keys need a look at the mask: any at or past the prefix's end
       // (causal, tree, end of the sequence) or below some row's window.
-      const bool edge = n0 + 16 * GK > u.P || p.window > 0;
+      const bool edge = n0 + 16 * GK > P || p.window > 0;
       if (__builtin_expect(edge, 0)) {
 #pragma unroll
         for (int k = 0; k < GK; ++k)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int x = n0 + 16 * k + ca_key(g + 8 * j) - u.P;  // index among the new tokens
+            const int x = n0 + 16 * k + ca_key(g + 8 * j) - P;  // index among the new tokens
 #pragma unroll
             for (int m = 0; m < NT; ++m)
 #pragma unroll
@@ -692,8 +752,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
                 const int i = ri[m][h];
                 bool keep = i >= 0 && x <= i;
                 if (keep && x >= 0 && p.mask != nullptr)
-                  keep = (__ldg(p.mask + __ldg(p.mask_indptr + u.b) +
-                                (long long)i * ((u.E + 31) >> 5) + (x >> 5)) >>
+                  keep = (__ldg(p.mask + (long long)d2.y + (long long)i * ((E + 31) >> 5) + (x >> 5)) >>
                           (x & 31)) & 1u;
                 if (keep && p.window > 0) {
                   const int place = x >= 0 && p.depths != nullptr ? __ldg(p.depths + cu0 + x) : x;
@@ -702,7 +761,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
                 if (!keep) s[m][k][2 * j + h] = -INFINITY;
               }
             if constexpr (C8)  // keys that no row sees may have any scale
-              if (x + u.P >= u.hi || (p.window > 0 && x <= -p.window)) wi[k][j] = 0.f;
+              if (x + P >= hi || (p.window > 0 && x <= -p.window)) wi[k][j] = 0.f;
           }
       }
       // ---- the references: moved when some score exceeds one by kCaSlack
@@ -765,7 +824,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int key = n0 + 16 * k + 4 * t + j;
-            if (key >= u.hi || (p.window > 0 && key <= u.P - p.window)) live &= ~(1u << j);
+            if (key >= hi || (p.window > 0 && key <= P - p.window)) live &= ~(1u << j);
           }
         }
 #pragma unroll
@@ -829,19 +888,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     // ---- the unit's (or piece's) rows: join the warps of a head, write.
     // Warp area [8 rows][64 columns] in shared memory, a tile and 64 columns
     // at a time; with one warp per head only that warp takes part.
-    const bool cut = u.t0 > 0 || u.t1 < u.n;
-    const long long pslot = 2ll * c + (u.t0 > 0 ? 0 : 1);
-    if (cut && u.t0 == 0 && hl == 0 && kw == 0 && lane == 0) {
-      int32_t* hd = p.hdr + 8 + 8ll * u.unit;
-      hd[0] = shares.owner(walk.at - u.t1 + u.n - 1) - c;  // pieces after the first
-      hd[1] = c;
-      hd[2] = u.rt * RT;
-      hd[3] = u.hg * p.HPC;
-      hd[4] = cu0;
-      hd[5] = u.E;
-    } else if (!walk.whole && !cut && hl == 0 && kw == 0 && lane == 0) {
-      p.hdr[8 + 8ll * u.unit] = 0;
-    }
+    const long long pslot = 2ll * blockIdx.x + (d0.y >> 1);
 #pragma unroll
     for (int m = 0; m < NT; ++m)
 #pragma unroll
@@ -875,9 +922,9 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
         join();
         // Four rows a warp at a time, 8 columns a lane.
         for (int r = 4 * kw + (lane >> 3); r < 8; r += 4 * p.KW) {
-          const int gr = u.rt * RT + m * 8 + r;  // row of the sequence
+          const int gr = row0 + m * 8 + r;  // row of the sequence
           const int i = p.div_g.div(gr);
-          if (i >= u.E || !ok) continue;
+          if (i >= E || !ok) continue;
           const int qh = head * p.G + (gr - i * p.G);
           float xs = -INFINITY;
           if (!cut && p.sinks != nullptr) xs = __ldg(p.sinks + qh) * kLog2e;
