@@ -65,20 +65,38 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]), pack2<BF16>(x[4], x[5]),
                     pack2<BF16>(x[6], x[7]));
 }
+// 8 values times f as e4m3, rounded to nearest even, infinities to the largest.
+__device__ __forceinline__ uint2 narrow8(const float (&x)[8], float f) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * f, x[4 * i + 1] * f),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * f, x[4 * i + 3] * f),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    w[i] = lo | hi << 16;
+  }
+  return make_uint2(w[0], w[1]);
+}
 template <bool BF16>
 __device__ __forceinline__ float load16(const uint16_t* p) {
   return unpack_lo<BF16>((uint32_t)*p);
 }
 
 // One CTA: up to `tokens` consecutive rows, all their heads (blockIdx.y takes
-// every gridDim.y-th slice of the heads).  A thread owns one vector of 8
+// every gridDim.y-th slice of the heads).  A thread owns two vectors of 8
 // values at a fixed place of a fixed token and walks the heads, so the angles
-// of its vector are found once: the CTA computes tokens * half pairs of
-// (cos, sin) into shared memory, each thread keeps its 8 (or 4) in registers.
+// are found once: the CTA computes tokens * half pairs of (cos, sin) into
+// shared memory and each thread keeps its own in registers.  The two vectors
+// are neighbours, or, when halves pair up, the two that rotate into each
+// other: every value is then read once.  The next head's loads are issued
+// before this head's arithmetic, the first ones before the angles.
 // Rotation, scale search and rounding run in fp32; the result is rounded once.
+// (One vector a thread that read its partner's as well: 16k rows of 64 / 8
+// heads 77 us.)
 template <bool BF16, int OUT, int PAIR>
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowsParams p) {
-  extern __shared__ float2 s_cs[];  // [tokens][half]
+  extern __shared__ float2 s_cs[];  // [tokens][half], then the steps [half]
   __shared__ int s_key[kMaxTokens];
   __shared__ long long s_slot[kMaxTokens];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -87,151 +105,168 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
   grid_dep_launch_dependents();
   grid_dep_wait();
 
-  if (OUT != kOutRows) {  // a warp per token: its sequence, key index and pool row
-    if (warp < ntok) {
-      const int r = row0 + warp;
-      const int b = warp_upper_bound(p.cu + 1, p.pt.num_seqs, r);
-      if (lane == 0) {
-        bool bad = false;
-        long long slot = -1;
-        int key = 0;
-        if (b < p.pt.num_seqs) {
-          const int c0 = __ldg(p.cu + b), P = __ldg(p.pre + b);
-          const long long at = (long long)P + (r - c0);
-          if (c0 < 0 || c0 > r || P < 0 || at > 0x7fffffffll)
-            bad = true;
-          else
-            slot = key_slot(p.pt, b, at, &bad);
-          key = (int)at;
-        }
-        if (bad) atomicOr(p.status, (unsigned)GQA_DEV_BAD_METADATA);
-        s_slot[warp] = slot;
-        s_key[warp] = key;
-      }
-    }
-    __syncthreads();
+  // ---- this thread's vectors
+  const int nt = (p.d + 15) >> 4;            // threads per head
+  const int slices = kRowThreads / nt / p.tokens;  // heads in flight
+  const int vec = tid % nt, rest = tid / nt;
+  const int t = rest % p.tokens, slice = rest / p.tokens;
+  const int rot = 2 * p.half, turning = p.half >> 3;  // threads of a head that rotate (halves)
+  int ea = 16 * vec, eb = 16 * vec + 8;
+  if (PAIR == kPairHalf8) {
+    ea = vec < turning ? 8 * vec : 16 * vec;
+    eb = vec < turning ? 8 * vec + p.half : 16 * vec + 8;
   }
+  const int heads = p.hq + p.hkv + (OUT != kOutRows ? p.hkv : 0);
+  const bool active = slice < slices && t < ntok;
+  const bool two = eb < p.d;
+  const int row = row0 + (active ? t : 0);
+  const int step = slices * gridDim.y;
+  const int first = blockIdx.y * slices + slice;
+  // All lanes take every turn: the scale search shuffles over the warp.
+  const int turns = (heads - (int)blockIdx.y * slices + step - 1) / step;
+  auto source = [&](int h) {  // head h of the row: q, then k, then v
+    const uint16_t* base = static_cast<const uint16_t*>(p.q) + row * p.q_stride + (long long)h * p.d;
+    if (h >= p.hq)
+      base = static_cast<const uint16_t*>(p.k) + row * p.k_stride + (long long)(h - p.hq) * p.d;
+    if (OUT != kOutRows && h >= p.hq + p.hkv)
+      base = static_cast<const uint16_t*>(p.v) + row * p.v_stride +
+             (long long)(h - p.hq - p.hkv) * p.d;
+    return base;
+  };
+  uint4 na = make_uint4(0u, 0u, 0u, 0u), nb = na;
+  auto fetch = [&](int h) {
+    if (!active || h >= heads) return;
+    const uint16_t* src = source(h);
+    na = *reinterpret_cast<const uint4*>(src + ea);
+    if (two) nb = *reinterpret_cast<const uint4*>(src + eb);
+  };
+  fetch(first);
+
+  // ---- tokens' places and angles
   if (PAIR != kPairNone) {
+    unsigned long long* s_step = reinterpret_cast<unsigned long long*>(s_cs + p.tokens * p.half);
+    for (int j = tid; j < p.half; j += kRowThreads) s_step[j] = phase_step(__ldg(p.inv_freq + j));
+  }
+  if (OUT != kOutRows && warp < ntok) {  // a warp per token: its sequence, key and pool row
+    const int r = row0 + warp;
+    const int b = warp_upper_bound(p.cu + 1, p.pt.num_seqs, r);
+    if (lane == 0) {
+      bool bad = false;
+      long long slot = -1;
+      int key = 0;
+      if (b < p.pt.num_seqs) {
+        const int c0 = __ldg(p.cu + b), P = __ldg(p.pre + b);
+        const long long at = (long long)P + (r - c0);
+        if (c0 < 0 || c0 > r || P < 0 || at > 0x7fffffffll)
+          bad = true;
+        else
+          slot = key_slot(p.pt, b, at, &bad);
+        key = (int)at;
+      }
+      if (bad) atomicOr(p.status, (unsigned)GQA_DEV_BAD_METADATA);
+      s_slot[warp] = slot;
+      s_key[warp] = key;
+    }
+  }
+  if (OUT != kOutRows || PAIR != kPairNone) __syncthreads();
+  if (PAIR != kPairNone) {
+    const unsigned long long* s_step =
+        reinterpret_cast<const unsigned long long*>(s_cs + p.tokens * p.half);
     for (int i = tid; i < ntok * p.half; i += kRowThreads) {
-      const int t = i / p.half, j = i - t * p.half;
-      const int pos = p.positions != nullptr ? __ldg(p.positions + row0 + t) : s_key[t];
-      float2 cs = phase_cos_sin(pos, phase_step(__ldg(p.inv_freq + j)));
+      const int tt = i / p.half, j = i - tt * p.half;
+      const int pos = p.positions != nullptr ? __ldg(p.positions + row0 + tt) : s_key[tt];
+      float2 cs = phase_cos_sin(pos, s_step[j]);
       cs.x *= p.factor;
       cs.y *= p.inverse ? -p.factor : p.factor;
       s_cs[i] = cs;
     }
     __syncthreads();
   }
-
-  const int nvec = p.d >> 3;
-  const int vec = tid % nvec, rest = tid / nvec;
-  const int per = kRowThreads / nvec;            // vectors' groups in the CTA
-  const int slices = per / p.tokens;             // heads in flight
-  const int t = rest % p.tokens, slice = rest / p.tokens;
-  const int e0 = vec * 8;
-  const int heads = p.hq + p.hkv + (OUT != kOutRows ? p.hkv : 0);
-  const bool active = rest < slices * p.tokens && t < ntok;
-  const int row = row0 + (active ? t : 0);
   const long long slot = OUT != kOutRows ? s_slot[active ? t : 0] : 0;
-
-  // This vector's part in the rotation: 0 none, 1 first of its pairs, -1 second.
-  const int rot = 2 * p.half;
-  int side = 0;
+  // The thread's angles: pairs of the two vectors, or the pairs within each.
   float2 cs[8];
-  if (PAIR == kPairHalf8 && active && e0 < rot) {
-    side = e0 < p.half ? 1 : -1;
-    const float2* c = s_cs + t * p.half + (side > 0 ? e0 : e0 - p.half);
+  const bool turner = PAIR == kPairHalf8 ? vec < turning : ea < rot;
+  if ((PAIR == kPairHalf8 || PAIR == kPairNext) && active && turner) {
+    const float2* c = s_cs + t * p.half + 8 * vec;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = c[i];
-  }
-  if (PAIR == kPairNext && active) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      cs[i] = e0 + 2 * i < rot ? s_cs[t * p.half + e0 / 2 + i] : make_float2(1.f, 0.f);
-    side = e0 < rot ? 1 : 0;
+    for (int i = 0; i < 8; ++i)
+      cs[i] = PAIR == kPairHalf8 || 16 * vec + 2 * i < rot ? c[i] : make_float2(1.f, 0.f);
   }
 
-  const int step = slices * gridDim.y;
-  const int first = blockIdx.y * slices + slice;
-  // All lanes take every turn: the scale search shuffles over the warp.
-  const int turns = (heads - (int)blockIdx.y * slices + step - 1) / step;
-#pragma unroll 2
   for (int n = 0; n < turns; ++n) {
     const int h = first + n * step;
     const bool on = active && h < heads;
     const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv;
     const int hh = is_q ? h : is_k ? h - p.hq : h - p.hq - p.hkv;
-    const uint16_t* src =
-        is_q ? static_cast<const uint16_t*>(p.q) + row * p.q_stride
-             : is_k ? static_cast<const uint16_t*>(p.k) + row * p.k_stride
-                    : static_cast<const uint16_t*>(p.v) + row * p.v_stride;
-    src += (long long)hh * p.d;
-    float x[8];
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (on) raw = *reinterpret_cast<const uint4*>(src + e0);
-    unpack8<BF16>(raw, x);
-    const bool turn = PAIR != kPairNone && on && (is_q || is_k);
-    if (PAIR == kPairHalf8 && turn && side != 0) {
-      float y[8];
-      unpack8<BF16>(*reinterpret_cast<const uint4*>(src + e0 + (side > 0 ? p.half : -p.half)), y);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        x[i] = side > 0 ? x[i] * cs[i].x - y[i] * cs[i].y : x[i] * cs[i].x + y[i] * cs[i].y;
-    }
-    if (PAIR == kPairHalf && turn && e0 < rot) {  // halves that do not fill vectors
+    float x[8], y[8];
+    unpack8<BF16>(na, x);
+    unpack8<BF16>(nb, y);
+    if (n + 1 < turns) fetch(h + step);
+    const bool turn = PAIR != kPairNone && on && turner && (is_q || is_k);
+    if (PAIR == kPairHalf8 && turn) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int e = e0 + i;
-        if (e < p.half) {
-          const float2 c = s_cs[t * p.half + e];
-          x[i] = x[i] * c.x - load16<BF16>(src + e + p.half) * c.y;
-        } else if (e < rot) {
-          const float2 c = s_cs[t * p.half + e - p.half];
-          x[i] = x[i] * c.x + load16<BF16>(src + e - p.half) * c.y;
+        const float a = x[i], b = y[i];
+        x[i] = a * cs[i].x - b * cs[i].y;
+        y[i] = b * cs[i].x + a * cs[i].y;
+      }
+    }
+    if (PAIR == kPairNext && turn) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = x[2 * i], b = x[2 * i + 1];
+        const float c = y[2 * i], d = y[2 * i + 1];
+        if (ea + 2 * i < rot) {  // values past the rotated part stay
+          x[2 * i] = a * cs[i].x - b * cs[i].y;
+          x[2 * i + 1] = b * cs[i].x + a * cs[i].y;
+        }
+        if (eb + 2 * i < rot) {
+          y[2 * i] = c * cs[4 + i].x - d * cs[4 + i].y;
+          y[2 * i + 1] = d * cs[4 + i].x + c * cs[4 + i].y;
         }
       }
     }
-    if (PAIR == kPairNext && turn && side != 0) {
+    if (PAIR == kPairHalf && turn) {  // halves that do not fill vectors: partners one by one
+      const uint16_t* src = source(h);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (e0 + 2 * i >= rot) break;  // values past the rotated part stay
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * cs[i].x - b * cs[i].y;
-        x[2 * i + 1] = b * cs[i].x + a * cs[i].y;
+      for (int i = 0; i < 16; ++i) {
+        const int e = (i < 8 ? ea : eb) + (i & 7);
+        float& z = i < 8 ? x[i & 7] : y[i & 7];
+        if (e < p.half) {
+          const float2 c = s_cs[t * p.half + e];
+          z = z * c.x - load16<BF16>(src + e + p.half) * c.y;
+        } else if (e < rot) {
+          const float2 c = s_cs[t * p.half + e - p.half];
+          z = z * c.x + load16<BF16>(src + e - p.half) * c.y;
+        }
       }
     }
-    if (OUT == kOutRows || is_q) {
-      if (on) {
-        uint16_t* dst = is_q ? static_cast<uint16_t*>(p.q_out) + row * p.q_out_stride
-                             : static_cast<uint16_t*>(p.k_out) + row * p.k_out_stride;
-        *reinterpret_cast<uint4*>(dst + (long long)hh * p.d + e0) = pack8<BF16>(x);
+    if (OUT == kOutRows || is_q || OUT == kOutCache16) {
+      if (on && (OUT == kOutRows || is_q || slot >= 0)) {
+        uint16_t* dst;
+        if (OUT == kOutRows || is_q)
+          dst = is_q ? static_cast<uint16_t*>(p.q_out) + row * p.q_out_stride
+                     : static_cast<uint16_t*>(p.k_out) + row * p.k_out_stride;
+        else
+          dst = static_cast<uint16_t*>(is_k ? p.k_out : p.v_out) + slot * p.hkv * p.d;
+        dst += (long long)hh * p.d;
+        *reinterpret_cast<uint4*>(dst + ea) = pack8<BF16>(x);
+        if (two) *reinterpret_cast<uint4*>(dst + eb) = pack8<BF16>(y);
       }
-      if (OUT != kOutCache8) continue;
-    }
-    if (OUT == kOutCache16 && on && slot >= 0) {
-      uint16_t* dst = static_cast<uint16_t*>(is_k ? p.k_out : p.v_out);
-      *reinterpret_cast<uint4*>(dst + (slot * p.hkv + hh) * p.d + e0) = pack8<BF16>(x);
     }
     if (OUT == kOutCache8) {
       float amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));  // NaN counts as absent
-      for (int o = nvec >> 1; o > 0; o >>= 1)
+      for (int i = 0; i < 8; ++i)  // NaN counts as absent
+        amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
+      for (int o = nt >> 1; o > 0; o >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (on && !is_q && slot >= 0) {
         const int e = e4m3_scale_exponent(amax);
         const float inv = pow2f(-e);
-        uint32_t w[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-              make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-          const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-              make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-          w[i] = lo | hi << 16;
-        }
-        uint8_t* dst = static_cast<uint8_t*>(is_k ? p.k_out : p.v_out);
-        *reinterpret_cast<uint2*>(dst + (slot * p.hkv + hh) * p.d + e0) = make_uint2(w[0], w[1]);
+        uint8_t* dst = static_cast<uint8_t*>(is_k ? p.k_out : p.v_out) + (slot * p.hkv + hh) * p.d;
+        *reinterpret_cast<uint2*>(dst + ea) = narrow8(x, inv);
+        *reinterpret_cast<uint2*>(dst + eb) = narrow8(y, inv);
         if (vec == 0) (is_k ? p.k_scales : p.v_scales)[slot * p.hkv + hh] = (uint8_t)(e + 127);
       }
     }
@@ -357,17 +392,16 @@ bool row_ok(const void* p, long long stride, long long width) {
   return p != nullptr && aligned(p, 16) && stride >= width && stride % 8 == 0;
 }
 
-// Tokens per CTA and head slices.  Many rows: 64 vector groups of 8 lanes
-// (d = 64) share a CTA's angles over up to 8 tokens, every head walked by the
-// same threads.  Few rows (the CTAs of that shape would not fill the SMs
-// twice): one token per CTA and its heads spread over blockIdx.y, so each
-// thread has one vector or two and the call is one round of loads.
+// Tokens per CTA and head slices.  Many rows: up to 8 tokens share a CTA's
+// angles (8 at d = 64: 4 threads a head, 8 heads in flight).  Few rows (the
+// CTAs of that shape would not fill the SMs twice): one token per CTA and its
+// heads spread over blockIdx.y, so that a thread has one head or two.
 int launch_row_op(RowsParams& p, int out, int interleaved, bool bf16, void* stream) {
   int sms = 0;
   if (call_device(&sms, &p.status) != GQA_OK) return GQA_ERR_CUDA;
-  const int nvec = p.d / 8, per = kRowThreads / nvec;
+  const int nt = (p.d + 15) / 16, per = kRowThreads / nt;
   const int heads = p.hq + p.hkv + (out != kOutRows ? p.hkv : 0);
-  int tokens = 64 / nvec;
+  int tokens = 32 / nt;
   if (tokens < 1) tokens = 1;
   if (tokens > kMaxTokens) tokens = kMaxTokens;
   int gy = 1;
@@ -380,7 +414,7 @@ int launch_row_op(RowsParams& p, int out, int interleaved, bool bf16, void* stre
   const int pair = p.half == 0 ? kPairNone
                    : interleaved ? kPairNext
                    : p.half % 8 == 0 ? kPairHalf8 : kPairHalf;
-  const unsigned smem = (unsigned)tokens * (unsigned)p.half * 8u;
+  const unsigned smem = (unsigned)(tokens + 1) * (unsigned)p.half * 8u;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (out == kOutRows)
