@@ -17,8 +17,9 @@ namespace gqa {
 
 namespace {
 
-constexpr int kRowThreads = 256;
-constexpr int kMaxTokens = 8;  // tokens a CTA handles at most
+constexpr int kRowThreads = 64;    // of the row kernel
+constexpr int kMaxTokens = 8;      // tokens one of its CTAs handles at most
+constexpr int kReadThreads = 256;  // of the read kernel
 
 // Where the values of one call come from and go to.
 struct RowsParams {
@@ -147,25 +148,24 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     unsigned long long* s_step = reinterpret_cast<unsigned long long*>(s_cs + p.tokens * p.half);
     for (int j = tid; j < p.half; j += kRowThreads) s_step[j] = phase_step(__ldg(p.inv_freq + j));
   }
-  if (OUT != kOutRows && warp < ntok) {  // a warp per token: its sequence, key and pool row
-    const int r = row0 + warp;
-    const int b = warp_upper_bound(p.cu + 1, p.pt.num_seqs, r);
-    if (lane == 0) {
+  if (OUT != kOutRows) {  // a warp per token: its sequence, key and pool row
+    for (int i = warp; i < ntok; i += kRowThreads / 32) {
+      const int r = row0 + i;
+      const int b = warp_upper_bound(p.cu + 1, p.pt.num_seqs, r);
+      if (lane != 0) continue;
       bool bad = false;
-      long long slot = -1;
-      int key = 0;
+      long long at = 0, place = -1;
       if (b < p.pt.num_seqs) {
         const int c0 = __ldg(p.cu + b), P = __ldg(p.pre + b);
-        const long long at = (long long)P + (r - c0);
+        at = (long long)P + (r - c0);
         if (c0 < 0 || c0 > r || P < 0 || at > 0x7fffffffll)
           bad = true;
         else
-          slot = key_slot(p.pt, b, at, &bad);
-        key = (int)at;
+          place = key_slot(p.pt, b, at, &bad);
       }
       if (bad) atomicOr(p.status, (unsigned)GQA_DEV_BAD_METADATA);
-      s_slot[warp] = slot;
-      s_key[warp] = key;
+      s_slot[i] = place;
+      s_key[i] = (int)at;
     }
   }
   if (OUT != kOutRows || PAIR != kPairNone) __syncthreads();
@@ -304,14 +304,14 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, float s) {
 // finds two rows' pool rows, then the CTA's threads walk 16-value (e4m3) or
 // 8-value (16-bit) vectors, 16-byte loads and stores.
 template <bool BF16, bool C8>
-__global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant__ ReadParams p) {
+__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
   __shared__ long long s_slot[kReadRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row0 = blockIdx.x * kReadRows;
   const int nrow = min(kReadRows, p.rows - row0);
   grid_dep_launch_dependents();
   grid_dep_wait();
-  for (int i = warp; i < nrow; i += kRowThreads / 32) {
+  for (int i = warp; i < nrow; i += kReadThreads / 32) {
     const int r = row0 + i;
     const int b = warp_upper_bound(p.kv_indptr + 1, p.pt.num_seqs, r);
     if (lane == 0) {
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
   const int per_row = p.hkv * per_head;  // vectors of a row
   const int total = nrow * per_row;
 #pragma unroll 4
-  for (int i = tid; i < 2 * total; i += kRowThreads) {
+  for (int i = tid; i < 2 * total; i += kReadThreads) {
     const bool is_v = i >= total;
     const int j = is_v ? i - total : i;
     const int rl = j / per_row, c = j - rl * per_row;
@@ -360,11 +360,11 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
 
 // ---------------------------------------------------------------- host side
 template <typename Kern, typename Params>
-cudaError_t launch_rows(Kern kern, const Params& p, int gx, int gy, unsigned smem,
-                        cudaStream_t st) {
+cudaError_t launch_rows(Kern kern, const Params& p, int gx, int gy, unsigned smem, cudaStream_t st,
+                        int threads = kRowThreads) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)gx, (unsigned)gy, 1);
-  cfg.blockDim = dim3(kRowThreads, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -401,7 +401,7 @@ int launch_row_op(RowsParams& p, int out, int interleaved, bool bf16, void* stre
   if (call_device(&sms, &p.status) != GQA_OK) return GQA_ERR_CUDA;
   const int nt = (p.d + 15) / 16, per = kRowThreads / nt;
   const int heads = p.hq + p.hkv + (out != kOutRows ? p.hkv : 0);
-  int tokens = 32 / nt;
+  int tokens = 8 / nt;
   if (tokens < 1) tokens = 1;
   if (tokens > kMaxTokens) tokens = kMaxTokens;
   int gy = 1;
@@ -564,11 +564,11 @@ int run_read(const void* k_pages, const void* v_pages, const void* k_scales, con
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (!c8)  // 16-bit pages are copied whatever their type
-    e = launch_rows(read_kernel<true, false>, p, grid, 1, 0, st);
+    e = launch_rows(read_kernel<true, false>, p, grid, 1, 0, st, kReadThreads);
   else if (dtype == GQA_BF16)
-    e = launch_rows(read_kernel<true, true>, p, grid, 1, 0, st);
+    e = launch_rows(read_kernel<true, true>, p, grid, 1, 0, st, kReadThreads);
   else
-    e = launch_rows(read_kernel<false, true>, p, grid, 1, 0, st);
+    e = launch_rows(read_kernel<false, true>, p, grid, 1, 0, st, kReadThreads);
   return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
