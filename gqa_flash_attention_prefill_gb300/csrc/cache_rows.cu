@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kRowThreads = 64;    // of the row kernel
 constexpr int kMaxTokens = 8;      // tokens one of its CTAs handles at most
-constexpr int kReadThreads = 256;  // of the read kernel
+constexpr int kReadThreads = 128;  // of the read kernel, a warp per row
 
 // Where the values of one call come from and go to.
 struct RowsParams {
@@ -96,7 +96,7 @@ __device__ __forceinline__ float load16(const uint16_t* p) {
 // (One vector a thread that read its partner's as well: 16k rows of 64 / 8
 // heads 77 us.)
 template <bool BF16, int OUT, int PAIR>
-__global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowsParams p) {
+__global__ void __launch_bounds__(kRowThreads, 14) rows_kernel(const __grid_constant__ RowsParams p) {
   extern __shared__ float2 s_cs[];  // [tokens][half], then the steps [half]
   __shared__ int s_key[kMaxTokens];
   __shared__ long long s_slot[kMaxTokens];
@@ -125,14 +125,16 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
   const int first = blockIdx.y * slices + slice;
   // All lanes take every turn: the scale search shuffles over the warp.
   const int turns = (heads - (int)blockIdx.y * slices + step - 1) / step;
-  auto source = [&](int h) {  // head h of the row: q, then k, then v
-    const uint16_t* base = static_cast<const uint16_t*>(p.q) + row * p.q_stride + (long long)h * p.d;
-    if (h >= p.hq)
-      base = static_cast<const uint16_t*>(p.k) + row * p.k_stride + (long long)(h - p.hq) * p.d;
-    if (OUT != kOutRows && h >= p.hq + p.hkv)
-      base = static_cast<const uint16_t*>(p.v) + row * p.v_stride +
-             (long long)(h - p.hq - p.hkv) * p.d;
-    return base;
+  // Head h of the row (q, then k, then v) starts at its base + h * d.
+  const uint16_t* const q_row = static_cast<const uint16_t*>(p.q) + row * p.q_stride;
+  const uint16_t* const k_row =
+      static_cast<const uint16_t*>(p.k) + row * p.k_stride - (long long)p.hq * p.d;
+  const uint16_t* const v_row = static_cast<const uint16_t*>(p.v) + row * p.v_stride -
+                                (long long)(p.hq + p.hkv) * p.d;
+  auto source = [&](int h) {
+    const uint16_t* base = h < p.hq ? q_row : k_row;
+    if (OUT != kOutRows && h >= p.hq + p.hkv) base = v_row;
+    return base + h * p.d;
   };
   uint4 na = make_uint4(0u, 0u, 0u, 0u), nb = na;
   auto fetch = [&](int h) {
@@ -148,24 +150,27 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
     unsigned long long* s_step = reinterpret_cast<unsigned long long*>(s_cs + p.tokens * p.half);
     for (int j = tid; j < p.half; j += kRowThreads) s_step[j] = phase_step(__ldg(p.inv_freq + j));
   }
-  if (OUT != kOutRows) {  // a warp per token: its sequence, key and pool row
-    for (int i = warp; i < ntok; i += kRowThreads / 32) {
-      const int r = row0 + i;
-      const int b = warp_upper_bound(p.cu + 1, p.pt.num_seqs, r);
-      if (lane != 0) continue;
-      bool bad = false;
-      long long at = 0, place = -1;
+  // A warp per token: its sequence, key index and page; the page number is
+  // used only after the angles, which hide its load.
+  int page = -1, in_page = 0;
+  if (OUT != kOutRows && warp < ntok) {
+    const int r = row0 + warp;
+    const int b = warp_upper_bound(p.cu + 1, p.pt.num_seqs, r);
+    if (lane == 0) {
+      int key = 0;
       if (b < p.pt.num_seqs) {
         const int c0 = __ldg(p.cu + b), P = __ldg(p.pre + b);
-        at = (long long)P + (r - c0);
-        if (c0 < 0 || c0 > r || P < 0 || at > 0x7fffffffll)
-          bad = true;
-        else
-          place = key_slot(p.pt, b, at, &bad);
+        const int i0 = __ldg(p.pt.indptr + b), i1 = __ldg(p.pt.indptr + b + 1);
+        const long long k = (long long)P + (r - c0);
+        const long long at = i0 + k / p.pt.page_size;
+        key = (int)k;
+        in_page = (int)(k % p.pt.page_size);
+        page = 0x7fffffff;  // bad, unless
+        if (c0 >= 0 && c0 <= r && P >= 0 && k <= 0x7fffffffll && i0 >= 0 && at < i1 &&
+            at < p.pt.entries)
+          page = (int)min((unsigned)__ldg(p.pt.indices + at), 0x7fffffffu);  // negative: bad too
       }
-      if (bad) atomicOr(p.status, (unsigned)GQA_DEV_BAD_METADATA);
-      s_slot[i] = place;
-      s_key[i] = (int)at;
+      s_key[warp] = key;
     }
   }
   if (OUT != kOutRows || PAIR != kPairNone) __syncthreads();
@@ -180,8 +185,13 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
       cs.y *= p.inverse ? -p.factor : p.factor;
       s_cs[i] = cs;
     }
-    __syncthreads();
   }
+  if (OUT != kOutRows && warp < ntok && lane == 0) {
+    const bool bad = page >= p.pt.num_pages;
+    if (bad) atomicOr(p.status, (unsigned)GQA_DEV_BAD_METADATA);
+    s_slot[warp] = page < 0 || bad ? -1 : (long long)page * p.pt.page_size + in_page;
+  }
+  if (OUT != kOutRows || PAIR != kPairNone) __syncthreads();
   const long long slot = OUT != kOutRows ? s_slot[active ? t : 0] : 0;
   // The thread's angles: pairs of the two vectors, or the pairs within each.
   float2 cs[8];
@@ -193,11 +203,19 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
       cs[i] = PAIR == kPairHalf8 || 16 * vec + 2 * i < rot ? c[i] : make_float2(1.f, 0.f);
   }
 
+  // Destinations as the sources: base + h * d.
+  constexpr int kOutBytes = OUT == kOutCache8 ? 1 : 2;
+  uint16_t* const q_dst = static_cast<uint16_t*>(p.q_out) + row * p.q_out_stride;
+  const long long dst_row = OUT == kOutRows ? row * p.k_out_stride : slot * p.hkv * p.d;
+  void* const k_dst =
+      static_cast<uint8_t*>(p.k_out) + (dst_row - (long long)p.hq * p.d) * kOutBytes;
+  void* const v_dst =
+      static_cast<uint8_t*>(p.v_out) + (dst_row - (long long)(p.hq + p.hkv) * p.d) * kOutBytes;
+
   for (int n = 0; n < turns; ++n) {
     const int h = first + n * step;
     const bool on = active && h < heads;
     const bool is_q = h < p.hq, is_k = !is_q && h < p.hq + p.hkv;
-    const int hh = is_q ? h : is_k ? h - p.hq : h - p.hq - p.hkv;
     float x[8], y[8];
     unpack8<BF16>(na, x);
     unpack8<BF16>(nb, y);
@@ -241,33 +259,29 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         }
       }
     }
-    if (OUT == kOutRows || is_q || OUT == kOutCache16) {
-      if (on && (OUT == kOutRows || is_q || slot >= 0)) {
-        uint16_t* dst;
-        if (OUT == kOutRows || is_q)
-          dst = is_q ? static_cast<uint16_t*>(p.q_out) + row * p.q_out_stride
-                     : static_cast<uint16_t*>(p.k_out) + row * p.k_out_stride;
-        else
-          dst = static_cast<uint16_t*>(is_k ? p.k_out : p.v_out) + slot * p.hkv * p.d;
-        dst += (long long)hh * p.d;
-        *reinterpret_cast<uint4*>(dst + ea) = pack8<BF16>(x);
-        if (two) *reinterpret_cast<uint4*>(dst + eb) = pack8<BF16>(y);
-      }
+    if (on && (OUT == kOutRows || is_q || (OUT == kOutCache16 && slot >= 0))) {
+      uint16_t* dst = is_q ? q_dst : static_cast<uint16_t*>(is_k ? k_dst : v_dst);
+      dst += h * p.d;
+      *reinterpret_cast<uint4*>(dst + ea) = pack8<BF16>(x);
+      if (two) *reinterpret_cast<uint4*>(dst + eb) = pack8<BF16>(y);
     }
-    if (OUT == kOutCache8) {
+    // Every lane comes here in the same turn; warps of query heads only pass by.
+    if (OUT == kOutCache8 && __any_sync(0xffffffffu, on && !is_q)) {
       float amax = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i)  // NaN counts as absent
-        amax = fmaxf(amax, fmaxf(fabsf(x[i]), fabsf(y[i])));
+        amax = max3(amax, fabsf(x[i]), fabsf(y[i]));
       for (int o = nt >> 1; o > 0; o >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (on && !is_q && slot >= 0) {
         const int e = e4m3_scale_exponent(amax);
         const float inv = pow2f(-e);
-        uint8_t* dst = static_cast<uint8_t*>(is_k ? p.k_out : p.v_out) + (slot * p.hkv + hh) * p.d;
+        uint8_t* dst = static_cast<uint8_t*>(is_k ? k_dst : v_dst) + h * p.d;
         *reinterpret_cast<uint2*>(dst + ea) = narrow8(x, inv);
         *reinterpret_cast<uint2*>(dst + eb) = narrow8(y, inv);
-        if (vec == 0) (is_k ? p.k_scales : p.v_scales)[slot * p.hkv + hh] = (uint8_t)(e + 127);
+        if (vec == 0)
+          (is_k ? p.k_scales + slot * p.hkv - p.hq : p.v_scales + slot * p.hkv - p.hq - p.hkv)[h] =
+              (uint8_t)(e + 127);
       }
     }
   }
@@ -288,7 +302,10 @@ struct ReadParams {
   unsigned int* status;
 };
 
-constexpr int kReadRows = 16;  // rows a CTA gathers
+// Rows a CTA gathers: one a warp, so that the lookups of all run at once
+// (16 rows on 8 warps: 8 x 8192 keys 38.6 us, 64 x 128 keys 8.1; 4 on 4: 36.4
+// and 5.1).
+constexpr int kReadRows = kReadThreads / 32;
 
 // 4 e4m3 values times 2^e (as fp32 `s`), rounded to 16 bits (exact in bf16
 // unless the result leaves bf16's normal range).
@@ -301,8 +318,8 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, float s) {
 }
 
 // One CTA: kReadRows consecutive output rows of k and v, all heads.  A warp
-// finds two rows' pool rows, then the CTA's threads walk 16-value (e4m3) or
-// 8-value (16-bit) vectors, 16-byte loads and stores.
+// finds a row's place in the pool, then the CTA's threads walk 16-value (e4m3)
+// or 8-value (16-bit) vectors, 16-byte loads and stores.
 template <bool BF16, bool C8>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
   __shared__ long long s_slot[kReadRows];
@@ -311,22 +328,26 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
   const int nrow = min(kReadRows, p.rows - row0);
   grid_dep_launch_dependents();
   grid_dep_wait();
-  for (int i = warp; i < nrow; i += kReadThreads / 32) {
-    const int r = row0 + i;
+  if (warp < nrow) {
+    const int r = row0 + warp;
     const int b = warp_upper_bound(p.kv_indptr + 1, p.pt.num_seqs, r);
     if (lane == 0) {
-      bool bad = false;
       long long slot = -1;
       if (b < p.pt.num_seqs) {
         const int r0 = __ldg(p.kv_indptr + b);
         const int f = p.first_keys != nullptr ? __ldg(p.first_keys + b) : 0;
-        if (r0 < 0 || r0 > r || f < 0)
-          bad = true;
+        const int i0 = __ldg(p.pt.indptr + b), i1 = __ldg(p.pt.indptr + b + 1);
+        const long long key = (long long)f + (r - r0);
+        const long long at = i0 + key / p.pt.page_size;
+        int page = -1;
+        if (r0 >= 0 && r0 <= r && f >= 0 && i0 >= 0 && at < i1 && at < p.pt.entries)
+          page = __ldg(p.pt.indices + at);
+        if (page >= 0 && page < p.pt.num_pages)
+          slot = (long long)page * p.pt.page_size + key % p.pt.page_size;
         else
-          slot = key_slot(p.pt, b, (long long)f + (r - r0), &bad);
+          atomicOr(p.status, (unsigned)GQA_DEV_BAD_METADATA);
       }
-      if (bad) atomicOr(p.status, (unsigned)GQA_DEV_BAD_METADATA);
-      s_slot[i] = slot;
+      s_slot[warp] = slot;
     }
   }
   __syncthreads();
@@ -392,10 +413,12 @@ bool row_ok(const void* p, long long stride, long long width) {
   return p != nullptr && aligned(p, 16) && stride >= width && stride % 8 == 0;
 }
 
-// Tokens per CTA and head slices.  Many rows: up to 8 tokens share a CTA's
-// angles (8 at d = 64: 4 threads a head, 8 heads in flight).  Few rows (the
-// CTAs of that shape would not fill the SMs twice): one token per CTA and its
-// heads spread over blockIdx.y, so that a thread has one head or two.
+// Tokens per CTA and head slices.  Many rows: small CTAs (2 tokens at d = 64:
+// 4 threads a head, 8 heads in flight), so that one's lookups and angles run
+// beside another's loads (16k rows of 64 / 8 heads: 64 threads 52 us, 128 54,
+// 256 64).  Few rows (the CTAs of that shape would not fill the SMs twice): one
+// token per CTA and its heads spread over blockIdx.y, so that a thread has one
+// head or two.
 int launch_row_op(RowsParams& p, int out, int interleaved, bool bf16, void* stream) {
   int sms = 0;
   if (call_device(&sms, &p.status) != GQA_OK) return GQA_ERR_CUDA;
@@ -404,6 +427,7 @@ int launch_row_op(RowsParams& p, int out, int interleaved, bool bf16, void* stre
   int tokens = 8 / nt;
   if (tokens < 1) tokens = 1;
   if (tokens > kMaxTokens) tokens = kMaxTokens;
+  if (out != kOutRows && tokens > kRowThreads / 32) tokens = kRowThreads / 32;  // a warp looks up a token
   int gy = 1;
   if ((long long)p.rows < 2ll * sms * tokens) {
     tokens = 1;

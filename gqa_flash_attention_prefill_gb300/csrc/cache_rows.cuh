@@ -59,30 +59,6 @@ __device__ __forceinline__ int warp_upper_bound(const int32_t* a, int n, int x) 
   return lo;
 }
 
-// Where a row lives: its sequence's key index, and the pool row (page *
-// page_size + slot); slot < 0 when the row belongs to no sequence or its
-// metadata is bad (then *bad is set).
-struct RowPlace {
-  int key;
-  long long slot;
-};
-
-// Lookup of key `key` of sequence b by one lane.
-__device__ __forceinline__ long long key_slot(const PageTable& pt, int b, long long key, bool* bad) {
-  const int i0 = __ldg(pt.indptr + b), i1 = __ldg(pt.indptr + b + 1);
-  const long long at = (long long)i0 + key / pt.page_size;
-  if (key < 0 || i0 < 0 || at >= i1 || at >= pt.entries) {
-    *bad = true;
-    return -1;
-  }
-  const int page = __ldg(pt.indices + at);
-  if (page < 0 || page >= pt.num_pages) {
-    *bad = true;
-    return -1;
-  }
-  return (long long)page * pt.page_size + key % pt.page_size;
-}
-
 // cos and sin of position * frequency.  `step` is the angle per position in
 // units of 2^-64 turns, so position * step modulo 2^64 is the phase within
 // one turn, exact for every position: a product in fp32 would be off by 0.06
