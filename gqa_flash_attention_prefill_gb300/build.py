@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libgqa_prefill.so")
 SOURCES = ["host.cu", "inst_d64.cu", "inst_d64_pair.cu", "inst_d128.cu", "inst_d256.cu",
            "inst_split.cu", "inst_paged.cu", "inst_mask.cu", "inst_balanced.cu", "merge.cu",
            "noalloc.cu", "cache_rows.cu", "cache_attn.cu", "inst_cache_d64.cu",
-           "inst_cache_d128.cu", "inst_cache_d256.cu"]
+           "inst_cache_d128.cu", "inst_cache_d256.cu",
+           "inst_cache_tile.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -15,33 +15,22 @@ namespace {
 constexpr unsigned kSmemMax = 227u * 1024u;
 
 struct CachePlan {
+  bool tile;  // the 128-row kernel
+  int RT;     // rows of a unit
   int G, HPC, HG, KW, NT, T, NS;
   uint32_t data_bytes, slot_bytes;
   int ctas, max_units;  // per launch of at most kMaxSeqs sequences
   size_t ml_off, hdr_off, bytes;
 };
 
-int cache_plan(int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hkv, int d, int dtype,
-               int cache_type, CachePlan* pl) {
-  if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 ||
-      Hq % Hkv != 0)
-    return GQA_ERR_INVALID;
-  if (dtype != GQA_F16 && dtype != GQA_BF16) return GQA_ERR_INVALID;
-  if (cache_type != GQA_CACHE_16 && cache_type != GQA_CACHE_E4M3) return GQA_ERR_INVALID;
-  if (d != 64 && d != 128 && d != 256) return GQA_ERR_UNSUPPORTED;
-  const bool c8 = cache_type == GQA_CACHE_E4M3;
-  pl->G = Hq / Hkv;
-  if (Hkv > 4096 || (long long)total_q * pl->G >= (1ll << 30)) return GQA_ERR_UNSUPPORTED;
-  // Rows of the longest sequence (all of them, without the hint) decide how
-  // many 8-row tiles share each key a warp loads.
-  const long long rows = (long long)(max_seqlen_q > 0 ? max_seqlen_q : total_q) * pl->G;
-  pl->NT = 1;
-  while (pl->NT < cache_attn_max_nt(d) && rows > 8 * pl->NT) pl->NT *= 2;
-  const int gk = ca_gk(d, c8, pl->NT), esz = c8 ? 1 : 2;
-  const int warps = ca_warps(d, c8, pl->NT);
-  // Heads per CTA: the largest divisor of Hkv up to 8; the warps left
-  // over share the heads' keys.  A tile that would leave the ring fewer than
-  // four slots (two tiles) takes fewer warps per head, then fewer heads.
+// Rows per KV head (tokens times query heads of the longest sequence) above
+// which the 128-row kernel takes over.
+constexpr int kTileRows = 64;
+
+// Heads per CTA: the largest divisor of Hkv up to 8; the warps left
+// over share the heads' keys.  A tile that would leave the ring fewer than
+// four slots (two tiles) takes fewer warps per head, then fewer heads.
+int ring_shape(int Hkv, int d, bool c8, int gk, int esz, int warps, CachePlan* pl) {
   int hpc = Hkv < 8 ? Hkv : 8;
   while (Hkv % hpc != 0) --hpc;
   int kw = 1;
@@ -65,13 +54,47 @@ int cache_plan(int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hkv, int
       return GQA_ERR_UNSUPPORTED;  // the scales of too many heads
     }
   }
-  pl->HG = Hkv / hpc;
+  return GQA_OK;
+}
+
+int cache_plan(int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hkv, int d, int dtype,
+               int cache_type, CachePlan* pl) {
+  if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 ||
+      Hq % Hkv != 0)
+    return GQA_ERR_INVALID;
+  if (dtype != GQA_F16 && dtype != GQA_BF16) return GQA_ERR_INVALID;
+  if (cache_type != GQA_CACHE_16 && cache_type != GQA_CACHE_E4M3) return GQA_ERR_INVALID;
+  if (d != 64 && d != 128 && d != 256) return GQA_ERR_UNSUPPORTED;
+  const bool c8 = cache_type == GQA_CACHE_E4M3;
+  pl->G = Hq / Hkv;
+  if (Hkv > 4096 || (long long)total_q * pl->G >= (1ll << 30)) return GQA_ERR_UNSUPPORTED;
+  // Rows of the longest sequence (all of them, without the hint) decide how
+  // many 8-row tiles share each key a warp loads.
+  const long long rows = (long long)(max_seqlen_q > 0 ? max_seqlen_q : total_q) * pl->G;
+  pl->tile = d <= 128 && rows > kTileRows;
+  pl->NT = 1;
+  while (pl->NT < cache_attn_max_nt(d) && rows > 8 * pl->NT) pl->NT *= 2;
+  const int gk = ca_gk(d, c8, pl->NT), esz = c8 ? 1 : 2;
+  const int warps = ca_warps(d, c8, pl->NT);
+  if (pl->tile) {
+    pl->HPC = 1;
+    pl->KW = 1;
+    pl->T = ct_bn(d);
+    pl->NS = 2;
+    pl->data_bytes = pl->slot_bytes = 0;
+    pl->RT = 128;
+  } else {
+    const int rc = ring_shape(Hkv, d, c8, gk, esz, warps, pl);
+    if (rc != GQA_OK) return rc;
+    pl->RT = 8 * pl->NT;
+  }
+  pl->HG = Hkv / pl->HPC;
   int sms = 152;
   unsigned int* status = nullptr;
   if (call_device(&sms, &status) != GQA_OK) sms = 152;
-  pl->ctas = sms;
+  pl->ctas = pl->tile ? 2 * sms : sms;
   const int seqs = num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs;
-  const int rt = 8 * pl->NT;
+  const int rt = pl->RT;
   const long long units =
       (long long)pl->HG * (((long long)total_q * pl->G + rt - 1) / rt + (long long)seqs);
   if (units > (1ll << 26)) return GQA_ERR_UNSUPPORTED;
@@ -168,6 +191,7 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
   p.window = window > 0 ? window : 0;
   p.smooth = smooth_softmax != 0 ? 1 : 0;
   p.max_units = pl.max_units;
+  p.whole_slack = pl.tile ? kCtWholeSlack : kCaWholeSlack;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.metadata_ready = metadata_ready_flag() ? 1 : 0;
   // A window bounds a unit's tiles on the host: where whole units dealt out
@@ -176,12 +200,12 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
   if (p.window > 0) {
     const long long new_max = max_seqlen_q > 0 ? max_seqlen_q : total_q;
     const long long n = ((long long)p.window + new_max + pl.T - 3) / pl.T + 1;
-    if ((pl.max_units + pl.ctas - 1) / pl.ctas * n <= kCaWholeSlack) {
+    if ((pl.max_units + pl.ctas - 1) / pl.ctas * n <= p.whole_slack) {
       p.whole = 1;
       merge_x = 0;
     }
   }
-  const int rows = pl.HPC * 8 * pl.NT;
+  const int rows = pl.HPC * pl.RT;
   int merge_y = merge_x > 0 ? 8 * pl.ctas / merge_x : 1;
   if (merge_y > rows) merge_y = rows;
   if (merge_y < 1) merge_y = 1;
@@ -196,7 +220,8 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
     p.num_seqs = num_seqs - b0 < kMaxSeqs ? num_seqs - b0 : kMaxSeqs;
     const bool bf16 = dtype == GQA_BF16;
     const cudaError_t e =
-        d == 64    ? launch_cache_attn_d64(p, bf16, c8, pl.NT, pl.ctas, smem, merge_x, merge_y, st)
+        pl.tile    ? launch_cache_tile(p, d, bf16, c8, pl.ctas, merge_x, merge_y, st)
+        : d == 64    ? launch_cache_attn_d64(p, bf16, c8, pl.NT, pl.ctas, smem, merge_x, merge_y, st)
         : d == 128 ? launch_cache_attn_d128(p, bf16, c8, pl.NT, pl.ctas, smem, merge_x, merge_y, st)
                    : launch_cache_attn_d256(p, bf16, c8, pl.NT, pl.ctas, smem, merge_x, merge_y, st);
     if (e != cudaSuccess) return GQA_ERR_CUDA;

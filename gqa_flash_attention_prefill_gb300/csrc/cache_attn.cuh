@@ -61,6 +61,7 @@ constexpr int kCaMaxSlots = 16;                    // ring slots at most
 constexpr int kCaPieces = 4;                       // pieces the producer may be ahead
 constexpr float kCaSlack = 4.f;
 constexpr int kCaWholeSlack = 6;                   // tiles a join is worth
+constexpr float kCaBias = 10.f;                    // f16 probabilities reach 2^(slack + bias)
 
 // Division of 0 <= n < 2^31 by a divisor fixed for the launch: with l =
 // ceil(log2 d) and m = ceil(2^(32 + l) / d) - 2^32, n / d = (hi(n m) + n) >> l
@@ -114,6 +115,7 @@ struct CacheAttnParams {
   uint32_t slot_bytes, data_bytes;  // a slot, and its values (scales follow)
   int window, smooth;
   int whole;         // units dealt whole whatever the lengths
+  int whole_slack;   // tiles that a join is worth
   int max_units;
   float scale_log2;
   int metadata_ready;
@@ -136,8 +138,8 @@ __host__ __device__ constexpr uint32_t ca_fixed_smem(int warps) {
 }
 
 struct CaTab {
-  const int32_t* tiles;  // [B + 1] exclusive scan of key tiles
-  const int32_t* units;  // [B + 1] exclusive scan of units
+  const int32_t* tiles;  // [B] exclusive scan of key tiles
+  const int32_t* units;  // [B] exclusive scan of units
   const int32_t* cu0;    // [B + 1]
   const int32_t* pre;    // [B]
   const int32_t* ipt;    // [B]
@@ -230,6 +232,141 @@ __device__ __forceinline__ bool ca_next(const CacheAttnParams& p, const CaTab& T
   return true;
 }
 
+// Per sequence its key tiles and units, and the checks of the metadata
+// (misc[1] set when something is inconsistent, misc[2] raised to the most
+// tiles of a unit).  Called by every thread of the CTA; a barrier follows.
+__device__ __forceinline__ void ca_tables(const CacheAttnParams& p, int32_t* tiles, int32_t* units,
+                                          int32_t* s_cu, int32_t* s_pre, int32_t* s_ipt,
+                                          uint32_t* misc, int RT, int tid, int nthreads) {
+  const int nseq = p.num_seqs;
+  bool bad = tid == 0 && p.first_seq == 0 && __ldg(p.cu) != 0;
+  int my_max = 0;
+  for (int b = tid; b < nseq; b += nthreads) {
+    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), P = __ldg(p.pre + b);
+    const int i0 = __ldg(p.indptr + b), i1 = __ldg(p.indptr + b + 1);
+    const int E = c1 - c0;
+    bool b_bad = c0 < 0 || c1 < c0 || c1 > p.total_q || P < 0 || P > 0x7fff0000 - E || i0 < 0 ||
+                 i1 > p.entries;
+    if (!b_bad) b_bad = i1 - i0 != (P + E > 0 ? p.div_page.div(P + E - 1) + 1 : 0);
+    if (p.mask != nullptr) {
+      const long long m0 = __ldg(p.mask_indptr + b), m1 = __ldg(p.mask_indptr + b + 1);
+      b_bad |= m0 < 0 || m1 > p.total_mask_words || m1 - m0 != (long long)E * ((E + 31) / 32);
+    }
+    bad |= b_bad;
+    long long w = 0;
+    int nu = 0;
+    if (!b_bad && E > 0) {
+      nu = (E * p.G + RT - 1) / RT;
+      for (int rt = 0; rt < nu; ++rt) {
+        int lo, hi, n;
+        ca_range(p, P, E, rt, RT, lo, hi, n);
+        w += n;
+        my_max = max(my_max, n);
+      }
+      w *= p.HG;
+      nu *= p.HG;
+    }
+    s_cu[b] = c0;
+    s_pre[b] = P;
+    s_ipt[b] = i0;
+    if (w > 0x7fffffffll) bad = true;  // more key tiles than the shares count
+    tiles[b] = (int)w;
+    units[b] = nu;
+    if (b == nseq - 1) s_cu[nseq] = c1;
+  }
+  if (bad) misc[1] = 1u;
+  const int lane = tid & 31;
+  my_max = __reduce_max_sync(0xffffffffu, my_max);
+  if (lane == 0 && my_max > 0) atomicMax(reinterpret_cast<int*>(misc + 2), my_max);
+}
+
+struct CaPlan {
+  CaTab T;
+  CaShares shares;
+  CaWalk walk;
+};
+
+// The CTA's part of the work; called by one converged warp after ca_tables.
+__device__ __forceinline__ CaPlan ca_plan(const CacheAttnParams& p, int32_t* tiles, int32_t* units,
+                                          int32_t* s_cu, int32_t* s_pre, int32_t* s_ipt,
+                                          const uint32_t* misc) {
+  const int lane = threadIdx.x & 31, nseq = p.num_seqs;
+  // Exclusive scans of the tiles and units, a run of sequences a lane.
+  const int run = (nseq + 31) >> 5, b0 = min(lane * run, nseq), b1 = min(b0 + run, nseq);
+  long long st = 0;
+  int su = 0;
+  for (int b = b0; b < b1; ++b) {
+    st += tiles[b];
+    su += units[b];
+  }
+  long long at = st;
+  int au = su;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, at, o);
+    const int y = __shfl_up_sync(0xffffffffu, au, o);
+    if (lane >= o) {
+      at += x;
+      au += y;
+    }
+  }
+  const long long total = __shfl_sync(0xffffffffu, at, 31);
+  const int n_all = __shfl_sync(0xffffffffu, au, 31);
+  at -= st;
+  au -= su;
+  for (int b = b0; b < b1; ++b) {
+    const int w = tiles[b], nu = units[b];
+    tiles[b] = (int)at;
+    units[b] = au;
+    at += w;
+    au += nu;
+  }
+  __syncwarp();
+  // More key tiles than the shares count: nothing is done.
+  const int W = total > 0x7fffffffll ? 0 : (int)total;
+  if (W != total && lane == 0) atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
+  const int n_units = W > 0 ? n_all : 0, grid = gridDim.x, c = blockIdx.x;
+  // No more shares than tiles: every share holds a tile, so the pieces of a
+  // cut unit lie on consecutive CTAs.
+  const int C = min(W, grid);
+  const int per = W < grid ? 1 : p.div_ctas.div(W);  // tiles of the smaller shares
+  CaPlan plan;
+  plan.T = CaTab{tiles, units, s_cu, s_pre, s_ipt};
+  plan.shares = CaShares{per, W < grid ? 0 : W - per * grid};
+  // Whole units when the deepest deal costs no more than an equal share and
+  // the join that cut units need.
+  CaWalk& w = plan.walk;
+  w.whole = p.whole != 0 || (long long)p.div_ctas.div(n_units + grid - 1) * (int)misc[2] <=
+                                per + p.whole_slack;
+  w.unit = c;
+  w.at = c < C ? plan.shares.lo(c) : 0;
+  w.end = w.whole ? n_units : c < C ? plan.shares.lo(c + 1) : 0;
+  if (c == 0 && lane == 0) p.hdr[0] = w.whole ? 0 : n_units;
+  return plan;
+}
+
+// What the other warps need of a piece, in 3 x 16 bytes: tiles (0: no more),
+// flags (1 cut, 2 the first piece of a cut unit), first key, prefix; tokens,
+// end of the keys, first row, first head; first token, first mask word.  The
+// unit's first piece also writes its entry for the join.
+__device__ __forceinline__ void ca_publish(const CacheAttnParams& p, const CaPlan& plan,
+                                           const CaPiece& u, bool more, int RT, int4* d) {
+  const bool cut = more && (u.t0 > 0 || u.t1 < u.n);
+  const int m0 = more && p.mask != nullptr ? __ldg(p.mask_indptr + u.b) : 0;
+  const int cu0 = more ? plan.T.cu0[u.b] : 0;
+  d[0] = make_int4(more ? u.t1 - u.t0 : 0, (cut ? 1 : 0) | (cut && u.t0 == 0 ? 2 : 0),
+                   u.lo + (u.t0 << p.log_T), u.P);
+  d[1] = make_int4(u.E, u.hi, u.rt * RT, u.hg * p.HPC);
+  d[2] = make_int4(cu0, m0, more ? plan.T.ipt[u.b] : 0, 0);
+  if (more && !plan.walk.whole && u.t0 == 0) {
+    const int c = blockIdx.x;
+    int4* hd = reinterpret_cast<int4*>(p.hdr + 8 + 8ll * u.unit);
+    hd[0] = make_int4(cut ? plan.shares.owner(plan.walk.at - u.t1 + u.n - 1) - c : 0, c, u.rt * RT,
+                      u.hg * p.HPC);
+    hd[1] = make_int4(cu0, u.E, 0, 0);
+  }
+}
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
   asm volatile(
@@ -313,7 +450,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
   constexpr int GK = ca_gk(D, C8, NT);
   constexpr int RT = 8 * NT;
   constexpr bool MBF = BF16 && !C8;          // product type
-  constexpr float kBias = MBF ? 0.f : 10.f;  // 2^(kCaSlack + kBias) fits f16
+  constexpr float kBias = MBF ? 0.f : kCaBias;
   constexpr int kEsz = C8 ? 1 : 2;
   constexpr int KS = D / 16;                 // k16 steps of the scores
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -356,45 +493,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
   grid_dep_launch_dependents();
   if (!p.metadata_ready) grid_dep_wait();
 
-  const int nseq = p.num_seqs;
-  bool bad = tid == 0 && p.first_seq == 0 && __ldg(p.cu) != 0;
-  int my_max = 0;
-  for (int b = tid; b < nseq; b += kThreads) {
-    const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), P = __ldg(p.pre + b);
-    const int i0 = __ldg(p.indptr + b), i1 = __ldg(p.indptr + b + 1);
-    const int E = c1 - c0;
-    bool b_bad = c0 < 0 || c1 < c0 || c1 > p.total_q || P < 0 || P > 0x7fff0000 - E || i0 < 0 ||
-                 i1 > p.entries;
-    if (!b_bad) b_bad = i1 - i0 != (P + E > 0 ? p.div_page.div(P + E - 1) + 1 : 0);
-    if (p.mask != nullptr) {
-      const long long m0 = __ldg(p.mask_indptr + b), m1 = __ldg(p.mask_indptr + b + 1);
-      b_bad |= m0 < 0 || m1 > p.total_mask_words || m1 - m0 != (long long)E * ((E + 31) / 32);
-    }
-    bad |= b_bad;
-    long long w = 0;
-    int nu = 0;
-    if (!b_bad && E > 0) {
-      nu = (E * p.G + RT - 1) / RT;
-      for (int rt = 0; rt < nu; ++rt) {
-        int lo, hi, n;
-        ca_range(p, P, E, rt, RT, lo, hi, n);
-        w += n;
-        my_max = max(my_max, n);
-      }
-      w *= p.HG;
-      nu *= p.HG;
-    }
-    s_cu[b] = c0;
-    s_pre[b] = P;
-    s_ipt[b] = i0;
-    if (w > 0x7fffffffll) bad = true;  // more key tiles than the shares count
-    tiles[b] = (int)w;
-    units[b] = nu;
-    if (b == nseq - 1) s_cu[nseq] = c1;
-  }
-  if (bad) misc[1] = 1u;
-  my_max = __reduce_max_sync(0xffffffffu, my_max);
-  if (lane == 0 && my_max > 0) atomicMax(reinterpret_cast<int*>(misc + 2), my_max);
+  ca_tables(p, tiles, units, s_cu, s_pre, s_ipt, misc, RT, tid, kThreads);
   __syncthreads();
   const bool bad_meta = misc[1] != 0u;
   if (p.metadata_ready) grid_dep_wait();  // before any global write or other read
@@ -413,70 +512,14 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     // Plans the CTA's work, tells the consumers piece by piece, and fills the
     // ring; the other warps would only repeat the planning (17 warps doing so
     // cost 3000 clocks before the first load).
-    // Exclusive scans of the tiles and units, a run of sequences a lane.
-    {
-      const int per = (nseq + 31) >> 5, b0 = min(lane * per, nseq), b1 = min(b0 + per, nseq);
-      long long st = 0;
-      int su = 0;
-      for (int b = b0; b < b1; ++b) {
-        st += tiles[b];
-        su += units[b];
-      }
-      long long at = st;
-      int au = su;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, at, o);
-        const int y = __shfl_up_sync(0xffffffffu, au, o);
-        if (lane >= o) {
-          at += x;
-          au += y;
-        }
-      }
-      const long long total = __shfl_sync(0xffffffffu, at, 31);
-      if (lane == 31) {
-        units[nseq] = au;
-        tiles[nseq] = total > 0x7fffffffll ? -1 : (int)total;
-      }
-      at -= st;
-      au -= su;
-      for (int b = b0; b < b1; ++b) {
-        const int w = tiles[b], nu = units[b];
-        tiles[b] = (int)at;
-        units[b] = au;
-        at += w;
-        au += nu;
-      }
-      __syncwarp();
-    }
-    const CaTab T{tiles, units, s_cu, s_pre, s_ipt};
-    int W = tiles[nseq];
-    if (W < 0) {  // more key tiles than the shares count: nothing is done
-      if (lane == 0) atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
-      W = 0;
-    }
-    const int n_units = W > 0 ? units[nseq] : 0, grid = gridDim.x, c = blockIdx.x;
-    // No more shares than tiles: every share holds a tile, so the pieces of a
-    // cut unit lie on consecutive CTAs.
-    const int C = min(W, grid);
-    const int per = W < grid ? 1 : p.div_ctas.div(W);  // tiles of the smaller shares
-    const CaShares shares{per, W < grid ? 0 : W - per * grid};
-    // Whole units when the deepest deal costs no more than an equal share and
-    // the join that cut units need.
-    CaWalk walk;
-    walk.whole = p.whole != 0 || (long long)p.div_ctas.div(n_units + grid - 1) * (int)misc[2] <=
-                                     per + kCaWholeSlack;
-    walk.unit = c;
-    walk.at = c < C ? shares.lo(c) : 0;
-    walk.end = walk.whole ? n_units : c < C ? shares.lo(c + 1) : 0;
-    if (c == 0 && lane == 0) p.hdr[0] = walk.whole ? 0 : n_units;
+    CaPlan plan = ca_plan(p, tiles, units, s_cu, s_pre, s_ipt, misc);
     // The tile's runs are spread over the lanes; slots alternate K and V.
     uint32_t slot = 0, ph = 0, issued = 0, pi = 0;
     bool ok = true;
     CaPiece u = {};
     const int nrun = p.T / p.run;  // the tile's copies, one a lane
     for (;; ++pi) {
-      const bool more = ca_next(p, T, walk, RT, u);
+      const bool more = ca_next(p, plan.T, plan.walk, RT, u);
       // ---- tell the consumers
       const uint32_t ps = pi % kCaPieces;
       if (lane == 0)
@@ -484,25 +527,13 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
                           p.status, tmo);
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       if (!ok) break;
-      const bool cut = more && (u.t0 > 0 || u.t1 < u.n);
       if (lane == 0) {
-        int4* d = s_piece + 4 * ps;
-        const int m0 = more && p.mask != nullptr ? __ldg(p.mask_indptr + u.b) : 0;
-        d[0] = make_int4(more ? u.t1 - u.t0 : 0, (cut ? 1 : 0) | (cut && u.t0 == 0 ? 2 : 0),
-                         u.lo + (u.t0 << p.log_T), u.P);
-        d[1] = make_int4(u.E, u.hi, u.rt * RT, u.hg * p.HPC);
-        d[2] = make_int4(more ? T.cu0[u.b] : 0, m0, 0, 0);
+        ca_publish(p, plan, u, more, RT, s_piece + 4 * ps);
         mbar_arrive(sPiece + 8u * ps);
-        if (more && !walk.whole && u.t0 == 0) {  // the unit's first piece: its entry for the join
-          int4* hd = reinterpret_cast<int4*>(p.hdr + 8 + 8ll * u.unit);
-          hd[0] = make_int4(cut ? shares.owner(walk.at - u.t1 + u.n - 1) - c : 0, c, u.rt * RT,
-                            u.hg * p.HPC);
-          hd[1] = make_int4(T.cu0[u.b], u.E, 0, 0);
-        }
       }
       if (!more) break;
       const int npg = p.div_page.div(u.P + u.E - 1) + 1;
-      const int32_t* table = p.indices + T.ipt[u.b];
+      const int32_t* table = p.indices + plan.T.ipt[u.b];
       for (int t = u.t0; ok && t < u.t1; ++t) {
         const int n0 = u.lo + t * p.T;
         // Tokens [skip, ntok) of the tile: keys below the window are not read.

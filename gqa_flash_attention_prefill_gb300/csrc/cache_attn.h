@@ -2,6 +2,7 @@
 // and the kernel instantiations, one translation unit per head dim.
 #pragma once
 #include "cache_attn.cuh"
+#include "cache_tile.cuh"
 #include "launch.h"
 
 namespace gqa {
@@ -17,14 +18,18 @@ cudaError_t launch_cache_attn_d128(const CacheAttnParams& p, bool bf16, bool c8,
 cudaError_t launch_cache_attn_d256(const CacheAttnParams& p, bool bf16, bool c8, int nt, int grid,
                                    unsigned smem, int merge_x, int merge_y, cudaStream_t st);
 
+// The 128-row form, d = 64 or 128.
+cudaError_t launch_cache_tile(const CacheAttnParams& p, int d, bool bf16, bool c8, int grid,
+                              int merge_x, int merge_y, cudaStream_t st);
+
 namespace {
 
-// The kernel, and its join when merge_x > 0.
-template <int D, bool BF16, bool C8, int NT, bool H8>
-cudaError_t launch_cache_attn(const CacheAttnParams& p, int grid, unsigned smem, int merge_x,
-                              int merge_y, cudaStream_t st) {
-  auto kern = cache_attn_kernel<D, BF16, C8, NT, H8>;
-  static SmemAttr attr{};
+// Launches `kern`, and the join of cut units when merge_x > 0: one attribute
+// slot per kernel remembers the shared memory allowed to it.
+template <int D, bool BF16, bool C8, typename Kern>
+cudaError_t launch_with_join(Kern kern, SmemAttr& attr, const CacheAttnParams& p, int rt, int grid,
+                             int threads, unsigned smem, int merge_x, int merge_y,
+                             cudaStream_t st) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -34,7 +39,7 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, int grid, unsigned smem,
     if (e != cudaSuccess) return e;
     attr.allowed[dev].store(smem, std::memory_order_release);
   }
-  e = launch_pdl(kern, p, grid, 32 * (ca_warps(D, C8, NT) + 1), smem, st);
+  e = launch_pdl(kern, p, grid, threads, smem, st);
   if (e != cudaSuccess || merge_x == 0) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)merge_x, (unsigned)merge_y, 1);
@@ -45,8 +50,16 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, int grid, unsigned smem,
   la[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = la;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, BF16>, p, 8 * NT,
-                            BF16 && !C8 ? 0.f : 10.f);
+  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, BF16>, p, rt, BF16 && !C8 ? 0.f : kCaBias);
+}
+
+template <int D, bool BF16, bool C8, int NT, bool H8>
+cudaError_t launch_cache_attn(const CacheAttnParams& p, int grid, unsigned smem, int merge_x,
+                              int merge_y, cudaStream_t st) {
+  static SmemAttr attr{};
+  return launch_with_join<D, BF16, C8>(cache_attn_kernel<D, BF16, C8, NT, H8>, attr, p, 8 * NT,
+                                       grid, 32 * (ca_warps(D, C8, NT) + 1), smem, merge_x, merge_y,
+                                       st);
 }
 
 template <int D, int NT, bool H8>
