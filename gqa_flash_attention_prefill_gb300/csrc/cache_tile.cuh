@@ -214,53 +214,49 @@ __global__ void __launch_bounds__(kCtThreads, 2)
   } else if (warp >= 4) {
     // -------------------------------------------------------------- K and V
     constexpr int kCpr = D * kEsz / 16;                          // 16-byte loads per key
-    constexpr int kLoads = (BN * kCpr + kCtLoaders - 1) / kCtLoaders;  // of a thread
-    constexpr int kSc = (BN + kCtLoaders - 1) / kCtLoaders;
-    const int lt = tid - 128;
+    constexpr int kStep = kCtLoaders / kCpr;                     // keys a round of all threads
+    constexpr int kLoads = (BN + kStep - 1) / kStep;             // of a thread, K or V
+    static_assert(kCtLoaders % kCpr == 0, "a thread keeps its place in a key");
+    // The thread loads 16 bytes, at place q, of keys j0, j0 + kStep, ..
+    const int lt = tid - 128, q = lt % kCpr, j0 = lt / kCpr;
     const long long tok_bytes = (long long)p.Hkv * D * kEsz;
     uint4 raw[kLoads];
-    uint32_t sc[kSc];
+    int row[kLoads];        // pool rows of the tile's keys, -1 for a key no row sees
+    uint32_t sc[kLoads];    // the keys' scale bytes, in the threads at place 0
     int4 d0 = {}, d1 = {}, d2 = {};
     uint32_t pi = 0, it = 0;
     bool ok = true;
-    // Pool row of a key, or -1 for a key no row sees.
-    auto place = [&](int key) -> long long {
-      if (key >= d1.y || (p.window > 0 && key <= d0.w - p.window)) return -1;
-      const int kp = p.div_page.div(key);
-      int pg = __ldg(p.indices + d2.z + kp);
-      if (pg < 0 || pg >= p.num_pages) {
-        atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
-        pg = 0;
-      }
-      return (long long)pg * p.page_size + (key - kp * p.page_size);
-    };
-    auto fetch = [&](int n0, bool is_v) {
-      const uint8_t* pages = (is_v ? p.v_pages : p.k_pages) + (long long)d1.w * (D * kEsz);
+    auto places = [&](int n0) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int c = lt + i * kCtLoaders;
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (c < BN * kCpr) {
-          const long long row = place(n0 + c / kCpr);
-          if (row >= 0)
-            raw[i] = __ldg(reinterpret_cast<const uint4*>(pages + row * tok_bytes) + c % kCpr);
-        }
-      }
-      if constexpr (C8) {
-        const uint8_t* scales = (is_v ? p.v_scales : p.k_scales) + d1.w;
-#pragma unroll
-        for (int i = 0; i < kSc; ++i) {
-          const int j = lt + i * kCtLoaders;
-          sc[i] = 0u;  // a key no row sees
-          if (j < BN) {
-            const long long row = place(n0 + j);
-            if (row >= 0) sc[i] = __ldg(scales + row * p.Hkv);
+        const int key = n0 + j0 + i * kStep;
+        row[i] = -1;
+        if (j0 + i * kStep < BN && key < d1.y && (p.window == 0 || key > d0.w - p.window)) {
+          const int kp = p.div_page.div(key);
+          int pg = __ldg(p.indices + d2.z + kp);
+          if ((unsigned)pg >= (unsigned)p.num_pages) {
+            atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
+            pg = 0;
           }
+          row[i] = pg * p.page_size + (key - kp * p.page_size);  // the pool has < 2^31 rows
         }
       }
     };
-    // Unswizzled 16-byte unit c of key row j at chunk x (64 values) goes to
-    // unit c ^ (j & 7) of that row.
+    auto fetch = [&](bool is_v) {
+      const uint8_t* src =
+          (is_v ? p.v_pages : p.k_pages) + (long long)d1.w * (D * kEsz) + 16 * q;
+      const uint8_t* scales = (is_v ? p.v_scales : p.k_scales) + d1.w;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        sc[i] = 0u;
+        if (row[i] >= 0) {
+          raw[i] = __ldg(reinterpret_cast<const uint4*>(src + row[i] * tok_bytes));
+          if (C8 && q == 0) sc[i] = __ldg(scales + (long long)row[i] * p.Hkv);
+        }
+      }
+    };
+    // 16-byte unit c of key row j goes to unit c ^ (j & 7) of its 128-byte row.
     auto put = [&](uint32_t base, int j, int unit, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
       st_shared_v4(base + (uint32_t)(unit >> 3) * kKVChunk + (uint32_t)j * 128u +
                        (uint32_t)(((unit & 7) ^ (j & 7)) << 4),
@@ -273,34 +269,26 @@ __global__ void __launch_bounds__(kCtThreads, 2)
       const uint32_t base = (is_v ? sV : sK) + s * kKVBytes;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int c = lt + i * kCtLoaders;
-        if (c < BN * kCpr) {
-          const int j = c / kCpr, q = c % kCpr;
-          if constexpr (C8) {
-            uint32_t h[8];
-            e4m3x4_f16(raw[i].x, h[0], h[1]);
-            e4m3x4_f16(raw[i].y, h[2], h[3]);
-            e4m3x4_f16(raw[i].z, h[4], h[5]);
-            e4m3x4_f16(raw[i].w, h[6], h[7]);
-            put(base, j, 2 * q, h[0], h[1], h[2], h[3]);
-            put(base, j, 2 * q + 1, h[4], h[5], h[6], h[7]);
-          } else {
-            put(base, j, q, raw[i].x, raw[i].y, raw[i].z, raw[i].w);
-          }
-        }
-      }
-      if constexpr (C8) {
-#pragma unroll
-        for (int i = 0; i < kSc; ++i) {
-          const int j = lt + i * kCtLoaders;
-          if (j < BN) {
+        const int j = j0 + i * kStep;
+        if (BN % kStep != 0 && j >= BN) break;
+        if constexpr (C8) {
+          uint32_t h[8];
+          e4m3x4_f16(raw[i].x, h[0], h[1]);
+          e4m3x4_f16(raw[i].y, h[2], h[3]);
+          e4m3x4_f16(raw[i].z, h[4], h[5]);
+          e4m3x4_f16(raw[i].w, h[6], h[7]);
+          put(base, j, 2 * q, h[0], h[1], h[2], h[3]);
+          put(base, j, 2 * q + 1, h[4], h[5], h[6], h[7]);
+          if (q == 0) {
             if (is_v) {
-              s_we[s * BN + j] = sc[i] ? (float)((int)sc[i] - 127) : 0.f;
+              s_we[s * BN + j] = sc[i] ? __uint_as_float(0x4B000000u | sc[i]) - 8388735.f : 0.f;
               s_wi[s * BN + j] = __uint_as_float((254u - sc[i]) << 23);
             } else {
               s_ks[s * BN + j] = __uint_as_float(sc[i] << 23);
             }
           }
+        } else {
+          put(base, j, q, raw[i].x, raw[i].y, raw[i].z, raw[i].w);
         }
       }
       fence_proxy_async_smem();
@@ -309,19 +297,24 @@ __global__ void __launch_bounds__(kCtThreads, 2)
     };
     // Loads run one half tile (K or V) ahead of the stores, across pieces.
     bool have = next_piece(pi++, d0, d1, d2, ok);
-    if (have) fetch(d0.z, false);
+    if (have) {
+      places(d0.z);
+      fetch(false);
+    }
     while (ok && have) {
       const int n = d0.x, first = d0.z;
       for (int j = 0; j < n; ++j, ++it) {
         if (!(ok = store(it, false))) break;
-        fetch(first + j * BN, true);
+        fetch(true);
         if (!(ok = store(it, true))) break;
-        if (j + 1 < n) {
-          fetch(first + (j + 1) * BN, false);
-        } else {
+        int next = first + (j + 1) * BN;
+        if (j + 1 == n) {
           have = next_piece(pi++, d0, d1, d2, ok);
-          if (have) fetch(d0.z, false);
+          if (!have) break;
+          next = d0.z;
         }
+        places(next);
+        fetch(false);
       }
     }
   } else {
