@@ -11,14 +11,22 @@
 // A CTA of 8 warps:
 //   0..3  softmax and output, thread = row = tensor-memory lane; they also
 //         bring the rows of Q into shared memory;
-//   4..6  bring K and V: 16-byte loads from the pages straight to registers,
-//         e4m3 widened to f16 (exact, the scales stay apart), stored in the
-//         128-byte swizzle the products read.  A tile is loaded while the one
-//         before waits for its slot.  Keys no row sees become zeros;
+//   4..6  bring K and V into the 128-byte swizzle the products read: 16-bit
+//         pages by cp.async, e4m3 pages through registers, widened to f16, the
+//         next tile's loads in flight meanwhile.  Keys no row sees become
+//         zeros;
 //   7     plans the work and issues the products.
-// The scales of an e4m3 tile go to shared memory as fp32: the softmax
-// multiplies a key's scores by its K scale, and takes its V scale into the
-// exponent (P) and out of the denominator, in pairs of keys.
+//
+// Scales of an e4m3 tile.  Widening multiplies a key's values by 2^(e - x)
+// with x 7 below the largest exponent e of the tile, which keeps every value
+// within f16 and exact where e lies at most 22 below the largest.  The tile's
+// 2^x multiplies all its scores alike, and V's x joins the exponent of all its
+// probabilities (and leaves the denominator) as w does in cache_attn.cuh.
+// Below those 22 powers of two a K value rounds at 2^-33 of the tile's largest,
+// less than the scores' own fp32; a V tile that spans more keeps its values
+// unscaled and hands the softmax an exponent per key.  (Always a scale per key:
+// the broadcast reads of three arrays took 1536 shared-memory clocks a tile of
+// 128 keys, three times its products.)
 #pragma once
 #include "cache_attn.cuh"
 
@@ -30,14 +38,42 @@ constexpr int kCtWholeSlack = 2;  // tiles a join is worth
 __host__ __device__ constexpr int ct_bn(int D) { return D == 64 ? 128 : 64; }
 // Q tile, two slots each of K and V, their scales, the tables of the sequences.
 __host__ __device__ constexpr uint32_t ct_smem(int D) {
-  return 1024u + 128u * D * 2u + 4u * ct_bn(D) * D * 2u + 2u * ct_bn(D) * 12u +
-         4u * (5 * kMaxSeqs + 3) + kCaPieces * 64u + 32u * 8u + 32u;
+  return 1024u + 128u * D * 2u + 4u * ct_bn(D) * D * 2u + 2u * ct_bn(D) * 8u + 4u * 16u +
+         4u * (5 * kMaxSeqs + 3) + kCaPieces * 64u + 32u * 8u + 64u;
 }
 
 struct CtBar {  // barrier numbers
   static constexpr int kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kSFree = 9,
                        kPFull = 10, kODone = 11, kQFull = 12, kDrain = 13, kPiece = 14;
 };
+
+// Keys x0 .. x0 + 31 (counted from the first new token) that row i of a
+// sequence of E new tokens keeps, one bit each.
+static __device__ __noinline__ uint32_t keep_bits(const CacheAttnParams& p, bool on, int i, int dep,
+                                           int x0, int E, int cu0, long long mask0) {
+  if (!on || x0 > i) return 0u;
+  uint32_t keep = i - x0 >= 31 ? ~0u : (2u << (i - x0)) - 1u;
+  if (p.mask != nullptr && x0 + 31 >= 0) {
+    const int W = (E + 31) >> 5, w0 = x0 >> 5;  // floor
+    const uint32_t* mw = p.mask + mask0 + (long long)i * W;
+    const uint32_t lo = w0 >= 0 && w0 < W ? __ldg(mw + w0) : w0 < 0 ? ~0u : 0u;
+    const uint32_t hi = w0 + 1 < W ? __ldg(mw + w0 + 1) : 0u;
+    keep &= __funnelshift_r(lo, hi, x0 & 31);
+  }
+  if (p.window > 0) {
+    if (p.depths == nullptr) {
+      const int gone = i - p.window + 1 - x0;  // keys below the window
+      if (gone > 0) keep = gone > 31 ? 0u : keep >> gone << gone;
+    } else {
+      for (int k = 0; k < 32; ++k) {
+        if (!(keep >> k & 1u)) continue;
+        const int y = x0 + k, place = y >= 0 ? __ldg(p.depths + cu0 + y) : y;
+        if (place <= dep - p.window) keep &= ~(1u << k);
+      }
+    }
+  }
+  return keep;
+}
 
 template <int D, bool BF16, bool C8>
 __global__ void __launch_bounds__(kCtThreads, 2)
@@ -58,12 +94,15 @@ __global__ void __launch_bounds__(kCtThreads, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sQ = smem_u32(smem), sK = sQ + kQBytes, sV = sK + 2u * kKVBytes;
-  float* s_ks = reinterpret_cast<float*>(smem + kQBytes + 4u * kKVBytes);  // [2][BN]
-  float* s_we = s_ks + 2 * BN;                                            // [2][BN]
+  // Exponents of a V tile that spans too many: w and 2^-w per key.
+  float* s_we = reinterpret_cast<float*>(smem + kQBytes + 4u * kKVBytes);  // [2][BN]
   float* s_wi = s_we + 2 * BN;                                            // [2][BN]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_wi + 2 * BN);
-  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 32);  // [0] abort [1] bad [2] most tiles [3] tmem
-  int4* s_piece = reinterpret_cast<int4*>(misc + 8);
+  // Per tile, four deep: K's exponent x, V's, whether V's stand per key.
+  int4* s_exp = reinterpret_cast<int4*>(s_wi + 2 * BN);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_exp + 4);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 32);  // [0] abort [1] bad [2] most tiles
+  int* s_red = reinterpret_cast<int*>(misc + 4);            // [3] tmem; the loaders' reductions
+  int4* s_piece = reinterpret_cast<int4*>(misc + 16);
   int32_t* tiles = reinterpret_cast<int32_t*>(s_piece + 4 * kCaPieces);
   int32_t* units = tiles + (kMaxSeqs + 1);
   int32_t* s_cu = units + (kMaxSeqs + 1);
@@ -80,10 +119,12 @@ __global__ void __launch_bounds__(kCtThreads, 2)
     for (int i = 0; i < 2; ++i) {
       mbar_init(sBar + 8u * (B::kKFull + i), kCtLoaders);
       mbar_init(sBar + 8u * (B::kVFull + i), kCtLoaders);
-      // Free once the product is done and, for e4m3, the softmax warps have
-      // read the scales.
-      mbar_init(sBar + 8u * (B::kKEmpty + i), C8 ? 5u : 1u);
-      mbar_init(sBar + 8u * (B::kVEmpty + i), C8 ? 5u : 1u);
+      // Free once the product is done.  What the softmax reads of a V slot it
+      // has read before the product starts (P is full); s_exp is four deep:
+      // entry t + 4 is written after the scores of t + 2, hence after t + 1 was
+      // read.
+      mbar_init(sBar + 8u * (B::kKEmpty + i), 1u);
+      mbar_init(sBar + 8u * (B::kVEmpty + i), 1u);
     }
     mbar_init(sBar + 8u * B::kSFull, 1u);
     mbar_init(sBar + 8u * B::kSFree, 128u);
@@ -220,9 +261,7 @@ __global__ void __launch_bounds__(kCtThreads, 2)
     // The thread loads 16 bytes, at place q, of keys j0, j0 + kStep, ..
     const int lt = tid - 128, q = lt % kCpr, j0 = lt / kCpr;
     const long long tok_bytes = (long long)p.Hkv * D * kEsz;
-    uint4 raw[kLoads];
-    int row[kLoads];        // pool rows of the tile's keys, -1 for a key no row sees
-    uint32_t sc[kLoads];    // the keys' scale bytes, in the threads at place 0
+    int row[kLoads];  // pool rows of the tile's keys, -1 for a key no row sees
     int4 d0 = {}, d1 = {}, d2 = {};
     uint32_t pi = 0, it = 0;
     bool ok = true;
@@ -242,80 +281,167 @@ __global__ void __launch_bounds__(kCtThreads, 2)
         }
       }
     };
-    auto fetch = [&](bool is_v) {
-      const uint8_t* src =
-          (is_v ? p.v_pages : p.k_pages) + (long long)d1.w * (D * kEsz) + 16 * q;
-      const uint8_t* scales = (is_v ? p.v_scales : p.k_scales) + d1.w;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        sc[i] = 0u;
-        if (row[i] >= 0) {
-          raw[i] = __ldg(reinterpret_cast<const uint4*>(src + row[i] * tok_bytes));
-          if (C8 && q == 0) sc[i] = __ldg(scales + (long long)row[i] * p.Hkv);
-        }
-      }
-    };
     // 16-byte unit c of key row j goes to unit c ^ (j & 7) of its 128-byte row.
-    auto put = [&](uint32_t base, int j, int unit, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-      st_shared_v4(base + (uint32_t)(unit >> 3) * kKVChunk + (uint32_t)j * 128u +
-                       (uint32_t)(((unit & 7) ^ (j & 7)) << 4),
-                   a, b, c, d);
+    auto unit_at = [&](uint32_t base, int j, int unit) {
+      return base + (uint32_t)(unit >> 3) * kKVChunk + (uint32_t)j * 128u +
+             (uint32_t)(((unit & 7) ^ (j & 7)) << 4);
     };
-    auto store = [&](uint32_t it2, bool is_v) -> bool {
-      const uint32_t s = it2 & 1u;
-      if (!wait_all(sBar + 8u * ((is_v ? B::kVEmpty : B::kKEmpty) + s), ((it2 >> 1) & 1u) ^ 1u))
-        return false;
-      const uint32_t base = (is_v ? sV : sK) + s * kKVBytes;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int j = j0 + i * kStep;
-        if (BN % kStep != 0 && j >= BN) break;
-        if constexpr (C8) {
-          uint32_t h[8];
-          e4m3x4_f16(raw[i].x, h[0], h[1]);
-          e4m3x4_f16(raw[i].y, h[2], h[3]);
-          e4m3x4_f16(raw[i].z, h[4], h[5]);
-          e4m3x4_f16(raw[i].w, h[6], h[7]);
-          put(base, j, 2 * q, h[0], h[1], h[2], h[3]);
-          put(base, j, 2 * q + 1, h[4], h[5], h[6], h[7]);
-          if (q == 0) {
-            if (is_v) {
-              s_we[s * BN + j] = sc[i] ? __uint_as_float(0x4B000000u | sc[i]) - 8388735.f : 0.f;
-              s_wi[s * BN + j] = __uint_as_float((254u - sc[i]) << 23);
-            } else {
-              s_ks[s * BN + j] = __uint_as_float(sc[i] << 23);
-            }
-          }
-        } else {
-          put(base, j, q, raw[i].x, raw[i].y, raw[i].z, raw[i].w);
-        }
+    auto slot_free = [&](uint32_t i, bool is_v) {
+      return wait_all(sBar + 8u * ((is_v ? B::kVEmpty : B::kKEmpty) + (i & 1u)),
+                      ((i >> 1) & 1u) ^ 1u);
+    };
+    // The next tile: the piece's, or the next piece's first.
+    int left = 0, n0 = 0;
+    auto next_tile = [&]() -> bool {
+      if (left == 0) {
+        if (!next_piece(pi++, d0, d1, d2, ok)) return false;
+        left = d0.x;
+        n0 = d0.z;
+      } else {
+        n0 += BN;
       }
-      fence_proxy_async_smem();
-      mbar_arrive(sBar + 8u * ((is_v ? B::kVFull : B::kKFull) + s));
+      --left;
+      places(n0);
       return true;
     };
-    // Loads run one half tile (K or V) ahead of the stores, across pieces.
-    bool have = next_piece(pi++, d0, d1, d2, ok);
-    if (have) {
-      places(d0.z);
-      fetch(false);
-    }
-    while (ok && have) {
-      const int n = d0.x, first = d0.z;
-      for (int j = 0; j < n; ++j, ++it) {
-        if (!(ok = store(it, false))) break;
-        fetch(true);
-        if (!(ok = store(it, true))) break;
-        int next = first + (j + 1) * BN;
-        if (j + 1 == n) {
-          have = next_piece(pi++, d0, d1, d2, ok);
-          if (!have) break;
-          next = d0.z;
+
+    if constexpr (C8) {
+      // K and V of the next tile are loaded, in registers of their own, while
+      // this tile's are widened and stored.
+      struct Half {
+        uint4 raw[kLoads];
+        uint32_t sc[kLoads];  // the keys' scale bytes, 0 for a key no row sees
+      } hk, hv;
+      auto fetch = [&](Half& h, const uint8_t* pages, const uint8_t* scales) {
+        const uint8_t* src = pages + (long long)d1.w * D + 16 * q;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          h.raw[i] = make_uint4(0u, 0u, 0u, 0u);
+          h.sc[i] = 0u;
+          if (row[i] >= 0) {
+            h.raw[i] = __ldg(reinterpret_cast<const uint4*>(src + row[i] * tok_bytes));
+            h.sc[i] = __ldg(scales + (long long)row[i] * p.Hkv + d1.w);
+          }
         }
-        places(next);
-        fetch(false);
+      };
+      // Largest and smallest scale byte of the tile's keys, over the three
+      // warps: each puts its own into one of two sets of words in turn.
+      uint32_t turn = 0;
+      auto span = [&](const Half& h, int& top, int& low) {
+        int hi = 0, lo = 255;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          hi = max(hi, (int)h.sc[i]);
+          if (h.sc[i] != 0u) lo = min(lo, (int)h.sc[i]);
+        }
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        int* red = s_red + 6 * (turn++ & 1u);
+        if (lane == 0) {
+          red[2 * (warp - 4)] = hi;
+          red[2 * (warp - 4) + 1] = lo;
+        }
+        named_bar_sync(1u, kCtLoaders);
+        top = max(max(red[0], red[2]), red[4]);
+        low = min(min(red[1], red[3]), red[5]);
+      };
+      auto store = [&](const Half& h, bool is_v) {
+        const uint32_t s = it & 1u;
+        const uint32_t base = (is_v ? sV : sK) + s * kKVBytes;
+        int top, low;
+        span(h, top, low);
+        const bool apart = is_v && top - low > 22;  // exponents per key
+        const int x = apart ? 0 : max(top, 8) - 127 - 7;  // the tile's exponent, >= -126
+        if (lt == 0) {
+          if (is_v) {
+            s_exp[it & 3u].y = x;
+            s_exp[it & 3u].z = apart ? 1 : 0;
+          } else {
+            s_exp[it & 3u].x = x;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int j = j0 + i * kStep;
+          if (BN % kStep != 0 && j >= BN) break;
+          uint32_t y[8];
+          e4m3x4_f16(h.raw[i].x, y[0], y[1]);
+          e4m3x4_f16(h.raw[i].y, y[2], y[3]);
+          e4m3x4_f16(h.raw[i].z, y[4], y[5]);
+          e4m3x4_f16(h.raw[i].w, y[6], y[7]);
+          // 2^(e - x) as an f16 pair: at most 2^7, zero below 2^-24.
+          const int e = apart ? 0 : max((int)h.sc[i] - 127 - x, -40);
+          const float f = __int_as_float((127 + e) << 23);
+          const uint32_t f2h = pack2<false>(f, f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[k]) : "r"(y[k]), "r"(f2h));
+          st_shared_v4(unit_at(base, j, 2 * q), y[0], y[1], y[2], y[3]);
+          st_shared_v4(unit_at(base, j, 2 * q + 1), y[4], y[5], y[6], y[7]);
+          if (apart && q == 0) {
+            s_we[s * BN + j] = h.sc[i] ? (float)((int)h.sc[i] - 127) : 0.f;
+            s_wi[s * BN + j] = __uint_as_float((254u - h.sc[i]) << 23);
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(sBar + 8u * ((is_v ? B::kVFull : B::kKFull) + s));
+      };
+      bool have = next_tile();
+      if (have) {
+        fetch(hk, p.k_pages, p.k_scales);
+        fetch(hv, p.v_pages, p.v_scales);
       }
+      for (; have; ++it) {
+        if (!slot_free(it, false)) break;
+        const bool more = next_tile();  // its page lookups run beside the stores
+        store(hk, false);
+        if (more) fetch(hk, p.k_pages, p.k_scales);
+        if (!slot_free(it, true)) break;
+        store(hv, true);
+        if (more) fetch(hv, p.v_pages, p.v_scales);
+        have = more;
+      }
+    } else {
+      // Straight to shared memory; two halves (K or V) stay in flight.
+      auto issue = [&](uint32_t i2, bool is_v) {
+        const uint8_t* src =
+            (is_v ? p.v_pages : p.k_pages) + (long long)d1.w * (D * kEsz) + 16 * q;
+        const uint32_t base = (is_v ? sV : sK) + (i2 & 1u) * kKVBytes;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int j = j0 + i * kStep;
+          if (BN % kStep != 0 && j >= BN) break;
+          const uint8_t* g = src + (row[i] >= 0 ? row[i] : 0) * tok_bytes;
+          // Source size 0 fills with zeros.
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(unit_at(base, j, q)),
+                       "l"(g), "r"(row[i] >= 0 ? 16u : 0u)
+                       : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      // Half h (2 t: K of tile t, 2 t + 1: V) has landed.
+      auto landed = [&](uint32_t h) {
+        fence_proxy_async_smem();
+        mbar_arrive(sBar + 8u * (((h & 1u) ? B::kVFull : B::kKFull) + ((h >> 1) & 1u)));
+      };
+      uint32_t h = 0;  // halves issued
+      while (next_tile()) {
+        if (!slot_free(it, false)) break;
+        issue(it, false);
+        if (++h > 2u) {
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+          landed(h - 3u);
+        }
+        if (!slot_free(it, true)) break;
+        issue(it, true);
+        if (++h > 2u) {
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+          landed(h - 3u);
+        }
+        ++it;
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      for (uint32_t x = h > 2u ? h - 2u : 0u; x < h; ++x) landed(x);
     }
   } else {
     // -------------------------------------------------------------- softmax, output
@@ -378,97 +504,75 @@ __global__ void __launch_bounds__(kCtThreads, 2)
       }
 
       float M = -1e30f, L = 0.f;
-      const uint64_t rs2 = f2(rs, rs);
       for (int j = 0; j < n; ++j, ++it) {
         const int n0 = d0.z + j * BN;
         const uint32_t s = it & 1u;
-        // The scales were written by the loading warps: their own barriers
-        // make them visible here.
-        if (C8 && !(ok = wait_all(sBar + 8u * (B::kKFull + s), (it >> 1) & 1u))) break;
-        if (C8 && !(ok = wait_all(sBar + 8u * (B::kVFull + s), (it >> 1) & 1u))) break;
+        // This tile's factor of the scores, and V's exponent.
+        float rk = rs, ve = 0.f, vi = 1.f;
+        bool apart = false;
+        if constexpr (C8) {
+          // The loaders' writes are visible after their own barriers.
+          if (!(ok = wait_all(sBar + 8u * (B::kKFull + s), (it >> 1) & 1u))) break;
+          if (!(ok = wait_all(sBar + 8u * (B::kVFull + s), (it >> 1) & 1u))) break;
+          const int4 x = s_exp[it & 3u];
+          rk = fmaxf(rs * __int_as_float((127 + x.x) << 23), 1e-37f);
+          ve = (float)x.y;
+          vi = __int_as_float((127 - x.y) << 23);
+          apart = x.z != 0;
+        }
         if (!(ok = wait_all(sBar + 8u * B::kSFull, it & 1u))) break;
         tc_fence_after();
         const bool edge = n0 + BN > P || p.window > 0 || !on;
-        float alpha = 1.f;  // this tile's moves of the reference
-#pragma unroll 1
+        float alpha = 1.f, sum = 0.f;  // this tile's moves of the reference, its sum of P
+        uint32_t x[2][32];
+        float top[2];
+        top[0] = tmem_ld32_max(t_lane + kColS, x[0]);
+#pragma unroll
         for (int c = 0; c < BN / 32; ++c) {
-          uint32_t x[32];
-          tmem_ld32(t_lane + kColS + 32 * c, x);
+          uint32_t(&sr)[32] = x[c & 1];
           tmem_wait_ld();
-          if (c == BN / 32 - 1) {
-            tc_fence_before();
-            mbar_arrive(sBar + 8u * B::kSFree);  // the next scores may come
-          }
-          uint64_t t2[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            t2[k] = f2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
-          if constexpr (C8) {
-            const ulonglong2* ks = reinterpret_cast<const ulonglong2*>(s_ks + s * BN + 32 * c);
-            const ulonglong2* we = reinterpret_cast<const ulonglong2*>(s_we + s * BN + 32 * c);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const ulonglong2 a = ks[k], b = we[k];
-              t2[2 * k] = ffma2(fmul2(t2[2 * k], rs2), a.x, b.x);
-              t2[2 * k + 1] = ffma2(fmul2(t2[2 * k + 1], rs2), a.y, b.y);
-            }
+          if (c + 1 < BN / 32) {  // the next 32 scores come meanwhile
+            top[(c + 1) & 1] = tmem_ld32_max(t_lane + kColS + 32 * (c + 1), x[(c + 1) & 1]);
           } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) t2[k] = fmul2(t2[k], rs2);
+            tc_fence_before();
+            mbar_arrive(sBar + 8u * B::kSFree);  // the next tile's scores may come
           }
-          if (edge) {  // keys this row keeps, one bit each
-            const int x0 = n0 + 32 * c - P;  // first key's index among the new tokens
-            uint32_t keep = 0u;
-            if (on && x0 <= i) {
-              keep = i - x0 >= 31 ? ~0u : (2u << (i - x0)) - 1u;
-              if (p.mask != nullptr && x0 + 31 >= 0) {
-                const int W = (E + 31) >> 5, w0 = x0 >> 5;  // floor
-                const uint32_t* mw = p.mask + (long long)d2.y + (long long)i * W;
-                const uint32_t lo = w0 >= 0 && w0 < W ? __ldg(mw + w0) : w0 < 0 ? ~0u : 0u;
-                const uint32_t hi = w0 + 1 < W ? __ldg(mw + w0 + 1) : 0u;
-                keep &= __funnelshift_r(lo, hi, x0 & 31);
-              }
-              if (p.window > 0) {
-                if (p.depths == nullptr) {
-                  const int gone = i - p.window + 1 - x0;  // keys below the window
-                  if (gone > 0) keep = gone > 31 ? 0u : keep >> gone << gone;
-                } else {
-                  for (int k = 0; k < 32; ++k) {
-                    if (!(keep >> k & 1u)) continue;
-                    const int y = x0 + k, place = y >= 0 ? __ldg(p.depths + cu0 + y) : y;
-                    if (place <= dep - p.window) keep &= ~(1u << k);
-                  }
-                }
-              }
-            }
+          float mx = top[c & 1];
+          if (__builtin_expect(edge || apart, 0)) {
+            if (edge) {  // keys this row keeps, one bit each
+              const uint32_t keep =
+                  keep_bits(p, on, i, dep, n0 + 32 * c - P, E, cu0, (long long)d2.y);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float a, b;
-              unf2(t2[k], a, b);
-              t2[k] = f2(keep >> (2 * k) & 1u ? a : -INFINITY, keep >> (2 * k + 1) & 1u ? b : -INFINITY);
+              for (int k = 0; k < 32; ++k)
+                if (!(keep >> k & 1u)) sr[k] = 0xFF800000u;  // -inf
+            }
+            mx = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float a = __uint_as_float(sr[k]), b = __uint_as_float(sr[k + 1]);
+              if (apart) {  // the whole exponent here, a key's own part of it included
+                a = fmaf(a, rk, s_we[s * BN + 32 * c + k]);
+                b = fmaf(b, rk, s_we[s * BN + 32 * c + k + 1]);
+                sr[k] = __float_as_uint(a), sr[k + 1] = __float_as_uint(b);
+              }
+              mx = max3(mx, a, b);
             }
           }
-          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            float a, b;
-            unf2(t2[k], a, b), m0 = max3(m0, a, b);
-            unf2(t2[k + 1], a, b), m1 = max3(m1, a, b);
-            unf2(t2[k + 2], a, b), m2 = max3(m2, a, b);
-            unf2(t2[k + 3], a, b), m3 = max3(m3, a, b);
-          }
-          const float mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
-          const bool raise = mx > M + kCaSlack;
+          const float rc = apart ? 1.f : rk;
+          mx = fmaf(mx, rc, ve);  // ve is 0 with exponents per key
           if (c == 0 && it > 0) {  // P of the tile before has been read
             if (!(ok = wait_all(sBar + 8u * B::kODone, (it - 1u) & 1u))) break;
             tc_fence_after();
           }
+          const bool raise = mx > M + kCaSlack;
           if (__any_sync(0xffffffffu, raise)) {  // rare after the first tiles
             const float a = raise ? ex2(M - mx) : 1.f;
             if (raise) M = mx;
             L *= a;
+            sum *= a;
             alpha *= a;
             tmem_wait_st();
+#pragma unroll 1
             for (int e = 0; e < c; ++e) {  // this tile's P so far
               uint32_t pk[16];
               tmem_ld16(t_lane + kColP + 16 * e, pk);
@@ -480,41 +584,32 @@ __global__ void __launch_bounds__(kCtThreads, 2)
               tmem_wait_st();
             }
           }
-          const float ref = kBias - M;
-          const uint64_t ref2 = f2(ref, ref);
+          const float ref = ve - M + kBias;
+          const uint64_t ref2 = f2(ref, ref), rk2 = f2(rc, rc);
           uint64_t l0 = 0, l1 = 0;
           uint32_t pk[16];
-          const ulonglong2* wi = reinterpret_cast<const ulonglong2*>(s_wi + s * BN + 32 * c);
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
             float a, b, e, f;
-            unf2(fadd2(t2[k], ref2), a, b);
-            unf2(fadd2(t2[k + 1], ref2), e, f);
+            unf2(ffma2(f2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), rk2, ref2), a, b);
+            unf2(ffma2(f2(__uint_as_float(sr[2 * k + 2]), __uint_as_float(sr[2 * k + 3])), rk2, ref2), e, f);
             a = ex2(a), b = ex2(b), e = ex2(e), f = ex2(f);
-            if constexpr (C8) {
-              const ulonglong2 w = wi[k / 2];
-              l0 = ffma2(f2(a, b), w.x, l0);
-              l1 = ffma2(f2(e, f), w.y, l1);
-            } else {
-              l0 = fadd2(l0, f2(a, b));
-              l1 = fadd2(l1, f2(e, f));
-            }
             pk[k] = pack2<MBF>(a, b);
             pk[k + 1] = pack2<MBF>(e, f);
+            if (C8 && __builtin_expect(apart, 0)) {
+              const float* w = s_wi + s * BN + 32 * c + 2 * k;
+              a *= w[0], b *= w[1], e *= w[2], f *= w[3];
+            }
+            l0 = fadd2(l0, f2(a, b));
+            l1 = fadd2(l1, f2(e, f));
           }
           float a, b;
           unf2(fadd2(l0, l1), a, b);
-          L += a + b;
+          sum += a + b;
           tmem_st16(t_lane + kColP + 16 * c, pk);
         }
         if (!ok) break;
-        if (C8) {
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(sBar + 8u * (B::kKEmpty + s));
-            mbar_arrive(sBar + 8u * (B::kVEmpty + s));
-          }
-        }
+        L = fmaf(sum, vi, L);
         if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {  // O so far, its products done
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
