@@ -306,21 +306,24 @@ __global__ void __launch_bounds__(kCtThreads, 2)
     };
 
     if constexpr (C8) {
-      // K and V of the next tile are loaded, in registers of their own, while
-      // this tile's are widened and stored.
+      // The next half tile (K or V) is loaded, in registers of its own, while
+      // this one is widened and stored.  One copy of the code serves both
+      // kinds: the loops of all roles have to stay in the instruction cache
+      // together.
       struct Half {
         uint4 raw[kLoads];
         uint32_t sc[kLoads];  // the keys' scale bytes, 0 for a key no row sees
-      } hk, hv;
-      auto fetch = [&](Half& h, const uint8_t* pages, const uint8_t* scales) {
-        const uint8_t* src = pages + (long long)d1.w * D + 16 * q;
+      } cur, nxt;
+      auto fetch = [&](Half& h, bool is_v) {
+        const uint8_t* src = (is_v ? p.v_pages : p.k_pages) + (long long)d1.w * D + 16 * q;
+        const uint8_t* scales = (is_v ? p.v_scales : p.k_scales) + d1.w;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           h.raw[i] = make_uint4(0u, 0u, 0u, 0u);
           h.sc[i] = 0u;
           if (row[i] >= 0) {
             h.raw[i] = __ldg(reinterpret_cast<const uint4*>(src + row[i] * tok_bytes));
-            h.sc[i] = __ldg(scales + (long long)row[i] * p.Hkv + d1.w);
+            h.sc[i] = __ldg(scales + (long long)row[i] * p.Hkv);
           }
         }
       };
@@ -386,20 +389,20 @@ __global__ void __launch_bounds__(kCtThreads, 2)
         fence_proxy_async_smem();
         mbar_arrive(sBar + 8u * ((is_v ? B::kVFull : B::kKFull) + s));
       };
-      bool have = next_tile();
-      if (have) {
-        fetch(hk, p.k_pages, p.k_scales);
-        fetch(hv, p.v_pages, p.v_scales);
-      }
-      for (; have; ++it) {
-        if (!slot_free(it, false)) break;
-        const bool more = next_tile();  // its page lookups run beside the stores
-        store(hk, false);
-        if (more) fetch(hk, p.k_pages, p.k_scales);
-        if (!slot_free(it, true)) break;
-        store(hv, true);
-        if (more) fetch(hv, p.v_pages, p.v_scales);
-        have = more;
+      bool have = next_tile(), v_next = false;
+#pragma unroll 1
+      for (bool first = true;; first = false) {
+        const bool v_now = !v_next;  // of the half in `nxt` until now
+        if (!first) cur = nxt;
+        if (have) fetch(nxt, v_next);
+        if (!first) {
+          if (!slot_free(it, v_now)) break;
+          store(cur, v_now);
+          if (v_now) ++it;
+        }
+        if (!have) break;
+        if (v_next) have = next_tile();
+        v_next = !v_next;
       }
     } else {
       // Straight to shared memory; two halves (K or V) stay in flight.
@@ -524,20 +527,17 @@ __global__ void __launch_bounds__(kCtThreads, 2)
         tc_fence_after();
         const bool edge = n0 + BN > P || p.window > 0 || !on;
         float alpha = 1.f, sum = 0.f;  // this tile's moves of the reference, its sum of P
-        uint32_t x[2][32];
-        float top[2];
-        top[0] = tmem_ld32_max(t_lane + kColS, x[0]);
-#pragma unroll
+        // Rolled: the unrolled loop and the loaders' did not fit the
+        // instruction cache together (half the stalls).
+#pragma unroll 1
         for (int c = 0; c < BN / 32; ++c) {
-          uint32_t(&sr)[32] = x[c & 1];
+          uint32_t sr[32];
+          float mx = tmem_ld32_max(t_lane + kColS + 32 * c, sr);
           tmem_wait_ld();
-          if (c + 1 < BN / 32) {  // the next 32 scores come meanwhile
-            top[(c + 1) & 1] = tmem_ld32_max(t_lane + kColS + 32 * (c + 1), x[(c + 1) & 1]);
-          } else {
+          if (c == BN / 32 - 1) {
             tc_fence_before();
             mbar_arrive(sBar + 8u * B::kSFree);  // the next tile's scores may come
           }
-          float mx = top[c & 1];
           if (__builtin_expect(edge || apart, 0)) {
             if (edge) {  // keys this row keeps, one bit each
               const uint32_t keep =
