@@ -15,7 +15,7 @@ namespace {
 constexpr unsigned kSmemMax = 227u * 1024u;
 
 struct CachePlan {
-  bool tile;  // the 128-row kernel
+  bool tile;  // the kernel of 128-row tiles
   int RT;     // rows of a unit
   int G, HPC, HG, KW, NT, T, NS;
   uint32_t data_bytes, slot_bytes;
@@ -24,7 +24,7 @@ struct CachePlan {
 };
 
 // Rows per KV head (tokens times query heads of the longest sequence) above
-// which the 128-row kernel takes over.
+// which the kernel of 128-row tiles takes over.
 constexpr int kTileRows = 64;
 
 // Heads per CTA: the largest divisor of Hkv up to 8; the warps left
@@ -79,10 +79,10 @@ int cache_plan(int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hkv, int
   if (pl->tile) {
     pl->HPC = 1;
     pl->KW = 1;
-    pl->T = ct_bn(d);
+    pl->T = ct_bn;
     pl->NS = 2;
     pl->data_bytes = pl->slot_bytes = 0;
-    pl->RT = 128;
+    pl->RT = 256;
   } else {
     const int rc = ring_shape(Hkv, d, c8, gk, esz, warps, pl);
     if (rc != GQA_OK) return rc;
@@ -92,7 +92,7 @@ int cache_plan(int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hkv, int
   int sms = 152;
   unsigned int* status = nullptr;
   if (call_device(&sms, &status) != GQA_OK) sms = 152;
-  pl->ctas = pl->tile ? 2 * sms : sms;
+  pl->ctas = sms;
   const int seqs = num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs;
   const int rt = pl->RT;
   const long long units =

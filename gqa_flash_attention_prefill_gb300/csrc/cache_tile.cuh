@@ -1,21 +1,23 @@
 // cache_tile.cuh -- the form of gqa_cache_attention for many query rows per KV
-// head (a draft tree of some tens of tokens, a short chunk): 128-row tiles on
-// the tensor memory, sm_103a.
+// head (a draft tree of some tens of tokens, a short chunk): two 128-row tiles
+// on the tensor memory, sm_103a.
 //
-// The mathematics is cache_attn.cuh's; here the rows fill a 128-row tile, so
-// the products go to tcgen05 and the bound moves from memory to the
-// exponentials (128 keys x 128 rows take the special-function units 1024
-// clocks, the two products 512 at d = 64).  Two CTAs per SM, so that one's
-// softmax runs beside the other's products.
+// The mathematics is cache_attn.cuh's; here the rows fill 128-row tiles, so the
+// products go to tcgen05 and the bound moves from memory to the softmax and,
+// for e4m3, to widening the keys.  A unit is 256 rows of one KV head, so a key
+// is widened once for two row tiles.
 //
-// A CTA of 8 warps:
-//   0..3  softmax and output, thread = row = tensor-memory lane; they also
-//         bring the rows of Q into shared memory;
-//   4..6  bring K and V into the 128-byte swizzle the products read: 16-bit
-//         pages by cp.async, e4m3 pages through registers, widened to f16, the
-//         next tile's loads in flight meanwhile.  Keys no row sees become
-//         zeros;
-//   7     plans the work and issues the products.
+// A CTA of 13 warps, one per SM:
+//   0..7   softmax and output: warps 0..3 row tile 0, 4..7 row tile 1, thread =
+//          row = tensor-memory lane; they also bring their rows of Q into
+//          shared memory.  A second tile without rows takes no part;
+//   8..11  bring K and V into the 128-byte swizzle the products read.  16-bit
+//          pages: cp.async.  e4m3 pages: cp.async of the raw bytes some tiles
+//          ahead, then each thread widens what it copied itself to f16.  Keys
+//          no row sees become zeros;
+//   12     plans the work and issues the products.
+// Where the tensor memory has room (d = 64) scores and probabilities have two
+// buffers: the products of the neighbouring tiles run beside a tile's softmax.
 //
 // Scales of an e4m3 tile.  Widening multiplies a key's values by 2^(e - x)
 // with x 7 below the largest exponent e of the tile, which keeps every value
@@ -32,19 +34,26 @@
 
 namespace gqa {
 
-constexpr int kCtThreads = 256;
-constexpr int kCtLoaders = 96;
+constexpr int kCtLoaders = 128;
+constexpr int kCtThreads = 256 + kCtLoaders + 32;
 constexpr int kCtWholeSlack = 2;  // tiles a join is worth
-__host__ __device__ constexpr int ct_bn(int D) { return D == 64 ? 128 : 64; }
-// Q tile, two slots each of K and V, their scales, the tables of the sequences.
-__host__ __device__ constexpr uint32_t ct_smem(int D) {
-  return 1024u + 128u * D * 2u + 4u * ct_bn(D) * D * 2u + 2u * ct_bn(D) * 8u + 4u * 16u +
-         4u * (5 * kMaxSeqs + 3) + kCaPieces * 64u + 32u * 8u + 64u;
+constexpr int ct_bn = 64;         // keys per tile
+// Slots of K and of V ready for the products; raw e4m3 tiles on their way.
+__host__ __device__ constexpr int ct_slots(bool C8) { return C8 ? 2 : 4; }
+constexpr int kCtRaw = 4;
+// Tensor-memory buffers of the scores and of the probabilities.
+__host__ __device__ constexpr int ct_buffers(int D) { return D == 64 ? 2 : 1; }
+// A raw half tile: the values, and 8 bytes a key for its scale.
+__host__ __device__ constexpr uint32_t ct_raw_half(int D) { return ct_bn * (D + 8u); }
+__host__ __device__ constexpr uint32_t ct_smem(int D, bool C8) {
+  return 1024u + 2u * 128u * D * 2u + 2u * ct_slots(C8) * ct_bn * D * 2u +
+         (C8 ? 2u * kCtRaw * ct_raw_half(D) + 2u * ct_slots(C8) * ct_bn * 4u : 0u) + 8u * 16u +
+         64u * 8u + 128u + kCaPieces * 64u + 4u * (5 * kMaxSeqs + 3);
 }
 
-struct CtBar {  // barrier numbers
-  static constexpr int kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kSFree = 9,
-                       kPFull = 10, kODone = 11, kQFull = 12, kDrain = 13, kPiece = 14;
+struct CtBar {  // barrier numbers: 4 a slot, 4 a (row tile, buffer)
+  static constexpr int kKFull = 0, kKEmpty = 4, kVFull = 8, kVEmpty = 12, kSFull = 16, kSFree = 20,
+                       kPFull = 24, kODone = 28, kQFull = 32, kDrain = 34, kPiece = 35;
 };
 
 // Keys x0 .. x0 + 31 (counted from the first new token) that row i of a
@@ -76,16 +85,16 @@ static __device__ __noinline__ uint32_t keep_bits(const CacheAttnParams& p, bool
 }
 
 template <int D, bool BF16, bool C8>
-__global__ void __launch_bounds__(kCtThreads, 2)
+__global__ void __launch_bounds__(kCtThreads, 1)
     cache_tile_kernel(const __grid_constant__ CacheAttnParams p) {
-  constexpr int BN = ct_bn(D), RT = 128;
+  constexpr int BN = ct_bn, RT = 256, NS = ct_slots(C8), NB = ct_buffers(D);
   constexpr bool MBF = BF16 && !C8;  // product type
   constexpr float kBias = MBF ? 0.f : kCaBias;
   constexpr int kEsz = C8 ? 1 : 2;
   constexpr uint32_t kQBytes = 128u * D * 2u, kKVBytes = (uint32_t)BN * D * 2u;
   constexpr uint32_t kQChunk = 128u * 128u, kKVChunk = (uint32_t)BN * 128u;
-  constexpr uint32_t kColS = 0, kColP = BN, kColO = BN + BN / 2;
-  static_assert(kColO + D <= 256, "two CTAs share the tensor memory");
+  constexpr uint32_t kColP = NB * BN, kColO = NB * (BN + BN / 2);  // scores at column 0
+  static_assert(kColO + D <= 256, "two row tiles share the tensor memory");
   constexpr uint32_t kIdescS = idesc_f16(MBF, 128, BN, false);
   constexpr uint32_t kIdescO = idesc_f16(MBF, 128, D, true);
   using B = CtBar;
@@ -93,16 +102,19 @@ __global__ void __launch_bounds__(kCtThreads, 2)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const uint32_t sQ = smem_u32(smem), sK = sQ + kQBytes, sV = sK + 2u * kKVBytes;
+  const uint32_t sQ = smem_u32(smem), sK = sQ + 2u * kQBytes, sV = sK + NS * kKVBytes;
+  const uint32_t sRaw = sV + NS * kKVBytes;  // [kCtRaw][K, V][values, scales]
+  uint8_t* after = smem + 2u * kQBytes + 2u * NS * kKVBytes +
+                   (C8 ? 2u * kCtRaw * ct_raw_half(D) : 0u);
   // Exponents of a V tile that spans too many: w and 2^-w per key.
-  float* s_we = reinterpret_cast<float*>(smem + kQBytes + 4u * kKVBytes);  // [2][BN]
-  float* s_wi = s_we + 2 * BN;                                            // [2][BN]
-  // Per tile, four deep: K's exponent x, V's, whether V's stand per key.
-  int4* s_exp = reinterpret_cast<int4*>(s_wi + 2 * BN);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(s_exp + 4);
-  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 32);  // [0] abort [1] bad [2] most tiles
+  float* s_we = reinterpret_cast<float*>(after);  // [NS][BN]
+  float* s_wi = s_we + (C8 ? NS * BN : 0);
+  // Per tile, eight deep: K's exponent x, V's, whether V's stand per key.
+  int4* s_exp = reinterpret_cast<int4*>(s_wi + (C8 ? NS * BN : 0));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_exp + 8);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 64);  // [0] abort [1] bad [2] most tiles
   int* s_red = reinterpret_cast<int*>(misc + 4);            // [3] tmem; the loaders' reductions
-  int4* s_piece = reinterpret_cast<int4*>(misc + 16);
+  int4* s_piece = reinterpret_cast<int4*>(misc + 32);
   int32_t* tiles = reinterpret_cast<int32_t*>(s_piece + 4 * kCaPieces);
   int32_t* units = tiles + (kMaxSeqs + 1);
   int32_t* s_cu = units + (kMaxSeqs + 1);
@@ -116,25 +128,28 @@ __global__ void __launch_bounds__(kCtThreads, 2)
 
   // ---------------------------------------------------------------- set-up
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    // A slot is free once its products are done.  What the softmax reads of a V
+    // slot it has read before those products start (P is full); s_exp is eight
+    // deep: entry t + 8 is written after the scores of t + 8 - NS are done,
+    // which were issued after tile t + 8 - NS - NB, or a later one, was read.
+    for (int i = 0; i < NS; ++i) {
       mbar_init(sBar + 8u * (B::kKFull + i), kCtLoaders);
       mbar_init(sBar + 8u * (B::kVFull + i), kCtLoaders);
-      // Free once the product is done.  What the softmax reads of a V slot it
-      // has read before the product starts (P is full); s_exp is four deep:
-      // entry t + 4 is written after the scores of t + 2, hence after t + 1 was
-      // read.
       mbar_init(sBar + 8u * (B::kKEmpty + i), 1u);
       mbar_init(sBar + 8u * (B::kVEmpty + i), 1u);
     }
-    mbar_init(sBar + 8u * B::kSFull, 1u);
-    mbar_init(sBar + 8u * B::kSFree, 128u);
-    mbar_init(sBar + 8u * B::kPFull, 128u);
-    mbar_init(sBar + 8u * B::kODone, 1u);
+    for (int i = 0; i < 4; ++i) {  // row tile i / 2, buffer i % 2
+      mbar_init(sBar + 8u * (B::kSFull + i), 1u);
+      mbar_init(sBar + 8u * (B::kSFree + i), 128u);
+      mbar_init(sBar + 8u * (B::kPFull + i), 128u);
+      mbar_init(sBar + 8u * (B::kODone + i), 1u);
+    }
     mbar_init(sBar + 8u * B::kQFull, 128u);
+    mbar_init(sBar + 8u * (B::kQFull + 1), 128u);
     mbar_init(sBar + 8u * B::kDrain, 1u);
     for (int i = 0; i < kCaPieces; ++i) {
       mbar_init(sPiece + 8u * i, 1u);
-      mbar_init(sPiece + 8u * (kCaPieces + i), 7u);  // 4 softmax and 3 loading warps
+      mbar_init(sPiece + 8u * (kCaPieces + i), 12u);  // 8 softmax and 4 loading warps
     }
     misc[0] = 0u;
     misc[1] = 0u;
@@ -155,8 +170,8 @@ __global__ void __launch_bounds__(kCtThreads, 2)
     }
     return;
   }
-  if (warp == 7) {
-    tmem_alloc(smem_u32(misc + 3), 256u);
+  if (warp == 12) {
+    tmem_alloc(smem_u32(misc + 3), 512u);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -180,116 +195,103 @@ __global__ void __launch_bounds__(kCtThreads, 2)
     return d0.x > 0;
   };
 
-  if (warp == 7) {
+  if (warp == 12) {
     // -------------------------------------------------------------- plan, products
-    const uint64_t dQ = smem_desc_sw128(sQ, 16, 1024);
+    const uint64_t dQ0 = smem_desc_sw128(sQ, 16, 1024);
     const uint64_t dK0 = smem_desc_sw128(sK, 16, 1024);
     const uint64_t dV0 = smem_desc_sw128(sV, kKVChunk, 1024);
     auto kstep = [](int kk, uint32_t chunk) -> uint64_t {
       return (uint64_t)(((uint32_t)(kk >> 2) * chunk + (uint32_t)(kk & 3) * 32u) >> 4);
     };
-    auto issue_pv = [&](uint32_t it, bool first) -> bool {
-      const uint32_t s = it & 1u;
-      if (!wait_all(sBar + 8u * (B::kVFull + s), (it >> 1) & 1u)) return false;
-      if (!wait_all(sBar + 8u * B::kPFull, it & 1u)) return false;
-      tc_fence_after();
+    uint32_t it = 0;               // tiles, the slots' count
+    uint32_t cnt[2] = {0u, 0u};    // tiles of each row tile, its buffers' count
+    uint32_t pieces[2] = {0u, 0u};
+    // O += P V of tile i2 for nt row tiles, the tile their last but `back`.
+    auto issue_pv = [&](uint32_t i2, int nt, uint32_t back, bool first) -> bool {
+      const uint32_t s = i2 % NS;
+      if (!wait_all(sBar + 8u * (B::kVFull + s), (i2 / NS) & 1u)) return false;
       const uint64_t dv = dV0 + s * (kKVBytes >> 4);
+      for (int t = 0; t < nt; ++t) {
+        const uint32_t c = cnt[t] - back, b = c % NB, tb = tmem + 256u * t;
+        if (!wait_all(sBar + 8u * (B::kPFull + 2 * t + b), (c / NB) & 1u)) return false;
+        tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < BN / 16; ++kk)
-        mma_ts(tmem + kColO, tmem + kColP + kk * 8, dv + (uint64_t)(kk * 128), kIdescO,
-               (first && kk == 0) ? 0u : 1u);
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts(tb + kColO, tb + kColP + b * (BN / 2) + kk * 8, dv + (uint64_t)(kk * 128), kIdescO,
+                 (first && kk == 0) ? 0u : 1u);
+        mma_commit(sBar + 8u * (B::kODone + 2 * t + b));
+      }
       mma_commit(sBar + 8u * (B::kVEmpty + s));
-      mma_commit(sBar + 8u * B::kODone);
       return true;
     };
     CaPlan plan = ca_plan(p, tiles, units, s_cu, s_pre, s_ipt, misc);
-    // A piece is told to the other warps one ahead of its products.
+    // The other warps hear of up to three pieces beyond the one at work: the
+    // loading warps are that many tiles ahead at most.
     uint32_t told = 0;
-    auto tell = [&](CaPiece& u, bool& more) -> bool {
-      more = ca_next(p, plan.T, plan.walk, RT, u);
-      const uint32_t ps = told % kCaPieces;
-      if (!wait_all(sPiece + 8u * (kCaPieces + ps), ((told / kCaPieces) & 1u) ^ 1u)) return false;
-      if (lane == 0) {
-        ca_publish(p, plan, u, more, RT, s_piece + 4 * ps);
-        mbar_arrive(sPiece + 8u * ps);
+    bool more = true, ok = true;
+    for (uint32_t pc = 0; ok; ++pc) {
+      while (more && told < pc + kCaPieces) {
+        CaPiece u = {};
+        more = ca_next(p, plan.T, plan.walk, RT, u);
+        const uint32_t ps = told % kCaPieces;
+        if (!(ok = wait_all(sPiece + 8u * (kCaPieces + ps), ((told / kCaPieces) & 1u) ^ 1u))) break;
+        if (lane == 0) {
+          ca_publish(p, plan, u, more, RT, s_piece + 4 * ps);
+          mbar_arrive(sPiece + 8u * ps);
+        }
+        ++told;
+        __syncwarp();
       }
-      ++told;
-      __syncwarp();
-      return true;
-    };
-    CaPiece u = {};
-    bool more = false;
-    bool ok = tell(u, more);
-    uint32_t it = 0, pc = 0;
-    while (ok && more) {
-      const int n = u.t1 - u.t0;
-      CaPiece un = {};
-      bool more_n = false;
-      if (!(ok = tell(un, more_n))) break;
-      if (!(ok = wait_all(sBar + 8u * B::kQFull, pc & 1u))) break;
+      if (!ok) break;
+      const int4 d0 = s_piece[4 * (pc % kCaPieces)], d1 = s_piece[4 * (pc % kCaPieces) + 1];
+      const int n = d0.x;
+      if (n == 0) break;
+      const int nt = d1.x * p.G - d1.z > 128 ? 2 : 1;  // row tiles that hold rows
+      for (int t = 0; t < nt && ok; ++t) {
+        ok = wait_all(sBar + 8u * (B::kQFull + t), pieces[t] & 1u);
+        ++pieces[t];
+      }
+      if (!ok) break;
       for (int j = 0; j < n; ++j, ++it) {
-        const uint32_t s = it & 1u;
-        if (!(ok = wait_all(sBar + 8u * (B::kKFull + s), (it >> 1) & 1u))) break;
-        if (it > 0 && !(ok = wait_all(sBar + 8u * B::kSFree, (it - 1u) & 1u))) break;
-        tc_fence_after();
+        const uint32_t s = it % NS;
+        if (!(ok = wait_all(sBar + 8u * (B::kKFull + s), (it / NS) & 1u))) break;
         const uint64_t dk = dK0 + s * (kKVBytes >> 4);
+        for (int t = 0; t < nt; ++t) {
+          const uint32_t c = cnt[t], b = c % NB;
+          if (c >= NB && !(ok = wait_all(sBar + 8u * (B::kSFree + 2 * t + b), ((c / NB) & 1u) ^ 1u)))
+            break;
+          tc_fence_after();
+          const uint64_t dq = dQ0 + t * (kQBytes >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + kColS, dQ + kstep(kk, kQChunk), dk + kstep(kk, kKVChunk), kIdescS,
-                 kk > 0 ? 1u : 0u);
-        mma_commit(sBar + 8u * B::kSFull);
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + 256u * t + b * BN, dq + kstep(kk, kQChunk), dk + kstep(kk, kKVChunk),
+                   kIdescS, kk > 0 ? 1u : 0u);
+          mma_commit(sBar + 8u * (B::kSFull + 2 * t + b));
+          ++cnt[t];
+        }
+        if (!ok) break;
         mma_commit(sBar + 8u * (B::kKEmpty + s));
         // The second product of a tile goes after the next tile's first, so
         // that the tensor core works on S(j) while the softmax is at S(j - 1).
-        if (j > 0 && !(ok = issue_pv(it - 1u, j == 1))) break;
+        if (j > 0 && !(ok = issue_pv(it - 1u, nt, 2u, j == 1))) break;
       }
-      if (!ok) break;
-      if (!(ok = issue_pv(it - 1u, n == 1))) break;
-      ++pc;
-      u = un;
-      more = more_n;
+      if (ok) ok = issue_pv(it - 1u, nt, 1u, n == 1);
     }
     mma_commit(sBar + 8u * B::kDrain);  // completes when every product issued is done
     wait_drain(sBar + 8u * B::kDrain, 0u, tmo);
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 8) {
     // -------------------------------------------------------------- K and V
-    constexpr int kCpr = D * kEsz / 16;                          // 16-byte loads per key
-    constexpr int kStep = kCtLoaders / kCpr;                     // keys a round of all threads
-    constexpr int kLoads = (BN + kStep - 1) / kStep;             // of a thread, K or V
-    static_assert(kCtLoaders % kCpr == 0, "a thread keeps its place in a key");
-    // The thread loads 16 bytes, at place q, of keys j0, j0 + kStep, ..
-    const int lt = tid - 128, q = lt % kCpr, j0 = lt / kCpr;
+    constexpr int kCpr = D * kEsz / 16;          // 16-byte pieces of a key
+    constexpr int kStep = kCtLoaders / kCpr;     // keys a round of all threads
+    constexpr int kLoads = BN / kStep;           // pieces of a thread, K or V
+    static_assert(kCtLoaders % kCpr == 0 && BN % kStep == 0, "whole rounds");
+    // The thread copies 16 bytes, at place q, of keys j0, j0 + kStep, ..
+    const int lt = tid - 256, q = lt % kCpr, j0 = lt / kCpr;
     const long long tok_bytes = (long long)p.Hkv * D * kEsz;
-    int row[kLoads];  // pool rows of the tile's keys, -1 for a key no row sees
     int4 d0 = {}, d1 = {}, d2 = {};
     uint32_t pi = 0, it = 0;
     bool ok = true;
-    auto places = [&](int n0) {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int key = n0 + j0 + i * kStep;
-        row[i] = -1;
-        if (j0 + i * kStep < BN && key < d1.y && (p.window == 0 || key > d0.w - p.window)) {
-          const int kp = p.div_page.div(key);
-          int pg = __ldg(p.indices + d2.z + kp);
-          if ((unsigned)pg >= (unsigned)p.num_pages) {
-            atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
-            pg = 0;
-          }
-          row[i] = pg * p.page_size + (key - kp * p.page_size);  // the pool has < 2^31 rows
-        }
-      }
-    };
-    // 16-byte unit c of key row j goes to unit c ^ (j & 7) of its 128-byte row.
-    auto unit_at = [&](uint32_t base, int j, int unit) {
-      return base + (uint32_t)(unit >> 3) * kKVChunk + (uint32_t)j * 128u +
-             (uint32_t)(((unit & 7) ^ (j & 7)) << 4);
-    };
-    auto slot_free = [&](uint32_t i, bool is_v) {
-      return wait_all(sBar + 8u * ((is_v ? B::kVEmpty : B::kKEmpty) + (i & 1u)),
-                      ((i >> 1) & 1u) ^ 1u);
-    };
     // The next tile: the piece's, or the next piece's first.
     int left = 0, n0 = 0;
     auto next_tile = [&]() -> bool {
@@ -301,79 +303,117 @@ __global__ void __launch_bounds__(kCtThreads, 2)
         n0 += BN;
       }
       --left;
-      places(n0);
       return true;
+    };
+    // Pool row of the tile's key j, -1 for a key no row sees.
+    auto place = [&](int j) -> int {
+      const int key = n0 + j;
+      if (key >= d1.y || (p.window > 0 && key <= d0.w - p.window)) return -1;
+      const int kp = p.div_page.div(key);
+      int pg = __ldg(p.indices + d2.z + kp);
+      if ((unsigned)pg >= (unsigned)p.num_pages) {
+        atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
+        pg = 0;
+      }
+      return pg * p.page_size + (key - kp * p.page_size);  // the pool has < 2^31 rows
+    };
+    // 16-byte unit c of key row j goes to unit c ^ (j & 7) of its 128-byte row.
+    auto unit_at = [&](uint32_t base, int j, int unit) {
+      return base + (uint32_t)(unit >> 3) * kKVChunk + (uint32_t)j * 128u +
+             (uint32_t)(((unit & 7) ^ (j & 7)) << 4);
+    };
+    // Asynchronous copies; a source size of 0 fills with zeros.
+    auto copy16 = [](uint32_t dst, const uint8_t* src, bool live) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                   "r"(live ? 16u : 0u)
+                   : "memory");
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    auto slot_free = [&](uint32_t i, bool is_v) {
+      return wait_all(sBar + 8u * ((is_v ? B::kVEmpty : B::kKEmpty) + i % NS),
+                      ((i / NS) & 1u) ^ 1u);
     };
 
     if constexpr (C8) {
-      // The next half tile (K or V) is loaded, in registers of its own, while
-      // this one is widened and stored.  One copy of the code serves both
-      // kinds: the loops of all roles have to stay in the instruction cache
-      // together.
-      struct Half {
-        uint4 raw[kLoads];
-        uint32_t sc[kLoads];  // the keys' scale bytes, 0 for a key no row sees
-      } cur, nxt;
-      auto fetch = [&](Half& h, bool is_v) {
-        const uint8_t* src = (is_v ? p.v_pages : p.k_pages) + (long long)d1.w * D + 16 * q;
-        const uint8_t* scales = (is_v ? p.v_scales : p.k_scales) + d1.w;
+      // Raw tile i to ring place i % kCtRaw: the thread's own pieces, and by
+      // the threads at place 0 the aligned word around the key's scale byte and
+      // the byte's shift within it.
+      uint32_t issued = 0;
+      auto issue = [&]() -> bool {
+        if (!next_tile()) return false;
+        const uint32_t at = sRaw + issued % kCtRaw * (2u * ct_raw_half(D));
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          h.raw[i] = make_uint4(0u, 0u, 0u, 0u);
-          h.sc[i] = 0u;
-          if (row[i] >= 0) {
-            h.raw[i] = __ldg(reinterpret_cast<const uint4*>(src + row[i] * tok_bytes));
-            h.sc[i] = __ldg(scales + (long long)row[i] * p.Hkv);
+          const int j = j0 + i * kStep, row = place(j);
+          const bool live = row >= 0;
+          const long long off = (long long)(live ? row : 0) * tok_bytes + d1.w * D + 16 * q;
+          copy16(at + (uint32_t)(j * D + 16 * q), p.k_pages + off, live);
+          copy16(at + ct_raw_half(D) + (uint32_t)(j * D + 16 * q), p.v_pages + off, live);
+          if (q == 0) {
+            const long long so = (long long)(live ? row : 0) * p.Hkv + d1.w;
+            const uint32_t sa = at + (uint32_t)(BN * D + 8 * j);
+            const uint32_t shift = 8u * (uint32_t)(so & 3);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sa),
+                         "l"(p.k_scales + (so & ~3ll)), "r"(live ? 4u : 0u)
+                         : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sa + ct_raw_half(D)),
+                         "l"(p.v_scales + (so & ~3ll)), "r"(live ? 4u : 0u)
+                         : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sa + 4u), "r"(shift) : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sa + ct_raw_half(D) + 4u), "r"(shift)
+                         : "memory");
           }
         }
+        ++issued;
+        return true;
       };
-      // Largest and smallest scale byte of the tile's keys, over the three
-      // warps: each puts its own into one of two sets of words in turn.
       uint32_t turn = 0;
-      auto span = [&](const Half& h, int& top, int& low) {
-        int hi = 0, lo = 255;
+      auto widen = [&](bool is_v) {
+        const uint32_t s = it % NS;
+        const uint32_t base = (is_v ? sV : sK) + s * kKVBytes;
+        const uint32_t at = sRaw + it % kCtRaw * (2u * ct_raw_half(D)) + (is_v ? ct_raw_half(D) : 0u);
+        // Scale bytes of the thread's keys, 0 for a key no row sees; the
+        // largest and smallest of the tile over the four warps, each of which
+        // puts its own into one of two sets of words in turn.
+        int sc[kLoads], top = 0, low = 255;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-          hi = max(hi, (int)h.sc[i]);
-          if (h.sc[i] != 0u) lo = min(lo, (int)h.sc[i]);
+          const uint2 w = lds64(at + (uint32_t)(BN * D + 8 * (j0 + i * kStep)));
+          sc[i] = (int)((w.x >> w.y) & 255u);
+          top = max(top, sc[i]);
+          if (sc[i] != 0) low = min(low, sc[i]);
         }
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        int* red = s_red + 6 * (turn++ & 1u);
+        top = __reduce_max_sync(0xffffffffu, top);
+        low = __reduce_min_sync(0xffffffffu, low);
+        int* red = s_red + 8 * (turn++ & 1u);
         if (lane == 0) {
-          red[2 * (warp - 4)] = hi;
-          red[2 * (warp - 4) + 1] = lo;
+          red[warp - 8] = top;
+          red[warp - 4] = low;
         }
         named_bar_sync(1u, kCtLoaders);
-        top = max(max(red[0], red[2]), red[4]);
-        low = min(min(red[1], red[3]), red[5]);
-      };
-      auto store = [&](const Half& h, bool is_v) {
-        const uint32_t s = it & 1u;
-        const uint32_t base = (is_v ? sV : sK) + s * kKVBytes;
-        int top, low;
-        span(h, top, low);
-        const bool apart = is_v && top - low > 22;  // exponents per key
+        top = max(max(red[0], red[1]), max(red[2], red[3]));
+        low = min(min(red[4], red[5]), min(red[6], red[7]));
+        const bool apart = is_v && top - low > 22;        // exponents per key
         const int x = apart ? 0 : max(top, 8) - 127 - 7;  // the tile's exponent, >= -126
         if (lt == 0) {
           if (is_v) {
-            s_exp[it & 3u].y = x;
-            s_exp[it & 3u].z = apart ? 1 : 0;
+            s_exp[it & 7u].y = x;
+            s_exp[it & 7u].z = apart ? 1 : 0;
           } else {
-            s_exp[it & 3u].x = x;
+            s_exp[it & 7u].x = x;
           }
         }
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
           const int j = j0 + i * kStep;
-          if (BN % kStep != 0 && j >= BN) break;
+          const uint4 raw = lds128(at + (uint32_t)(j * D + 16 * q));
           uint32_t y[8];
-          e4m3x4_f16(h.raw[i].x, y[0], y[1]);
-          e4m3x4_f16(h.raw[i].y, y[2], y[3]);
-          e4m3x4_f16(h.raw[i].z, y[4], y[5]);
-          e4m3x4_f16(h.raw[i].w, y[6], y[7]);
+          e4m3x4_f16(raw.x, y[0], y[1]);
+          e4m3x4_f16(raw.y, y[2], y[3]);
+          e4m3x4_f16(raw.z, y[4], y[5]);
+          e4m3x4_f16(raw.w, y[6], y[7]);
           // 2^(e - x) as an f16 pair: at most 2^7, zero below 2^-24.
-          const int e = apart ? 0 : max((int)h.sc[i] - 127 - x, -40);
+          const int e = apart ? 0 : max(sc[i] - 127 - x, -40);
           const float f = __int_as_float((127 + e) << 23);
           const uint32_t f2h = pack2<false>(f, f);
 #pragma unroll
@@ -381,66 +421,63 @@ __global__ void __launch_bounds__(kCtThreads, 2)
             asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[k]) : "r"(y[k]), "r"(f2h));
           st_shared_v4(unit_at(base, j, 2 * q), y[0], y[1], y[2], y[3]);
           st_shared_v4(unit_at(base, j, 2 * q + 1), y[4], y[5], y[6], y[7]);
-          if (apart && q == 0) {
-            s_we[s * BN + j] = h.sc[i] ? (float)((int)h.sc[i] - 127) : 0.f;
-            s_wi[s * BN + j] = __uint_as_float((254u - h.sc[i]) << 23);
+          if (__builtin_expect(apart, 0) && q == 0) {
+            s_we[s * BN + j] = sc[i] ? (float)(sc[i] - 127) : 0.f;
+            s_wi[s * BN + j] = __uint_as_float((uint32_t)(254 - sc[i]) << 23);
           }
         }
         fence_proxy_async_smem();
         mbar_arrive(sBar + 8u * ((is_v ? B::kVFull : B::kKFull) + s));
       };
-      bool have = next_tile(), v_next = false;
+      // kCtRaw - 1 tiles ahead; every turn commits a group, empty at the end.
+      bool more = true;
 #pragma unroll 1
-      for (bool first = true;; first = false) {
-        const bool v_now = !v_next;  // of the half in `nxt` until now
-        if (!first) cur = nxt;
-        if (have) fetch(nxt, v_next);
-        if (!first) {
-          if (!slot_free(it, v_now)) break;
-          store(cur, v_now);
-          if (v_now) ++it;
-        }
-        if (!have) break;
-        if (v_next) have = next_tile();
-        v_next = !v_next;
+      for (int i = 0; i < kCtRaw - 1; ++i) {
+        if (more) more = issue();
+        commit();
       }
+#pragma unroll 1
+      for (; ok; ++it) {
+        if (more) more = issue();
+        commit();
+        if (it >= issued) break;  // no tile left
+        asm volatile("cp.async.wait_group %0;" ::"n"(kCtRaw - 1) : "memory");
+        __syncwarp();  // the scale words were copied by other lanes of the warp
+        if (!(ok = slot_free(it, false))) break;
+        widen(false);
+        if (!(ok = slot_free(it, true))) break;
+        widen(true);
+        __syncwarp();  // before the ring place is filled again
+      }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else {
-      // Straight to shared memory; two halves (K or V) stay in flight.
-      auto issue = [&](uint32_t i2, bool is_v) {
-        const uint8_t* src =
-            (is_v ? p.v_pages : p.k_pages) + (long long)d1.w * (D * kEsz) + 16 * q;
-        const uint32_t base = (is_v ? sV : sK) + (i2 & 1u) * kKVBytes;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int j = j0 + i * kStep;
-          if (BN % kStep != 0 && j >= BN) break;
-          const uint8_t* g = src + (row[i] >= 0 ? row[i] : 0) * tok_bytes;
-          // Source size 0 fills with zeros.
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(unit_at(base, j, q)),
-                       "l"(g), "r"(row[i] >= 0 ? 16u : 0u)
-                       : "memory");
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-      };
+      // Straight to the products' slots; two halves (K or V) stay in flight.
       // Half h (2 t: K of tile t, 2 t + 1: V) has landed.
       auto landed = [&](uint32_t h) {
         fence_proxy_async_smem();
-        mbar_arrive(sBar + 8u * (((h & 1u) ? B::kVFull : B::kKFull) + ((h >> 1) & 1u)));
+        mbar_arrive(sBar + 8u * (((h & 1u) ? B::kVFull : B::kKFull) + (h >> 1) % NS));
       };
       uint32_t h = 0;  // halves issued
       while (next_tile()) {
-        if (!slot_free(it, false)) break;
-        issue(it, false);
-        if (++h > 2u) {
-          asm volatile("cp.async.wait_group 2;" ::: "memory");
-          landed(h - 3u);
+        int row[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) row[i] = place(j0 + i * kStep);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          if (!(ok = slot_free(it, kv != 0))) break;
+          const uint8_t* src = (kv ? p.v_pages : p.k_pages) + (long long)d1.w * (D * kEsz) + 16 * q;
+          const uint32_t base = (kv ? sV : sK) + it % NS * kKVBytes;
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i)
+            copy16(unit_at(base, j0 + i * kStep, q), src + (row[i] >= 0 ? row[i] : 0) * tok_bytes,
+                   row[i] >= 0);
+          commit();
+          if (++h > 2u) {
+            asm volatile("cp.async.wait_group 2;" ::: "memory");
+            landed(h - 3u);
+          }
         }
-        if (!slot_free(it, true)) break;
-        issue(it, true);
-        if (++h > 2u) {
-          asm volatile("cp.async.wait_group 2;" ::: "memory");
-          landed(h - 3u);
-        }
+        if (!ok) break;
         ++it;
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -448,15 +485,20 @@ __global__ void __launch_bounds__(kCtThreads, 2)
     }
   } else {
     // -------------------------------------------------------------- softmax, output
-    const int r = tid;  // row of the tile, lane of the tensor memory
-    const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
+    const int t = warp >> 2;    // row tile
+    const int r = tid & 127;    // its row, lane of the tensor memory
+    const uint32_t t_lane = tmem + 256u * t + ((uint32_t)((warp & 3) * 32) << 16);
     int4 d0 = {}, d1 = {}, d2 = {};
-    uint32_t pi = 0, it = 0;
+    uint32_t pi = 0, it = 0, c = 0;  // tiles of the CTA, and of this row tile
     bool ok = true;
     while (next_piece(pi++, d0, d1, d2, ok)) {
       const int n = d0.x, P = d0.w, E = d1.x, head = d1.w, cu0 = d2.x;
       const bool cut = (d0.y & 1) != 0;
-      const int gr = d1.z + r;  // row of the sequence
+      if (d1.z + 128 * t >= E * p.G) {  // no rows in this tile
+        it += n;
+        continue;
+      }
+      const int gr = d1.z + 128 * t + r;  // row of the sequence
       const int i = p.div_g.div(gr);
       const bool on = i < E;
       const int qh = head * p.G + (gr - i * p.G);
@@ -473,15 +515,15 @@ __global__ void __launch_bounds__(kCtThreads, 2)
         const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + row * D);
         uint4 w[D / 8];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) w[c] = on ? __ldg(q + c) : make_uint4(0u, 0u, 0u, 0u);
+        for (int k8 = 0; k8 < D / 8; ++k8) w[k8] = on ? __ldg(q + k8) : make_uint4(0u, 0u, 0u, 0u);
         float f = 1.f;
         if constexpr (C8) {
           // f16 operands: the row scaled by the power of two that brings its
           // largest magnitude into [1, 2); smaller values round at 2^-25.
           float amax = 0.f;
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+          for (int k8 = 0; k8 < D / 8; ++k8) {
+            const uint32_t x[4] = {w[k8].x, w[k8].y, w[k8].z, w[k8].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               amax = max3(amax, fabsf(unpack_lo<BF16>(x[k])), fabsf(unpack_hi<BF16>(x[k])));
@@ -491,57 +533,61 @@ __global__ void __launch_bounds__(kCtThreads, 2)
           rs *= __int_as_float((127 + e) << 23);
         }
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+        for (int k8 = 0; k8 < D / 8; ++k8) {
+          uint32_t x[4] = {w[k8].x, w[k8].y, w[k8].z, w[k8].w};
           if constexpr (C8) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               x[k] = pack2<false>(unpack_lo<BF16>(x[k]) * f, unpack_hi<BF16>(x[k]) * f);
           }
-          st_shared_v4(sQ + (uint32_t)(c >> 3) * kQChunk + (uint32_t)r * 128u +
-                           (uint32_t)(((c & 7) ^ (r & 7)) << 4),
+          st_shared_v4(sQ + t * kQBytes + (uint32_t)(k8 >> 3) * kQChunk + (uint32_t)r * 128u +
+                           (uint32_t)(((k8 & 7) ^ (r & 7)) << 4),
                        x[0], x[1], x[2], x[3]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(sBar + 8u * B::kQFull);
+        mbar_arrive(sBar + 8u * (B::kQFull + t));
       }
 
       float M = -1e30f, L = 0.f;
-      for (int j = 0; j < n; ++j, ++it) {
+      for (int j = 0; j < n; ++j, ++it, ++c) {
         const int n0 = d0.z + j * BN;
-        const uint32_t s = it & 1u;
+        const uint32_t s = it % NS, b = c % NB, tb = 2 * t + b;
         // This tile's factor of the scores, and V's exponent.
         float rk = rs, ve = 0.f, vi = 1.f;
         bool apart = false;
         if constexpr (C8) {
           // The loaders' writes are visible after their own barriers.
-          if (!(ok = wait_all(sBar + 8u * (B::kKFull + s), (it >> 1) & 1u))) break;
-          if (!(ok = wait_all(sBar + 8u * (B::kVFull + s), (it >> 1) & 1u))) break;
-          const int4 x = s_exp[it & 3u];
+          if (!(ok = wait_all(sBar + 8u * (B::kKFull + s), (it / NS) & 1u))) break;
+          if (!(ok = wait_all(sBar + 8u * (B::kVFull + s), (it / NS) & 1u))) break;
+          const int4 x = s_exp[it & 7u];
           rk = fmaxf(rs * __int_as_float((127 + x.x) << 23), 1e-37f);
           ve = (float)x.y;
           vi = __int_as_float((127 - x.y) << 23);
           apart = x.z != 0;
         }
-        if (!(ok = wait_all(sBar + 8u * B::kSFull, it & 1u))) break;
+        if (!(ok = wait_all(sBar + 8u * (B::kSFull + tb), (c / NB) & 1u))) break;
         tc_fence_after();
-        const bool edge = n0 + BN > P || p.window > 0 || !on;
+        const bool edge = n0 + BN > P || p.window > 0;
+        const uint32_t col_s = t_lane + b * BN, col_p = t_lane + kColP + b * (BN / 2);
         float alpha = 1.f, sum = 0.f;  // this tile's moves of the reference, its sum of P
-        // Rolled: the unrolled loop and the loaders' did not fit the
-        // instruction cache together (half the stalls).
-#pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) {
-          uint32_t sr[32];
-          float mx = tmem_ld32_max(t_lane + kColS + 32 * c, sr);
+        uint32_t x[2][32];
+        float top[2];
+        top[0] = tmem_ld32_max(col_s, x[0]);
+#pragma unroll
+        for (int h = 0; h < BN / 32; ++h) {
+          uint32_t(&sr)[32] = x[h & 1];
           tmem_wait_ld();
-          if (c == BN / 32 - 1) {
+          if (h + 1 < BN / 32) {  // the next 32 scores come meanwhile
+            top[(h + 1) & 1] = tmem_ld32_max(col_s + 32 * (h + 1), x[(h + 1) & 1]);
+          } else {
             tc_fence_before();
-            mbar_arrive(sBar + 8u * B::kSFree);  // the next tile's scores may come
+            mbar_arrive(sBar + 8u * (B::kSFree + tb));  // the buffer's next scores may come
           }
+          float mx = top[h & 1];
           if (__builtin_expect(edge || apart, 0)) {
             if (edge) {  // keys this row keeps, one bit each
               const uint32_t keep =
-                  keep_bits(p, on, i, dep, n0 + 32 * c - P, E, cu0, (long long)d2.y);
+                  keep_bits(p, on, i, dep, n0 + 32 * h - P, E, cu0, (long long)d2.y);
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if (!(keep >> k & 1u)) sr[k] = 0xFF800000u;  // -inf
@@ -551,8 +597,8 @@ __global__ void __launch_bounds__(kCtThreads, 2)
             for (int k = 0; k < 32; k += 2) {
               float a = __uint_as_float(sr[k]), b = __uint_as_float(sr[k + 1]);
               if (apart) {  // the whole exponent here, a key's own part of it included
-                a = fmaf(a, rk, s_we[s * BN + 32 * c + k]);
-                b = fmaf(b, rk, s_we[s * BN + 32 * c + k + 1]);
+                a = fmaf(a, rk, s_we[s * BN + 32 * h + k]);
+                b = fmaf(b, rk, s_we[s * BN + 32 * h + k + 1]);
                 sr[k] = __float_as_uint(a), sr[k + 1] = __float_as_uint(b);
               }
               mx = max3(mx, a, b);
@@ -560,8 +606,8 @@ __global__ void __launch_bounds__(kCtThreads, 2)
           }
           const float rc = apart ? 1.f : rk;
           mx = fmaf(mx, rc, ve);  // ve is 0 with exponents per key
-          if (c == 0 && it > 0) {  // P of the tile before has been read
-            if (!(ok = wait_all(sBar + 8u * B::kODone, (it - 1u) & 1u))) break;
+          if (h == 0 && c >= NB) {  // the buffer's last P has been read
+            if (!(ok = wait_all(sBar + 8u * (B::kODone + tb), ((c / NB) & 1u) ^ 1u))) break;
             tc_fence_after();
           }
           const bool raise = mx > M + kCaSlack;
@@ -573,14 +619,14 @@ __global__ void __launch_bounds__(kCtThreads, 2)
             alpha *= a;
             tmem_wait_st();
 #pragma unroll 1
-            for (int e = 0; e < c; ++e) {  // this tile's P so far
+            for (int e = 0; e < h; ++e) {  // this tile's P so far
               uint32_t pk[16];
-              tmem_ld16(t_lane + kColP + 16 * e, pk);
+              tmem_ld16(col_p + 16 * e, pk);
               tmem_wait_ld();
 #pragma unroll
               for (int k = 0; k < 16; ++k)
                 pk[k] = pack2<MBF>(unpack_lo<MBF>(pk[k]) * a, unpack_hi<MBF>(pk[k]) * a);
-              tmem_st16(t_lane + kColP + 16 * e, pk);
+              tmem_st16(col_p + 16 * e, pk);
               tmem_wait_st();
             }
           }
@@ -590,54 +636,57 @@ __global__ void __launch_bounds__(kCtThreads, 2)
           uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
-            float a, b, e, f;
-            unf2(ffma2(f2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), rk2, ref2), a, b);
+            float a, a2, e, f;
+            unf2(ffma2(f2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), rk2, ref2), a, a2);
             unf2(ffma2(f2(__uint_as_float(sr[2 * k + 2]), __uint_as_float(sr[2 * k + 3])), rk2, ref2), e, f);
-            a = ex2(a), b = ex2(b), e = ex2(e), f = ex2(f);
-            pk[k] = pack2<MBF>(a, b);
+            a = ex2(a), a2 = ex2(a2), e = ex2(e), f = ex2(f);
+            pk[k] = pack2<MBF>(a, a2);
             pk[k + 1] = pack2<MBF>(e, f);
             if (C8 && __builtin_expect(apart, 0)) {
-              const float* w = s_wi + s * BN + 32 * c + 2 * k;
-              a *= w[0], b *= w[1], e *= w[2], f *= w[3];
+              const float* w = s_wi + s * BN + 32 * h + 2 * k;
+              a *= w[0], a2 *= w[1], e *= w[2], f *= w[3];
             }
-            l0 = fadd2(l0, f2(a, b));
+            l0 = fadd2(l0, f2(a, a2));
             l1 = fadd2(l1, f2(e, f));
           }
-          float a, b;
-          unf2(fadd2(l0, l1), a, b);
-          sum += a + b;
-          tmem_st16(t_lane + kColP + 16 * c, pk);
+          float la, lb;
+          unf2(fadd2(l0, l1), la, lb);
+          sum += la + lb;
+          tmem_st16(col_p + 16 * h, pk);
         }
         if (!ok) break;
         L = fmaf(sum, vi, L);
         if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {  // O so far, its products done
+          if (!(ok = wait_all(sBar + 8u * (B::kODone + 2 * t + (c - 1u) % NB), ((c - 1u) / NB) & 1u)))
+            break;
+          tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int x8 = 0; x8 < D / 32; ++x8) {
             uint32_t o[32];
-            tmem_ld32(t_lane + kColO + c * 32, o);
+            tmem_ld32(t_lane + kColO + x8 * 32, o);
             tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tmem_st32(t_lane + kColO + c * 32, o);
+            tmem_st32(t_lane + kColO + x8 * 32, o);
           }
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(sBar + 8u * B::kPFull);
+        mbar_arrive(sBar + 8u * (B::kPFull + tb));
       }
       if (!ok) break;
-      if (!(ok = wait_all(sBar + 8u * B::kODone, (it - 1u) & 1u))) break;
+      if (!(ok = wait_all(sBar + 8u * (B::kODone + 2 * t + (c - 1u) % NB), ((c - 1u) / NB) & 1u))) break;
       tc_fence_after();
       // ---- the row: a partial, or the result
       if (cut) {
-        const long long pr = (2ll * blockIdx.x + (d0.y >> 1)) * RT + r;
+        const long long pr = (2ll * blockIdx.x + (d0.y >> 1)) * RT + 128 * t + r;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int x8 = 0; x8 < D / 32; ++x8) {
           uint32_t o[32];
-          tmem_ld32(t_lane + kColO + c * 32, o);
+          tmem_ld32(t_lane + kColO + x8 * 32, o);
           tmem_wait_ld();
           if (on) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + pr * D + 32 * c);
+            float4* dst = reinterpret_cast<float4*>(p.part_o + pr * D + 32 * x8);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
@@ -652,13 +701,13 @@ __global__ void __launch_bounds__(kCtThreads, 2)
         const float den = fmaf(L, f, ex2(sink - mm));
         const float inv = any ? f / den : 0.f;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int x8 = 0; x8 < D / 32; ++x8) {
           uint32_t o[32];
-          tmem_ld32(t_lane + kColO + c * 32, o);
+          tmem_ld32(t_lane + kColO + x8 * 32, o);
           tmem_wait_ld();
           if (on) {
             uint4* dst =
-                reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + 32 * c);
+                reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + 32 * x8);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t y[4];
@@ -675,12 +724,12 @@ __global__ void __launch_bounds__(kCtThreads, 2)
       }
     }
   }
-  // The products are done (warp 7 drained them) and every row has been read.
+  // The products are done (warp 12 drained them) and every row has been read.
   tc_fence_before();
   __syncthreads();
-  if (warp == 7) {
+  if (warp == 12) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256u);
+    tmem_dealloc(tmem, 512u);
   }
 }
 

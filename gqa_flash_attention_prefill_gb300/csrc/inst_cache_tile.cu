@@ -1,4 +1,4 @@
-// inst_cache_tile.cu -- gqa_cache_attention's 128-row kernels.
+// inst_cache_tile.cu -- gqa_cache_attention's kernels of 128-row tiles.
 #include "cache_attn.h"
 
 namespace gqa {
@@ -8,8 +8,8 @@ namespace {
 template <int D, bool BF16, bool C8>
 cudaError_t launch_tile(const CacheAttnParams& p, int grid, int mx, int my, cudaStream_t st) {
   static SmemAttr attr{};
-  return launch_with_join<D, BF16, C8>(cache_tile_kernel<D, BF16, C8>, attr, p, 128, grid,
-                                       kCtThreads, ct_smem(D), mx, my, st);
+  return launch_with_join<D, BF16, C8>(cache_tile_kernel<D, BF16, C8>, attr, p, 256, grid,
+                                       kCtThreads, ct_smem(D, C8), mx, my, st);
 }
 
 template <int D>
