@@ -58,7 +58,7 @@ __host__ __device__ constexpr int ca_warps(int D, bool C8, int NT) {
   return NT == 1 && (D == 64 || (D == 128 && C8)) ? 16 : 8;
 }
 constexpr int kCaMaxSlots = 16;                    // ring slots at most
-constexpr int kCaPieces = 4;                       // pieces the producer may be ahead
+constexpr int kCaPieces = 8;                       // pieces the planning warp may be ahead
 constexpr float kCaSlack = 4.f;
 constexpr int kCaWholeSlack = 6;                   // tiles a join is worth
 constexpr float kCaBias = 10.f;                    // f16 probabilities reach 2^(slack + bias)

@@ -11,7 +11,8 @@
 //   0..7   softmax and output: warps 0..3 row tile 0, 4..7 row tile 1, thread =
 //          row = tensor-memory lane; they also bring their rows of Q into
 //          shared memory.  A second tile without rows takes no part;
-//   8..11  bring K and V into the 128-byte swizzle the products read.  16-bit
+//   8..11  bring K (two warps) and V (two) into the 128-byte swizzle the
+//          products read, each warp 32 keys of a tile on its own.  16-bit
 //          pages: cp.async.  e4m3 pages: cp.async of the raw bytes some tiles
 //          ahead, then each thread widens what it copied itself to f16.  Keys
 //          no row sees become zeros;
@@ -43,8 +44,9 @@ __host__ __device__ constexpr int ct_slots(bool C8) { return C8 ? 2 : 4; }
 constexpr int kCtRaw = 4;
 // Tensor-memory buffers of the scores and of the probabilities.
 __host__ __device__ constexpr int ct_buffers(int D) { return D == 64 ? 2 : 1; }
-// A raw half tile: the values, and 8 bytes a key for its scale.
-__host__ __device__ constexpr uint32_t ct_raw_half(int D) { return ct_bn * (D + 8u); }
+// A raw half tile (K or V): the values, and for each of its two warps 8 bytes a
+// key for the scales.
+__host__ __device__ constexpr uint32_t ct_raw_half(int D) { return ct_bn * (D + 16u); }
 __host__ __device__ constexpr uint32_t ct_smem(int D, bool C8) {
   return 1024u + 2u * 128u * D * 2u + 2u * ct_slots(C8) * ct_bn * D * 2u +
          (C8 ? 2u * kCtRaw * ct_raw_half(D) + 2u * ct_slots(C8) * ct_bn * 4u : 0u) + 8u * 16u +
@@ -53,7 +55,9 @@ __host__ __device__ constexpr uint32_t ct_smem(int D, bool C8) {
 
 struct CtBar {  // barrier numbers: 4 a slot, 4 a (row tile, buffer)
   static constexpr int kKFull = 0, kKEmpty = 4, kVFull = 8, kVEmpty = 12, kSFull = 16, kSFree = 20,
-                       kPFull = 24, kODone = 28, kQFull = 32, kDrain = 34, kPiece = 35;
+                       kPFull = 24, kODone = 28, kQFull = 32, kDrain = 34, kPiece = 35,
+                       kExp = kPiece + 2 * kCaPieces;  // 8, one an entry of s_exp
+  static_assert(kExp + 8 <= 64, "barriers");
 };
 
 // Keys x0 .. x0 + 31 (counted from the first new token) that row i of a
@@ -112,8 +116,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   // Per tile, eight deep: K's exponent x, V's, whether V's stand per key.
   int4* s_exp = reinterpret_cast<int4*>(s_wi + (C8 ? NS * BN : 0));
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_exp + 8);
-  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 64);  // [0] abort [1] bad [2] most tiles
-  int* s_red = reinterpret_cast<int*>(misc + 4);            // [3] tmem; the loaders' reductions
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 64);  // [0] abort [1] bad [2] most tiles [3] tmem
   int4* s_piece = reinterpret_cast<int4*>(misc + 32);
   int32_t* tiles = reinterpret_cast<int32_t*>(s_piece + 4 * kCaPieces);
   int32_t* units = tiles + (kMaxSeqs + 1);
@@ -133,8 +136,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     // deep: entry t + 8 is written after the scores of t + 8 - NS are done,
     // which were issued after tile t + 8 - NS - NB, or a later one, was read.
     for (int i = 0; i < NS; ++i) {
-      mbar_init(sBar + 8u * (B::kKFull + i), kCtLoaders);
-      mbar_init(sBar + 8u * (B::kVFull + i), kCtLoaders);
+      mbar_init(sBar + 8u * (B::kKFull + i), kCtLoaders / 2);
+      mbar_init(sBar + 8u * (B::kVFull + i), kCtLoaders / 2);
       mbar_init(sBar + 8u * (B::kKEmpty + i), 1u);
       mbar_init(sBar + 8u * (B::kVEmpty + i), 1u);
     }
@@ -144,6 +147,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       mbar_init(sBar + 8u * (B::kPFull + i), 128u);
       mbar_init(sBar + 8u * (B::kODone + i), 1u);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(sBar + 8u * (B::kExp + i), 1u);
     mbar_init(sBar + 8u * B::kQFull, 128u);
     mbar_init(sBar + 8u * (B::kQFull + 1), 128u);
     mbar_init(sBar + 8u * B::kDrain, 1u);
@@ -225,8 +229,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       return true;
     };
     CaPlan plan = ca_plan(p, tiles, units, s_cu, s_pre, s_ipt, misc);
-    // The other warps hear of up to three pieces beyond the one at work: the
-    // loading warps are that many tiles ahead at most.
+    // The other warps hear of up to seven pieces beyond the one at work, more
+    // than the five tiles (of a piece each, at the least) that the loading
+    // warps look ahead: they never wait for a piece that waits for them.
     uint32_t told = 0;
     bool more = true, ok = true;
     for (uint32_t pc = 0; ok; ++pc) {
@@ -282,18 +287,34 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     __syncwarp();
   } else if (warp >= 8) {
     // -------------------------------------------------------------- K and V
-    constexpr int kCpr = D * kEsz / 16;          // 16-byte pieces of a key
-    constexpr int kStep = kCtLoaders / kCpr;     // keys a round of all threads
-    constexpr int kLoads = BN / kStep;           // pieces of a thread, K or V
-    static_assert(kCtLoaders % kCpr == 0 && BN % kStep == 0, "whole rounds");
-    // The thread copies 16 bytes, at place q, of keys j0, j0 + kStep, ..
-    const int lt = tid - 256, q = lt % kCpr, j0 = lt / kCpr;
+    constexpr int kCpr = D * kEsz / 16;  // 16-byte pieces of a key, and pieces of a lane
+    constexpr int kStep = 32 / kCpr;     // keys a round of the warp's lanes
+    const bool is_v = warp >= 10;
+    const int half = warp & 1;           // keys 32 half .. of a tile
+    const int q = lane % kCpr, k0 = lane / kCpr;  // the lane's place in a key, its first key
     const long long tok_bytes = (long long)p.Hkv * D * kEsz;
+    const uint8_t* const pages = is_v ? p.v_pages : p.k_pages;
+    const uint8_t* const scales = is_v ? p.v_scales : p.k_scales;
+    const uint32_t sT = is_v ? sV : sK;
+    const uint32_t full = sBar + 8u * (is_v ? B::kVFull : B::kKFull);
+    const uint32_t empty = sBar + 8u * (is_v ? B::kVEmpty : B::kKEmpty);
     int4 d0 = {}, d1 = {}, d2 = {};
     uint32_t pi = 0, it = 0;
     bool ok = true;
-    // The next tile: the piece's, or the next piece's first.
     int left = 0, n0 = 0;
+    int r0 = -1, r1 = -1;  // pool rows of the tile's keys lane and lane + 32, -1: no row sees it
+    auto place = [&](int key) -> int {
+      if (key >= d1.y || (p.window > 0 && key <= d0.w - p.window)) return -1;
+      const int kp = p.div_page.div(key);
+      int pg = __ldg(p.indices + d2.z + kp);
+      if ((unsigned)pg >= (unsigned)p.num_pages) {
+        atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
+        pg = 0;
+      }
+      return pg * p.page_size + (key - kp * p.page_size);  // the pool has < 2^31 rows
+    };
+    // The next tile (the piece's, or the next piece's first) and its rows,
+    // whose lookups are under way while the tile before is handled.
     auto next_tile = [&]() -> bool {
       if (left == 0) {
         if (!next_piece(pi++, d0, d1, d2, ok)) return false;
@@ -303,19 +324,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         n0 += BN;
       }
       --left;
+      r0 = place(n0 + lane);
+      r1 = place(n0 + 32 + lane);
       return true;
-    };
-    // Pool row of the tile's key j, -1 for a key no row sees.
-    auto place = [&](int j) -> int {
-      const int key = n0 + j;
-      if (key >= d1.y || (p.window > 0 && key <= d0.w - p.window)) return -1;
-      const int kp = p.div_page.div(key);
-      int pg = __ldg(p.indices + d2.z + kp);
-      if ((unsigned)pg >= (unsigned)p.num_pages) {
-        atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
-        pg = 0;
-      }
-      return pg * p.page_size + (key - kp * p.page_size);  // the pool has < 2^31 rows
     };
     // 16-byte unit c of key row j goes to unit c ^ (j & 7) of its 128-byte row.
     auto unit_at = [&](uint32_t base, int j, int unit) {
@@ -329,159 +340,126 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                    : "memory");
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-    auto slot_free = [&](uint32_t i, bool is_v) {
-      return wait_all(sBar + 8u * ((is_v ? B::kVEmpty : B::kKEmpty) + i % NS),
-                      ((i / NS) & 1u) ^ 1u);
-    };
+    auto slot_free = [&](uint32_t i) { return wait_all(empty + 8u * (i % NS), ((i / NS) & 1u) ^ 1u); };
 
+    bool more = next_tile();
     if constexpr (C8) {
-      // Raw tile i to ring place i % kCtRaw: the thread's own pieces, and by
-      // the threads at place 0 the aligned word around the key's scale byte and
-      // the byte's shift within it.
+      // Raw tile i to ring place i % kCtRaw: the lane's own pieces, and the
+      // aligned word around the scale byte of every key of the tile, with the
+      // byte's shift within it.
       uint32_t issued = 0;
-      auto issue = [&]() -> bool {
-        if (!next_tile()) return false;
-        const uint32_t at = sRaw + issued % kCtRaw * (2u * ct_raw_half(D));
+      const uint32_t ring = sRaw + (is_v ? ct_raw_half(D) : 0u);
+      const uint32_t words = (uint32_t)(BN * D + 8 * (BN * half + lane));  // of this warp
+      auto issue = [&]() {
+        const uint32_t at = ring + issued % kCtRaw * (2u * ct_raw_half(D));
+        const int own = half ? r1 : r0;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int j = j0 + i * kStep, row = place(j);
-          const bool live = row >= 0;
-          const long long off = (long long)(live ? row : 0) * tok_bytes + d1.w * D + 16 * q;
-          copy16(at + (uint32_t)(j * D + 16 * q), p.k_pages + off, live);
-          copy16(at + ct_raw_half(D) + (uint32_t)(j * D + 16 * q), p.v_pages + off, live);
-          if (q == 0) {
-            const long long so = (long long)(live ? row : 0) * p.Hkv + d1.w;
-            const uint32_t sa = at + (uint32_t)(BN * D + 8 * j);
-            const uint32_t shift = 8u * (uint32_t)(so & 3);
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sa),
-                         "l"(p.k_scales + (so & ~3ll)), "r"(live ? 4u : 0u)
-                         : "memory");
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sa + ct_raw_half(D)),
-                         "l"(p.v_scales + (so & ~3ll)), "r"(live ? 4u : 0u)
-                         : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sa + 4u), "r"(shift) : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(sa + ct_raw_half(D) + 4u), "r"(shift)
-                         : "memory");
-          }
+        for (int i = 0; i < kCpr; ++i) {
+          const int k = k0 + i * kStep, row = __shfl_sync(0xffffffffu, own, k);
+          const long long off = (long long)max(row, 0) * tok_bytes + d1.w * D + 16 * q;
+          copy16(at + (uint32_t)((32 * half + k) * D + 16 * q), pages + off, row >= 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = i ? r1 : r0;
+          const long long so = (long long)max(row, 0) * p.Hkv + d1.w;
+          const uint32_t sa = at + words + 256u * i;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sa),
+                       "l"(scales + (so & ~3ll)), "r"(row >= 0 ? 4u : 0u)
+                       : "memory");
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(sa + 4u), "r"(8u * (uint32_t)(so & 3))
+                       : "memory");
         }
         ++issued;
-        return true;
+        more = next_tile();
       };
-      uint32_t turn = 0;
-      auto widen = [&](bool is_v) {
-        const uint32_t s = it % NS;
-        const uint32_t base = (is_v ? sV : sK) + s * kKVBytes;
-        const uint32_t at = sRaw + it % kCtRaw * (2u * ct_raw_half(D)) + (is_v ? ct_raw_half(D) : 0u);
-        // Scale bytes of the thread's keys, 0 for a key no row sees; the
-        // largest and smallest of the tile over the four warps, each of which
-        // puts its own into one of two sets of words in turn.
-        int sc[kLoads], top = 0, low = 255;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const uint2 w = lds64(at + (uint32_t)(BN * D + 8 * (j0 + i * kStep)));
-          sc[i] = (int)((w.x >> w.y) & 255u);
-          top = max(top, sc[i]);
-          if (sc[i] != 0) low = min(low, sc[i]);
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
-        low = __reduce_min_sync(0xffffffffu, low);
-        int* red = s_red + 8 * (turn++ & 1u);
-        if (lane == 0) {
-          red[warp - 8] = top;
-          red[warp - 4] = low;
-        }
-        named_bar_sync(1u, kCtLoaders);
-        top = max(max(red[0], red[1]), max(red[2], red[3]));
-        low = min(min(red[4], red[5]), min(red[6], red[7]));
+      // kCtRaw - 1 tiles ahead; every turn commits a group, empty at the end.
+#pragma unroll 1
+      for (int i = 0; i < kCtRaw - 1; ++i) {
+        if (more) issue();
+        commit();
+      }
+#pragma unroll 1
+      for (; ok; ++it) {
+        if (more) issue();
+        commit();
+        if (it >= issued) break;  // no tile left
+        asm volatile("cp.async.wait_group %0;" ::"n"(kCtRaw - 1) : "memory");
+        if (!(ok = slot_free(it))) break;
+        const uint32_t s = it % NS, base = sT + s * kKVBytes;
+        const uint32_t at = ring + it % kCtRaw * (2u * ct_raw_half(D));
+        // Scale bytes of keys lane and lane + 32, 0 for a key no row sees.
+        const uint2 w0 = lds64(at + words), w1 = lds64(at + words + 256u);
+        const int sc0 = (int)((w0.x >> w0.y) & 255u), sc1 = (int)((w1.x >> w1.y) & 255u);
+        const int top = __reduce_max_sync(0xffffffffu, max(sc0, sc1));
+        const int low =
+            __reduce_min_sync(0xffffffffu, min(sc0 != 0 ? sc0 : 255, sc1 != 0 ? sc1 : 255));
+        const int own = half ? sc1 : sc0;
         const bool apart = is_v && top - low > 22;        // exponents per key
         const int x = apart ? 0 : max(top, 8) - 127 - 7;  // the tile's exponent, >= -126
-        if (lt == 0) {
+        // 2^(e - x) as an f16 pair: at most 2^7, zero below 2^-24.
+        const int e = apart ? 0 : max(own - 127 - x, -40);
+        const float f = __int_as_float((127 + e) << 23);
+        const uint32_t f2h = pack2<false>(f, f);
+        if (half == 0 && lane == 0) {
           if (is_v) {
             s_exp[it & 7u].y = x;
             s_exp[it & 7u].z = apart ? 1 : 0;
           } else {
             s_exp[it & 7u].x = x;
+            mbar_arrive(sBar + 8u * (B::kExp + (it & 7u)));
           }
         }
+        if (__builtin_expect(apart, 0)) {
+          s_we[s * BN + 32 * half + lane] = own != 0 ? (float)(own - 127) : 0.f;
+          s_wi[s * BN + 32 * half + lane] = __uint_as_float((uint32_t)(254 - own) << 23);
+        }
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int j = j0 + i * kStep;
+        for (int i = 0; i < kCpr; ++i) {
+          const int k = k0 + i * kStep, j = 32 * half + k;
           const uint4 raw = lds128(at + (uint32_t)(j * D + 16 * q));
+          const uint32_t m = __shfl_sync(0xffffffffu, f2h, k);
           uint32_t y[8];
           e4m3x4_f16(raw.x, y[0], y[1]);
           e4m3x4_f16(raw.y, y[2], y[3]);
           e4m3x4_f16(raw.z, y[4], y[5]);
           e4m3x4_f16(raw.w, y[6], y[7]);
-          // 2^(e - x) as an f16 pair: at most 2^7, zero below 2^-24.
-          const int e = apart ? 0 : max(sc[i] - 127 - x, -40);
-          const float f = __int_as_float((127 + e) << 23);
-          const uint32_t f2h = pack2<false>(f, f);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[k]) : "r"(y[k]), "r"(f2h));
+          for (int n = 0; n < 8; ++n)
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[n]) : "r"(y[n]), "r"(m));
           st_shared_v4(unit_at(base, j, 2 * q), y[0], y[1], y[2], y[3]);
           st_shared_v4(unit_at(base, j, 2 * q + 1), y[4], y[5], y[6], y[7]);
-          if (__builtin_expect(apart, 0) && q == 0) {
-            s_we[s * BN + j] = sc[i] ? (float)(sc[i] - 127) : 0.f;
-            s_wi[s * BN + j] = __uint_as_float((uint32_t)(254 - sc[i]) << 23);
-          }
         }
         fence_proxy_async_smem();
-        mbar_arrive(sBar + 8u * ((is_v ? B::kVFull : B::kKFull) + s));
-      };
-      // kCtRaw - 1 tiles ahead; every turn commits a group, empty at the end.
-      bool more = true;
-#pragma unroll 1
-      for (int i = 0; i < kCtRaw - 1; ++i) {
-        if (more) more = issue();
-        commit();
-      }
-#pragma unroll 1
-      for (; ok; ++it) {
-        if (more) more = issue();
-        commit();
-        if (it >= issued) break;  // no tile left
-        asm volatile("cp.async.wait_group %0;" ::"n"(kCtRaw - 1) : "memory");
-        __syncwarp();  // the scale words were copied by other lanes of the warp
-        if (!(ok = slot_free(it, false))) break;
-        widen(false);
-        if (!(ok = slot_free(it, true))) break;
-        widen(true);
-        __syncwarp();  // before the ring place is filled again
+        mbar_arrive(full + 8u * s);
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else {
-      // Straight to the products' slots; two halves (K or V) stay in flight.
-      // Half h (2 t: K of tile t, 2 t + 1: V) has landed.
-      auto landed = [&](uint32_t h) {
+      // Straight to the products' slots; two tiles stay in flight.
+      auto landed = [&](uint32_t i) {
         fence_proxy_async_smem();
-        mbar_arrive(sBar + 8u * (((h & 1u) ? B::kVFull : B::kKFull) + (h >> 1) % NS));
+        mbar_arrive(full + 8u * (i % NS));
       };
-      uint32_t h = 0;  // halves issued
-      while (next_tile()) {
-        int row[kLoads];
+      while (more) {
+        if (!slot_free(it)) break;
+        const uint32_t base = sT + it % NS * kKVBytes;
+        const int own = half ? r1 : r0;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) row[i] = place(j0 + i * kStep);
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          if (!(ok = slot_free(it, kv != 0))) break;
-          const uint8_t* src = (kv ? p.v_pages : p.k_pages) + (long long)d1.w * (D * kEsz) + 16 * q;
-          const uint32_t base = (kv ? sV : sK) + it % NS * kKVBytes;
-#pragma unroll
-          for (int i = 0; i < kLoads; ++i)
-            copy16(unit_at(base, j0 + i * kStep, q), src + (row[i] >= 0 ? row[i] : 0) * tok_bytes,
-                   row[i] >= 0);
-          commit();
-          if (++h > 2u) {
-            asm volatile("cp.async.wait_group 2;" ::: "memory");
-            landed(h - 3u);
-          }
+        for (int i = 0; i < kCpr; ++i) {
+          const int k = k0 + i * kStep, row = __shfl_sync(0xffffffffu, own, k);
+          const long long off =
+              (long long)max(row, 0) * tok_bytes + (long long)d1.w * (D * kEsz) + 16 * q;
+          copy16(unit_at(base, 32 * half + k, q), pages + off, row >= 0);
         }
-        if (!ok) break;
-        ++it;
+        commit();
+        if (++it > 2u) {
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+          landed(it - 3u);
+        }
+        more = next_tile();
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
-      for (uint32_t x = h > 2u ? h - 2u : 0u; x < h; ++x) landed(x);
+      for (uint32_t i = it > 2u ? it - 2u : 0u; i < it; ++i) landed(i);
     }
   } else {
     // -------------------------------------------------------------- softmax, output
@@ -556,8 +534,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         float rk = rs, ve = 0.f, vi = 1.f;
         bool apart = false;
         if constexpr (C8) {
-          // The loaders' writes are visible after their own barriers.
-          if (!(ok = wait_all(sBar + 8u * (B::kKFull + s), (it / NS) & 1u))) break;
+          // The loaders' writes are visible after their own barriers.  K's
+          // slot may be two tiles further on by now, so its exponent has a
+          // barrier per entry; V's slot waits for this tile's probabilities.
+          if (!(ok = wait_all(sBar + 8u * (B::kExp + (it & 7u)), (it >> 3) & 1u))) break;
           if (!(ok = wait_all(sBar + 8u * (B::kVFull + s), (it / NS) & 1u))) break;
           const int4 x = s_exp[it & 7u];
           rk = fmaxf(rs * __int_as_float((127 + x.x) << 23), 1e-37f);

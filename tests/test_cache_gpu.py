@@ -354,6 +354,38 @@ def test_long_sequence_is_split_and_joined(pkg, hq, hkv, d, kind):
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("hq,hkv,d,kind,window", [
+    (64, 8, 64, "e4m3", 0), (16, 2, 128, "e4m3", 0), (64, 8, 64, "16", 0), (16, 2, 128, "16", 700), (16, 1, 64, "e4m3", 300)])
+def test_many_rows_over_long_prefixes(pkg, hq, hkv, d, kind, window):
+    """Trees whose rows fill several 128-row tiles (one a little, one half)
+    over prefixes of many key tiles, and a sequence of a single tile."""
+    pre, new = [5000, 3, 2500], [64, 20, 17]
+    b, cache, keep, depths = attention_case(pre, new, hq, hkv, d, 64, kind, "bf16", window, "head", tree=True, seed=12)
+    poison(cache, pre, new)
+    first = check(pkg, b, cache, keep, depths)
+    again = check(pkg, b, cache, keep, depths)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_many_short_sequences_of_many_rows(pkg):
+    """More units of one key tile than CTAs, each with 80 rows."""
+    pre, new = [(5 * i) % 30 for i in range(200)], [10] * 200
+    for kind in ("16", "e4m3"):
+        b, cache, _, _ = attention_case(pre, new, 16, 2, 64, 16, kind, "bf16", 0, "head", seed=13)
+        check(pkg, b, cache)
+
+
+@pytest.mark.parametrize("new", [2, 40])
+def test_value_scales_far_apart_in_a_tile(pkg, new):
+    """V rows 2^40 apart in magnitude within one key tile, K rows as well."""
+    pre = [150, 20]
+    b, cache, _, _ = attention_case(pre, [new, new], 8, 2, 64, 16, "e4m3", "f16", 0, "none", seed=14)
+    gen = torch.Generator().manual_seed(3)
+    cache.v_scales.copy_(torch.randint(95, 136, cache.v_scales.shape, generator=gen).to(torch.uint8))
+    cache.k_scales.copy_(torch.randint(90, 121, cache.k_scales.shape, generator=gen).to(torch.uint8))
+    check(pkg, b, cache)
+
+
 def test_more_sequences_than_one_launch(pkg):
     pre = [(7 * i) % 90 for i in range(1100)]
     b, cache, _, _ = attention_case(pre, [1] * 1100, 4, 2, 64, 16, "e4m3", "bf16", 0, "head", seed=6)
