@@ -79,7 +79,7 @@ int cache_plan(int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hkv, int
   if (pl->tile) {
     pl->HPC = 1;
     pl->KW = 1;
-    pl->T = ct_bn;
+    pl->T = ct_bn(d);
     pl->NS = 2;
     pl->data_bytes = pl->slot_bytes = 0;
     pl->RT = 256;

@@ -7,18 +7,22 @@
 // for e4m3, to widening the keys.  A unit is 256 rows of one KV head, so a key
 // is widened once for two row tiles.
 //
-// A CTA of 13 warps, one per SM:
+// A CTA of 14 warps, one per SM:
 //   0..7   softmax and output: warps 0..3 row tile 0, 4..7 row tile 1, thread =
 //          row = tensor-memory lane; they also bring their rows of Q into
 //          shared memory.  A second tile without rows takes no part;
 //   8..11  bring K (two warps) and V (two) into the 128-byte swizzle the
-//          products read, each warp 32 keys of a tile on its own.  16-bit
+//          products read, each warp half of a tile's keys on its own.  16-bit
 //          pages: cp.async.  e4m3 pages: cp.async of the raw bytes some tiles
 //          ahead, then each thread widens what it copied itself to f16.  Keys
 //          no row sees become zeros;
-//   12     plans the work and issues the products.
-// Where the tensor memory has room (d = 64) scores and probabilities have two
-// buffers: the products of the neighbouring tiles run beside a tile's softmax.
+//   12, 13 issue the products, a warp per row tile; 12 plans the work as well.
+// A round of barriers around the products costs an issuing warp about as much
+// as 64 keys of softmax (one warp for both tiles, 64-key tiles with double-
+// buffered scores: 8 trees of 64 tokens over 8k e4m3 keys 176 us, 146 of them
+// with softmax and widening left out), so a tile takes as many keys as the
+// tensor memory holds beside P and O, and the two row tiles do not wait for
+// each other.
 //
 // Scales of an e4m3 tile.  Widening multiplies a key's values by 2^(e - x)
 // with x 7 below the largest exponent e of the tile, which keeps every value
@@ -36,26 +40,24 @@
 namespace gqa {
 
 constexpr int kCtLoaders = 128;
-constexpr int kCtThreads = 256 + kCtLoaders + 32;
+constexpr int kCtThreads = 256 + kCtLoaders + 64;
 constexpr int kCtWholeSlack = 2;  // tiles a join is worth
-constexpr int ct_bn = 64;         // keys per tile
+__host__ __device__ constexpr int ct_bn(int D) { return D == 64 ? 128 : 64; }  // keys per tile
 // Slots of K and of V ready for the products; raw e4m3 tiles on their way.
 __host__ __device__ constexpr int ct_slots(bool C8) { return C8 ? 2 : 4; }
 constexpr int kCtRaw = 4;
-// Tensor-memory buffers of the scores and of the probabilities.
-__host__ __device__ constexpr int ct_buffers(int D) { return D == 64 ? 2 : 1; }
 // A raw half tile (K or V): the values, and for each of its two warps 8 bytes a
 // key for the scales.
-__host__ __device__ constexpr uint32_t ct_raw_half(int D) { return ct_bn * (D + 16u); }
+__host__ __device__ constexpr uint32_t ct_raw_half(int D) { return (uint32_t)ct_bn(D) * (D + 16u); }
 __host__ __device__ constexpr uint32_t ct_smem(int D, bool C8) {
-  return 1024u + 2u * 128u * D * 2u + 2u * ct_slots(C8) * ct_bn * D * 2u +
-         (C8 ? 2u * kCtRaw * ct_raw_half(D) + 2u * ct_slots(C8) * ct_bn * 4u : 0u) + 8u * 16u +
+  return 1024u + 2u * 128u * D * 2u + 2u * ct_slots(C8) * ct_bn(D) * D * 2u +
+         (C8 ? 2u * kCtRaw * ct_raw_half(D) + 2u * ct_slots(C8) * ct_bn(D) * 4u : 0u) + 8u * 16u +
          64u * 8u + 128u + kCaPieces * 64u + 4u * (5 * kMaxSeqs + 3);
 }
 
-struct CtBar {  // barrier numbers: 4 a slot, 4 a (row tile, buffer)
-  static constexpr int kKFull = 0, kKEmpty = 4, kVFull = 8, kVEmpty = 12, kSFull = 16, kSFree = 20,
-                       kPFull = 24, kODone = 28, kQFull = 32, kDrain = 34, kPiece = 35,
+struct CtBar {  // barrier numbers: 4 for the slots, 2 for the row tiles
+  static constexpr int kKFull = 0, kKEmpty = 4, kVFull = 8, kVEmpty = 12, kSFull = 16, kSFree = 18,
+                       kPFull = 20, kODone = 22, kQFull = 24, kDrain = 26, kPiece = 28,
                        kExp = kPiece + 2 * kCaPieces;  // 8, one an entry of s_exp
   static_assert(kExp + 8 <= 64, "barriers");
 };
@@ -91,13 +93,13 @@ static __device__ __noinline__ uint32_t keep_bits(const CacheAttnParams& p, bool
 template <int D, bool BF16, bool C8>
 __global__ void __launch_bounds__(kCtThreads, 1)
     cache_tile_kernel(const __grid_constant__ CacheAttnParams p) {
-  constexpr int BN = ct_bn, RT = 256, NS = ct_slots(C8), NB = ct_buffers(D);
+  constexpr int BN = ct_bn(D), RT = 256, NS = ct_slots(C8);
   constexpr bool MBF = BF16 && !C8;  // product type
   constexpr float kBias = MBF ? 0.f : kCaBias;
   constexpr int kEsz = C8 ? 1 : 2;
   constexpr uint32_t kQBytes = 128u * D * 2u, kKVBytes = (uint32_t)BN * D * 2u;
   constexpr uint32_t kQChunk = 128u * 128u, kKVChunk = (uint32_t)BN * 128u;
-  constexpr uint32_t kColP = NB * BN, kColO = NB * (BN + BN / 2);  // scores at column 0
+  constexpr uint32_t kColP = BN, kColO = BN + BN / 2;  // scores at column 0
   static_assert(kColO + D <= 256, "two row tiles share the tensor memory");
   constexpr uint32_t kIdescS = idesc_f16(MBF, 128, BN, false);
   constexpr uint32_t kIdescO = idesc_f16(MBF, 128, D, true);
@@ -131,29 +133,28 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 
   // ---------------------------------------------------------------- set-up
   if (tid == 0) {
-    // A slot is free once its products are done.  What the softmax reads of a V
-    // slot it has read before those products start (P is full); s_exp is eight
-    // deep: entry t + 8 is written after the scores of t + 8 - NS are done,
-    // which were issued after tile t + 8 - NS - NB, or a later one, was read.
+    // A slot is free once both row tiles' products are done.  What the softmax
+    // reads of a V slot it has read before those products start (P is full);
+    // s_exp is eight deep: entry t + 8 is written after the scores of t + 8 - NS
+    // are done, which were issued after tile t + 7 - NS was read.
     for (int i = 0; i < NS; ++i) {
       mbar_init(sBar + 8u * (B::kKFull + i), kCtLoaders / 2);
       mbar_init(sBar + 8u * (B::kVFull + i), kCtLoaders / 2);
-      mbar_init(sBar + 8u * (B::kKEmpty + i), 1u);
-      mbar_init(sBar + 8u * (B::kVEmpty + i), 1u);
+      mbar_init(sBar + 8u * (B::kKEmpty + i), 2u);
+      mbar_init(sBar + 8u * (B::kVEmpty + i), 2u);
     }
-    for (int i = 0; i < 4; ++i) {  // row tile i / 2, buffer i % 2
+    for (int i = 0; i < 2; ++i) {
       mbar_init(sBar + 8u * (B::kSFull + i), 1u);
       mbar_init(sBar + 8u * (B::kSFree + i), 128u);
       mbar_init(sBar + 8u * (B::kPFull + i), 128u);
       mbar_init(sBar + 8u * (B::kODone + i), 1u);
+      mbar_init(sBar + 8u * (B::kQFull + i), 128u);
+      mbar_init(sBar + 8u * (B::kDrain + i), 1u);
     }
     for (int i = 0; i < 8; ++i) mbar_init(sBar + 8u * (B::kExp + i), 1u);
-    mbar_init(sBar + 8u * B::kQFull, 128u);
-    mbar_init(sBar + 8u * (B::kQFull + 1), 128u);
-    mbar_init(sBar + 8u * B::kDrain, 1u);
     for (int i = 0; i < kCaPieces; ++i) {
       mbar_init(sPiece + 8u * i, 1u);
-      mbar_init(sPiece + 8u * (kCaPieces + i), 12u);  // 8 softmax and 4 loading warps
+      mbar_init(sPiece + 8u * (kCaPieces + i), 13u);  // 8 softmax, 4 loading, 1 issuing
     }
     misc[0] = 0u;
     misc[1] = 0u;
@@ -199,98 +200,101 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     return d0.x > 0;
   };
 
-  if (warp == 12) {
+  if (warp >= 12) {
     // -------------------------------------------------------------- plan, products
-    const uint64_t dQ0 = smem_desc_sw128(sQ, 16, 1024);
+    const int t = warp - 12;  // row tile
+    const uint64_t dQ = smem_desc_sw128(sQ + t * kQBytes, 16, 1024);
     const uint64_t dK0 = smem_desc_sw128(sK, 16, 1024);
     const uint64_t dV0 = smem_desc_sw128(sV, kKVChunk, 1024);
+    const uint32_t tb = tmem + 256u * t;
     auto kstep = [](int kk, uint32_t chunk) -> uint64_t {
       return (uint64_t)(((uint32_t)(kk >> 2) * chunk + (uint32_t)(kk & 3) * 32u) >> 4);
     };
-    uint32_t it = 0;               // tiles, the slots' count
-    uint32_t cnt[2] = {0u, 0u};    // tiles of each row tile, its buffers' count
-    uint32_t pieces[2] = {0u, 0u};
-    // O += P V of tile i2 for nt row tiles, the tile their last but `back`.
-    auto issue_pv = [&](uint32_t i2, int nt, uint32_t back, bool first) -> bool {
-      const uint32_t s = i2 % NS;
-      if (!wait_all(sBar + 8u * (B::kVFull + s), (i2 / NS) & 1u)) return false;
+    uint32_t it = 0, c = 0, pieces = 0;  // tiles of the CTA, of the row tile; its pieces
+    // O += P V of the tile before tile i2 of the CTA, c2 of the row tile.
+    auto issue_pv = [&](uint32_t i2, uint32_t c2, bool first) -> bool {
+      const uint32_t s = (i2 - 1u) % NS;
+      if (!wait_all(sBar + 8u * (B::kVFull + s), ((i2 - 1u) / NS) & 1u)) return false;
+      if (!wait_all(sBar + 8u * (B::kPFull + t), (c2 - 1u) & 1u)) return false;
+      tc_fence_after();
       const uint64_t dv = dV0 + s * (kKVBytes >> 4);
-      for (int t = 0; t < nt; ++t) {
-        const uint32_t c = cnt[t] - back, b = c % NB, tb = tmem + 256u * t;
-        if (!wait_all(sBar + 8u * (B::kPFull + 2 * t + b), (c / NB) & 1u)) return false;
-        tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(tb + kColO, tb + kColP + b * (BN / 2) + kk * 8, dv + (uint64_t)(kk * 128), kIdescO,
-                 (first && kk == 0) ? 0u : 1u);
-        mma_commit(sBar + 8u * (B::kODone + 2 * t + b));
-      }
+      for (int kk = 0; kk < BN / 16; ++kk)
+        mma_ts(tb + kColO, tb + kColP + kk * 8, dv + (uint64_t)(kk * 128), kIdescO,
+               (first && kk == 0) ? 0u : 1u);
+      mma_commit(sBar + 8u * (B::kODone + t));
       mma_commit(sBar + 8u * (B::kVEmpty + s));
       return true;
     };
-    CaPlan plan = ca_plan(p, tiles, units, s_cu, s_pre, s_ipt, misc);
+    CaPlan plan = {};
+    if (t == 0) plan = ca_plan(p, tiles, units, s_cu, s_pre, s_ipt, misc);
     // The other warps hear of up to seven pieces beyond the one at work, more
     // than the five tiles (of a piece each, at the least) that the loading
     // warps look ahead: they never wait for a piece that waits for them.
     uint32_t told = 0;
     bool more = true, ok = true;
     for (uint32_t pc = 0; ok; ++pc) {
-      while (more && told < pc + kCaPieces) {
-        CaPiece u = {};
-        more = ca_next(p, plan.T, plan.walk, RT, u);
-        const uint32_t ps = told % kCaPieces;
-        if (!(ok = wait_all(sPiece + 8u * (kCaPieces + ps), ((told / kCaPieces) & 1u) ^ 1u))) break;
-        if (lane == 0) {
-          ca_publish(p, plan, u, more, RT, s_piece + 4 * ps);
-          mbar_arrive(sPiece + 8u * ps);
-        }
-        ++told;
-        __syncwarp();
-      }
-      if (!ok) break;
-      const int4 d0 = s_piece[4 * (pc % kCaPieces)], d1 = s_piece[4 * (pc % kCaPieces) + 1];
-      const int n = d0.x;
-      if (n == 0) break;
-      const int nt = d1.x * p.G - d1.z > 128 ? 2 : 1;  // row tiles that hold rows
-      for (int t = 0; t < nt && ok; ++t) {
-        ok = wait_all(sBar + 8u * (B::kQFull + t), pieces[t] & 1u);
-        ++pieces[t];
-      }
-      if (!ok) break;
-      for (int j = 0; j < n; ++j, ++it) {
-        const uint32_t s = it % NS;
-        if (!(ok = wait_all(sBar + 8u * (B::kKFull + s), (it / NS) & 1u))) break;
-        const uint64_t dk = dK0 + s * (kKVBytes >> 4);
-        for (int t = 0; t < nt; ++t) {
-          const uint32_t c = cnt[t], b = c % NB;
-          if (c >= NB && !(ok = wait_all(sBar + 8u * (B::kSFree + 2 * t + b), ((c / NB) & 1u) ^ 1u)))
+      int4 d0, d1, d2;
+      if (t == 0) {
+        while (more && told < pc + kCaPieces) {
+          CaPiece u = {};
+          more = ca_next(p, plan.T, plan.walk, RT, u);
+          const uint32_t ps = told % kCaPieces;
+          if (!(ok = wait_all(sPiece + 8u * (kCaPieces + ps), ((told / kCaPieces) & 1u) ^ 1u)))
             break;
-          tc_fence_after();
-          const uint64_t dq = dQ0 + t * (kQBytes >> 4);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + 256u * t + b * BN, dq + kstep(kk, kQChunk), dk + kstep(kk, kKVChunk),
-                   kIdescS, kk > 0 ? 1u : 0u);
-          mma_commit(sBar + 8u * (B::kSFull + 2 * t + b));
-          ++cnt[t];
+          if (lane == 0) {
+            ca_publish(p, plan, u, more, RT, s_piece + 4 * ps);
+            mbar_arrive(sPiece + 8u * ps);
+          }
+          ++told;
+          __syncwarp();
         }
         if (!ok) break;
-        mma_commit(sBar + 8u * (B::kKEmpty + s));
-        // The second product of a tile goes after the next tile's first, so
-        // that the tensor core works on S(j) while the softmax is at S(j - 1).
-        if (j > 0 && !(ok = issue_pv(it - 1u, nt, 2u, j == 1))) break;
+        d0 = s_piece[4 * (pc % kCaPieces)];
+        d1 = s_piece[4 * (pc % kCaPieces) + 1];
+        if (d0.x == 0) break;
+      } else if (!next_piece(pc, d0, d1, d2, ok)) {
+        break;
       }
-      if (ok) ok = issue_pv(it - 1u, nt, 1u, n == 1);
+      const int n = d0.x;
+      if (d1.z + 128 * t >= d1.x * p.G) {  // no rows in this tile: its share of the slots
+        for (int j = 0; j < n; ++j, ++it) {
+          const uint32_t s = it % NS;
+          if (!(ok = wait_all(sBar + 8u * (B::kKFull + s), (it / NS) & 1u))) break;
+          if (lane == 0) mbar_arrive(sBar + 8u * (B::kKEmpty + s));
+          if (!(ok = wait_all(sBar + 8u * (B::kVFull + s), (it / NS) & 1u))) break;
+          if (lane == 0) mbar_arrive(sBar + 8u * (B::kVEmpty + s));
+        }
+        continue;
+      }
+      if (!(ok = wait_all(sBar + 8u * (B::kQFull + t), pieces & 1u))) break;
+      ++pieces;
+      for (int j = 0; j < n; ++j, ++it, ++c) {
+        const uint32_t s = it % NS;
+        if (!(ok = wait_all(sBar + 8u * (B::kKFull + s), (it / NS) & 1u))) break;
+        if (c > 0 && !(ok = wait_all(sBar + 8u * (B::kSFree + t), (c - 1u) & 1u))) break;
+        tc_fence_after();
+        const uint64_t dk = dK0 + s * (kKVBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(tb, dQ + kstep(kk, kQChunk), dk + kstep(kk, kKVChunk), kIdescS, kk > 0 ? 1u : 0u);
+        mma_commit(sBar + 8u * (B::kSFull + t));
+        mma_commit(sBar + 8u * (B::kKEmpty + s));
+        // The second product of a tile goes after the next tile's first.
+        if (j > 0 && !(ok = issue_pv(it, c, j == 1))) break;
+      }
+      if (ok) ok = issue_pv(it, c, n == 1);
     }
-    mma_commit(sBar + 8u * B::kDrain);  // completes when every product issued is done
-    wait_drain(sBar + 8u * B::kDrain, 0u, tmo);
+    mma_commit(sBar + 8u * (B::kDrain + t));  // completes when every product issued is done
+    wait_drain(sBar + 8u * (B::kDrain + t), 0u, tmo);
     __syncwarp();
   } else if (warp >= 8) {
     // -------------------------------------------------------------- K and V
     constexpr int kCpr = D * kEsz / 16;  // 16-byte pieces of a key, and pieces of a lane
     constexpr int kStep = 32 / kCpr;     // keys a round of the warp's lanes
     const bool is_v = warp >= 10;
-    const int half = warp & 1;           // keys 32 half .. of a tile
+    constexpr int kOwn = BN / 64;        // 32-key groups of a warp, the tile's half
+    const int half = warp & 1;           // keys BN / 2 * half .. of a tile
     const int q = lane % kCpr, k0 = lane / kCpr;  // the lane's place in a key, its first key
     const long long tok_bytes = (long long)p.Hkv * D * kEsz;
     const uint8_t* const pages = is_v ? p.v_pages : p.k_pages;
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     uint32_t pi = 0, it = 0;
     bool ok = true;
     int left = 0, n0 = 0;
-    int r0 = -1, r1 = -1;  // pool rows of the tile's keys lane and lane + 32, -1: no row sees it
+    int row[BN / 32];  // pool rows of the tile's keys lane, lane + 32, .., -1: no row sees it
     auto place = [&](int key) -> int {
       if (key >= d1.y || (p.window > 0 && key <= d0.w - p.window)) return -1;
       const int kp = p.div_page.div(key);
@@ -324,8 +328,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         n0 += BN;
       }
       --left;
-      r0 = place(n0 + lane);
-      r1 = place(n0 + 32 + lane);
+#pragma unroll
+      for (int g = 0; g < BN / 32; ++g) row[g] = place(n0 + 32 * g + lane);
       return true;
     };
     // 16-byte unit c of key row j goes to unit c ^ (j & 7) of its 128-byte row.
@@ -352,20 +356,22 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       const uint32_t words = (uint32_t)(BN * D + 8 * (BN * half + lane));  // of this warp
       auto issue = [&]() {
         const uint32_t at = ring + issued % kCtRaw * (2u * ct_raw_half(D));
-        const int own = half ? r1 : r0;
 #pragma unroll
-        for (int i = 0; i < kCpr; ++i) {
-          const int k = k0 + i * kStep, row = __shfl_sync(0xffffffffu, own, k);
-          const long long off = (long long)max(row, 0) * tok_bytes + d1.w * D + 16 * q;
-          copy16(at + (uint32_t)((32 * half + k) * D + 16 * q), pages + off, row >= 0);
+        for (int g = 0; g < kOwn; ++g) {
+          const int own = half ? row[kOwn + g] : row[g];
+#pragma unroll
+          for (int i = 0; i < kCpr; ++i) {
+            const int k = k0 + i * kStep, r = __shfl_sync(0xffffffffu, own, k);
+            const long long off = (long long)max(r, 0) * tok_bytes + d1.w * D + 16 * q;
+            copy16(at + (uint32_t)((BN / 2 * half + 32 * g + k) * D + 16 * q), pages + off, r >= 0);
+          }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = i ? r1 : r0;
-          const long long so = (long long)max(row, 0) * p.Hkv + d1.w;
-          const uint32_t sa = at + words + 256u * i;
+        for (int g = 0; g < BN / 32; ++g) {
+          const long long so = (long long)max(row[g], 0) * p.Hkv + d1.w;
+          const uint32_t sa = at + words + 256u * g;
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(sa),
-                       "l"(scales + (so & ~3ll)), "r"(row >= 0 ? 4u : 0u)
+                       "l"(scales + (so & ~3ll)), "r"(row[g] >= 0 ? 4u : 0u)
                        : "memory");
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(sa + 4u), "r"(8u * (uint32_t)(so & 3))
                        : "memory");
@@ -388,19 +394,19 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         if (!(ok = slot_free(it))) break;
         const uint32_t s = it % NS, base = sT + s * kKVBytes;
         const uint32_t at = ring + it % kCtRaw * (2u * ct_raw_half(D));
-        // Scale bytes of keys lane and lane + 32, 0 for a key no row sees.
-        const uint2 w0 = lds64(at + words), w1 = lds64(at + words + 256u);
-        const int sc0 = (int)((w0.x >> w0.y) & 255u), sc1 = (int)((w1.x >> w1.y) & 255u);
-        const int top = __reduce_max_sync(0xffffffffu, max(sc0, sc1));
-        const int low =
-            __reduce_min_sync(0xffffffffu, min(sc0 != 0 ? sc0 : 255, sc1 != 0 ? sc1 : 255));
-        const int own = half ? sc1 : sc0;
+        // Scale bytes of keys lane, lane + 32, .., 0 for a key no row sees.
+        int sc[BN / 32], top = 0, low = 255;
+#pragma unroll
+        for (int g = 0; g < BN / 32; ++g) {
+          const uint2 w = lds64(at + words + 256u * g);
+          sc[g] = (int)((w.x >> w.y) & 255u);
+          top = max(top, sc[g]);
+          if (sc[g] != 0) low = min(low, sc[g]);
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        low = __reduce_min_sync(0xffffffffu, low);
         const bool apart = is_v && top - low > 22;        // exponents per key
         const int x = apart ? 0 : max(top, 8) - 127 - 7;  // the tile's exponent, >= -126
-        // 2^(e - x) as an f16 pair: at most 2^7, zero below 2^-24.
-        const int e = apart ? 0 : max(own - 127 - x, -40);
-        const float f = __int_as_float((127 + e) << 23);
-        const uint32_t f2h = pack2<false>(f, f);
         if (half == 0 && lane == 0) {
           if (is_v) {
             s_exp[it & 7u].y = x;
@@ -410,25 +416,36 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             mbar_arrive(sBar + 8u * (B::kExp + (it & 7u)));
           }
         }
-        if (__builtin_expect(apart, 0)) {
-          s_we[s * BN + 32 * half + lane] = own != 0 ? (float)(own - 127) : 0.f;
-          s_wi[s * BN + 32 * half + lane] = __uint_as_float((uint32_t)(254 - own) << 23);
-        }
+#pragma unroll 1
+        for (int g = 0; g < kOwn; ++g) {
+          const int own = half * kOwn + g == 0   ? sc[0]
+                          : half * kOwn + g == 1 ? sc[1]
+                          : half * kOwn + g == 2 ? sc[BN / 32 - 2] : sc[BN / 32 - 1];
+          // 2^(e - x) as an f16 pair: at most 2^7, zero below 2^-24.
+          const int e = apart ? 0 : max(own - 127 - x, -40);
+          const float f = __int_as_float((127 + e) << 23);
+          const uint32_t f2h = pack2<false>(f, f);
+          const int j0 = BN / 2 * half + 32 * g;
+          if (__builtin_expect(apart, 0)) {
+            s_we[s * BN + j0 + lane] = own != 0 ? (float)(own - 127) : 0.f;
+            s_wi[s * BN + j0 + lane] = __uint_as_float((uint32_t)(254 - own) << 23);
+          }
 #pragma unroll
-        for (int i = 0; i < kCpr; ++i) {
-          const int k = k0 + i * kStep, j = 32 * half + k;
-          const uint4 raw = lds128(at + (uint32_t)(j * D + 16 * q));
-          const uint32_t m = __shfl_sync(0xffffffffu, f2h, k);
-          uint32_t y[8];
-          e4m3x4_f16(raw.x, y[0], y[1]);
-          e4m3x4_f16(raw.y, y[2], y[3]);
-          e4m3x4_f16(raw.z, y[4], y[5]);
-          e4m3x4_f16(raw.w, y[6], y[7]);
+          for (int i = 0; i < kCpr; ++i) {
+            const int k = k0 + i * kStep, j = j0 + k;
+            const uint4 raw = lds128(at + (uint32_t)(j * D + 16 * q));
+            const uint32_t m = __shfl_sync(0xffffffffu, f2h, k);
+            uint32_t y[8];
+            e4m3x4_f16(raw.x, y[0], y[1]);
+            e4m3x4_f16(raw.y, y[2], y[3]);
+            e4m3x4_f16(raw.z, y[4], y[5]);
+            e4m3x4_f16(raw.w, y[6], y[7]);
 #pragma unroll
-          for (int n = 0; n < 8; ++n)
-            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[n]) : "r"(y[n]), "r"(m));
-          st_shared_v4(unit_at(base, j, 2 * q), y[0], y[1], y[2], y[3]);
-          st_shared_v4(unit_at(base, j, 2 * q + 1), y[4], y[5], y[6], y[7]);
+            for (int n = 0; n < 8; ++n)
+              asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[n]) : "r"(y[n]), "r"(m));
+            st_shared_v4(unit_at(base, j, 2 * q), y[0], y[1], y[2], y[3]);
+            st_shared_v4(unit_at(base, j, 2 * q + 1), y[4], y[5], y[6], y[7]);
+          }
         }
         fence_proxy_async_smem();
         mbar_arrive(full + 8u * s);
@@ -443,13 +460,16 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       while (more) {
         if (!slot_free(it)) break;
         const uint32_t base = sT + it % NS * kKVBytes;
-        const int own = half ? r1 : r0;
 #pragma unroll
-        for (int i = 0; i < kCpr; ++i) {
-          const int k = k0 + i * kStep, row = __shfl_sync(0xffffffffu, own, k);
-          const long long off =
-              (long long)max(row, 0) * tok_bytes + (long long)d1.w * (D * kEsz) + 16 * q;
-          copy16(unit_at(base, 32 * half + k, q), pages + off, row >= 0);
+        for (int g = 0; g < kOwn; ++g) {
+          const int own = half ? row[kOwn + g] : row[g];
+#pragma unroll
+          for (int i = 0; i < kCpr; ++i) {
+            const int k = k0 + i * kStep, r = __shfl_sync(0xffffffffu, own, k);
+            const long long off =
+                (long long)max(r, 0) * tok_bytes + (long long)d1.w * (D * kEsz) + 16 * q;
+            copy16(unit_at(base, BN / 2 * half + 32 * g + k, q), pages + off, r >= 0);
+          }
         }
         commit();
         if (++it > 2u) {
@@ -529,7 +549,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       float M = -1e30f, L = 0.f;
       for (int j = 0; j < n; ++j, ++it, ++c) {
         const int n0 = d0.z + j * BN;
-        const uint32_t s = it % NS, b = c % NB, tb = 2 * t + b;
+        const uint32_t s = it % NS;
         // This tile's factor of the scores, and V's exponent.
         float rk = rs, ve = 0.f, vi = 1.f;
         bool apart = false;
@@ -545,25 +565,30 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           vi = __int_as_float((127 - x.y) << 23);
           apart = x.z != 0;
         }
-        if (!(ok = wait_all(sBar + 8u * (B::kSFull + tb), (c / NB) & 1u))) break;
+        if (!(ok = wait_all(sBar + 8u * (B::kSFull + t), c & 1u))) break;
         tc_fence_after();
         const bool edge = n0 + BN > P || p.window > 0;
-        const uint32_t col_s = t_lane + b * BN, col_p = t_lane + kColP + b * (BN / 2);
+        const uint32_t col_p = t_lane + kColP;
         float alpha = 1.f, sum = 0.f;  // this tile's moves of the reference, its sum of P
+        // Two chunks of 32 keys at a time, the second's scores on their way
+        // during the first; a longer unrolled loop leaves the instruction cache.
+#pragma unroll 1
+        for (int h2 = 0; h2 < BN / 32 && ok; h2 += 2) {
         uint32_t x[2][32];
         float top[2];
-        top[0] = tmem_ld32_max(col_s, x[0]);
+        top[0] = tmem_ld32_max(t_lane + 32 * h2, x[0]);
 #pragma unroll
-        for (int h = 0; h < BN / 32; ++h) {
-          uint32_t(&sr)[32] = x[h & 1];
+        for (int hh = 0; hh < 2; ++hh) {
+          const int h = h2 + hh;
+          uint32_t(&sr)[32] = x[hh];
           tmem_wait_ld();
-          if (h + 1 < BN / 32) {  // the next 32 scores come meanwhile
-            top[(h + 1) & 1] = tmem_ld32_max(col_s + 32 * (h + 1), x[(h + 1) & 1]);
-          } else {
+          if (hh == 0) {
+            top[1] = tmem_ld32_max(t_lane + 32 * (h + 1), x[1]);
+          } else if (h == BN / 32 - 1) {
             tc_fence_before();
-            mbar_arrive(sBar + 8u * (B::kSFree + tb));  // the buffer's next scores may come
+            mbar_arrive(sBar + 8u * (B::kSFree + t));  // the next tile's scores may come
           }
-          float mx = top[h & 1];
+          float mx = top[hh];
           if (__builtin_expect(edge || apart, 0)) {
             if (edge) {  // keys this row keeps, one bit each
               const uint32_t keep =
@@ -586,8 +611,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           }
           const float rc = apart ? 1.f : rk;
           mx = fmaf(mx, rc, ve);  // ve is 0 with exponents per key
-          if (h == 0 && c >= NB) {  // the buffer's last P has been read
-            if (!(ok = wait_all(sBar + 8u * (B::kODone + tb), ((c / NB) & 1u) ^ 1u))) break;
+          if (h == 0 && c > 0) {  // P of the tile before has been read
+            if (!(ok = wait_all(sBar + 8u * (B::kODone + t), (c - 1u) & 1u))) break;
             tc_fence_after();
           }
           const bool raise = mx > M + kCaSlack;
@@ -634,12 +659,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           sum += la + lb;
           tmem_st16(col_p + 16 * h, pk);
         }
+        }
         if (!ok) break;
         L = fmaf(sum, vi, L);
         if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {  // O so far, its products done
-          if (!(ok = wait_all(sBar + 8u * (B::kODone + 2 * t + (c - 1u) % NB), ((c - 1u) / NB) & 1u)))
-            break;
-          tc_fence_after();
 #pragma unroll 1
           for (int x8 = 0; x8 < D / 32; ++x8) {
             uint32_t o[32];
@@ -652,10 +675,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(sBar + 8u * (B::kPFull + tb));
+        mbar_arrive(sBar + 8u * (B::kPFull + t));
       }
       if (!ok) break;
-      if (!(ok = wait_all(sBar + 8u * (B::kODone + 2 * t + (c - 1u) % NB), ((c - 1u) / NB) & 1u))) break;
+      if (!(ok = wait_all(sBar + 8u * (B::kODone + t), (c - 1u) & 1u))) break;
       tc_fence_after();
       // ---- the row: a partial, or the result
       if (cut) {
@@ -704,7 +727,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       }
     }
   }
-  // The products are done (warp 12 drained them) and every row has been read.
+  // The products are done (warps 12 and 13 drained them) and every row has been read.
   tc_fence_before();
   __syncthreads();
   if (warp == 12) {
