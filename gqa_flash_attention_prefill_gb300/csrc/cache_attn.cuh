@@ -5,13 +5,15 @@
 // Mathematics.  One pass over the keys with a running reference per row, in
 // the log2 domain.  With s = scale log2(e) <q, k> and, for an e4m3 cache, the
 // key's value scale 2^w (w = 0 otherwise),
-//   M   >= max (s + w) - kSlack             the row's reference, moved lazily
+//   M   >= max (s + w) - kCaSlack           the row's reference, moved lazily
 //   P_j  = 2^(s_j + w_j - M + kBias)        fp32, rounded once to 16 bits
 //   O    = sum P_j V_j,  L = sum P_j 2^-w_j   (fp32; V_j the stored values)
 //   out  = O / (L + 2^(x - M + kBias)),   lse = (M - kBias + log2(L + ..)) ln 2
 // so the value scales cost no pass of their own and L keeps the unrounded
-// probabilities.  kBias uses f16's range upwards: P reaches 2^14, and keys
-// 2^-38 below the reference still count.
+// probabilities.  A reference moves to kCaHead above the score that made it,
+// so it moves once or twice in a sequence (each move rescales O); kBias uses
+// f16's range upwards: P stays below 2^15, and a key weighs in down to 2^-30 of
+// the largest at the least.
 //
 // Layout.  A page holds page_size tokens x Hkv heads x d values: the K of one
 // token's heads is one run of memory, and so is a page's.  A CTA therefore
@@ -59,9 +61,11 @@ __host__ __device__ constexpr int ca_warps(int D, bool C8, int NT) {
 }
 constexpr int kCaMaxSlots = 16;                    // ring slots at most
 constexpr int kCaPieces = 8;                       // pieces the planning warp may be ahead
-constexpr float kCaSlack = 4.f;
+// In powers of two: what a score may exceed its row's reference by before the
+// reference moves, how far above the score it then moves, and the exponent
+// that a probability at the reference gets.
+constexpr float kCaSlack = 6.f, kCaHead = 4.f, kCaBias = 9.f;
 constexpr int kCaWholeSlack = 6;                   // tiles a join is worth
-constexpr float kCaBias = 10.f;                    // f16 probabilities reach 2^(slack + bias)
 
 // Division of 0 <= n < 2^31 by a divisor fixed for the launch: with l =
 // ceil(log2 d) and m = ceil(2^(32 + l) / d) - 2^32, n / d = (hi(n m) + n) >> l
@@ -811,11 +815,12 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
         for (int m = 0; m < NT; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float mx = M[m][h];
+            float mx = s[m][0][h];
 #pragma unroll
             for (int k = 0; k < GK; ++k) mx = max3(mx, s[m][k][h], s[m][k][2 + h]);
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            mx = mx > M[m][h] + kCaSlack ? mx + kCaHead : M[m][h];
             const float f = ex2(M[m][h] - mx);
             M[m][h] = mx;
             L[m][h] *= f;

@@ -64,7 +64,7 @@ struct CtBar {  // barrier numbers: 4 for the slots, 2 for the row tiles
 
 // Keys x0 .. x0 + 31 (counted from the first new token) that row i of a
 // sequence of E new tokens keeps, one bit each.
-static __device__ __noinline__ uint32_t keep_bits(const CacheAttnParams& p, bool on, int i, int dep,
+__device__ __forceinline__ uint32_t keep_bits(const CacheAttnParams& p, bool on, int i, int dep,
                                            int x0, int E, int cu0, long long mask0) {
   if (!on || x0 > i) return 0u;
   uint32_t keep = i - x0 >= 31 ? ~0u : (2u << (i - x0)) - 1u;
@@ -567,29 +567,72 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
         if (!(ok = wait_all(sBar + 8u * (B::kSFull + t), c & 1u))) break;
         tc_fence_after();
-        const bool edge = n0 + BN > P || p.window > 0;
         const uint32_t col_p = t_lane + kColP;
+        const bool edge = n0 + BN > P || p.window > 0;
         float alpha = 1.f, sum = 0.f;  // this tile's moves of the reference, its sum of P
-        // Two chunks of 32 keys at a time, the second's scores on their way
-        // during the first; a longer unrolled loop leaves the instruction cache.
-#pragma unroll 1
-        for (int h2 = 0; h2 < BN / 32 && ok; h2 += 2) {
-        uint32_t x[2][32];
-        float top[2];
-        top[0] = tmem_ld32_max(t_lane + 32 * h2, x[0]);
+        // Exponents of 32 scores and their sum; the packed pairs go to P.
+        auto exps = [&](const uint32_t(&sr)[32], float scale, float ref, uint32_t(&pk)[16]) {
+          const uint64_t sc2 = f2(scale, scale), ref2 = f2(ref, ref);
+          uint64_t l0 = 0, l1 = 0;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int h = h2 + hh;
-          uint32_t(&sr)[32] = x[hh];
-          tmem_wait_ld();
-          if (hh == 0) {
-            top[1] = tmem_ld32_max(t_lane + 32 * (h + 1), x[1]);
-          } else if (h == BN / 32 - 1) {
-            tc_fence_before();
-            mbar_arrive(sBar + 8u * (B::kSFree + t));  // the next tile's scores may come
+          for (int k = 0; k < 16; k += 2) {
+            float a, a2, e, f;
+            unf2(ffma2(f2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), sc2, ref2), a, a2);
+            unf2(ffma2(f2(__uint_as_float(sr[2 * k + 2]), __uint_as_float(sr[2 * k + 3])), sc2, ref2), e, f);
+            a = ex2(a), a2 = ex2(a2), e = ex2(e), f = ex2(f);
+            pk[k] = pack2<MBF>(a, a2);
+            pk[k + 1] = pack2<MBF>(e, f);
+            l0 = fadd2(l0, f2(a, a2));
+            l1 = fadd2(l1, f2(e, f));
           }
-          float mx = top[hh];
-          if (__builtin_expect(edge || apart, 0)) {
+          float la, lb;
+          unf2(fadd2(l0, l1), la, lb);
+          sum += la + lb;
+        };
+        // P of the tile before has been read.
+        if (c > 0 && !(ok = wait_all(sBar + 8u * (B::kODone + t), (c - 1u) & 1u))) break;
+        tc_fence_after();
+        bool plain = !edge && !apart;
+        if (plain) {
+          // No mask, no exponents per key: the next 32 scores load during these.
+          // A score above the reference ends this form; the tile starts again
+          // in the general one (its scores are still there).  Kept apart, since
+          // the general form's code between the chunks cost 48 of 176 us.
+          uint32_t x[2][32];
+          float top[2];
+          const float ref = ve - M + kBias;
+          top[0] = tmem_ld32_max(t_lane, x[0]);
+#pragma unroll
+          for (int h = 0; h < BN / 32; ++h) {
+            tmem_wait_ld();
+            if (h + 1 < BN / 32)
+              top[(h + 1) & 1] = tmem_ld32_max(t_lane + 32 * (h + 1), x[(h + 1) & 1]);
+            plain = !__any_sync(0xffffffffu, fmaf(top[h & 1], rk, ve) > M + kCaSlack);
+            if (!plain) break;
+            if (h + 1 == BN / 32) {
+              tc_fence_before();
+              mbar_arrive(sBar + 8u * (B::kSFree + t));  // the next tile's scores may come
+            }
+            uint32_t pk[16];
+            exps(x[h & 1], rk, ref, pk);
+            tmem_st16(col_p + 16 * h, pk);
+          }
+          if (!plain) {
+            sum = 0.f;
+            tmem_wait_ld();
+            tmem_wait_st();
+          }
+        }
+        if (!plain) {
+#pragma unroll 1
+          for (int h = 0; h < BN / 32; ++h) {
+            uint32_t sr[32], pk[16];
+            float mx = tmem_ld32_max(t_lane + 32 * h, sr);
+            tmem_wait_ld();
+            if (h + 1 == BN / 32) {
+              tc_fence_before();
+              mbar_arrive(sBar + 8u * (B::kSFree + t));
+            }
             if (edge) {  // keys this row keeps, one bit each
               const uint32_t keep =
                   keep_bits(p, on, i, dep, n0 + 32 * h - P, E, cu0, (long long)d2.y);
@@ -597,70 +640,54 @@ __global__ void __launch_bounds__(kCtThreads, 1)
               for (int k = 0; k < 32; ++k)
                 if (!(keep >> k & 1u)) sr[k] = 0xFF800000u;  // -inf
             }
-            mx = -INFINITY;
+            if (edge || apart) {
+              mx = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float a = __uint_as_float(sr[k]), b = __uint_as_float(sr[k + 1]);
-              if (apart) {  // the whole exponent here, a key's own part of it included
-                a = fmaf(a, rk, s_we[s * BN + 32 * h + k]);
-                b = fmaf(b, rk, s_we[s * BN + 32 * h + k + 1]);
-                sr[k] = __float_as_uint(a), sr[k + 1] = __float_as_uint(b);
+              for (int k = 0; k < 32; ++k) {
+                if (apart)  // the whole exponent here, a key's own part of it included
+                  sr[k] = __float_as_uint(fmaf(__uint_as_float(sr[k]), rk, s_we[s * BN + 32 * h + k]));
+                mx = fmaxf(mx, __uint_as_float(sr[k]));
               }
-              mx = max3(mx, a, b);
             }
-          }
-          const float rc = apart ? 1.f : rk;
-          mx = fmaf(mx, rc, ve);  // ve is 0 with exponents per key
-          if (h == 0 && c > 0) {  // P of the tile before has been read
-            if (!(ok = wait_all(sBar + 8u * (B::kODone + t), (c - 1u) & 1u))) break;
-            tc_fence_after();
-          }
-          const bool raise = mx > M + kCaSlack;
-          if (__any_sync(0xffffffffu, raise)) {  // rare after the first tiles
-            const float a = raise ? ex2(M - mx) : 1.f;
-            if (raise) M = mx;
-            L *= a;
-            sum *= a;
-            alpha *= a;
-            tmem_wait_st();
-#pragma unroll 1
-            for (int e = 0; e < h; ++e) {  // this tile's P so far
-              uint32_t pk[16];
-              tmem_ld16(col_p + 16 * e, pk);
-              tmem_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                pk[k] = pack2<MBF>(unpack_lo<MBF>(pk[k]) * a, unpack_hi<MBF>(pk[k]) * a);
-              tmem_st16(col_p + 16 * e, pk);
+            const float rc = apart ? 1.f : rk;
+            mx = fmaf(mx, rc, ve);  // ve is 0 with exponents per key
+            const bool raise = mx > M + kCaSlack;
+            if (__any_sync(0xffffffffu, raise)) {
+              const float to = raise ? mx + kCaHead : M, a = ex2(M - to);
+              M = to;
+              L *= a;
+              sum *= a;
+              alpha *= a;
               tmem_wait_st();
-            }
-          }
-          const float ref = ve - M + kBias;
-          const uint64_t ref2 = f2(ref, ref), rk2 = f2(rc, rc);
-          uint64_t l0 = 0, l1 = 0;
-          uint32_t pk[16];
+#pragma unroll 1
+              for (int e = 0; e < h; ++e) {  // this tile's P so far
+                tmem_ld16(col_p + 16 * e, pk);
+                tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            float a, a2, e, f;
-            unf2(ffma2(f2(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), rk2, ref2), a, a2);
-            unf2(ffma2(f2(__uint_as_float(sr[2 * k + 2]), __uint_as_float(sr[2 * k + 3])), rk2, ref2), e, f);
-            a = ex2(a), a2 = ex2(a2), e = ex2(e), f = ex2(f);
-            pk[k] = pack2<MBF>(a, a2);
-            pk[k + 1] = pack2<MBF>(e, f);
-            if (C8 && __builtin_expect(apart, 0)) {
-              const float* w = s_wi + s * BN + 32 * h + 2 * k;
-              a *= w[0], a2 *= w[1], e *= w[2], f *= w[3];
+                for (int k = 0; k < 16; ++k)
+                  pk[k] = pack2<MBF>(unpack_lo<MBF>(pk[k]) * a, unpack_hi<MBF>(pk[k]) * a);
+                tmem_st16(col_p + 16 * e, pk);
+                tmem_wait_st();
+              }
             }
-            l0 = fadd2(l0, f2(a, a2));
-            l1 = fadd2(l1, f2(e, f));
+            const float ref = ve - M + kBias;
+            if (apart) {
+              float part = 0.f;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float a = ex2(__uint_as_float(sr[2 * k]) + ref);
+                const float e = ex2(__uint_as_float(sr[2 * k + 1]) + ref);
+                pk[k] = pack2<MBF>(a, e);
+                part = fmaf(a, s_wi[s * BN + 32 * h + 2 * k], part);
+                part = fmaf(e, s_wi[s * BN + 32 * h + 2 * k + 1], part);
+              }
+              sum += part;
+            } else {
+              exps(sr, rc, ref, pk);
+            }
+            tmem_st16(col_p + 16 * h, pk);
           }
-          float la, lb;
-          unf2(fadd2(l0, l1), la, lb);
-          sum += la + lb;
-          tmem_st16(col_p + 16 * h, pk);
         }
-        }
-        if (!ok) break;
         L = fmaf(sum, vi, L);
         if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {  // O so far, its products done
 #pragma unroll 1
