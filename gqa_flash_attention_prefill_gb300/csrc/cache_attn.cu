@@ -195,20 +195,29 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.metadata_ready = metadata_ready_flag() ? 1 : 0;
   // A window bounds a unit's tiles on the host: where whole units dealt out
-  // always cost less than a join (the device's own rule), no join is launched.
-  int merge_x = pl.max_units < 8 * pl.ctas ? pl.max_units : 8 * pl.ctas;
+  // cost less than a join (the device's own rule), no join is launched.  The
+  // hint may be wrong: then whole units are the slower choice, not a wrong one.
+  const int seqs = num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs;
+  const int rows = pl.HPC * pl.RT;
+  const long long new_max = max_seqlen_q > 0 ? max_seqlen_q : total_q;
+  long long units = (long long)pl.HG * seqs * ((new_max * pl.G + pl.RT - 1) / pl.RT);
+  if (units > pl.max_units) units = pl.max_units;
+  bool join = true;
   if (p.window > 0) {
-    const long long new_max = max_seqlen_q > 0 ? max_seqlen_q : total_q;
     const long long n = ((long long)p.window + new_max + pl.T - 3) / pl.T + 1;
-    if ((pl.max_units + pl.ctas - 1) / pl.ctas * n <= p.whole_slack) {
+    if ((units + pl.ctas - 1) / pl.ctas * n <= p.whole_slack) {
       p.whole = 1;
-      merge_x = 0;
+      join = false;
     }
   }
-  const int rows = pl.HPC * pl.RT;
-  int merge_y = merge_x > 0 ? 8 * pl.ctas / merge_x : 1;
-  if (merge_y > rows) merge_y = rows;
-  if (merge_y < 1) merge_y = 1;
+  // Blocks of the join: enough for a warp per row of every unit (at most one
+  // unit is cut per CTA), 16 blocks an SM at most.
+  int merge_x = 0, merge_y = 1;
+  if (join) {
+    merge_x = (int)(units < pl.ctas ? units : pl.ctas);
+    merge_y = 16 * pl.ctas / merge_x;
+    if (merge_y > rows) merge_y = rows;
+  }
   const unsigned smem = ca_fixed_smem(ca_warps(d, c8, pl.NT)) + (unsigned)pl.NS * pl.slot_bytes;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   for (int b0 = 0; b0 < num_seqs; b0 += kMaxSeqs) {

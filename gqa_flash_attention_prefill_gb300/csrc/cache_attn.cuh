@@ -1015,7 +1015,8 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
 //   out = sum O_s 2^(M_s - mf) / (sum L_s 2^(M_s - mf) + 2^(x - mf)).
 // blockIdx.x walks the units, blockIdx.y a unit's rows.  A unit of few pieces
 // takes a warp per row; one of many (a long sequence over all CTAs) the whole
-// block per row, its warps sharing the pieces.
+// block per row, its warps sharing the pieces.  Bound by latency: the loads of
+// 8 pieces go out at once, so a row is two rounds of them.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant__ CacheAttnParams p,
                                                           int RT, float bias) {
@@ -1027,40 +1028,59 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant_
   const int n_units = __ldcg(p.hdr);
   const int rows = p.HPC * RT;
   for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
-    const int32_t* hd = p.hdr + 8 + 8ll * u;
-    const int4 h4 = __ldcg(reinterpret_cast<const int4*>(hd));
+    const int4* hd = reinterpret_cast<const int4*>(p.hdr + 8 + 8ll * u);
+    const int4 h4 = __ldcg(hd), g4 = __ldcg(hd + 1);
     const int np = h4.x + 1;
     if (np == 1) continue;
-    const int c0 = h4.y, r0 = h4.z, h0 = h4.w, cu0 = __ldcg(hd + 4), E = __ldcg(hd + 5);
+    const int c0 = h4.y, r0 = h4.z, h0 = h4.w, cu0 = g4.x, E = g4.y;
     const bool wide = np > 8;  // the whole block per row
     const int step = wide ? gridDim.y : gridDim.y * 8;
     for (int r = wide ? blockIdx.y : blockIdx.y * 8 + warp; r < rows; r += step) {
       const int hl = r / RT, gr = r0 + (r - hl * RT), i = p.div_g.div(gr);
       if (i >= E) continue;
       const int qh = (h0 + hl) * p.G + (gr - i * p.G);
-      const int s0 = wide ? warp : 0, ds = wide ? 8 : 1;
+      float xs = -INFINITY;
+      if (p.sinks != nullptr) xs = __ldg(p.sinks + qh) * kLog2e;
+      else if (p.smooth) xs = 0.f;
+      const int ds = wide ? 8 : 1;
       // Piece s of the unit: slot 2 c + 1 of its first CTA, slot 2 (c + s) after.
-      auto at = [&](int s) { return (2ll * (c0 + s) + (s == 0 ? 1 : 0)) * rows + r; };
-      float mf = -1e30f;
-      for (int s = s0 + lane * ds; s < np; s += 32 * ds)
-        mf = fmaxf(mf, __ldcg(reinterpret_cast<const float2*>(p.part_ml) + at(s)).x);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mf = fmaxf(mf, __shfl_xor_sync(0xffffffffu, mf, o));
-      float acc[D / 32], l = 0.f;
+      float mf = -1e30f, l = 0.f, acc[D / 32];
 #pragma unroll
       for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
-#pragma unroll 4
-      for (int s = s0; s < np; s += ds) {
-        const long long a = at(s);
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + a);
-        const float f = ex2(ml.x - mf);
-        l = fmaf(ml.y, f, l);
+      for (int s0 = wide ? warp : 0; s0 < np; s0 += 8 * ds) {
+        float2 ml[8], v[8][D / 64];
 #pragma unroll
-        for (int k = 0; k < D / 64; ++k) {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part_o + a * D) + 32 * k + lane);
-          acc[2 * k] = fmaf(v.x, f, acc[2 * k]);
-          acc[2 * k + 1] = fmaf(v.y, f, acc[2 * k + 1]);
+        for (int j = 0; j < 8; ++j) {
+          const int s = s0 + j * ds;
+          ml[j] = make_float2(-1e30f, 0.f);
+#pragma unroll
+          for (int k = 0; k < D / 64; ++k) v[j][k] = make_float2(0.f, 0.f);
+          if (s < np) {
+            const long long a = (2ll * (c0 + s) + (s == 0 ? 1 : 0)) * rows + r;
+            ml[j] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + a);
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k)
+              v[j][k] = __ldcg(reinterpret_cast<const float2*>(p.part_o + a * D) + 32 * k + lane);
+          }
         }
+        float m = mf;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, ml[j].x);
+        const float f0 = ex2(mf - m);
+        l *= f0;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) acc[k] *= f0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float f = ex2(ml[j].x - m);
+          l = fmaf(ml[j].y, f, l);
+#pragma unroll
+          for (int k = 0; k < D / 64; ++k) {
+            acc[2 * k] = fmaf(v[j][k].x, f, acc[2 * k]);
+            acc[2 * k + 1] = fmaf(v[j][k].y, f, acc[2 * k + 1]);
+          }
+        }
+        mf = m;
       }
       if (wide) {
         __syncthreads();
@@ -1086,9 +1106,6 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant_
           }
         }
       }
-      float xs = -INFINITY;
-      if (p.sinks != nullptr) xs = __ldg(p.sinks + qh) * kLog2e;
-      else if (p.smooth) xs = 0.f;
       const bool any = l > 0.f;
       const float mm = fmaxf(mf - bias, xs), f = ex2(mf - bias - mm);
       const float den = fmaf(l, f, ex2(xs - mm));
