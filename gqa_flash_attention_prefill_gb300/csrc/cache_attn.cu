@@ -24,12 +24,18 @@ struct CachePlan {
 };
 
 // Rows per KV head (tokens times query heads of the longest sequence) above
-// which the kernel of 128-row tiles takes over.
-constexpr int kTileRows = 64;
+// which the kernel of 128-row tiles takes over from the one whose warps stream
+// all heads.  It reads a head's slices and pays a tile's products whatever the
+// rows, and has to widen e4m3 keys through shared memory: with 8 sequences of
+// 8k keys, 64 / 8 heads of 64, it takes 50 us (16-bit) or 76..82 us (e4m3) for
+// 24..64 rows; the streaming kernel 72, 73, 120, 125 us (16-bit) or 56, 58, 92,
+// 98 us (e4m3) for 24, 32, 48, 64 rows.  At d = 128 (16 / 2 heads) they meet at
+// 24 rows (36 us, 16-bit) and between 48 and 64 (47..50 us, e4m3).
+constexpr int kTileRows16 = 16, kTileRows8 = 32;
 
-// Heads per CTA: the largest divisor of Hkv up to 8; the warps left
-// over share the heads' keys.  A tile that would leave the ring fewer than
-// four slots (two tiles) takes fewer warps per head, then fewer heads.
+// Heads per CTA: the largest divisor of Hkv up to 8; the warps left over share
+// the heads' keys.  A tile that would leave the ring fewer than four slots (two
+// tiles) takes fewer warps per head, then fewer heads.
 int ring_shape(int Hkv, int d, bool c8, int gk, int esz, int warps, CachePlan* pl) {
   int hpc = Hkv < 8 ? Hkv : 8;
   while (Hkv % hpc != 0) --hpc;
@@ -71,7 +77,7 @@ int cache_plan(int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hkv, int
   // Rows of the longest sequence (all of them, without the hint) decide how
   // many 8-row tiles share each key a warp loads.
   const long long rows = (long long)(max_seqlen_q > 0 ? max_seqlen_q : total_q) * pl->G;
-  pl->tile = d <= 128 && rows > kTileRows;
+  pl->tile = d <= 128 && rows > (c8 ? kTileRows8 : kTileRows16);
   pl->NT = 1;
   while (pl->NT < cache_attn_max_nt(d) && rows > 8 * pl->NT) pl->NT *= 2;
   const int gk = ca_gk(d, c8, pl->NT), esz = c8 ? 1 : 2;
