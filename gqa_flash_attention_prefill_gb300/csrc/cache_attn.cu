@@ -204,7 +204,6 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
   // cost less than a join (the device's own rule), no join is launched.  The
   // hint may be wrong: then whole units are the slower choice, not a wrong one.
   const int seqs = num_seqs < kMaxSeqs ? num_seqs : kMaxSeqs;
-  const int rows = pl.HPC * pl.RT;
   const long long new_max = max_seqlen_q > 0 ? max_seqlen_q : total_q;
   long long units = (long long)pl.HG * seqs * ((new_max * pl.G + pl.RT - 1) / pl.RT);
   if (units > pl.max_units) units = pl.max_units;
@@ -216,13 +215,15 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
       join = false;
     }
   }
-  // Blocks of the join: enough for a warp per row of every unit (at most one
-  // unit is cut per CTA), 16 blocks an SM at most.
+  // Blocks of the join: at most one unit is cut per CTA; a block per row of a
+  // unit, 8 blocks an SM at most.
   int merge_x = 0, merge_y = 1;
   if (join) {
     merge_x = (int)(units < pl.ctas ? units : pl.ctas);
-    merge_y = 16 * pl.ctas / merge_x;
-    if (merge_y > rows) merge_y = rows;
+    merge_y = 8 * pl.ctas / merge_x;
+    const long long live = pl.HPC * (new_max * pl.G < pl.RT ? new_max * pl.G : pl.RT);
+    if (merge_y > live) merge_y = (int)live;
+    if (merge_y < 1) merge_y = 1;
   }
   const unsigned smem = ca_fixed_smem(ca_warps(d, c8, pl.NT)) + (unsigned)pl.NS * pl.slot_bytes;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -1013,9 +1013,10 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
 // Joins the partials of the units that share boundaries cut: with mf the
 // largest reference (the sink's included),
 //   out = sum O_s 2^(M_s - mf) / (sum L_s 2^(M_s - mf) + 2^(x - mf)).
-// blockIdx.x walks the units, blockIdx.y a unit's rows.  A unit of few pieces
-// takes a warp per row; one of many (a long sequence over all CTAs) the whole
-// block per row, its warps sharing the pieces.  Bound by latency: the loads of
+// blockIdx.x walks the units, blockIdx.y the rows of a unit that exist.  A unit
+// of few pieces takes a warp per row, the rows dealt to the blocks first; one of
+// many (a long sequence over all CTAs) the whole block per row, its warps
+// sharing the pieces.  Bound by latency: the loads of
 // 8 pieces go out at once, so a row is two rounds of them.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant__ CacheAttnParams p,
@@ -1034,10 +1035,11 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant_
     if (np == 1) continue;
     const int c0 = h4.y, r0 = h4.z, h0 = h4.w, cu0 = g4.x, E = g4.y;
     const bool wide = np > 8;  // the whole block per row
+    const int per_head = min(RT, E * p.G - r0), live = p.HPC * per_head;
     const int step = wide ? gridDim.y : gridDim.y * 8;
-    for (int r = wide ? blockIdx.y : blockIdx.y * 8 + warp; r < rows; r += step) {
-      const int hl = r / RT, gr = r0 + (r - hl * RT), i = p.div_g.div(gr);
-      if (i >= E) continue;
+    for (int x = wide ? blockIdx.y : warp * gridDim.y + blockIdx.y; x < live; x += step) {
+      const int hl = x / per_head, rr = x - hl * per_head, r = hl * RT + rr;
+      const int gr = r0 + rr, i = p.div_g.div(gr);
       const int qh = (h0 + hl) * p.G + (gr - i * p.G);
       float xs = -INFINITY;
       if (p.sinks != nullptr) xs = __ldg(p.sinks + qh) * kLog2e;
