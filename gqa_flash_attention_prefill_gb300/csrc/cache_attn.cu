@@ -216,11 +216,11 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
     }
   }
   // Blocks of the join: at most one unit is cut per CTA; a block per row of a
-  // unit, 8 blocks an SM at most.
+  // unit, 16 blocks an SM at most.
   int merge_x = 0, merge_y = 1;
   if (join) {
     merge_x = (int)(units < pl.ctas ? units : pl.ctas);
-    merge_y = 8 * pl.ctas / merge_x;
+    merge_y = 16 * pl.ctas / merge_x;
     const long long live = pl.HPC * (new_max * pl.G < pl.RT ? new_max * pl.G : pl.RT);
     if (merge_y > live) merge_y = (int)live;
     if (merge_y < 1) merge_y = 1;

@@ -371,12 +371,21 @@ __device__ __forceinline__ void ca_publish(const CacheAttnParams& p, const CaPla
   }
 }
 
+// L2 policies: keys that this CTA alone reads leave L2 first, so the call's
+// tables, partials and results stay (one 131k sequence 35.7 -> 33.6 us, 256
+// sequences 355 -> 351).
+__device__ __forceinline__ uint64_t l2_policy(bool first) {
+  uint64_t a, b;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(a));
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(b));
+  return first ? a : b;
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
+                                          uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+      "[%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
       : "memory");
 }
 // Named barrier over `count` threads that tells whether all of them said yes.
@@ -538,6 +547,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
       if (!more) break;
       const int npg = p.div_page.div(u.P + u.E - 1) + 1;
       const int32_t* table = p.indices + plan.T.ipt[u.b];
+      const uint64_t policy = l2_policy(u.E * p.G <= RT);  // one row tile reads these keys
       for (int t = u.t0; ok && t < u.t1; ++t) {
         const int n0 = u.lo + t * p.T;
         // Tokens [skip, ntok) of the tile: keys below the window are not read.
@@ -572,14 +582,14 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
             const uint8_t* src = pages + (row + first) * tok_bytes + (long long)u.hg * row_bytes;
             const uint32_t to = dst + (uint32_t)(r * p.run + first) * row_bytes;
             if (p.HG == 1)
-              bulk_load(to, src, (uint32_t)cnt * row_bytes, bar);
+              bulk_load(to, src, (uint32_t)cnt * row_bytes, bar, policy);
             else
               for (int i = 0; i < cnt; ++i)
-                bulk_load(to + i * row_bytes, src + i * tok_bytes, row_bytes, bar);
+                bulk_load(to + i * row_bytes, src + i * tok_bytes, row_bytes, bar, policy);
             if (C8)  // the scales of all heads, whole runs: within the page
               bulk_load(dst + p.data_bytes + (uint32_t)(r * p.run * p.Hkv),
                         (kv ? p.v_scales : p.k_scales) + row * p.Hkv, (uint32_t)(p.run * p.Hkv),
-                        bar);
+                        bar, policy);
           }
           ++issued;
           if (++slot == (uint32_t)p.NS) {
@@ -1014,16 +1024,19 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
 // largest reference (the sink's included),
 //   out = sum O_s 2^(M_s - mf) / (sum L_s 2^(M_s - mf) + 2^(x - mf)).
 // blockIdx.x walks the units, blockIdx.y the rows of a unit that exist.  A unit
-// of few pieces takes a warp per row, the rows dealt to the blocks first; one of
-// many (a long sequence over all CTAs) the whole block per row, its warps
-// sharing the pieces.  Bound by latency: the loads of
-// 8 pieces go out at once, so a row is two rounds of them.
+// of few pieces takes a warp per row (per two rows at d = 64), the rows dealt to
+// the blocks first; one of many (a long sequence over all CTAs) the whole block,
+// its warps (half warps at d = 64) sharing the pieces.  Bound by latency: the
+// loads of 4 pieces go out at once.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant__ CacheAttnParams p,
                                                           int RT, float bias) {
-  __shared__ float s_o[8][D];
-  __shared__ float2 s_ml[8];
+  constexpr int kLanes = D == 64 ? 16 : 32;  // lanes of a row, 4 values each (twice at d = 256)
+  constexpr int kRows = 32 / kLanes, kVec = D / (4 * kLanes);
+  __shared__ float4 s_o[8][kRows][D / 4];
+  __shared__ float2 s_ml[8][kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane / kLanes, ll = lane % kLanes;
   grid_dep_launch_dependents();
   grid_dep_wait();
   const int n_units = __ldcg(p.hdr);
@@ -1036,88 +1049,96 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant_
     const int c0 = h4.y, r0 = h4.z, h0 = h4.w, cu0 = g4.x, E = g4.y;
     const bool wide = np > 8;  // the whole block per row
     const int per_head = min(RT, E * p.G - r0), live = p.HPC * per_head;
+    const int groups = wide ? live : (live + kRows - 1) / kRows;
     const int step = wide ? gridDim.y : gridDim.y * 8;
-    for (int x = wide ? blockIdx.y : warp * gridDim.y + blockIdx.y; x < live; x += step) {
-      const int hl = x / per_head, rr = x - hl * per_head, r = hl * RT + rr;
+    for (int x = wide ? blockIdx.y : warp * gridDim.y + blockIdx.y; x < groups; x += step) {
+      const int row_x = wide ? x : x * kRows + sub;
+      const bool on = row_x < live;
+      const int lr = on ? row_x : 0;  // lanes past the last row repeat the first
+      const int hl = lr / per_head, rr = lr - hl * per_head, r = hl * RT + rr;
       const int gr = r0 + rr, i = p.div_g.div(gr);
       const int qh = (h0 + hl) * p.G + (gr - i * p.G);
       float xs = -INFINITY;
       if (p.sinks != nullptr) xs = __ldg(p.sinks + qh) * kLog2e;
       else if (p.smooth) xs = 0.f;
-      const int ds = wide ? 8 : 1;
+      const int ds = wide ? 8 * kRows : 1;
       // Piece s of the unit: slot 2 c + 1 of its first CTA, slot 2 (c + s) after.
-      float mf = -1e30f, l = 0.f, acc[D / 32];
+      float mf = -1e30f, l = 0.f;
+      float4 acc[kVec];
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
-      for (int s0 = wide ? warp : 0; s0 < np; s0 += 8 * ds) {
-        float2 ml[8], v[8][D / 64];
+      for (int k = 0; k < kVec; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](int k, const float4& v, float f) {
+        acc[k].x = fmaf(v.x, f, acc[k].x), acc[k].y = fmaf(v.y, f, acc[k].y);
+        acc[k].z = fmaf(v.z, f, acc[k].z), acc[k].w = fmaf(v.w, f, acc[k].w);
+      };
+      for (int s0 = wide ? warp * kRows + sub : 0; s0 < np; s0 += 4 * ds) {
+        float2 ml[4];
+        float4 v[4][kVec];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const int s = s0 + j * ds;
           ml[j] = make_float2(-1e30f, 0.f);
 #pragma unroll
-          for (int k = 0; k < D / 64; ++k) v[j][k] = make_float2(0.f, 0.f);
+          for (int k = 0; k < kVec; ++k) v[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (s < np) {
             const long long a = (2ll * (c0 + s) + (s == 0 ? 1 : 0)) * rows + r;
             ml[j] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + a);
 #pragma unroll
-            for (int k = 0; k < D / 64; ++k)
-              v[j][k] = __ldcg(reinterpret_cast<const float2*>(p.part_o + a * D) + 32 * k + lane);
+            for (int k = 0; k < kVec; ++k)
+              v[j][k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + a * D) + kLanes * k + ll);
           }
         }
-        float m = mf;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = fmaxf(m, ml[j].x);
+        const float m = fmaxf(fmaxf(mf, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
         const float f0 = ex2(mf - m);
         l *= f0;
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) acc[k] *= f0;
+        for (int k = 0; k < kVec; ++k)
+          acc[k] = make_float4(acc[k].x * f0, acc[k].y * f0, acc[k].z * f0, acc[k].w * f0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           const float f = ex2(ml[j].x - m);
           l = fmaf(ml[j].y, f, l);
 #pragma unroll
-          for (int k = 0; k < D / 64; ++k) {
-            acc[2 * k] = fmaf(v[j][k].x, f, acc[2 * k]);
-            acc[2 * k + 1] = fmaf(v[j][k].y, f, acc[2 * k + 1]);
-          }
+          for (int k = 0; k < kVec; ++k) add(k, v[j][k], f);
         }
         mf = m;
       }
       if (wide) {
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < D / 64; ++k)
-          *reinterpret_cast<float2*>(&s_o[warp][64 * k + 2 * lane]) =
-              make_float2(acc[2 * k], acc[2 * k + 1]);
-        if (lane == 0) s_ml[warp] = make_float2(mf, l);
+        for (int k = 0; k < kVec; ++k) s_o[warp][sub][kLanes * k + ll] = acc[k];
+        if (ll == 0) s_ml[warp][sub] = make_float2(mf, l);
         __syncthreads();
-        if (warp != 0) continue;
-        mf = -1e30f;
-        for (int w = 0; w < 8; ++w) mf = fmaxf(mf, s_ml[w].x);
-        l = 0.f;
+        if (warp == 0 && sub == 0) {
+          mf = -1e30f;
+          for (int w = 0; w < 8 * kRows; ++w) mf = fmaxf(mf, s_ml[w / kRows][w % kRows].x);
+          l = 0.f;
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) acc[k] = 0.f;
-        for (int w = 0; w < 8; ++w) {
-          const float f = ex2(s_ml[w].x - mf);
-          l = fmaf(s_ml[w].y, f, l);
+          for (int k = 0; k < kVec; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int w = 0; w < 8 * kRows; ++w) {
+            const float2 y = s_ml[w / kRows][w % kRows];
+            const float f = ex2(y.x - mf);
+            l = fmaf(y.y, f, l);
 #pragma unroll
-          for (int k = 0; k < D / 64; ++k) {
-            acc[2 * k] = fmaf(s_o[w][64 * k + 2 * lane], f, acc[2 * k]);
-            acc[2 * k + 1] = fmaf(s_o[w][64 * k + 2 * lane + 1], f, acc[2 * k + 1]);
+            for (int k = 0; k < kVec; ++k) add(k, s_o[w / kRows][w % kRows][kLanes * k + ll], f);
           }
         }
       }
-      const bool any = l > 0.f;
-      const float mm = fmaxf(mf - bias, xs), f = ex2(mf - bias - mm);
-      const float den = fmaf(l, f, ex2(xs - mm));
-      const float inv = any ? f / den : 0.f;
-      const long long row = (long long)(cu0 + i) * p.Hq + qh;
+      if (on && (!wide || (warp == 0 && sub == 0))) {
+        const bool any = l > 0.f;
+        const float mm = fmaxf(mf - bias, xs), f = ex2(mf - bias - mm);
+        const float den = fmaf(l, f, ex2(xs - mm));
+        const float inv = any ? f / den : 0.f;
+        const long long row = (long long)(cu0 + i) * p.Hq + qh;
 #pragma unroll
-      for (int k = 0; k < D / 64; ++k)
-        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + 64 * k + 2 * lane) =
-            pack2<BF16>(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-      if (lane == 0 && p.lse != nullptr) p.lse[row] = any ? (mm + log2f(den)) * kLn2 : -INFINITY;
+        for (int k = 0; k < kVec; ++k)
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + 4 * (kLanes * k + ll)) =
+              make_uint2(pack2<BF16>(acc[k].x * inv, acc[k].y * inv),
+                         pack2<BF16>(acc[k].z * inv, acc[k].w * inv));
+        if (ll == 0 && p.lse != nullptr) p.lse[row] = any ? (mm + log2f(den)) * kLn2 : -INFINITY;
+      }
+      __syncwarp();
     }
   }
 }

@@ -367,6 +367,14 @@ def test_many_rows_over_long_prefixes(pkg, hq, hkv, d, kind, window):
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("hq,hkv,new,kind", [(64, 16, 64, "e4m3"), (64, 16, 64, "16"), (8, 8, 1, "16")])
+def test_units_cut_into_many_pieces(pkg, hq, hkv, new, kind):
+    """One sequence whose units are cut over nine CTAs or more each, with more
+    rows than the join has blocks for them."""
+    b, cache, _, _ = attention_case([12000], [new], hq, hkv, 64, 64, kind, "bf16", 0, "head", seed=15)
+    check(pkg, b, cache)
+
+
 def test_many_short_sequences_of_many_rows(pkg):
     """More units of one key tile than CTAs, each with 80 rows."""
     pre, new = [(5 * i) % 30 for i in range(200)], [10] * 200
