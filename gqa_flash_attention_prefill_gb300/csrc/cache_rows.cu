@@ -302,9 +302,9 @@ struct ReadParams {
   unsigned int* status;
 };
 
-// Rows a CTA gathers: one a warp, so that the lookups of all run at once
-// (16 rows on 8 warps: 8 x 8192 keys 38.6 us, 64 x 128 keys 8.1; 4 on 4: 36.4
-// and 5.1).
+// Rows a CTA gathers: one a warp, so that the lookups of all run at once and
+// nothing is shared (16 rows on 8 warps with a barrier after the lookups: 8 x
+// 8192 keys 38.6 us, 64 x 128 keys 8.1; now 36.9 and 4.5).
 constexpr int kReadRows = kReadThreads / 32;
 
 // 4 e4m3 values times 2^e (as fp32 `s`), rounded to 16 bits (exact in bf16
@@ -317,64 +317,56 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, float s) {
   return make_uint2(pack2<BF16>(a.x * s, a.y * s), pack2<BF16>(b.x * s, b.y * s));
 }
 
-// One CTA: kReadRows consecutive output rows of k and v, all heads.  A warp
-// finds a row's place in the pool, then the CTA's threads walk 16-value (e4m3)
-// or 8-value (16-bit) vectors, 16-byte loads and stores.
+// A warp per output row of k and v, all heads: it finds the row's place in the
+// pool, then its lanes walk 16-value (e4m3) or 8-value (16-bit) vectors, 16-byte
+// loads and stores.
 template <bool BF16, bool C8>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
-  __shared__ long long s_slot[kReadRows];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int row0 = blockIdx.x * kReadRows;
-  const int nrow = min(kReadRows, p.rows - row0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.x * kReadRows + warp;
   grid_dep_launch_dependents();
   grid_dep_wait();
-  if (warp < nrow) {
-    const int r = row0 + warp;
-    const int b = warp_upper_bound(p.kv_indptr + 1, p.pt.num_seqs, r);
-    if (lane == 0) {
-      long long slot = -1;
-      if (b < p.pt.num_seqs) {
-        const int r0 = __ldg(p.kv_indptr + b);
-        const int f = p.first_keys != nullptr ? __ldg(p.first_keys + b) : 0;
-        const int i0 = __ldg(p.pt.indptr + b), i1 = __ldg(p.pt.indptr + b + 1);
-        const long long key = (long long)f + (r - r0);
-        const long long at = i0 + key / p.pt.page_size;
-        int page = -1;
-        if (r0 >= 0 && r0 <= r && f >= 0 && i0 >= 0 && at < i1 && at < p.pt.entries)
-          page = __ldg(p.pt.indices + at);
-        if (page >= 0 && page < p.pt.num_pages)
-          slot = (long long)page * p.pt.page_size + key % p.pt.page_size;
-        else
-          atomicOr(p.status, (unsigned)GQA_DEV_BAD_METADATA);
-      }
-      s_slot[warp] = slot;
-    }
+  if (r >= p.rows) return;
+  const int b = warp_upper_bound(p.kv_indptr + 1, p.pt.num_seqs, r);
+  if (b >= p.pt.num_seqs) return;  // a row of no sequence
+  // Every lane looks the same words up (one request a warp).
+  const int r0 = __ldg(p.kv_indptr + b);
+  const int f = p.first_keys != nullptr ? __ldg(p.first_keys + b) : 0;
+  const int i0 = __ldg(p.pt.indptr + b), i1 = __ldg(p.pt.indptr + b + 1);
+  const long long key = (long long)f + (r - r0);
+  const long long at = i0 + key / p.pt.page_size;
+  int page = -1;
+  if (r0 >= 0 && r0 <= r && f >= 0 && i0 >= 0 && at < i1 && at < p.pt.entries)
+    page = __ldg(p.pt.indices + at);
+  if (page < 0 || page >= p.pt.num_pages) {
+    if (lane == 0) atomicOr(p.status, (unsigned)GQA_DEV_BAD_METADATA);
+    return;
   }
-  __syncthreads();
-  constexpr int kVec = C8 ? 16 : 8;
-  const int per_head = p.d / kVec;
-  const int per_row = p.hkv * per_head;  // vectors of a row
-  const int total = nrow * per_row;
-#pragma unroll 4
-  for (int i = tid; i < 2 * total; i += kReadThreads) {
-    const bool is_v = i >= total;
-    const int j = is_v ? i - total : i;
-    const int rl = j / per_row, c = j - rl * per_row;
-    const long long slot = s_slot[rl];
-    if (slot < 0) continue;
-    const void* pages = is_v ? p.v_pages : p.k_pages;
-    const uint4 raw = __ldg(reinterpret_cast<const uint4*>(pages) + slot * per_row + c);
-    uint4* dst = static_cast<uint4*>(is_v ? p.v_out : p.k_out);
-    const long long at = (long long)(row0 + rl) * per_row + c;
+  const long long slot = (long long)page * p.pt.page_size + key % p.pt.page_size;
+  const int per_row = p.hkv * p.d / (C8 ? 16 : 8);
+  const uint4* const k = static_cast<const uint4*>(p.k_pages) + slot * per_row;
+  const uint4* const v = static_cast<const uint4*>(p.v_pages) + slot * per_row;
+  uint4* const ko = static_cast<uint4*>(p.k_out) + (long long)r * per_row * (C8 ? 2 : 1);
+  uint4* const vo = static_cast<uint4*>(p.v_out) + (long long)r * per_row * (C8 ? 2 : 1);
+  const int shift = p.d == 64 ? 2 : p.d == 128 ? 3 : 4;  // vectors of a head (e4m3)
+  auto wide = [](uint4* dst, const uint4& raw, uint8_t e) {
+    const float s = __int_as_float((int)e << 23);
+    const uint2 a = widen4<BF16>(raw.x, s), c = widen4<BF16>(raw.y, s);
+    const uint2 g = widen4<BF16>(raw.z, s), h = widen4<BF16>(raw.w, s);
+    dst[0] = make_uint4(a.x, a.y, c.x, c.y);
+    dst[1] = make_uint4(g.x, g.y, h.x, h.y);
+  };
+#pragma unroll 2
+  for (int c = lane; c < per_row; c += 32) {
+    const uint4 x = __ldg(k + c), y = __ldg(v + c);
     if (!C8) {
-      dst[at] = raw;
+      ko[c] = x;
+      vo[c] = y;
     } else {
-      const uint8_t e = __ldg((is_v ? p.v_scales : p.k_scales) + slot * p.hkv + c / per_head);
-      const float s = __int_as_float((int)e << 23);
-      const uint2 a = widen4<BF16>(raw.x, s), b = widen4<BF16>(raw.y, s);
-      const uint2 f = widen4<BF16>(raw.z, s), g = widen4<BF16>(raw.w, s);
-      dst[2 * at] = make_uint4(a.x, a.y, b.x, b.y);
-      dst[2 * at + 1] = make_uint4(f.x, f.y, g.x, g.y);
+      const uint8_t ek = __ldg(p.k_scales + slot * p.hkv + (c >> shift));
+      const uint8_t ev = __ldg(p.v_scales + slot * p.hkv + (c >> shift));
+      wide(ko + 2 * c, x, ek);
+      wide(vo + 2 * c, y, ev);
     }
   }
 }
@@ -432,6 +424,7 @@ int launch_row_op(RowsParams& p, int out, int interleaved, bool bf16, void* stre
   if ((long long)p.rows < 2ll * sms * tokens) {
     tokens = 1;
     gy = (heads + per - 1) / per;
+    if (gy > 65535) gy = 65535;
   }
   p.tokens = tokens;
   const long long gx = ((long long)p.rows + tokens - 1) / tokens;
@@ -458,10 +451,11 @@ bool overlap(const void* a, long long an, const void* b, long long bn) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
 }
-// Output rows may not share memory with input rows: a pair's values are read
-// by two threads.
-bool rows_overlap(const void* a, long long as, const void* b, long long bs, int rows, int width) {
-  return overlap(a, ((rows - 1) * as + width) * 2, b, ((rows - 1) * bs + width) * 2);
+// Output rows may not share memory with input rows: the next head is read
+// before this one is written.
+bool rows_overlap(const void* a, long long as, const void* b, long long bs, int rows, int wa,
+                  int wb) {
+  return overlap(a, ((rows - 1) * as + wa) * 2, b, ((rows - 1) * bs + wb) * 2);
 }
 
 bool rotation_ok(const double* inv_freq, int rot_dim, int interleaved, float factor, int d) {
@@ -490,10 +484,15 @@ int run_rope(const gqa_rope_t* rope, const void* k, long long k_stride, void* k_
   if (rope->Hq > 0 && (!row_ok(rope->q, rope->q_stride, qw) ||
                        !row_ok(rope->q_out, rope->q_out_stride, qw) ||
                        rows_overlap(rope->q, rope->q_stride, rope->q_out, rope->q_out_stride, rows,
-                                    (int)qw)))
+                                    (int)qw, (int)qw)))
     return GQA_ERR_INVALID;
   if (Hkv > 0 && (!row_ok(k, k_stride, kw) || !row_ok(k_out, k_out_stride, kw) ||
-                  rows_overlap(k, k_stride, k_out, k_out_stride, rows, (int)kw)))
+                  rows_overlap(k, k_stride, k_out, k_out_stride, rows, (int)kw, (int)kw)))
+    return GQA_ERR_INVALID;
+  // Nor with the other input's: both are read by the CTA that writes.
+  if (rope->Hq > 0 && Hkv > 0 &&
+      (rows_overlap(k, k_stride, rope->q_out, rope->q_out_stride, rows, (int)kw, (int)qw) ||
+       rows_overlap(rope->q, rope->q_stride, k_out, k_out_stride, rows, (int)qw, (int)kw)))
     return GQA_ERR_INVALID;
   RowsParams p = {};
   p.positions = rope->positions;
@@ -535,6 +534,10 @@ int run_write(const void* k, long long k_stride, const void* v, long long v_stri
   if (Hq > 0 && (!row_ok(rope->q, rope->q_stride, qw) ||
                  !row_ok(rope->q_out, rope->q_out_stride, qw) ||
                  rows_overlap(rope->q, rope->q_stride, rope->q_out, rope->q_out_stride, total_q,
+                              (int)qw, (int)qw) ||
+                 rows_overlap(k, k_stride, rope->q_out, rope->q_out_stride, total_q, (int)kw,
+                              (int)qw) ||
+                 rows_overlap(v, v_stride, rope->q_out, rope->q_out_stride, total_q, (int)kw,
                               (int)qw)))
     return GQA_ERR_INVALID;
   RowsParams p = {};

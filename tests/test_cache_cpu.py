@@ -41,6 +41,7 @@ def call_rope(lib, **over):
     (dict(attn_factor=float("nan")), -1), (dict(attn_factor=float("inf")), -1), (dict(positions=None), -1),
     (dict(inv_freq=None), -1), (dict(inv_freq=FAKE + 4), -1), (dict(q=None), -1), (dict(q=FAKE + 8), -1),
     (dict(q_stride=248), -1), (dict(q_stride=260), -1), (dict(q_out=FAKE + 256), -1), (dict(k_out=FAKE), -1),
+    (dict(q=FAR + (1 << 31), q_out=FAKE + 64), -1), (dict(k=FAR + (1 << 31), k_out=FAKE + 64), -1),
     (dict(k=None), -1), (dict(d=68, rot_dim=64), -2), (dict(d=2048), -2), (dict(d=1024, rot_dim=600), -2),
     (dict(rows=0, positions=None), 0), (dict(Hq=0, hkv=0), 0)])
 def test_rope_refusals(lib, over, code):
