@@ -184,6 +184,10 @@ struct CaWalk {
   int at, end;  // share mode: tiles left; whole mode: end is the unit count
   int unit;     // whole mode: next unit, every gridDim.x-th
   bool whole;
+  // Share mode: the sequence of the last piece, its row tile and the tiles of
+  // the sequence before that (pieces come in order, so a long sequence's row
+  // tiles are counted once).
+  int b, rt, before;
 };
 
 // Largest i in [0, n) with a[i] <= x (a[0] = 0 <= x) for a non-decreasing
@@ -222,12 +226,20 @@ __device__ __forceinline__ bool ca_next(const CacheAttnParams& p, const CaTab& T
     w.unit += gridDim.x;
     return true;
   }
-  for (u.rt = 0;; ++u.rt) {  // ends: off lies within the sequence's tiles
-    ca_range(p, u.P, u.E, u.rt, RT, u.lo, u.hi, u.n);
+  if (w.b != lo) {
+    w.b = lo;
+    w.rt = 0;
+    w.before = 0;
+  }
+  off -= w.before;
+  for (;; ++w.rt) {  // ends: off lies within the sequence's tiles
+    ca_range(p, u.P, u.E, w.rt, RT, u.lo, u.hi, u.n);
     const int all = u.n * p.HG;
     if (off < all) break;
     off -= all;
+    w.before += all;
   }
+  u.rt = w.rt;
   u.hg = p.HG == 1 ? 0 : off / u.n;
   u.t0 = off - u.hg * u.n;
   u.t1 = min(u.n, u.t0 + w.end - w.at);
@@ -343,6 +355,7 @@ __device__ __forceinline__ CaPlan ca_plan(const CacheAttnParams& p, int32_t* til
   w.whole = p.whole != 0 || (long long)p.div_ctas.div(n_units + grid - 1) * (int)misc[2] <=
                                 per + p.whole_slack;
   w.unit = c;
+  w.b = -1;
   w.at = c < C ? plan.shares.lo(c) : 0;
   w.end = w.whole ? n_units : c < C ? plan.shares.lo(c + 1) : 0;
   if (c == 0 && lane == 0) p.hdr[0] = w.whole ? 0 : n_units;

@@ -222,8 +222,8 @@ enum { GQA_CACHE_16 = 0, GQA_CACHE_E4M3 = 1 };
  *   q, q_out     [rows] of Hq * d values, rows q_stride / q_out_stride
  *                elements apart (multiples of 8, at least Hq * d), bases
  *                16-byte aligned.  Hq = 0: no q.
- * Output rows must not share memory with their input rows (the range from the
- * first row to the last).
+ * Output rows must not share memory with input rows (the ranges from a first
+ * row to a last).
  */
 typedef struct {
     const int32_t* positions;
@@ -336,9 +336,10 @@ GQA_API int gqa_cache_read(const void* k_pages, const void* v_pages, const void*
  *
  * Keys that no row of a sequence sees (the rest of its last page, keys below
  * the window) may hold anything; keys that some row sees must hold finite
- * values.  A row with no key gets out = 0 and lse = -inf.  The result is the
- * same run to run.  Errors as gqa_flash_prefill_paged; a missing or small
- * workspace is GQA_ERR_INVALID.
+ * values, and value scales within 2^100 of each other.  A row with no key gets
+ * out = 0 and lse = -inf.  The result is the same run to run.  A launch counts
+ * key tiles in 32 bits; more raise GQA_DEV_BAD_METADATA.  Errors as
+ * gqa_flash_prefill_paged; a missing or small workspace is GQA_ERR_INVALID.
  */
 GQA_API int gqa_cache_attention(const void* q, const void* k_pages, const void* v_pages,
                                 const void* k_scales, const void* v_scales, int cache_type,

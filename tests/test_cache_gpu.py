@@ -375,6 +375,16 @@ def test_units_cut_into_many_pieces(pkg, hq, hkv, new, kind):
     check(pkg, b, cache)
 
 
+@pytest.mark.parametrize("d,kind", [(256, "16"), (64, "e4m3")])
+def test_long_chunk_of_many_row_tiles(pkg, d, kind):
+    """A chunk of 700 tokens after 40 cached ones: many row tiles of one
+    sequence, each with its own causal key range."""
+    b, cache, _, _ = attention_case([40, 5], [700, 300], 4, 2, d, 16, kind, "bf16", 0, "none", seed=16)
+    check(pkg, b, cache)
+    b, cache, _, _ = attention_case([40, 5], [700, 300], 4, 2, d, 16, kind, "bf16", 200, "head", seed=17)
+    check(pkg, b, cache)
+
+
 def test_many_short_sequences_of_many_rows(pkg):
     """More units of one key tile than CTAs, each with 80 rows."""
     pre, new = [(5 * i) % 30 for i in range(200)], [10] * 200
