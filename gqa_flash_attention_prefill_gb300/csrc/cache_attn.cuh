@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     const int4 d0 = s_piece[4 * ps], d1 = s_piece[4 * ps + 1], d2 = s_piece[4 * ps + 2];
     __syncwarp();
     if (lane == 0) mbar_arrive(sPiece + 8u * (kCaPieces + ps));
-    const int n_tiles = d0.x, P = d0.w, E = d1.x, hi = d1.y, row0 = d1.z;
+    const int n_tiles = d0.x, P = d0.w, E = d1.x, row0 = d1.z;
     const bool cut = (d0.y & 1) != 0;
     if (n_tiles == 0) break;
     const int head = d1.w + hl;  // KV head
@@ -797,11 +797,16 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
       // Which keys need a look at the mask: any at or past the prefix's end
       // (causal, tree, end of the sequence) or below some row's window.
       const bool edge = n0 + 16 * GK > P || p.window > 0;
+      uint32_t live[GK];  // which of the keys 4 t .. 4 t + 3 some row sees
+#pragma unroll
+      for (int k = 0; k < GK; ++k) live[k] = 15u;
       if (__builtin_expect(edge, 0)) {
 #pragma unroll
-        for (int k = 0; k < GK; ++k)
+        for (int k = 0; k < GK; ++k) {
+          uint32_t seen[2];  // bit 4 g + t': rows 2 t', 2 t' + 1 of a tile see key g (+ 8)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
+            bool any = false;
             const int x = n0 + 16 * k + ca_key(g + 8 * j) - P;  // index among the new tokens
 #pragma unroll
             for (int m = 0; m < NT; ++m)
@@ -817,10 +822,16 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
                   keep = place > rdep[m][h] - p.window;
                 }
                 if (!keep) s[m][k][2 * j + h] = -INFINITY;
+                any |= keep;
               }
+            seen[j] = __ballot_sync(0xffffffffu, any);
             if constexpr (C8)  // keys that no row sees may have any scale
-              if (x + P >= hi || (p.window > 0 && x <= -p.window)) wi[k][j] = 0.f;
+              if (!(seen[j] >> (4 * g) & 15u)) wi[k][j] = 0.f;
           }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)  // key 4 t + j: row 2 t + j % 2 + 8 (j / 2) of the scores
+            if (!(seen[j >> 1] >> (4 * (2 * t + (j & 1))) & 15u)) live[k] &= ~(1u << j);
+        }
       }
       // ---- the references: moved when some score exceeds one by kCaSlack
       bool raise = false;
@@ -878,14 +889,6 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
       for (int k = 0; k < GK; ++k) {
         const uint32_t vk = vbase + voff + (uint32_t)(16 * k) * row_bytes;
         // Keys that no row sees may hold anything: zeros in their place.
-        uint32_t live = 15u;
-        if (__builtin_expect(edge, 0)) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int key = n0 + 16 * k + 4 * t + j;
-            if (key >= hi || (p.window > 0 && key <= P - p.window)) live &= ~(1u << j);
-          }
-        }
 #pragma unroll
         for (int c64 = 0; c64 < D / 64; ++c64) {
           if constexpr (C8) {
@@ -895,7 +898,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
             if (__builtin_expect(edge, 0)) {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                if (!(live >> j & 1u)) w[j] = make_uint2(0u, 0u);
+                if (!(live[k] >> j & 1u)) w[j] = make_uint2(0u, 0u);
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {  // values 2 n and 2 n + 1 of the lane's 8
@@ -916,7 +919,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
             if (__builtin_expect(edge, 0)) {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                if (!(live >> j & 1u)) w[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (!(live[k] >> j & 1u)) w[j] = make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
             for (int n = 0; n < 4; ++n) {

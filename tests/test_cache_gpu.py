@@ -269,7 +269,7 @@ def poison(cache, pre, new):
             getattr(cache, x + "_scales").flatten(0, 1)[~used] = 255
 
 
-def check(pkg, b, cache, keep=None, depths=None, workspace=None, label=""):
+def run_attention(pkg, b, cache, keep=None, depths=None, workspace=None):
     dev, gpu = b.to("cuda"), R.on_gpu(cache)
     mask = indptr = dep = None
     if keep is not None:
@@ -281,6 +281,11 @@ def check(pkg, b, cache, keep=None, depths=None, workspace=None, label=""):
     pkg.cache_attention(dev, gpu, custom_mask=mask, mask_indptr=indptr, depths=dep, out=out, lse=lse,
                         workspace=workspace)
     status_ok(pkg)
+    return out, lse
+
+
+def check(pkg, b, cache, keep=None, depths=None, workspace=None, label=""):
+    out, lse = run_attention(pkg, b, cache, keep, depths, workspace)
     ref, z, bo, bl = R.attention(b.q, cache, b.cu_seqlens_q.tolist(), b.prefix_lens.tolist(), b.scale, b.window,
                                  b.sinks, b.smooth, keep, depths)
     n = b.cu_seqlens_q.tolist()[-1]
@@ -330,6 +335,45 @@ def test_tree_without_depths_and_rows_without_keys(pkg):
         keep[0][:] = False
         keep[1][20:, 10:] = False  # rows 20.. keep only tokens below 10, outside their window
         check(pkg, b, cache, keep)
+
+
+@pytest.mark.parametrize("kind", ["16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv,d,new", [(8, 8, 64, 12), (4, 2, 256, 40), (16, 1, 64, 40), (40, 2, 128, 20)])
+def test_hidden_tokens_may_hold_anything(pkg, hq, hkv, d, new, kind):
+    """Drafted tokens that no row sees, by the bitmap or by their depth, keys
+    below the window and their pages' table entries: NaN with NaN scales, and
+    infinities, change nothing."""
+    for window in (0, 30):
+        pre = [37, 90]
+        b, cache, keep, depths = attention_case(pre, [new] * 2, hq, hkv, d, 16, kind, "bf16", window, "none",
+                                                tree=True, seed=7 + new)
+        hidden = [1, 3, new - 1]
+        for m in keep:
+            m[:, hidden] = False
+        if window:  # token 5 lies a window below every row that its bitmap gives it
+            window = b.window = 2
+            for m, dep in zip(keep, depths):
+                dep[6:] = [max(x, 3) for x in dep[6:]]
+                dep[5] = 0
+                m[5, 5] = False
+            hidden.append(5)
+        want, _ = check(pkg, b, cache, keep, depths)
+        for i, p in enumerate(pre):
+            at = [R.keys_of(cache, i, p + h, p + h + 1) for h in hidden]
+            at += [R.keys_of(cache, i, 0, p - window + 1)] if window else []
+            for n, rows in enumerate(at):
+                for x in "kv":
+                    pages = getattr(cache, x + "_pages")
+                    if kind == "e4m3":
+                        pages.view(torch.uint8).flatten(0, 1)[rows] = 0x7F
+                        getattr(cache, x + "_scales").flatten(0, 1)[rows] = 255
+                    else:
+                        pages.flatten(0, 1)[rows] = math.nan if n % 2 == 0 else math.inf
+            if window:  # pages wholly below the window are no longer this sequence's
+                first = int(cache.page_indptr[i])
+                cache.page_indices[first:first + (p - window + 1) // 16] = -7
+        got, _ = run_attention(pkg, b, cache, keep, depths)
+        assert torch.equal(got, want)
 
 
 def test_new_tokens_in_a_run_are_causal(pkg):
