@@ -196,7 +196,6 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
   p.data_bytes = pl.data_bytes;
   p.window = window > 0 ? window : 0;
   p.smooth = smooth_softmax != 0 ? 1 : 0;
-  p.max_units = pl.max_units;
   p.whole_slack = pl.tile ? kCtWholeSlack : kCaWholeSlack;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.metadata_ready = metadata_ready_flag() ? 1 : 0;

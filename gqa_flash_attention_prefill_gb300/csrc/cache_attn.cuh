@@ -120,7 +120,6 @@ struct CacheAttnParams {
   int window, smooth;
   int whole;         // units dealt whole whatever the lengths
   int whole_slack;   // tiles that a join is worth
-  int max_units;
   float scale_log2;
   int metadata_ready;
 };
