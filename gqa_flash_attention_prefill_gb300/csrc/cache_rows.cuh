@@ -63,13 +63,18 @@ __device__ __forceinline__ int warp_upper_bound(const int32_t* a, int n, int x) 
 // units of 2^-64 turns, so position * step modulo 2^64 is the phase within
 // one turn, exact for every position: a product in fp32 would be off by 0.06
 // radians at a million positions, one in fp64 costs the slow units.  The
-// phase is rounded once to fp32 (a signed half turn, 2^-25 of it at most).
+// phase is taken from the nearest quarter turn before it is rounded to fp32,
+// which leaves it within 2^-28 of a turn (from the nearest whole turn it would
+// be 2^-26, three times what the rounding of the cosine is off by).
 __device__ __forceinline__ float2 phase_cos_sin(int pos, unsigned long long step) {
   const unsigned long long ph = (unsigned long long)(long long)pos * step;
-  const float half_turns = (float)(int)(ph >> 32) * 4.656612873077393e-10f;  // 2^-31
-  float2 cs;
-  sincospif(half_turns, &cs.y, &cs.x);
-  return cs;
+  const uint32_t hi = (uint32_t)(ph >> 32);           // 2^-32 turns
+  const uint32_t quarter = (hi + (1u << 29)) >> 30;   // 0 .. 3
+  const float half_turns = (float)(int)(hi - (quarter << 30)) * 4.656612873077393e-10f;  // 2^-31
+  float s, c;
+  sincospif(half_turns, &s, &c);
+  const float x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;
+  return make_float2((quarter + 1u) & 2u ? -x : x, quarter & 2u ? -y : y);
 }
 // The step of a frequency in radians per position (|f| < 2^20, say): turns
 // modulo one, in 2^-64.
