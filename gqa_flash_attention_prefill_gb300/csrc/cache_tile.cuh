@@ -115,6 +115,41 @@ inline __device__ __noinline__ uint32_t ct_hidden(const uint32_t* mask, const in
   return hid;
 }
 
+// Products and commits as the one elected thread of a warp issues them, all
+// under one election (one an instruction: 164.7 -> 158.6 us).
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, e;\n\t}"
+      : "=r"(r)::"memory");
+  return r != 0;
+}
+__device__ __forceinline__ void one_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void one_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void one_commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+
 template <int D, bool BF16, bool C8>
 __global__ void __launch_bounds__(kCtThreads, 1)
     cache_tile_kernel(const __grid_constant__ CacheAttnParams p) {
@@ -160,23 +195,24 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   if (tid == 0) {
     // A slot is free once both row tiles' products are done.  What the softmax
     // reads of a V slot it has read before those products start (P is full);
-    // s_exp is eight deep: entry t + 8 is written after the scores of t + 8 - NS
-    // are done, which were issued after tile t + 7 - NS was read.
+    // s_exp is eight deep: entry t + 8 is written after slot t + 7's turn, when
+    // the scores of t + 7 - NS are done, which were issued after the softmax of
+    // t + 6 - NS had read its entry.
     for (int i = 0; i < NS; ++i) {
-      mbar_init(sBar + 8u * (B::kKFull + i), kCtLoaders / 2);
-      mbar_init(sBar + 8u * (B::kVFull + i), kCtLoaders / 2);
+      mbar_init(sBar + 8u * (B::kKFull + i), 2u);
+      mbar_init(sBar + 8u * (B::kVFull + i), 2u);
       mbar_init(sBar + 8u * (B::kKEmpty + i), 2u);
       mbar_init(sBar + 8u * (B::kVEmpty + i), 2u);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sBar + 8u * (B::kSFull + i), 1u);
-      mbar_init(sBar + 8u * (B::kSFree + i), 128u);
-      mbar_init(sBar + 8u * (B::kPFull + i), 128u);
+      mbar_init(sBar + 8u * (B::kSFree + i), 4u);
+      mbar_init(sBar + 8u * (B::kPFull + i), 4u);
       mbar_init(sBar + 8u * (B::kODone + i), 1u);
-      mbar_init(sBar + 8u * (B::kQFull + i), 128u);
+      mbar_init(sBar + 8u * (B::kQFull + i), 4u);
       mbar_init(sBar + 8u * (B::kDrain + i), 1u);
     }
-    for (int i = 0; i < 8; ++i) mbar_init(sBar + 8u * (B::kExp + i), 1u);
+    for (int i = 0; i < 8; ++i) mbar_init(sBar + 8u * (B::kExp + i), 2u);
     for (int i = 0; i < kCaPieces; ++i) {
       mbar_init(sPiece + 8u * i, 1u);
       mbar_init(sPiece + 8u * (kCaPieces + i), 13u);  // 8 softmax, 4 loading, 1 issuing
@@ -212,6 +248,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   auto wait_all = [&](uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort_flag, p.status, tmo)) != 0;
   };
+  // One arrival for a warp whose lanes are all done (32 arrivals: 158.6 us, one:
+  // 155.7).
+  auto warp_arrive = [&](uint32_t bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
   // The next piece from the planning warp; false when there is none.
   auto next_piece = [&](uint32_t pi, int4& d0, int4& d1, int4& d2, bool& ok) {
     const uint32_t ps = pi % kCaPieces;
@@ -243,12 +285,15 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       if (!wait_all(sBar + 8u * (B::kPFull + t), (c2 - 1u) & 1u)) return false;
       tc_fence_after();
       const uint64_t dv = dV0 + s * (kKVBytes >> 4);
+      if (elected()) {
 #pragma unroll
-      for (int kk = 0; kk < BN / 16; ++kk)
-        mma_ts(tb + kColO, tb + kColP + kk * 8, dv + (uint64_t)(kk * 128), kIdescO,
-               (first && kk == 0) ? 0u : 1u);
-      mma_commit(sBar + 8u * (B::kODone + t));
-      mma_commit(sBar + 8u * (B::kVEmpty + s));
+        for (int kk = 0; kk < BN / 16; ++kk)
+          one_mma_ts(tb + kColO, tb + kColP + kk * 8, dv + (uint64_t)(kk * 128), kIdescO,
+                     (first && kk == 0) ? 0u : 1u);
+        one_commit(sBar + 8u * (B::kODone + t));
+        one_commit(sBar + 8u * (B::kVEmpty + s));
+      }
+      __syncwarp();
       return true;
     };
     CaPlan plan = {};
@@ -300,11 +345,15 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         if (c > 0 && !(ok = wait_all(sBar + 8u * (B::kSFree + t), (c - 1u) & 1u))) break;
         tc_fence_after();
         const uint64_t dk = dK0 + s * (kKVBytes >> 4);
+        if (elected()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tb, dQ + kstep(kk, kQChunk), dk + kstep(kk, kKVChunk), kIdescS, kk > 0 ? 1u : 0u);
-        mma_commit(sBar + 8u * (B::kSFull + t));
-        mma_commit(sBar + 8u * (B::kKEmpty + s));
+          for (int kk = 0; kk < D / 16; ++kk)
+            one_mma_ss(tb, dQ + kstep(kk, kQChunk), dk + kstep(kk, kKVChunk), kIdescS,
+                       kk > 0 ? 1u : 0u);
+          one_commit(sBar + 8u * (B::kSFull + t));
+          one_commit(sBar + 8u * (B::kKEmpty + s));
+        }
+        __syncwarp();
         // The second product of a tile goes after the next tile's first.
         if (j > 0 && !(ok = issue_pv(it, c, j == 1))) break;
       }
@@ -425,8 +474,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         commit();
         if (it >= issued) break;  // no tile left
         asm volatile("cp.async.wait_group %0;" ::"n"(kCtRaw - 1) : "memory");
-        if (!(ok = slot_free(it))) break;
-        const uint32_t s = it % NS, base = sT + s * kKVBytes;
         const uint32_t at = ring + it % kCtRaw * (2u * ct_raw_half(D));
         // Scale bytes of keys lane, lane + 32, .., 0 for a key no row sees.
         int sc[BN / 32], top = 0, low = 255;
@@ -447,9 +494,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             s_exp[it & 7u].z = apart ? 1 : 0;
           } else {
             s_exp[it & 7u].x = x;
-            mbar_arrive(sBar + 8u * (B::kExp + (it & 7u)));
           }
+          mbar_arrive(sBar + 8u * (B::kExp + (it & 7u)));
         }
+        if (!(ok = slot_free(it))) break;
+        const uint32_t s = it % NS, base = sT + s * kKVBytes;
 #pragma unroll 1
         for (int g = 0; g < kOwn; ++g) {
           const int own = half * kOwn + g == 0   ? sc[0]
@@ -482,14 +531,14 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(full + 8u * s);
+        warp_arrive(full + 8u * s);
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else {
       // Straight to the products' slots; two tiles stay in flight.
       auto landed = [&](uint32_t i) {
         fence_proxy_async_smem();
-        mbar_arrive(full + 8u * (i % NS));
+        warp_arrive(full + 8u * (i % NS));
       };
       while (more) {
         if (!slot_free(it)) break;
@@ -577,7 +626,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                        x[0], x[1], x[2], x[3]);
         }
         fence_proxy_async_smem();
-        mbar_arrive(sBar + 8u * (B::kQFull + t));
+        warp_arrive(sBar + 8u * (B::kQFull + t));
       }
 
       float M = -1e30f, L = 0.f;
@@ -588,12 +637,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         float rk = rs, ve = 0.f, vi = 1.f;
         bool apart = false;
         if constexpr (C8) {
-          // The loaders' writes are visible after their own barriers.  K's
-          // slot may be two tiles further on by now, so its exponent has a
-          // barrier per entry; V's slot waits for this tile's probabilities.
+          // The exponents are there before the values are widened.  K's slot
+          // may be two tiles further on by now, so they have a barrier per
+          // entry; V's slot waits for this tile's probabilities.
           if (!(ok = wait_all(sBar + 8u * (B::kExp + (it & 7u)), (it >> 3) & 1u))) break;
-          if (!(ok = wait_all(sBar + 8u * (B::kVFull + s), (it / NS) & 1u))) break;
           const int4 x = s_exp[it & 7u];
+          if (x.z != 0 && !(ok = wait_all(sBar + 8u * (B::kVFull + s), (it / NS) & 1u))) break;
           rk = fmaxf(rs * __int_as_float((127 + x.x) << 23), 1e-37f);
           ve = (float)x.y;
           vi = __int_as_float((127 - x.y) << 23);
@@ -645,7 +694,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             if (!plain) break;
             if (h + 1 == BN / 32) {
               tc_fence_before();
-              mbar_arrive(sBar + 8u * (B::kSFree + t));  // the next tile's scores may come
+              warp_arrive(sBar + 8u * (B::kSFree + t));  // the next tile's scores may come
             }
             uint32_t pk[16];
             exps(x[h & 1], rk, ref, pk);
@@ -665,7 +714,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             tmem_wait_ld();
             if (h + 1 == BN / 32) {
               tc_fence_before();
-              mbar_arrive(sBar + 8u * (B::kSFree + t));
+              warp_arrive(sBar + 8u * (B::kSFree + t));
             }
             if (edge) {  // keys this row keeps, one bit each
               const uint32_t keep =
@@ -736,7 +785,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(sBar + 8u * (B::kPFull + t));
+        warp_arrive(sBar + 8u * (B::kPFull + t));
       }
       if (!ok) break;
       if (!(ok = wait_all(sBar + 8u * (B::kODone + t), (c - 1u) & 1u))) break;
