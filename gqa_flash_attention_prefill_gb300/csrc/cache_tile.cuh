@@ -22,7 +22,9 @@
 // buffered scores: 8 trees of 64 tokens over 8k e4m3 keys 176 us, 146 of them
 // with softmax and widening left out), so a tile takes as many keys as the
 // tensor memory holds beside P and O, and the two row tiles do not wait for
-// each other.
+// each other: 156 us, 440 TFLOP/s.  A tile takes 4300 clocks: 2500 of softmax
+// work, the rest its waits for exponents, scores and the product before, each
+// some hundreds although the slots are rarely full.
 //
 // Scales of an e4m3 tile.  Widening multiplies a key's values by 2^(e - x)
 // with x 7 below the largest exponent e of the tile, which keeps every value
