@@ -573,12 +573,13 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const uint32_t t_lane = tmem + 256u * t + ((uint32_t)((warp & 3) * 32) << 16);
     int4 d0 = {}, d1 = {}, d2 = {};
     uint32_t pi = 0, it = 0, c = 0;  // tiles of the CTA, and of this row tile
-    bool ok = true;
+    bool ok = true, skipped = false;
     while (next_piece(pi++, d0, d1, d2, ok)) {
       const int n = d0.x, P = d0.w, E = d1.x, head = d1.w, cu0 = d2.x;
       const bool cut = (d0.y & 1) != 0;
       if (d1.z + 128 * t >= E * p.G) {  // no rows in this tile
         it += n;
+        skipped = true;
         continue;
       }
       const int gr = d1.z + 128 * t + r;  // row of the sequence
@@ -641,7 +642,14 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         if constexpr (C8) {
           // The exponents are there before the values are widened.  K's slot
           // may be two tiles further on by now, so they have a barrier per
-          // entry; V's slot waits for this tile's probabilities.
+          // entry; V's slot waits for this tile's probabilities.  A barrier
+          // tells a phase only from the one before it.  A row tile that was in
+          // the tiles before has seen theirs; after tiles without its rows it
+          // may be any number of phases ahead of the loading warps, so there
+          // the scores come first: they are counted by the row tile's own
+          // tiles, and every entry and slot before them has been told.
+          if (skipped && !(ok = wait_all(sBar + 8u * (B::kSFull + t), c & 1u))) break;
+          skipped = false;
           if (!(ok = wait_all(sBar + 8u * (B::kExp + (it & 7u)), (it >> 3) & 1u))) break;
           const int4 x = s_exp[it & 7u];
           if (x.z != 0 && !(ok = wait_all(sBar + 8u * (B::kVFull + s), (it / NS) & 1u))) break;
