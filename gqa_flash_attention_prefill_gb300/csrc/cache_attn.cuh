@@ -105,12 +105,14 @@ struct CacheAttnParams {
   float* part_ml;    // [2 per CTA][HPC * RT rows][2] (M, L)
   int32_t* hdr;      // [0] units to look at; [8 + 8 u ..] unit u: pieces after its first, the
                      // first's CTA, first row, first head, first token, tokens
+  int32_t* gave_up;  // per CTA: 1 when one of its waits ran out
   long long total_mask_words;
   unsigned long long timeout_ns;
   int entries, num_pages, page_size;
   int num_seqs, first_seq, total_q;
   int Hq, Hkv, G;
   int HPC, HG;       // heads per CTA, head groups
+  int ctas;          // of the launch
   int KW;            // warps that share a head's keys
   int T, log_T;      // keys per tile (16 GK KW, a power of two)
   FastDiv div_g, div_page, div_ctas;
@@ -516,12 +518,19 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
   }
   __syncthreads();
   grid_dep_launch_dependents();
-  if (!p.metadata_ready) grid_dep_wait();
+  if (!p.metadata_ready) {
+    grid_dep_wait();
+    if (tid == 0) p.gave_up[blockIdx.x] = 0;
+  }
 
   ca_tables(p, tiles, units, s_cu, s_pre, s_ipt, misc, RT, tid, kThreads);
   __syncthreads();
   const bool bad_meta = misc[1] != 0u;
-  if (p.metadata_ready) grid_dep_wait();  // before any global write or other read
+  if (p.metadata_ready) {
+    grid_dep_wait();  // before any global write or other read
+    if (tid == 0) p.gave_up[blockIdx.x] = 0;
+    __syncthreads();  // before a warp can give up
+  }
   if (bad_meta) {
     if (tid == 0) {
       atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
@@ -612,6 +621,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
       }
       if (!ok) break;
     }
+    if (!ok && lane == 0) p.gave_up[blockIdx.x] = 1;
     // Let every copy issued land before the CTA can exit.
     __syncwarp();
     if (lane < p.NS) {
@@ -1033,11 +1043,16 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
       }
     }
   }
+  if (!ok && lane == 0) p.gave_up[blockIdx.x] = 1;
 }
 
 // Joins the partials of the units that share boundaries cut: with mf the
 // largest reference (the sink's included),
 //   out = sum O_s 2^(M_s - mf) / (sum L_s 2^(M_s - mf) + 2^(x - mf)).
+// A CTA that gave up (GQA_DEV_TIMEOUT) leaves units without an entry and pieces
+// without partials: then nothing is joined, since the workspace holds anything
+// there.  An entry out of range, which only another writer of the workspace can
+// leave, raises GQA_DEV_BAD_METADATA and is passed over.
 // blockIdx.x walks the units, blockIdx.y the rows of a unit that exist.  A unit
 // of few pieces takes a warp per row (per two rows at d = 64), the rows dealt to
 // the blocks first; one of many (a long sequence over all CTAs) the whole block,
@@ -1054,7 +1069,10 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant_
   const int sub = lane / kLanes, ll = lane % kLanes;
   grid_dep_launch_dependents();
   grid_dep_wait();
+  bool gone = false;
+  for (int c = threadIdx.x; c < p.ctas; c += 256) gone |= __ldcg(p.gave_up + c) != 0;
   const int n_units = __ldcg(p.hdr);
+  if (__syncthreads_or(gone)) return;
   const int rows = p.HPC * RT;
   for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
     const int4* hd = reinterpret_cast<const int4*>(p.hdr + 8 + 8ll * u);
@@ -1062,6 +1080,11 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant_
     const int np = h4.x + 1;
     if (np == 1) continue;
     const int c0 = h4.y, r0 = h4.z, h0 = h4.w, cu0 = g4.x, E = g4.y;
+    if (c0 < 0 || h4.x < 0 || (unsigned)c0 + (unsigned)h4.x >= (unsigned)p.ctas || h0 < 0 ||
+        h0 > p.Hkv - p.HPC || cu0 < 0 || E < 0 || cu0 > p.total_q - E || r0 < 0 || r0 >= E * p.G) {
+      if (threadIdx.x == 0) atomicOr(p.status, 2u);
+      continue;
+    }
     const bool wide = np > 8;  // the whole block per row
     const int per_head = min(RT, E * p.G - r0), live = p.HPC * per_head;
     const int groups = wide ? live : (live + kRows - 1) / kRows;

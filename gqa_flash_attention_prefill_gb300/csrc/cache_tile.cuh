@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     }
     return;
   }
+  if (tid == 0) p.gave_up[blockIdx.x] = 0;
   if (warp == 12) {
     tmem_alloc(smem_u32(misc + 3), 512u);
     tmem_relinquish();
@@ -850,6 +851,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   // The products are done (warps 12 and 13 drained them) and every row has been read.
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *abort_flag != 0u) p.gave_up[blockIdx.x] = 1;
   if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, 512u);
