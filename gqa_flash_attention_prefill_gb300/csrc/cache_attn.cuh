@@ -640,19 +640,31 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     return __all_sync(0xffffffffu, wait_bounded(sBar + 8u * sl, parity, abort_flag, p.status, tmo)) != 0;
   };
   uint32_t slot = 0, ph = 0;
+  // Warps that share a head's keys go on together or not at all: each takes
+  // part in one such barrier per piece, the one that finds no piece or whose
+  // wait ran out included, so none waits for a warp that has left.
+  auto together = [&](bool yes) {
+    return p.KW > 1 ? named_bar_all(1u + (uint32_t)hl, 32u * (uint32_t)p.KW, yes) : yes;
+  };
   bool ok = true;
-  for (uint32_t pi = 0; ok; ++pi) {
+  for (uint32_t pi = 0;; ++pi) {
     // ---- the next piece
     const uint32_t ps = pi % kCaPieces;
     ok = __all_sync(0xffffffffu, wait_bounded(sPiece + 8u * ps, (pi / kCaPieces) & 1u, abort_flag,
                                               p.status, tmo)) != 0;
-    if (!ok) break;
+    if (!ok) {
+      together(false);
+      break;
+    }
     const int4 d0 = s_piece[4 * ps], d1 = s_piece[4 * ps + 1], d2 = s_piece[4 * ps + 2];
     __syncwarp();
     if (lane == 0) mbar_arrive(sPiece + 8u * (kCaPieces + ps));
     const int n_tiles = d0.x, P = d0.w, E = d1.x, row0 = d1.z;
     const bool cut = (d0.y & 1) != 0;
-    if (n_tiles == 0) break;
+    if (n_tiles == 0) {
+      together(true);
+      break;
+    }
     const int head = d1.w + hl;  // KV head
     const int cu0 = d2.x;
     // Softmax rows of the thread: 2 t and 2 t + 1 of every 8-row tile.
@@ -954,7 +966,8 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
     }
     // A wait that ran out in one warp ends the piece for all that join rows
     // with it: nothing more is written.
-    if (p.KW > 1) ok = named_bar_all(1u + (uint32_t)hl, 32u * (uint32_t)p.KW, ok);
+    ok = together(ok);
+    if (!ok) break;
 
     // ---- the unit's (or piece's) rows: join the warps of a head, write.
     // Warp area [8 rows][64 columns] in shared memory, a tile and 64 columns
@@ -995,7 +1008,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
         for (int r = 4 * kw + (lane >> 3); r < 8; r += 4 * p.KW) {
           const int gr = row0 + m * 8 + r;  // row of the sequence
           const int i = p.div_g.div(gr);
-          if (i >= E || !ok) continue;
+          if (i >= E) continue;
           const int qh = head * p.G + (gr - i * p.G);
           float xs = -INFINITY;
           if (!cut && p.sinks != nullptr) xs = __ldg(p.sinks + qh) * kLog2e;

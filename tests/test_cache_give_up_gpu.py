@@ -59,8 +59,9 @@ print(json.dumps(dict(before=before, status=status, after=right())))
 """
 
 
-# KV heads (8: a warp per head), new tokens, query heads per KV head.
-@pytest.mark.parametrize("hkv,tokens,group", [(8, 64, 10000)])
+# KV heads (8: a warp per head; 2, 1: four, eight warps that share a head's
+# keys), new tokens, query heads per KV head.
+@pytest.mark.parametrize("hkv,tokens,group", [(8, 64, 10000), (2, 200, 4000), (1, 300, 2200)])
 def test_waits_that_run_out_end_the_call(hkv, tokens, group):
     import __graft_entry__
     __graft_entry__.build()
