@@ -20,7 +20,7 @@ struct CachePlan {
   int G, HPC, HG, KW, NT, T, NS;
   uint32_t data_bytes, slot_bytes;
   int ctas, max_units;  // per launch of at most kMaxSeqs sequences
-  size_t ml_off, hdr_off, gave_up_off, bytes;
+  size_t ml_off, head_off, hdr_off, bytes;
 };
 
 // Rows per KV head (tokens times query heads of the longest sequence) above
@@ -109,9 +109,9 @@ int cache_plan(int num_seqs, int total_q, int max_seqlen_q, int Hq, int Hkv, int
   auto al = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   const size_t prow = 2u * (size_t)pl->ctas * pl->HPC * rt;
   pl->ml_off = al(prow * d * 4u);
-  pl->hdr_off = pl->ml_off + al(prow * 8u);
-  pl->gave_up_off = pl->hdr_off + 32u + 32u * (size_t)pl->max_units;
-  pl->bytes = al(pl->gave_up_off + 4u * (size_t)pl->ctas);
+  pl->head_off = pl->ml_off + al(prow * 8u);
+  pl->hdr_off = pl->head_off + al(32u + (size_t)pl->ctas);
+  pl->bytes = pl->hdr_off + al(32u * (size_t)pl->max_units);
   return GQA_OK;
 }
 
@@ -173,8 +173,8 @@ int run_attention(const void* q, const void* k_pages, const void* v_pages, const
   p.lse = lse;
   p.part_o = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + pl.ml_off);
+  p.head = reinterpret_cast<int32_t*>(ws + pl.head_off);
   p.hdr = reinterpret_cast<int32_t*>(ws + pl.hdr_off);
-  p.gave_up = reinterpret_cast<int32_t*>(ws + pl.gave_up_off);
   p.ctas = pl.ctas;
   p.total_mask_words = total_mask_words;
   p.timeout_ns = wait_limit_ns();

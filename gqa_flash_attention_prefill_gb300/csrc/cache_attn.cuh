@@ -103,9 +103,9 @@ struct CacheAttnParams {
   unsigned int* status;
   float* part_o;     // [2 per CTA][HPC * RT rows][D]
   float* part_ml;    // [2 per CTA][HPC * RT rows][2] (M, L)
-  int32_t* hdr;      // [0] units to look at; [8 + 8 u ..] unit u: pieces after its first, the
-                     // first's CTA, first row, first head, first token, tokens
-  int32_t* gave_up;  // per CTA: 1 when one of its waits ran out
+  int32_t* head;     // [0] units to look at; byte 16 + c: 1 when a wait of CTA c ran out
+  int32_t* hdr;      // [8 u ..] unit u: pieces after its first, the first's CTA, first row, first
+                     // head, first token, tokens
   long long total_mask_words;
   unsigned long long timeout_ns;
   int entries, num_pages, page_size;
@@ -140,6 +140,15 @@ __device__ __forceinline__ int ca_key(int m) {
 __host__ __device__ constexpr uint32_t ca_fixed_smem(int warps) {
   return 1024u + 128u + (uint32_t)warps * (8u * 64u * 4u + 8u * 8u) + 2u * kCaMaxSlots * 8u + 32u +
          4u * (5 * kMaxSeqs + 3) + kCaPieces * (16u * 4u + 2u * 8u);
+}
+
+// The CTA's mark for the join: cleared before any of its warps can give up, by a
+// thread that has no sequence to look up in a small batch.  Bytes, so that a
+// block of the join reads all in ten 16-byte loads (a word a CTA: a join of many
+// small blocks 0.5 us longer); the ones that fill the last 16 are some CTA's too.
+__device__ __forceinline__ void ca_mark(const CacheAttnParams& p, uint8_t gave_up) {
+  uint8_t* marks = reinterpret_cast<uint8_t*>(p.head + 4);
+  for (int c = blockIdx.x; c < (p.ctas + 15) / 16 * 16; c += p.ctas) marks[c] = gave_up;
 }
 
 struct CaTab {
@@ -359,7 +368,7 @@ __device__ __forceinline__ CaPlan ca_plan(const CacheAttnParams& p, int32_t* til
   w.b = -1;
   w.at = c < C ? plan.shares.lo(c) : 0;
   w.end = w.whole ? n_units : c < C ? plan.shares.lo(c + 1) : 0;
-  if (c == 0 && lane == 0) p.hdr[0] = w.whole ? 0 : n_units;
+  if (c == 0 && lane == 0) p.head[0] = w.whole ? 0 : n_units;
   return plan;
 }
 
@@ -378,7 +387,7 @@ __device__ __forceinline__ void ca_publish(const CacheAttnParams& p, const CaPla
   d[2] = make_int4(cu0, m0, more ? plan.T.ipt[u.b] : 0, 0);
   if (more && !plan.walk.whole && u.t0 == 0) {
     const int c = blockIdx.x;
-    int4* hd = reinterpret_cast<int4*>(p.hdr + 8 + 8ll * u.unit);
+    int4* hd = reinterpret_cast<int4*>(p.hdr + 8ll * u.unit);
     hd[0] = make_int4(cut ? plan.shares.owner(plan.walk.at - u.t1 + u.n - 1) - c : 0, c, u.rt * RT,
                       u.hg * p.HPC);
     hd[1] = make_int4(cu0, u.E, 0, 0);
@@ -520,7 +529,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
   grid_dep_launch_dependents();
   if (!p.metadata_ready) {
     grid_dep_wait();
-    if (tid == 0) p.gave_up[blockIdx.x] = 0;
+    if (tid == kThreads - 1) ca_mark(p, 0);
   }
 
   ca_tables(p, tiles, units, s_cu, s_pre, s_ipt, misc, RT, tid, kThreads);
@@ -528,13 +537,13 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
   const bool bad_meta = misc[1] != 0u;
   if (p.metadata_ready) {
     grid_dep_wait();  // before any global write or other read
-    if (tid == 0) p.gave_up[blockIdx.x] = 0;
+    if (tid == kThreads - 1) ca_mark(p, 0);
     __syncthreads();  // before a warp can give up
   }
   if (bad_meta) {
     if (tid == 0) {
       atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
-      if (blockIdx.x == 0) p.hdr[0] = 0;
+      if (blockIdx.x == 0) p.head[0] = 0;
     }
     return;
   }
@@ -621,7 +630,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
       }
       if (!ok) break;
     }
-    if (!ok && lane == 0) p.gave_up[blockIdx.x] = 1;
+    if (!ok && lane == 0) ca_mark(p, 1);
     // Let every copy issued land before the CTA can exit.
     __syncwarp();
     if (lane < p.NS) {
@@ -1056,7 +1065,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
       }
     }
   }
-  if (!ok && lane == 0) p.gave_up[blockIdx.x] = 1;
+  if (!ok && lane == 0) ca_mark(p, 1);
 }
 
 // Joins the partials of the units that share boundaries cut: with mf the
@@ -1082,14 +1091,25 @@ __global__ void __launch_bounds__(256) cache_merge_kernel(const __grid_constant_
   const int sub = lane / kLanes, ll = lane % kLanes;
   grid_dep_launch_dependents();
   grid_dep_wait();
+  // The marks, the count and the block's first entry at once (the grid has no
+  // more blocks than there are entries).
   bool gone = false;
-  for (int c = threadIdx.x; c < p.ctas; c += 256) gone |= __ldcg(p.gave_up + c) != 0;
-  const int n_units = __ldcg(p.hdr);
+  for (int o = threadIdx.x; o < (p.ctas + 15) / 16; o += 256) {
+    const int4 x = __ldcg(reinterpret_cast<const int4*>(p.head) + 1 + o);
+    gone |= (x.x | x.y | x.z | x.w) != 0;
+  }
+  const int n_units = __ldcg(p.head);
+  auto entry = [&](int u, int4& a, int4& b) {
+    const int4* hd = reinterpret_cast<const int4*>(p.hdr + 8ll * u);
+    a = __ldcg(hd);
+    b = __ldcg(hd + 1);
+  };
+  int4 h4, g4;
+  entry(blockIdx.x, h4, g4);
   if (__syncthreads_or(gone)) return;
   const int rows = p.HPC * RT;
   for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
-    const int4* hd = reinterpret_cast<const int4*>(p.hdr + 8 + 8ll * u);
-    const int4 h4 = __ldcg(hd), g4 = __ldcg(hd + 1);
+    if (u != blockIdx.x) entry(u, h4, g4);
     const int np = h4.x + 1;
     if (np == 1) continue;
     const int c0 = h4.y, r0 = h4.z, h0 = h4.w, cu0 = g4.x, E = g4.y;

@@ -234,11 +234,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   if (bad_meta) {
     if (tid == 0) {
       atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
-      if (blockIdx.x == 0) p.hdr[0] = 0;
+      if (blockIdx.x == 0) p.head[0] = 0;
     }
     return;
   }
-  if (tid == 0) p.gave_up[blockIdx.x] = 0;
+  if (tid == 0) ca_mark(p, 0);
   if (warp == 12) {
     tmem_alloc(smem_u32(misc + 3), 512u);
     tmem_relinquish();
@@ -574,13 +574,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const uint32_t t_lane = tmem + 256u * t + ((uint32_t)((warp & 3) * 32) << 16);
     int4 d0 = {}, d1 = {}, d2 = {};
     uint32_t pi = 0, it = 0, c = 0;  // tiles of the CTA, and of this row tile
-    bool ok = true, skipped = false;
+    bool ok = true;
     while (next_piece(pi++, d0, d1, d2, ok)) {
       const int n = d0.x, P = d0.w, E = d1.x, head = d1.w, cu0 = d2.x;
       const bool cut = (d0.y & 1) != 0;
       if (d1.z + 128 * t >= E * p.G) {  // no rows in this tile
         it += n;
-        skipped = true;
         continue;
       }
       const int gr = d1.z + 128 * t + r;  // row of the sequence
@@ -637,20 +636,22 @@ __global__ void __launch_bounds__(kCtThreads, 1)
       for (int j = 0; j < n; ++j, ++it, ++c) {
         const int n0 = d0.z + j * BN;
         const uint32_t s = it % NS;
+        // The scores come first.  The barriers of the exponents and of V's slots
+        // tell a phase only from the one before it, and a row tile that had no
+        // rows in the tiles before waited for nothing there: it may be any
+        // number of phases ahead of the loading warps.  The scores are counted
+        // by the row tile's own tiles, and once they are here every entry and
+        // slot of an earlier tile has been told.  (Exponents first, scores first
+        // only after such tiles: 160 us where this order takes 157, for the code
+        // it adds to the loop.)
+        if (!(ok = wait_all(sBar + 8u * (B::kSFull + t), c & 1u))) break;
         // This tile's factor of the scores, and V's exponent.
         float rk = rs, ve = 0.f, vi = 1.f;
         bool apart = false;
         if constexpr (C8) {
-          // The exponents are there before the values are widened.  K's slot
-          // may be two tiles further on by now, so they have a barrier per
-          // entry; V's slot waits for this tile's probabilities.  A barrier
-          // tells a phase only from the one before it.  A row tile that was in
-          // the tiles before has seen theirs; after tiles without its rows it
-          // may be any number of phases ahead of the loading warps, so there
-          // the scores come first: they are counted by the row tile's own
-          // tiles, and every entry and slot before them has been told.
-          if (skipped && !(ok = wait_all(sBar + 8u * (B::kSFull + t), c & 1u))) break;
-          skipped = false;
+          // The exponents are told before the values are widened.  K's slot may
+          // be two tiles further on by now, so they have a barrier per entry;
+          // V's slot waits for this tile's probabilities.
           if (!(ok = wait_all(sBar + 8u * (B::kExp + (it & 7u)), (it >> 3) & 1u))) break;
           const int4 x = s_exp[it & 7u];
           if (x.z != 0 && !(ok = wait_all(sBar + 8u * (B::kVFull + s), (it / NS) & 1u))) break;
@@ -659,7 +660,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           vi = __int_as_float((127 - x.y) << 23);
           apart = x.z != 0;
         }
-        if (!(ok = wait_all(sBar + 8u * (B::kSFull + t), c & 1u))) break;
         tc_fence_after();
         const uint32_t col_p = t_lane + kColP;
         const bool edge = n0 + BN > P || p.window > 0;
@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
   // The products are done (warps 12 and 13 drained them) and every row has been read.
   tc_fence_before();
   __syncthreads();
-  if (tid == 0 && *abort_flag != 0u) p.gave_up[blockIdx.x] = 1;
+  if (tid == 0 && *abort_flag != 0u) ca_mark(p, 1);
   if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, 512u);
