@@ -180,6 +180,40 @@ def _stream_handle(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _allocating(stream):
+    """Context in which torch allocates for `stream`: the allocator hands a
+    freed block to the next allocation of the stream it was made on, so memory
+    that only a call on another stream uses has to be made on that one."""
+    import contextlib
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _result(shape, dtype, device, stream):
+    """A new tensor that a call on `stream` fills and the caller's current
+    stream may read: once freed, its block waits for both."""
+    import torch
+    with _allocating(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _outputs(q, out, lse, with_lse, stream):
+    """(out, lse) of a call on `stream`, new where not given."""
+    import torch
+    if out is None:
+        out = _result(q.shape, q.dtype, q.device, stream)
+    if lse is None and with_lse:
+        lse = _result(q.shape[:2], torch.float32, q.device, stream)
+    return out, lse
+
+
 def _args(q, k, v, cu_seqlens_q, prefix_lens, kv_indptr, scale, window, sinks,
           smooth_softmax, out, lse, stream, max_seqlen_q):
     for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
@@ -237,11 +271,7 @@ def prefill_masked(batch, custom_mask, mask_indptr, out=None, lse=None, with_lse
     """gqa_flash_prefill_masked on one ``workloads.Batch`` already on the GPU
     (custom_mask / mask_indptr from ``workloads.pack_custom_mask``, on the
     GPU); allocates out/lse with torch when not given.  Returns (out, lse)."""
-    import torch
-    if out is None:
-        out = torch.empty_like(batch.q)
-    if lse is None and with_lse:
-        lse = torch.empty(batch.q.shape[:2], dtype=torch.float32, device=batch.q.device)
+    out, lse = _outputs(batch.q, out, lse, with_lse, stream)
     gqa_flash_prefill_masked(batch.q, batch.k, batch.v, batch.cu_seqlens_q, batch.prefix_lens,
                              batch.kv_indptr, batch.scale, custom_mask, mask_indptr,
                              window=batch.window, sinks=batch.sinks, smooth_softmax=batch.smooth,
@@ -323,15 +353,13 @@ def prefill_splitkv(batch, num_splits=0, workspace=None, out=None, lse=None, wit
     """Split-KV run of one ``workloads.Batch`` already on the GPU; allocates the
     workspace (and out/lse) with torch when not given.  Returns (out, lse)."""
     import torch
-    if out is None:
-        out = torch.empty_like(batch.q)
-    if lse is None and with_lse:
-        lse = torch.empty(batch.q.shape[:2], dtype=torch.float32, device=batch.q.device)
+    out, lse = _outputs(batch.q, out, lse, with_lse, stream)
     used, nbytes = splitkv_workspace(batch.num_seqs, batch.total_q, batch.max_seqlen_q,
                                      batch.hq, batch.hkv, batch.d, batch.dtype_name,
                                      batch.window, num_splits)
     if workspace is None and nbytes > 0:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=batch.q.device)
+        with _allocating(stream):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=batch.q.device)
     gqa_flash_prefill_splitkv(batch.q, batch.k, batch.v, batch.cu_seqlens_q,
                               batch.prefix_lens, batch.kv_indptr, batch.scale, workspace,
                               num_splits=num_splits, window=batch.window, sinks=batch.sinks,
@@ -370,12 +398,8 @@ def gqa_flash_prefill_paged(q, k_pages, v_pages, cu_seqlens_q, prefix_lens, kv_p
 
 def prefill_paged(paged, out=None, lse=None, with_lse=True, stream=None):
     """Run one ``workloads.PagedBatch`` already on the GPU.  Returns (out, lse)."""
-    import torch
     b = paged.batch
-    if out is None:
-        out = torch.empty_like(b.q)
-    if lse is None and with_lse:
-        lse = torch.empty(b.q.shape[:2], dtype=torch.float32, device=b.q.device)
+    out, lse = _outputs(b.q, out, lse, with_lse, stream)
     gqa_flash_prefill_paged(b.q, paged.k_pages, paged.v_pages, b.cu_seqlens_q, b.prefix_lens,
                             paged.page_indptr, paged.page_indices, b.scale, window=b.window,
                             sinks=b.sinks, smooth_softmax=b.smooth, out=out, lse=lse,
@@ -386,11 +410,7 @@ def prefill_paged(paged, out=None, lse=None, with_lse=True, stream=None):
 def prefill(batch, out=None, lse=None, with_lse=True, stream=None):
     """Run one ``workloads.Batch`` already on the GPU; allocates out/lse with
     torch when not given.  Returns (out, lse)."""
-    import torch
-    if out is None:
-        out = torch.empty_like(batch.q)
-    if lse is None and with_lse:
-        lse = torch.empty(batch.q.shape[:2], dtype=torch.float32, device=batch.q.device)
+    out, lse = _outputs(batch.q, out, lse, with_lse, stream)
     gqa_flash_prefill(batch.q, batch.k, batch.v, batch.cu_seqlens_q,
                       batch.prefix_lens, batch.kv_indptr, batch.scale,
                       window=batch.window, sinks=batch.sinks,
@@ -762,10 +782,8 @@ def cache_write(batch, cache, rope=None, stream=None):
 
 def cache_read(cache, kv_indptr, total_kv, dtype, first_keys=None, stream=None):
     """gqa_cache_read of a ``workloads.Cache`` into new rows.  Returns (k, v)."""
-    import torch
     _, _, hkv, d = cache.k_pages.shape
-    k, v = (torch.empty(total_kv, hkv, d, dtype=dtype, device=cache.k_pages.device)
-            for _ in range(2))
+    k, v = (_result((total_kv, hkv, d), dtype, cache.k_pages.device, stream) for _ in range(2))
     return gqa_cache_read(cache.k_pages, cache.v_pages, cache.page_indptr, cache.page_indices,
                           kv_indptr, k, v, first_keys=first_keys, k_scales=cache.k_scales,
                           v_scales=cache.v_scales, stream=stream)
@@ -778,15 +796,12 @@ def cache_attention(batch, cache, q=None, custom_mask=None, mask_indptr=None, de
     workspace, out and lse with torch when not given.  Returns (out, lse)."""
     import torch
     q = batch.q if q is None else q
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None and with_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    out, lse = _outputs(q, out, lse, with_lse, stream)
     if workspace is None:
-        workspace = torch.empty(
-            cache_attention_workspace(batch.num_seqs, batch.total_q, batch.max_seqlen_q, batch.hq,
-                                      batch.hkv, batch.d, batch.dtype_name, cache.kind),
-            dtype=torch.uint8, device=q.device)
+        size = cache_attention_workspace(batch.num_seqs, batch.total_q, batch.max_seqlen_q,
+                                         batch.hq, batch.hkv, batch.d, batch.dtype_name, cache.kind)
+        with _allocating(stream):
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     gqa_cache_attention(q, cache.k_pages, cache.v_pages, batch.cu_seqlens_q, batch.prefix_lens,
                         cache.page_indptr, cache.page_indices, batch.scale, workspace,
                         window=batch.window, sinks=batch.sinks, smooth_softmax=batch.smooth,
