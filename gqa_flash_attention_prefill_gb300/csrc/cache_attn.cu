@@ -12,8 +12,6 @@ namespace gqa {
 
 namespace {
 
-constexpr unsigned kSmemMax = 227u * 1024u;
-
 struct CachePlan {
   bool tile;  // the kernel of 128-row tiles
   int RT;     // rows of a unit

@@ -7,6 +7,10 @@
 
 namespace gqa {
 
+// Shared memory a CTA may have, and what every kernel here is allowed: the ring
+// takes as many slots as fit, so the size of one kernel differs between calls.
+constexpr unsigned kSmemMax = 227u * 1024u;
+
 // 8-row tiles a warp takes at most for head dim d: the accumulators and the
 // query fragments stay in registers.
 constexpr int cache_attn_max_nt(int d) { return d == 64 ? 4 : d == 128 ? 2 : 1; }
@@ -25,7 +29,8 @@ cudaError_t launch_cache_tile(const CacheAttnParams& p, int d, bool bf16, bool c
 namespace {
 
 // Launches `kern`, and the join of cut units when merge_x > 0: one attribute
-// slot per kernel remembers the shared memory allowed to it.
+// slot per kernel remembers that it was allowed kSmemMax.  Threads that come
+// here at once all set the same value.
 template <int D, bool BF16, bool C8, typename Kern>
 cudaError_t launch_with_join(Kern kern, SmemAttr& attr, const CacheAttnParams& p, int rt, int grid,
                              int threads, unsigned smem, int merge_x, int merge_y,
@@ -34,10 +39,10 @@ cudaError_t launch_with_join(Kern kern, SmemAttr& attr, const CacheAttnParams& p
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (attr.allowed[dev].load(std::memory_order_acquire) < smem) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (attr.allowed[dev].load(std::memory_order_acquire) < kSmemMax) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
-    attr.allowed[dev].store(smem, std::memory_order_release);
+    attr.allowed[dev].store(kSmemMax, std::memory_order_release);
   }
   e = launch_pdl(kern, p, grid, threads, smem, st);
   if (e != cudaSuccess || merge_x == 0) return e;
