@@ -60,12 +60,13 @@ __device__ __forceinline__ int warp_upper_bound(const int32_t* a, int n, int x) 
 }
 
 // cos and sin of position * frequency.  `step` is the angle per position in
-// units of 2^-64 turns, so position * step modulo 2^64 is the phase within
-// one turn, exact for every position: a product in fp32 would be off by 0.06
-// radians at a million positions, one in fp64 costs the slow units.  The
-// phase is taken from the nearest quarter turn before it is rounded to fp32,
-// which leaves it within 2^-28 of a turn (from the nearest whole turn it would
-// be 2^-26, three times what the rounding of the cosine is off by).
+// units of 2^-64 turns, so position * step modulo 2^64 is the phase within one
+// turn, within 2^-33 of it at the farthest position: a product in fp32 would be
+// off by 0.06 radians at a million positions, one in fp64 costs the slow units.
+// The phase is taken from the nearest quarter turn before it is rounded to
+// fp32, which leaves it within 2^-27.8 of a turn (from the nearest whole turn it
+// would be 2^-26, three times what the rounding of the cosine is off by), and
+// within 2^-31 near the zeros of sine and cosine.
 __device__ __forceinline__ float2 phase_cos_sin(int pos, unsigned long long step) {
   const unsigned long long ph = (unsigned long long)(long long)pos * step;
   const uint32_t hi = (uint32_t)(ph >> 32);           // 2^-32 turns
@@ -76,12 +77,24 @@ __device__ __forceinline__ float2 phase_cos_sin(int pos, unsigned long long step
   const float x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;
   return make_float2((quarter + 1u) & 2u ? -x : x, quarter & 2u ? -y : y);
 }
-// The step of a frequency in radians per position (|f| < 2^20, say): turns
-// modulo one, in 2^-64.
+// The step of a frequency in radians per position: turns modulo one, in 2^-64,
+// off by one unit at most for |f| < 2^40.  A double's product with 1 / (2 pi) is
+// rounded at 2^-56 turns at one radian, 2^-25 turns at position 2^31, so the 53
+// bits of f are multiplied in integers by 128 bits of 1 / (2 pi), and the bits
+// from 2^-1 to 2^-64 turns taken out.  (In fp64, with 1 / (2 pi) in two
+// doubles and fma: as exact; the gradient of 2047 rows 10.5 us, here 9.5.)
 __device__ __forceinline__ unsigned long long phase_step(double f) {
-  const double turns = f * 0.15915494309189533577;  // 1 / (2 pi)
-  const double frac = turns - floor(turns);           // [0, 1]
-  return (unsigned long long)__double2ull_rn(frac * 9223372036854775808.0) << 1;  // 2^63, then * 2
+  constexpr unsigned long long kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;  // 2^128 / (2 pi)
+  const long long bits = __double_as_longlong(f);
+  const int ex = (int)(bits >> 52) & 2047;  // f = m * 2^(ex - 1075)
+  const unsigned long long m = ((unsigned long long)bits & ((1ull << 52) - 1)) | (ex ? 1ull << 52 : 0);
+  const unsigned long long mid = m * kHi, p1 = mid + __umul64hi(m, kLo);
+  const unsigned long long p2 = __umul64hi(m, kHi) + (p1 < mid ? 1 : 0);
+  const int t = max(1075 - ex, 1);  // m * (kHi, kLo) / 2^(64 + t), of which p1 and p2 count
+  const unsigned long long step = t < 64    ? p1 >> t | p2 << (64 - t)
+                                  : t < 128 ? p2 >> (t - 64)
+                                            : 0ull;
+  return bits < 0 ? 0ull - step : step;
 }
 
 }  // namespace gqa

@@ -207,9 +207,9 @@ enum { GQA_CACHE_16 = 0, GQA_CACHE_E4M3 = 1 };
  *     (a, b) -> attn_factor * (a cos t - b sin t, b cos t + a sin t).
  * Pairs are (x[i], x[i + rot_dim / 2]), or neighbours (x[2 i], x[2 i + 1])
  * when interleaved; values from rot_dim on pass unchanged.  The angle is
- * exact modulo a turn for every int32 position; long-context scalings are
- * the caller's choice of inv_freq and attn_factor.  Arithmetic is fp32,
- * rounded once.
+ * reduced modulo a turn before it is rounded: within 2^-27 of a turn for every
+ * int32 position and |inv_freq| < 2^40.  Long-context scalings are the caller's
+ * choice of inv_freq and attn_factor.  Arithmetic is fp32, rounded once.
  *
  *   positions    device int32 [rows].  gqa_cache_write: NULL for
  *                prefix_lens[b] + i.
