@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(kRowThreads, 14) rows_kernel(const __grid_cons
         }
       }
     }
-    if (on && (OUT == kOutRows || is_q || (OUT == kOutCache16 && slot >= 0))) {
+    // A row without a place in the cache is nobody's: its q_out stays too.
+    if (on && (OUT == kOutRows || (slot >= 0 && (is_q || OUT == kOutCache16)))) {
       uint16_t* dst = is_q ? q_dst : static_cast<uint16_t*>(is_k ? k_dst : v_dst);
       dst += h * p.d;
       *reinterpret_cast<uint4*>(dst + ea) = pack8<BF16>(x);

@@ -272,10 +272,11 @@ GQA_API int gqa_rope(const gqa_rope_t* rope, const void* k, long long k_stride, 
  * rounded to the nearest e4m3, ties to even.  An infinity becomes +-448 times
  * its row's scale, NaN stays NaN and does not count in the row's magnitude.
  *
- * Rows that belong to no sequence are not read; pages and slots that no row
- * maps to are left as they were.  A row whose metadata is inconsistent (a key
- * past the sequence's pages, a page outside the pool) is not written and
- * raises GQA_DEV_BAD_METADATA.  Rows that share a slot (two sequences with
+ * Rows that belong to no sequence change nothing; pages and slots that no row
+ * maps to, and rows of q_out without a sequence, are left as they were.  A row
+ * whose metadata is inconsistent (a key past the sequence's pages, a page
+ * outside the pool) is not written, in the cache or in q_out, and raises
+ * GQA_DEV_BAD_METADATA.  Rows that share a slot (two sequences with
  * the same page) race.  Returns as gqa_flash_prefill.
  */
 GQA_API int gqa_cache_write(const void* k, long long k_stride, const void* v, long long v_stride,
