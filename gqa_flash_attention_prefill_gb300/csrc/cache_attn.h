@@ -11,9 +11,22 @@ namespace gqa {
 // takes as many slots as fit, so the size of one kernel differs between calls.
 constexpr unsigned kSmemMax = 227u * 1024u;
 
+// Rows per KV head (tokens times query heads of the longest sequence) above
+// which the kernel of 128-row tiles takes over from the one whose warps stream
+// all heads.  It reads a head's slices and pays a tile's products whatever the
+// rows, and has to widen e4m3 keys through shared memory: with 8 sequences of
+// 8k keys, 64 / 8 heads of 64, it takes 49..56 us (16-bit) or 65..81 us (e4m3)
+// for 16..64 rows; the streaming kernel 45, 61, 65, 116, 122 us (16-bit) or 46,
+// 54, 58, 92, 99 us (e4m3) for 16, 24, 32, 48, 64 rows.  At d = 128 (16 / 2
+// heads) they meet at 16 rows (30 us, 16-bit) and between 32 and 40 (36..44 us,
+// e4m3).
+constexpr int kTileRows16 = 16, kTileRows8 = 32;
+
 // 8-row tiles a warp takes at most for head dim d: the accumulators and the
-// query fragments stay in registers.
+// query fragments stay in registers.  (d = 64 has 4 for e4m3 pages alone: 16-bit
+// ones leave this kernel at 16 rows.)
 constexpr int cache_attn_max_nt(int d) { return d == 64 ? 4 : d == 128 ? 2 : 1; }
+static_assert(kTileRows16 <= 16, "16-bit pages at d = 64 with four row tiles have no kernel");
 
 cudaError_t launch_cache_attn_d64(const CacheAttnParams& p, bool bf16, bool c8, int nt, int grid,
                                   unsigned smem, int merge_x, int merge_y, cudaStream_t st);
