@@ -457,15 +457,23 @@ def prepare(batch, out, lse=None, stream=None, num_splits=None, workspace=None) 
 # ------------------------------------------------------- the paged cache's operators
 class PreparedOp:
     """One C ABI call with its arguments marshalled: calling the object issues
-    it again (same buffers, same stream).  Made by :func:`prepare_call`; holds
-    the tensors it points to."""
+    it again (same buffers, same stream, on the device that was current when it
+    was made, which has to be current again).  Made by :func:`prepare_call`;
+    holds the tensors it points to."""
 
-    __slots__ = ("_fn", "_args", "_name", "_keep")
+    __slots__ = ("_fn", "_args", "_name", "_keep", "_current", "_device")
 
     def __init__(self, fn, args, name, keep):
+        import torch
         self._fn, self._args, self._name, self._keep = fn, args, name, keep
+        self._current = torch.cuda.current_device
+        # Asked at every call only where there is another device: it takes 1 us.
+        self._device = self._current() if torch.cuda.device_count() > 1 else None
 
     def __call__(self):
+        if self._device is not None and self._current() != self._device:
+            raise ValueError(f"{self._name} was prepared on cuda:{self._device}, which is not the "
+                             "current device")
         rc = self._fn(*self._args)
         if rc != GQA_OK:
             raise GQAError(rc, self._name)
