@@ -66,6 +66,9 @@ constexpr int kCaPieces = 8;                       // pieces the planning warp m
 // that a probability at the reference gets.
 constexpr float kCaSlack = 6.f, kCaHead = 4.f, kCaBias = 9.f;
 constexpr int kCaWholeSlack = 6;                   // tiles a join is worth
+// Least byte of a value scale that counts, 2^-100: the denominators hold 2^-w,
+// which overflows for the zero bytes of slots that were never written.
+constexpr uint32_t kCaLeast = 27;
 
 // Division of 0 <= n < 2^31 by a divisor fixed for the launch: with l =
 // ceil(log2 d) and m = ceil(2^(32 + l) / d) - 2^32, n / d = (hi(n m) + n) >> l
@@ -807,7 +810,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
         for (int k = 0; k < GK; ++k)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint32_t e = lds8(vbase + soff + (uint32_t)((16 * k + 2 * j) * p.Hkv));
+            const uint32_t e = max(lds8(vbase + soff + (uint32_t)((16 * k + 2 * j) * p.Hkv)), kCaLeast);
             we[k][j] = __uint_as_float(0x4B000000u | e) - 8388735.f;  // 2^23 + e - (2^23 + 127)
             wi[k][j] = __uint_as_float((254u << 23) - e * (1u << 23));
           }

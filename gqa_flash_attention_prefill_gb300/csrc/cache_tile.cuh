@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         top = __reduce_max_sync(0xffffffffu, top);
         low = __reduce_min_sync(0xffffffffu, low);
         const bool apart = is_v && top - low > 22;        // exponents per key
-        const int x = apart ? 0 : max(top, 8) - 127 - 7;  // the tile's exponent, >= -126
+        const int x = apart ? 0 : max(top, (int)kCaLeast + 7) - 127 - 7;  // the tile's exponent
         if (half == 0 && lane == 0) {
           if (is_v) {
             s_exp[it & 7u].y = x;
@@ -513,8 +513,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
           const uint32_t f2h = pack2<false>(f, f);
           const int j0 = BN / 2 * half + 32 * g;
           if (__builtin_expect(apart, 0)) {
-            s_we[s * BN + j0 + lane] = own != 0 ? (float)(own - 127) : 0.f;
-            s_wi[s * BN + j0 + lane] = __uint_as_float((uint32_t)(254 - own) << 23);
+            const int w = max(own, (int)kCaLeast);
+            s_we[s * BN + j0 + lane] = (float)(w - 127);
+            s_wi[s * BN + j0 + lane] = __uint_as_float((uint32_t)(254 - w) << 23);
           }
 #pragma unroll
           for (int i = 0; i < kCpr; ++i) {

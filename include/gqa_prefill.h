@@ -337,8 +337,12 @@ GQA_API int gqa_cache_read(const void* k_pages, const void* v_pages, const void*
  *
  * Keys that no row of a sequence sees (the rest of its last page, keys below
  * the window) may hold anything; keys that some row sees must hold finite
- * values, and value scales within 2^100 of each other.  A row with no key gets
- * out = 0 and lse = -inf.  The result is the same run to run.  A launch counts
+ * values, and value scales of at most 2^120, within 2^100 of each other; one
+ * below 2^-100 counts as 2^-100, so that rows of zeros with a scale byte of 0
+ * (slots of a zeroed pool) count as rows of zeros.  Probabilities are rounded
+ * once to 16 bits for their product with the values (q's type; f16 over an e4m3
+ * pool), the sums and the denominator are fp32.  A row with no key gets out = 0
+ * and lse = -inf.  The result is the same run to run.  A launch counts
  * key tiles in 32 bits; more raise GQA_DEV_BAD_METADATA.  Errors as
  * gqa_flash_prefill_paged; a missing or small workspace is GQA_ERR_INVALID.
  */
