@@ -333,7 +333,9 @@ GQA_API int gqa_cache_read(const void* k_pages, const void* v_pages, const void*
  *                 Calls that may run at the same time, captured graphs
  *                 included, need one each.
  *   max_seqlen_q  as gqa_flash_prefill; with 0 the launch is shaped for one
- *                 sequence of total_q tokens.
+ *                 sequence of total_q tokens.  It chooses the kernel: a batch
+ *                 of single tokens with a few long sequences of new tokens runs
+ *                 faster as two calls.
  *
  * Keys that no row of a sequence sees (the rest of its last page, keys below
  * the window) may hold anything; keys that some row sees must hold finite
