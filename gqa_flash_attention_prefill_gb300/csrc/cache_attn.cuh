@@ -6,11 +6,17 @@
 // the log2 domain.  With s = scale log2(e) <q, k> and, for an e4m3 cache, the
 // key's value scale 2^w (w = 0 otherwise),
 //   M   >= max (s + w) - kCaSlack           the row's reference, moved lazily
-//   P_j  = 2^(s_j + w_j - M + kBias)        fp32, rounded once to 16 bits
+//   P_j  = 2^(s_j + w_j - M + kBias)        fp32, see below
 //   O    = sum P_j V_j,  L = sum P_j 2^-w_j   (fp32; V_j the stored values)
 //   out  = O / (L + 2^(x - M + kBias)),   lse = (M - kBias + log2(L + ..)) ln 2
 // so the value scales cost no pass of their own and L keeps the unrounded
-// probabilities.  A reference moves to kCaHead above the score that made it,
+// probabilities.  The second product takes P in 16 bits.  Rounded once that would
+// add as much as the rounding of out where both have as many bits: over few keys
+// and heads the error against 64 bits was up to twice the output's own.  So P is
+// the sum of two 16-bit terms there (16-bit pages, and e4m3 under an f16 out),
+// good to 2^-16 (bf16) or 2^-22, and one f16 term for e4m3 under a bf16 out (two
+// terms: 256 sequences of 1k..16k keys 360 us, one 350; 16-bit pages are bound by
+// memory all the same, 168 us for 64 such sequences either way).  A reference moves to kCaHead above the score that made it,
 // so it moves once or twice in a sequence (each move rescales O); kBias uses
 // f16's range upwards: P stays below 2^15, and a key weighs in down to 2^-30 of
 // the largest at the least.
@@ -489,6 +495,9 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
   constexpr int GK = ca_gk(D, C8, NT);
   constexpr int RT = 8 * NT;
   constexpr bool MBF = BF16 && !C8;          // product type
+  // P as two terms of the product type, where one would round it as coarsely as
+  // out is rounded: an f16 P under a bf16 out is fine enough.
+  constexpr bool kTwoTerms = !(C8 && BF16);
   constexpr float kBias = MBF ? 0.f : kCaBias;
   constexpr int kEsz = C8 ? 1 : 2;
   constexpr int KS = D / 16;                 // k16 steps of the scores
@@ -898,7 +907,7 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
             }
           }
       }
-      uint32_t pf[NT][GK][2];
+      uint32_t pf[NT][GK][2], pr[kTwoTerms ? NT : 1][kTwoTerms ? GK : 1][2];  // P, and its rest
 #pragma unroll
       for (int m = 0; m < NT; ++m) {
         const float r0 = M[m][0] - kBias, r1 = M[m][1] - kBias;
@@ -914,7 +923,10 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
               L[m][0] += a;
               L[m][1] += b;
             }
-            pf[m][k][j] = transpose8(pack2<MBF>(a, b));
+            const uint32_t near = pack2<MBF>(a, b);
+            pf[m][k][j] = transpose8(near);
+            if constexpr (kTwoTerms)
+              pr[m][k][j] = transpose8(pack2<MBF>(a - unpack_lo<MBF>(near), b - unpack_hi<MBF>(near)));
           }
       }
       // ---- O^T += V^T P^T
@@ -942,8 +954,11 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
               e4m3x4_f16(x, a[0], a[1]);
               e4m3x4_f16(y, a[2], a[3]);
 #pragma unroll
-              for (int m = 0; m < NT; ++m)
+              for (int m = 0; m < NT; ++m) {
                 mma16816<MBF>(o[m][4 * c64 + n], a, pf[m][k][0], pf[m][k][1]);
+                if constexpr (kTwoTerms)
+                  mma16816<MBF>(o[m][4 * c64 + n], a, pr[m][k][0], pr[m][k][1]);
+              }
             }
           } else {
             uint4 w[4];
@@ -963,8 +978,11 @@ __global__ void __launch_bounds__(32 * (ca_warps(D, C8, NT) + 1), 1)
               const uint32_t a[4] = {__byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632),
                                      __byte_perm(x2, x3, 0x5410), __byte_perm(x2, x3, 0x7632)};
 #pragma unroll
-              for (int m = 0; m < NT; ++m)
+              for (int m = 0; m < NT; ++m) {
                 mma16816<MBF>(o[m][4 * c64 + n], a, pf[m][k][0], pf[m][k][1]);
+                if constexpr (kTwoTerms)
+                  mma16816<MBF>(o[m][4 * c64 + n], a, pr[m][k][0], pr[m][k][1]);
+              }
             }
           }
         }

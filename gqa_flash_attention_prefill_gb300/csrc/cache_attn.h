@@ -16,8 +16,8 @@ constexpr unsigned kSmemMax = 227u * 1024u;
 // all heads.  It reads a head's slices and pays a tile's products whatever the
 // rows, and has to widen e4m3 keys through shared memory: with 8 sequences of
 // 8k keys, 64 / 8 heads of 64, it takes 49..56 us (16-bit) or 65..81 us (e4m3)
-// for 16..64 rows; the streaming kernel 45, 61, 65, 116, 122 us (16-bit) or 46,
-// 54, 58, 92, 99 us (e4m3) for 16, 24, 32, 48, 64 rows.  At d = 128 (16 / 2
+// for 16..64 rows; the streaming kernel 46, 61, 65, 116, 122 us (16-bit) or 46,
+// 54, 58, 92, 99 us (e4m3, bf16; 2 to 4% more in f16) for 16, 24, 32, 48, 64 rows.  At d = 128 (16 / 2
 // heads) they meet at 16 rows (30 us, 16-bit) and between 32 and 40 (36..44 us,
 // e4m3).
 constexpr int kTileRows16 = 16, kTileRows8 = 32;

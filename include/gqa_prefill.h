@@ -341,9 +341,10 @@ GQA_API int gqa_cache_read(const void* k_pages, const void* v_pages, const void*
  * the window) may hold anything; keys that some row sees must hold finite
  * values, and value scales of at most 2^120, within 2^100 of each other; one
  * below 2^-100 counts as 2^-100, so that rows of zeros with a scale byte of 0
- * (slots of a zeroed pool) count as rows of zeros.  Probabilities are rounded
- * once to 16 bits for their product with the values (q's type; f16 over an e4m3
- * pool), the sums and the denominator are fp32.  A row with no key gets out = 0
+ * (slots of a zeroed pool) count as rows of zeros.  Sums and denominators are
+ * fp32.  For their product with the values, probabilities are held in one term
+ * of 16 bits (q's type; f16 over an e4m3 pool) above the row counts where the
+ * tensor-memory kernel runs and under a bf16 out over an e4m3 pool, else in two.  A row with no key gets out = 0
  * and lse = -inf.  The result is the same run to run.  A launch counts
  * key tiles in 32 bits; more raise GQA_DEV_BAD_METADATA.  Errors as
  * gqa_flash_prefill_paged; a missing or small workspace is GQA_ERR_INVALID.
