@@ -189,7 +189,9 @@ def _allocating(stream):
     if stream is None:
         return contextlib.nullcontext()
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
+        # Handles 0 and 1 are the legacy default stream; torch takes 0 for "a new one".
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
 
 

@@ -42,9 +42,12 @@ cpu.prefix_lens = torch.tensor([700], dtype=torch.int32)
 small = R.fill(W.empty_cache([701], hkv, d, 64, "bf16", "16"), None, 1)
 ref, _, bound, _ = R.attention(cpu.q, small, [0, 1], [700], cpu.scale)
 
-def right():
-    out, status = call(cpu, R.on_gpu(small), hkv)
-    return status == 0 and bool(((out.cpu().double() - ref).abs() <= bound).all())
+def right():  # a millisecond is short: a wait may run out by chance, and says so
+    for _ in range(3):
+        out, status = call(cpu, R.on_gpu(small), hkv)
+        if status == 0:
+            return bool(((out.cpu().double() - ref).abs() <= bound).all())
+    return False
 
 before = right()
 cache = R.on_gpu(W.empty_cache([tokens], hkv, d, 64, "bf16", "16"))

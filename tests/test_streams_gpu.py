@@ -55,3 +55,15 @@ def test_memory_of_a_call_on_another_stream(pkg, name, handle):  # noqa: F811
         assert all(bool((x == 255).all()) for x in blocks)
         del blocks
     assert pkg.get_device_status() == 0
+
+
+def test_handles_name_their_stream(pkg):  # noqa: F811
+    """A raw handle allocates on the stream it names, 0 on the default one."""
+    other = torch.cuda.Stream()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        mine = torch.cuda.current_stream().cuda_stream
+        for stream, handle in ((None, mine), (0, 0), (other, other.cuda_stream), (other.cuda_stream, other.cuda_stream),
+                               (torch.cuda.default_stream(), 0)):
+            with pkg._allocating(stream):
+                assert torch.cuda.current_stream().cuda_stream == handle
+            assert torch.cuda.current_stream().cuda_stream == mine
