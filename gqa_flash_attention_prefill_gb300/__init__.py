@@ -25,6 +25,7 @@ __all__ = ["load", "gqa_flash_prefill", "gqa_flash_prefill_debug", "prefill", "p
            "GQA_CACHE_16", "GQA_CACHE_E4M3", "Rope", "gqa_rope", "gqa_cache_write",
            "gqa_cache_read", "gqa_cache_attention", "cache_attention_workspace",
            "prepare_call", "PreparedOp", "cache_write", "cache_read", "cache_attention",
+           "gqa_prefill_backward", "prefill_backward_workspace", "prefill_backward",
            "EXPORTED_SYMBOLS"]
 
 GQA_F16, GQA_BF16 = 0, 1
@@ -45,7 +46,7 @@ EXPORTED_SYMBOLS = [
     "gqa_prefill_get_stream_status", "gqa_flash_prefill_masked",
     "gqa_prefill_set_call_flags", "gqa_prefill_get_call_flags",
     "gqa_rope", "gqa_cache_write", "gqa_cache_read", "gqa_cache_attention",
-    "gqa_cache_attention_workspace",
+    "gqa_cache_attention_workspace", "gqa_prefill_backward", "gqa_prefill_backward_workspace",
 ]
 NOALLOC_SCRATCH_BYTES = 32 << 20  # the library's file-scope split-KV scratch (gqa_prefill.h)
 
@@ -145,8 +146,12 @@ def load(path: Optional[str] = None):
     lib.gqa_cache_attention.argtypes = [vp] * 5 + [i] + [vp] * 4 + [i] * 10 + [
         ctypes.c_float, i, vp, i, vp, vp, ll, vp, vp, vp, vp, ctypes.c_size_t, vp]
     lib.gqa_cache_attention_workspace.argtypes = [i] * 8 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.gqa_prefill_backward.argtypes = [vp] * 6 + [i] * 7 + [ctypes.c_float, i] + [vp] * 10 + [
+        ctypes.c_size_t, vp]
+    lib.gqa_prefill_backward_workspace.argtypes = [i] * 7 + [ctypes.POINTER(ctypes.c_size_t)]
     for f in (lib.gqa_rope, lib.gqa_cache_write, lib.gqa_cache_read, lib.gqa_cache_attention,
-              lib.gqa_cache_attention_workspace):
+              lib.gqa_cache_attention_workspace, lib.gqa_prefill_backward,
+              lib.gqa_prefill_backward_workspace):
         f.restype = i
     if path is None:
         _lib = lib
@@ -483,12 +488,12 @@ class PreparedOp:
 
 def prepare_call(function, *args, **kwargs) -> PreparedOp:
     """The call ``function(*args, **kwargs)`` marshalled once, to be issued by
-    calling the result.  For gqa_rope, gqa_cache_write, gqa_cache_read and
-    gqa_cache_attention."""
+    calling the result.  For gqa_rope, gqa_cache_write, gqa_cache_read,
+    gqa_cache_attention and gqa_prefill_backward."""
     marshal = _MARSHAL.get(function)
     if marshal is None:
-        raise ValueError("prepare_call takes gqa_rope, gqa_cache_write, gqa_cache_read or "
-                         "gqa_cache_attention")
+        raise ValueError("prepare_call takes gqa_rope, gqa_cache_write, gqa_cache_read, "
+                         "gqa_cache_attention or gqa_prefill_backward")
     return marshal(*args, **kwargs)
 
 
@@ -777,8 +782,110 @@ def gqa_cache_attention(q, k_pages, v_pages, cu_seqlens_q, prefix_lens, kv_page_
     return out
 
 
+# ------------------------------------------------------------------ gradients
+def _type_code(dtype) -> int:
+    if isinstance(dtype, int):
+        return dtype
+    return GQA_BF16 if "bf16" in str(dtype) or "bfloat16" in str(dtype) else GQA_F16
+
+
+def prefill_backward_workspace(num_seqs, total_q, total_kv, hq, hkv, d, dtype):
+    """Workspace bytes of a gqa_prefill_backward call with these shapes."""
+    nbytes = ctypes.c_size_t(0)
+    rc = load().gqa_prefill_backward_workspace(int(num_seqs), int(total_q), int(total_kv), int(hq),
+                                               int(hkv), int(d), _type_code(dtype),
+                                               ctypes.byref(nbytes))
+    if rc != GQA_OK:
+        raise GQAError(rc, "gqa_prefill_backward_workspace")
+    return nbytes.value
+
+
+def _float32(shape, **tensors):
+    import torch
+    for name, t in tensors.items():
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous float32 tensor {list(shape)}")
+
+
+def _marshal_prefill_backward(q, k, v, cu_seqlens_q, prefix_lens, kv_indptr, scale, out, lse, dout,
+                              dq, dk, dv, workspace, window=0, sinks=None, dsinks=None, dlse=None,
+                              stream=None):
+    _on_device(q=q, k=k, v=v, cu_seqlens_q=cu_seqlens_q, prefix_lens=prefix_lens,
+               kv_indptr=kv_indptr, out=out, lse=lse, dout=dout, dq=dq, dk=dk, dv=dv,
+               workspace=workspace, sinks=sinks, dsinks=dsinks, dlse=dlse)
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out), ("dout", dout), ("dq", dq),
+                    ("dk", dk), ("dv", dv)):
+        if t.dim() != 3 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [rows, heads, d] tensor")
+    for name, t, like in (("out", out, q), ("dout", dout, q), ("dq", dq, q), ("v", v, k),
+                          ("dk", dk, k), ("dv", dv, k)):
+        if t.shape != like.shape or t.dtype != q.dtype:
+            raise ValueError(f"{name} must have the shape and type of its input")
+    if k.dtype != q.dtype or k.shape[2] != q.shape[2]:
+        raise ValueError("k must have q's head dim and type")
+    _int32(cu_seqlens_q=cu_seqlens_q, prefix_lens=prefix_lens, kv_indptr=kv_indptr)
+    n = int(prefix_lens.numel())
+    if cu_seqlens_q.numel() != n + 1 or kv_indptr.numel() != n + 1:
+        raise ValueError("cu_seqlens_q and kv_indptr must have one entry more than prefix_lens")
+    total_q, hq, d = (int(x) for x in q.shape)
+    total_kv, hkv = int(k.shape[0]), int(k.shape[1])
+    if lse is None:
+        raise ValueError("lse is required")
+    _float32((total_q, hq), lse=lse, dlse=dlse)
+    _float32((hq,), sinks=sinks, dsinks=dsinks)
+    if dsinks is not None and sinks is None:
+        raise ValueError("dsinks needs sinks")
+    if dsinks is None:
+        sinks = None  # their gradient is left out; lse holds their weight
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return PreparedOp(load().gqa_prefill_backward,
+                      (_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens_q), _ptr(prefix_lens),
+                       _ptr(kv_indptr), n, total_q, total_kv, hq, hkv, d, _dtype_code(q),
+                       float(scale), int(window), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dlse),
+                       _ptr(sinks), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dsinks), _ptr(workspace),
+                       nbytes, _stream_handle(stream)), "gqa_prefill_backward",
+                      (q, k, v, cu_seqlens_q, prefix_lens, kv_indptr, out, lse, dout, dlse, sinks,
+                       dq, dk, dv, dsinks, workspace))
+
+
+def gqa_prefill_backward(q, k, v, cu_seqlens_q, prefix_lens, kv_indptr, scale, out, lse, dout, dq,
+                         dk, dv, workspace, window=0, sinks=None, dsinks=None, dlse=None,
+                         stream=None):
+    """The gradient of gqa_flash_prefill (see gqa_prefill.h) into ``dq``,
+    ``dk``, ``dv`` and, when given, ``dsinks``; ``workspace`` is a device
+    tensor of at least ``prefill_backward_workspace(...)`` bytes.  Returns
+    (dq, dk, dv)."""
+    _marshal_prefill_backward(q, k, v, cu_seqlens_q, prefix_lens, kv_indptr, scale, out, lse, dout,
+                              dq, dk, dv, workspace, window, sinks, dsinks, dlse, stream)()
+    return dq, dk, dv
+
+
+def prefill_backward(batch, out, lse, dout, dlse=None, workspace=None, stream=None):
+    """gqa_prefill_backward of one ``workloads.Batch`` already on the GPU, from
+    what ``prefill`` returned and the gradient of its out; allocates the
+    results (and the workspace, when not given) with torch.  Returns
+    (dq, dk, dv, dsinks), dsinks None for a batch without sinks."""
+    import torch
+    dq, dk, dv = (_result(t.shape, t.dtype, t.device, stream) for t in (batch.q, batch.k, batch.v))
+    dsinks = None
+    if batch.sinks is not None:
+        dsinks = _result(batch.sinks.shape, torch.float32, batch.q.device, stream)
+    if workspace is None:
+        size = prefill_backward_workspace(batch.num_seqs, batch.total_q, batch.total_kv, batch.hq,
+                                          batch.hkv, batch.d, batch.dtype_name)
+        with _allocating(stream):
+            workspace = torch.empty(size, dtype=torch.uint8, device=batch.q.device)
+    gqa_prefill_backward(batch.q, batch.k, batch.v, batch.cu_seqlens_q, batch.prefix_lens,
+                         batch.kv_indptr, batch.scale, out, lse, dout, dq, dk, dv, workspace,
+                         window=batch.window, sinks=batch.sinks, dsinks=dsinks, dlse=dlse,
+                         stream=stream)
+    return dq, dk, dv, dsinks
+
+
 _MARSHAL = {gqa_rope: _marshal_rope, gqa_cache_write: _marshal_cache_write,
-            gqa_cache_read: _marshal_cache_read, gqa_cache_attention: _marshal_cache_attention}
+            gqa_cache_read: _marshal_cache_read, gqa_cache_attention: _marshal_cache_attention,
+            gqa_prefill_backward: _marshal_prefill_backward}
 
 
 def cache_write(batch, cache, rope=None, stream=None):

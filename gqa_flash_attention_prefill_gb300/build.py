@@ -22,7 +22,8 @@ SOURCES = ["host.cu", "inst_d64.cu", "inst_d64_pair.cu", "inst_d128.cu", "inst_d
            "inst_split.cu", "inst_paged.cu", "inst_mask.cu", "inst_balanced.cu", "merge.cu",
            "noalloc.cu", "cache_rows.cu", "cache_attn.cu", "inst_cache_d64.cu",
            "inst_cache_d128.cu", "inst_cache_d256.cu",
-           "inst_cache_tile.cu"]
+           "inst_cache_tile.cu", "backward.cu", "inst_bwd_d64.cu", "inst_bwd_d128.cu",
+           "inst_bwd_d256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

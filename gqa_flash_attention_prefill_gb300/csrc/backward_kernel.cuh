@@ -1,0 +1,591 @@
+// backward_kernel.cuh -- the products of the attention's gradient on tcgen05.
+//
+// Mathematics: backward.h.  A unit keeps 128 rows of one side in shared memory
+// (A1, A2) and streams tiles of N rows of the other (B1, B2):
+//                 A1  A2    B1  B2    S = A1 B1^T   T = A2 B2^T
+//   dq unit       q   dout  k   v     S [queries, keys]
+//   dk, dv unit   k   v     q   dout  S^T [keys, queries]
+// Both products land in tensor memory with a row of A in each lane.  The
+// softmax warps turn S into P and T into dS = P (T - D), write both back in 16
+// bits over their own fp32 columns, and they are the left operand, in tensor
+// memory, of the second products  acc1 += dS B1 (dq or dk)  and  acc0 += P B2
+// (dv), whose right operand is the streamed tile read with its rows as the
+// contraction.  So P and dS never pass through shared memory, and every row of
+// the result has one writer: no atomics, the same bits run to run.  (The price
+// is that S and T are computed for both kinds of unit: 7 products, not 5.)
+//
+// CTA: 8 softmax warps (warpgroup w takes the columns of half w), a loading
+// warp, a warp that issues the products.  Persistent: units are taken from a
+// list sorted by cost with an atomic counter.
+#pragma once
+#include "backward.h"
+#include "launch.h"
+#include "prefill_kernel.cuh"
+#include "ptx.cuh"
+
+namespace gqa {
+
+constexpr int kBwdSoftWarps = 8;
+constexpr int kBwdThreads = 32 * (kBwdSoftWarps + 2);
+constexpr int kBwdRecs = 4;  // unit records in flight
+
+constexpr int bwd_a_buffers(int D) { return D == 64 ? 2 : 1; }
+constexpr int bwd_stages(int D) { return D == 64 ? 4 : D == 128 ? 2 : 1; }
+constexpr int bwd_s_buffers(int D) { return D == 64 ? 2 : 1; }
+constexpr uint32_t bwd_a_bytes(int D) { return 128u * D * 2u; }            // one tile
+constexpr uint32_t bwd_b_bytes(int D) { return (uint32_t)bwd_n(D) * D * 2u; }
+constexpr uint32_t bwd_stat_bytes(int D) { return 8u * bwd_n(D); }         // -lse, -D of a tile
+constexpr uint32_t bwd_smem(int D) {
+  return 1024u + bwd_a_buffers(D) * 2u * bwd_a_bytes(D) +
+         bwd_stages(D) * (2u * bwd_b_bytes(D) + bwd_stat_bytes(D)) + 64u * 8u + 16u +
+         kBwdRecs * 64u;
+}
+
+struct BwdBar {
+  static constexpr int kRecFull = 0, kRecEmpty = 4, kAFull = 8, kAEmpty = 10, kBFull = 12,
+                       kBEmpty = 16, kLand = 20, kSFull = 21, kPFull = 23, kTFull = 25, kDFull = 26,
+                       kAccDone = 27, kAccFree = 28, kDrain = 29, kCount = 30;
+};
+
+template <int D, bool BF16>
+struct Bwd {
+  static constexpr int N = bwd_n(D), NS = bwd_stages(D), NA = bwd_a_buffers(D),
+                       NSB = bwd_s_buffers(D), NCH = D / 64, CW = N / 2;
+  static constexpr uint32_t kABytes = bwd_a_bytes(D), kBBytes = bwd_b_bytes(D),
+                            kStat = bwd_stat_bytes(D);
+  static constexpr uint32_t kAChunk = 128u * 128u, kBChunk = N * 128u;
+  static constexpr uint32_t kColT = NSB * N, kColAcc0 = D == 64 ? 384 : 256,
+                            kColAcc1 = D == 64 ? 448 : D == 128 ? 384 : 256;
+  static_assert(kColT + N <= kColAcc0 && kColAcc1 + D <= 512, "tensor memory");
+};
+
+// One tile of one unit in the hands of a softmax thread: lane row `r` of A,
+// columns [col0, col0 + CW) of the tile.  lo, hi: the columns the row keeps.
+struct BwdTile {
+  uint32_t t_s, t_t;  // tensor-memory addresses of the thread's columns of S and T
+  uint32_t stats;     // shared memory: -lse of the tile's columns, then -D (dk, dv units)
+  float row_nlse, row_nd;
+  int lo, hi;
+  bool masked;
+};
+
+template <int KIND, int D, bool BF16>
+__device__ __forceinline__ bool bwd_tile(const BwdTile& t, float sl2, float mul, uint32_t bar_s,
+                                         uint32_t par_s, uint32_t bar_p, uint32_t bar_t,
+                                         uint32_t par_t, uint32_t bar_d,
+                                         volatile uint32_t* abort_flag, const BwdParams& p) {
+  constexpr int CW = Bwd<D, BF16>::CW;
+  auto wait = [&](uint32_t bar, uint32_t par) {
+    return __all_sync(0xffffffffu, wait_bounded(bar, par, abort_flag, p.status, p.timeout_ns));
+  };
+  if (!wait(bar_s, par_s)) return false;
+  tc_fence_after();
+  float x[CW];
+#pragma unroll
+  for (int c = 0; c < CW; c += 32)
+    tmem_ld32(t.t_s + c, *reinterpret_cast<uint32_t(*)[32]>(x + c));
+  tmem_wait_ld();
+  const uint64_t sc = f2(sl2, sl2);
+#pragma unroll
+  for (int c = 0; c < CW; c += 4) {
+    float l[4];
+    if constexpr (KIND == kBwdQ) {
+      l[0] = l[1] = l[2] = l[3] = t.row_nlse;
+    } else {
+      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                   : "=f"(l[0]), "=f"(l[1]), "=f"(l[2]), "=f"(l[3])
+                   : "r"(t.stats + 4u * c));
+    }
+    unf2(ffma2(f2(x[c], x[c + 1]), sc, f2(l[0], l[1])), x[c], x[c + 1]);
+    unf2(ffma2(f2(x[c + 2], x[c + 3]), sc, f2(l[2], l[3])), x[c + 2], x[c + 3]);
+  }
+  if (t.masked) {
+#pragma unroll
+    for (int c = 0; c < CW; ++c)
+      if (c < t.lo || c > t.hi) x[c] = -INFINITY;
+  }
+#pragma unroll
+  for (int c = 0; c < CW; ++c) x[c] = ex2(x[c]);
+  if constexpr (KIND == kBwdKV || KIND == kBwdV) {
+    // P in 16 bits, over this thread's own columns of S.
+    uint32_t pk[CW / 2];
+#pragma unroll
+    for (int c = 0; c < CW; c += 2) pk[c / 2] = pack2<BF16>(x[c], x[c + 1]);
+    if constexpr (CW == 64)
+      tmem_st32(t.t_s, *reinterpret_cast<uint32_t(*)[32]>(pk));
+    else
+      tmem_st16(t.t_s, *reinterpret_cast<uint32_t(*)[16]>(pk));
+    tmem_wait_st();
+  }
+  tc_fence_before();
+  mbar_arrive(bar_p);  // S is read (and P written)
+  if constexpr (KIND == kBwdV) return true;
+
+  if (!wait(bar_t, par_t)) return false;
+  tc_fence_after();
+  uint32_t dk[CW / 2];
+  const uint64_t rnd = f2(t.row_nd, t.row_nd), mm = f2(mul, mul);
+#pragma unroll
+  for (int h = 0; h < CW; h += 32) {
+    uint32_t y[32];
+    tmem_ld32(t.t_t + h, y);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+      uint64_t n0 = rnd, n1 = rnd;
+      if constexpr (KIND != kBwdQ) {
+        float l[4];
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(l[0]), "=f"(l[1]), "=f"(l[2]), "=f"(l[3])
+                     : "r"(t.stats + 4u * (uint32_t)Bwd<D, BF16>::N + 4u * (h + c)));
+        n0 = f2(l[0], l[1]);
+        n1 = f2(l[2], l[3]);
+      }
+      uint64_t a = fadd2(f2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), n0);
+      uint64_t b = fadd2(f2(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), n1);
+      if constexpr (!BF16) {  // f16: times a power of two, so that dS keeps its bits
+        a = fmul2(a, mm);
+        b = fmul2(b, mm);
+      }
+      float d0, d1, d2, d3;
+      unf2(fmul2(a, f2(x[h + c], x[h + c + 1])), d0, d1);
+      unf2(fmul2(b, f2(x[h + c + 2], x[h + c + 3])), d2, d3);
+      dk[(h + c) / 2] = pack2<BF16>(d0, d1);
+      dk[(h + c) / 2 + 1] = pack2<BF16>(d2, d3);
+    }
+  }
+  if constexpr (CW == 64)
+    tmem_st32(t.t_t, *reinterpret_cast<uint32_t(*)[32]>(dk));
+  else
+    tmem_st16(t.t_t, *reinterpret_cast<uint32_t(*)[16]>(dk));
+  tmem_wait_st();
+  tc_fence_before();
+  mbar_arrive(bar_d);
+  return true;
+}
+
+// `cols` accumulator columns of this lane's row, times `mul`, to a row of the
+// result or to a partial ([d / 4][128][4], from its column `col0`).
+template <int D, bool BF16>
+__device__ __forceinline__ void bwd_store(uint32_t t_acc, int cols, int col0, float mul,
+                                          uint16_t* row, float4* part, int r, bool zero) {
+#pragma unroll 1
+  for (int c = 0; c < cols; c += 32) {
+    uint32_t o[32];
+    if (!zero) {
+      tmem_ld32(t_acc + c, o);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = 0u;
+    }
+    if (part != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        part[(size_t)((col0 + c) / 4 + i) * 128 + r] =
+            make_float4(__uint_as_float(o[4 * i]) * mul, __uint_as_float(o[4 * i + 1]) * mul,
+                        __uint_as_float(o[4 * i + 2]) * mul, __uint_as_float(o[4 * i + 3]) * mul);
+    } else if (row != nullptr) {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        w[i] = pack2<BF16>(__uint_as_float(o[2 * i]) * mul, __uint_as_float(o[2 * i + 1]) * mul);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<uint4*>(row + col0 + c)[i] =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+  }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    backward_kernel(const __grid_constant__ BwdParams p) {
+  using K = Bwd<D, BF16>;
+  using B = BwdBar;
+  constexpr int N = K::N, NS = K::NS, NA = K::NA, NSB = K::NSB, NCH = K::NCH, CW = K::CW;
+  constexpr int kLoadWarp = kBwdSoftWarps, kMmaWarp = kBwdSoftWarps + 1;
+  constexpr uint32_t kIdescS = idesc_f16(BF16, 128, N, false);
+  constexpr uint32_t kIdescO = idesc_f16(BF16, 128, D, true);
+
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sA = smem_u32(smem);                      // [NA][2] tiles
+  const uint32_t sB = sA + NA * 2u * K::kABytes;           // [NS][2] tiles
+  const uint32_t sStat = sB + NS * 2u * K::kBBytes;        // [NS] -lse, -D
+  uint8_t* tail = smem + NA * 2u * K::kABytes + NS * (2u * K::kBBytes + K::kStat);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(tail);
+  const uint32_t sBar = smem_u32(bars);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 64);  // [0] tensor memory, [1] abort
+  int32_t* recs = reinterpret_cast<int32_t*>(misc + 4);     // [kBwdRecs][16]
+  volatile uint32_t* abort_flag = misc + 1;
+  auto bar = [&](int i) { return sBar + 8u * (uint32_t)i; };
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < B::kCount; ++i) {
+      uint32_t cnt = 1u;
+      if (i >= B::kRecEmpty && i < B::kRecEmpty + kBwdRecs) cnt = kBwdSoftWarps + 1u;
+      if (i == B::kPFull || i == B::kPFull + 1 || i == B::kDFull || i == B::kAccFree)
+        cnt = 32u * kBwdSoftWarps;
+      mbar_init(bar(i), cnt);
+    }
+    misc[1] = 0u;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(misc), 512u);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  const int items = p.hdr[kBwdUnits] * p.Hkv;
+
+  // ---------------------------------------------------------------- loads
+  if (warp == kLoadWarp) {
+    auto wait = [&](int b, uint32_t par) {
+      return __all_sync(0xffffffffu,
+                        wait_bounded(bar(b), par, abort_flag, p.status, p.timeout_ns));
+    };
+    uint32_t it = 0, ua = 0, lands = 0;
+    for (uint32_t un = 0;; ++un) {
+      const uint32_t rs = un % kBwdRecs;
+      if (!wait(B::kRecEmpty + rs, ((un / kBwdRecs) & 1u) ^ 1u)) break;
+      int item = (int)blockIdx.x;
+      if (un > 0) {
+        if (lane == 0) item = (int)gridDim.x + atomicAdd(&p.hdr[kBwdNext], 1);
+        item = __shfl_sync(0xffffffffu, item, 0);
+      }
+      const bool end = item >= items;
+      const int e = end ? 0 : item / p.Hkv, g = end ? 0 : item - e * p.Hkv;
+      int word = 0;
+      if (lane < 16) {
+        word = end ? -1 : reinterpret_cast<const int32_t*>(p.units + e)[lane];
+        if (lane == 13) word = g;
+        recs[rs * 16 + lane] = word;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B::kRecFull + rs));
+      if (end) break;
+      auto field = [&](int i) { return __shfl_sync(0xffffffffu, word, i); };
+      const int kind = field(0), n = field(1), a_base = field(2), a_off = field(3),
+                b_base = field(5), b_off = field(6), b_len = field(7), stat = field(11);
+      if (n == 0) continue;
+      const bool qa = kind == kBwdQ;
+      const uint32_t ab = ua % NA;
+      if (!wait(B::kAEmpty + ab, ((ua / NA) & 1u) ^ 1u)) break;
+      if (lane == 0) {
+        const uint32_t full = bar(B::kAFull + ab), dst = sA + ab * 2u * K::kABytes;
+        mbar_arrive_expect_tx(full, 2u * K::kABytes);
+        // Queries are counted in packed rows, token by token: the G heads of a
+        // KV head, one after the other.  A tile of 128 starts at a token.
+        const int head = qa ? g * p.G : g, row = a_base + (qa ? a_off >> p.log_G : a_off);
+        for (int c = 0; c < NCH; ++c) {
+          tma_load_3d(dst + c * K::kAChunk, qa ? &p.a_q : &p.a_k, full, c * 64, head, row);
+          tma_load_3d(dst + K::kABytes + c * K::kAChunk, qa ? &p.a_do : &p.a_v, full, c * 64, head,
+                      row);
+        }
+      }
+      ++ua;
+      bool ok = true;
+      for (int j = 0; j < n; ++j, ++it) {
+        const uint32_t s = it % NS;
+        if (!(ok = wait(B::kBEmpty + s, ((it / NS) & 1u) ^ 1u))) break;
+        const int off = b_off + j * N, valid = b_len - off;
+        const bool whole = valid >= N;
+        const uint32_t dst = sB + s * 2u * K::kBBytes;
+        const uint32_t full = bar(whole ? B::kBFull + s : B::kLand);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full, 2u * K::kBBytes + (qa ? 0u : K::kStat));
+          const int head = qa ? g : g * p.G + (off & (p.G - 1));
+          const int row = b_base + (qa ? off : off >> p.log_G);
+          for (int c = 0; c < NCH; ++c) {
+            tma_load_3d(dst + c * K::kBChunk, qa ? &p.b_k : &p.b_q, full, c * 64, head, row);
+            tma_load_3d(dst + K::kBBytes + c * K::kBChunk, qa ? &p.b_v : &p.b_do, full, c * 64, head,
+                        row);
+          }
+          if (!qa) {
+            const size_t at = (size_t)g * p.stat_rows + stat + off;
+            bulk_load(sStat + s * K::kStat, p.nlse + at, 4u * N, full);
+            bulk_load(sStat + s * K::kStat + 4u * N, p.nd + at, 4u * N, full);
+          }
+        }
+        if (!whole) {
+          // Rows past the sequence's last are another's, or hold anything: they
+          // become zeros, so that their zero probabilities add nothing.
+          const bool landed = wait(B::kLand, lands & 1u);
+          ++lands;
+          if (!(ok = landed)) {
+            ++it;
+            break;
+          }
+          for (int c = 0; c < 2 * NCH; ++c)
+            for (int x = valid * 128 + lane * 16; x < N * 128; x += 512)
+              st_shared_v4(dst + c * K::kBChunk + x, 0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B::kBFull + s));
+        }
+      }
+      if (!ok) break;
+    }
+    // Let every copy issued land before the CTA can exit.
+    if (*abort_flag) {
+      for (uint32_t b = 0; b < NA; ++b)
+        if (ua > b)
+          wait_drain(bar(B::kAFull + (ua - 1u - b) % NA), ((ua - 1u - b) / NA) & 1u, p.timeout_ns);
+      if (lands > 0) wait_drain(bar(B::kLand), (lands - 1u) & 1u, p.timeout_ns);
+      for (uint32_t b = 0; b < NS; ++b)
+        if (it > b)
+          wait_drain(bar(B::kBFull + (it - 1u - b) % NS), ((it - 1u - b) / NS) & 1u, p.timeout_ns);
+    }
+    __syncwarp();
+  }
+
+  // ---------------------------------------------------------------- products
+  if (warp == kMmaWarp) {
+    const uint64_t dA0 = smem_desc_sw128(sA, 16, 1024);
+    const uint64_t dB0 = smem_desc_sw128(sB, 16, 1024);           // rows are N
+    const uint64_t dBt0 = smem_desc_sw128(sB, K::kBChunk, 1024);  // rows are the contraction
+    auto kstep = [](int kk, uint32_t chunk) -> uint64_t {
+      return (uint64_t)(((uint32_t)(kk >> 2) * chunk + (uint32_t)(kk & 3) * 32u) >> 4);
+    };
+    auto wait = [&](int b, uint32_t par) {
+      return __all_sync(0xffffffffu,
+                        wait_bounded(bar(b), par, abort_flag, p.status, p.timeout_ns));
+    };
+    // it: tiles; td: tiles with a T; uc: units with tiles.
+    uint32_t it = 0, td = 0, uc = 0;
+    bool ok = true;
+    for (uint32_t un = 0; ok; ++un) {
+      const uint32_t rs = un % kBwdRecs;
+      if (!(ok = wait(B::kRecFull + rs, (un / kBwdRecs) & 1u))) break;
+      const int kind = recs[rs * 16], n = recs[rs * 16 + 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B::kRecEmpty + rs));
+      if (kind < 0) break;
+      if (n == 0) continue;
+      const bool has_t = kind != kBwdV, has_p = kind == kBwdKV || kind == kBwdV;
+      const uint32_t ab = uc % NA;
+      if (!(ok = wait(B::kAFull + ab, (uc / NA) & 1u))) break;
+      const uint64_t dA1 = dA0 + ab * 2u * (K::kABytes >> 4), dA2 = dA1 + (K::kABytes >> 4);
+      auto issue_s = [&](uint32_t t) -> bool {  // S of tile t, once it is in
+        const uint32_t s = t % NS;
+        if (!wait(B::kBFull + s, (t / NS) & 1u)) return false;
+        tc_fence_after();
+        const uint64_t b1 = dB0 + s * 2u * (K::kBBytes >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(tmem + (t % NSB) * N, dA1 + kstep(kk, K::kAChunk), b1 + kstep(kk, K::kBChunk),
+                 kIdescS, kk > 0 ? 1u : 0u);
+        mma_commit(bar(B::kSFull + t % NSB));
+        return true;
+      };
+      // acc (+)= (the 16-bit tile at `src`) B: the tile's two halves stand
+      // each at the start of their fp32 columns.
+      auto issue_acc = [&](uint32_t acc, uint32_t src, uint64_t b, bool first) {
+#pragma unroll
+        for (int kk = 0; kk < N / 16; ++kk)
+          mma_ts(acc, src + (kk / (N / 32)) * (N / 2) + (kk % (N / 32)) * 8,
+                 b + (uint64_t)(kk * 128), kIdescO, (first && kk == 0) ? 0u : 1u);
+      };
+      if constexpr (NS > 1) {
+        if (!(ok = issue_s(it))) break;
+      }
+      for (int j = 0; j < n; ++j, ++it) {
+        const uint32_t s = it % NS, sb = it % NSB;
+        if constexpr (NS == 1) {
+          if (!(ok = issue_s(it))) break;
+        }
+        const uint64_t dB = dB0 + s * 2u * (K::kBBytes >> 4), dBt = dBt0 + s * 2u * (K::kBBytes >> 4);
+        if (has_t) {
+          const uint64_t b2 = dB + (K::kBBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tmem + K::kColT, dA2 + kstep(kk, K::kAChunk), b2 + kstep(kk, K::kBChunk), kIdescS,
+                   kk > 0 ? 1u : 0u);
+          mma_commit(bar(B::kTFull));
+        }
+        if (j == n - 1) mma_commit(bar(B::kAEmpty + ab));
+        if constexpr (NSB == 2) {
+          if (j + 1 < n && !(ok = issue_s(it + 1))) break;
+        }
+        if (!(ok = wait(B::kPFull + (it & 1u), (it >> 1) & 1u))) break;
+        if (j == 0 && uc > 0 && !(ok = wait(B::kAccFree, (uc - 1u) & 1u))) break;
+        tc_fence_after();
+        if (has_p)
+          issue_acc(tmem + K::kColAcc0, tmem + sb * N, dBt + (K::kBBytes >> 4), j == 0);
+        if constexpr (NS > 1 && NSB == 1) {
+          if (j + 1 < n && !(ok = issue_s(it + 1))) break;
+        }
+        if (has_t) {
+          if (!(ok = wait(B::kDFull, td & 1u))) break;
+          tc_fence_after();
+          issue_acc(tmem + K::kColAcc1, tmem + K::kColT, dBt, j == 0);
+          ++td;
+        }
+        mma_commit(bar(B::kBEmpty + s));
+      }
+      if (!ok) break;
+      mma_commit(bar(B::kAccDone));
+      ++uc;
+    }
+    mma_commit(bar(B::kDrain));
+    wait_drain(bar(B::kDrain), 0u, p.timeout_ns);
+    __syncwarp();
+  }
+
+  // ---------------------------------------------------------------- softmax, results
+  if (warp < kBwdSoftWarps) {
+    const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const float sl2 = p.scale_log2;
+    auto wait = [&](int b, uint32_t par) {
+      return __all_sync(0xffffffffu,
+                        wait_bounded(bar(b), par, abort_flag, p.status, p.timeout_ns));
+    };
+    uint32_t it = 0, td = 0, uc = 0;
+    bool ok = true;
+    for (uint32_t un = 0; ok; ++un) {
+      const uint32_t rs = un % kBwdRecs;
+      if (!(ok = wait(B::kRecFull + rs, (un / kBwdRecs) & 1u))) break;
+      const int32_t* rec = recs + rs * 16;
+      const int kind = rec[0], n = rec[1], a_base = rec[2], a_off = rec[3], a_valid = rec[4],
+                b_off = rec[6], P = rec[8], E = rec[9], slot = rec[10], stat = rec[11],
+                seq = rec[12], g = rec[13];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B::kRecEmpty + rs));
+      if (kind < 0) break;
+      const bool qa = kind == kBwdQ;
+      BwdTile t;
+      t.row_nlse = t.row_nd = 0.f;
+      if (qa) {
+        const size_t at = (size_t)g * p.stat_rows + stat + a_off + r;
+        t.row_nlse = __ldcg(p.nlse + at);
+        t.row_nd = __ldcg(p.nd + at);
+      }
+      float mul = 1.f, undo = 1.f;  // of dS, and of the results it enters
+      if constexpr (!BF16) {
+        const int k = bwd_exponent(p.most + ((size_t)seq * p.Hkv + g) * 4);
+        mul = ldexpf(1.f, k - (int)kBwdBias);
+        undo = ldexpf(1.f, -k);
+      }
+      // Columns the row keeps, counted from B's first row: key or packed row
+      // c of tile j is kept iff lo0 <= b_off + j N + c <= hi0.
+      const int last = a_off + a_valid - 1;
+      int lo0, hi0, lo_max, hi_min;  // this row's; over the rows: the largest lo0, the least hi0
+      auto bounds = [&](int a, int& lo, int& hi) {
+        if (qa) {
+          const int pos = P + (a >> p.log_G);
+          hi = pos;
+          lo = p.window > 0 ? pos - p.window + 1 : 0;
+        } else {
+          lo = max(a - P, 0) * p.G;
+          const long long i = p.window > 0 ? (long long)a + p.window - P : (long long)E;
+          hi = (int)(i < 0 ? 0 : i < (long long)E ? i : (long long)E) * p.G - 1;
+        }
+      };
+      {
+        int x;
+        bounds(a_off + r, lo0, hi0);
+        bounds(last, lo_max, x);
+        bounds(a_off, x, hi_min);
+        lo0 -= half * CW;
+        hi0 -= half * CW;
+      }
+      for (int j = 0; j < n; ++j, ++it) {
+        const uint32_t s = it % NS, sb = it % NSB;
+        const int off = b_off + j * N;
+        t.t_s = t_lane + sb * N + half * CW;
+        t.t_t = t_lane + K::kColT + half * CW;
+        t.stats = sStat + s * K::kStat + (uint32_t)half * CW * 4u;
+        t.lo = lo0 - off;
+        t.hi = hi0 - off;
+        t.masked = lo_max > off || hi_min < off + N - 1;
+        const uint32_t bs = bar(B::kSFull + sb), ps = (it / NSB) & 1u, bp = bar(B::kPFull + (it & 1u)),
+                       bt = bar(B::kTFull), bd = bar(B::kDFull);
+        if (qa) {
+          ok = bwd_tile<kBwdQ, D, BF16>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+        } else {
+          // The statistics came with B (this thread has to see their barrier).
+          if (!(ok = wait(B::kBFull + s, (it / NS) & 1u))) break;
+          if constexpr (D < 256)
+            ok = bwd_tile<kBwdKV, D, BF16>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+          else if (kind == kBwdK)
+            ok = bwd_tile<kBwdK, D, BF16>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+          else
+            ok = bwd_tile<kBwdV, D, BF16>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+        }
+        if (!ok) break;
+        if (kind != kBwdV) ++td;
+      }
+      if (!ok) break;
+      if (n > 0) {
+        if (!(ok = wait(B::kAccDone, uc & 1u))) break;
+        tc_fence_after();
+      }
+      // Warpgroup `half` takes dv (0) or dk (1) of a unit with both, else half
+      // of the columns of its one result.
+      const bool both = kind == kBwdKV;
+      const bool is_v = kind == kBwdV || (both && half == 0);
+      const float out_mul = is_v ? (BF16 ? 1.f : 1.f / 32768.f) : p.scale * undo;
+      const uint32_t acc = is_v ? K::kColAcc0 : K::kColAcc1;
+      const int cols = both ? D : D / 2, col0 = both ? 0 : half * (D / 2);
+      uint16_t* row = nullptr;
+      float4* part = nullptr;
+      if (slot >= 0) {
+        part = reinterpret_cast<float4*>(p.part) +
+               (((size_t)slot * p.Hkv + g) * bwd_accs(D) + (both && half == 1 ? 1 : 0)) * (D / 4) * 128;
+      } else if (r < a_valid) {
+        if (qa) {
+          const int a = a_off + r;
+          row = static_cast<uint16_t*>(p.dq) +
+                ((size_t)(a_base + (a >> p.log_G)) * p.Hq + g * p.G + (a & (p.G - 1))) * D;
+        } else {
+          row = static_cast<uint16_t*>(is_v ? p.dv : p.dk) + ((size_t)(a_base + a_off + r) * p.Hkv + g) * D;
+        }
+      }
+      bwd_store<D, BF16>(t_lane + acc + col0, cols, col0, out_mul, row, part, r, n == 0);
+      if (n > 0) {
+        tc_fence_before();
+        mbar_arrive(bar(B::kAccFree));
+        ++uc;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && *abort_flag) p.hdr[kBwdFailed] = 1;  // nothing is joined
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512u);
+}
+
+namespace {
+
+template <int D, bool BF16>
+cudaError_t launch_backward(const BwdParams& p, cudaStream_t st) {
+  auto kern = backward_kernel<D, BF16>;
+  static SmemAttr attr{};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  constexpr unsigned smem = bwd_smem(D);
+  static_assert(smem <= 227u * 1024u, "shared memory");
+  if (attr.allowed[dev].load(std::memory_order_acquire) < smem) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attr.allowed[dev].store(smem, std::memory_order_release);
+  }
+  return launch_pdl(kern, p, p.ctas, kBwdThreads, smem, st);
+}
+
+}  // namespace
+
+}  // namespace gqa

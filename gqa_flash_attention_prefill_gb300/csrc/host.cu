@@ -881,6 +881,11 @@ int call_device(int* sms, unsigned int** status) {
 
 unsigned long long wait_limit_ns() { return timeout_ns(); }
 
+int rows_map(CUtensorMap* m, const void* base, int dtype, int d, int heads, int rows,
+             int box_heads, int box_rows) {
+  return encode_map(m, base, dtype, d, heads, rows, box_heads, box_rows);
+}
+
 bool metadata_ready_flag() { return (t_call_flags & GQA_FLAG_METADATA_READY) != 0u; }
 
 bool kernel_shape(int d, int block_n, int q_tiles, KernelShape* out) {

@@ -1,0 +1,10 @@
+// Instantiations of the gradient's products for head dim 256.
+#include "backward_kernel.cuh"
+
+namespace gqa {
+
+cudaError_t launch_bwd_d256(const BwdParams& p, bool bf16, cudaStream_t st) {
+  return bf16 ? launch_backward<256, true>(p, st) : launch_backward<256, false>(p, st);
+}
+
+}  // namespace gqa

@@ -68,6 +68,11 @@ int call_device(int* sms, unsigned int** status);
 unsigned long long wait_limit_ns();
 bool metadata_ready_flag();
 
+// Tensor map of 16-bit rows [rows, heads, d], 64-value boxes of box_heads heads
+// of box_rows rows, 128-byte swizzle, zero fill (host.cu).  GQA_OK or GQA_ERR_CUDA.
+int rows_map(CUtensorMap* m, const void* base, int dtype, int d, int heads, int rows,
+             int box_heads, int box_rows);
+
 // Scratch provider of a split-KV call without a caller workspace: given the
 // bytes the call's plan needs, stores the scratch address and its capacity,
 // or returns GQA_ERR_UNSUPPORTED when the need exceeds the capacity.

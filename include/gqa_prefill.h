@@ -364,6 +364,55 @@ GQA_API int gqa_cache_attention(const void* q, const void* k_pages, const void* 
 GQA_API int gqa_cache_attention_workspace(int num_seqs, int total_q, int max_seqlen_q, int Hq,
                                           int Hkv, int d, int dtype, int cache_type, size_t* bytes);
 
+/*
+ * gqa_prefill_backward -- the gradient of gqa_flash_prefill: given dout, the
+ * gradient of its out (and dlse, of its lse), those of q, k, v and the sinks.
+ * With s_ij, the kept pairs, out and lse of gqa_flash_prefill's definition,
+ *     p_ij = e^(s_ij - lse_i)                D_i = <dout_i, out_i> - dlse_i
+ *     dv_j = sum_i p_ij dout_i               ds_ij = p_ij (<dout_i, v_j> - D_i)
+ *     dq_i = scale sum_j ds_ij k_j           dk_j = scale sum_i ds_ij q_i
+ *     dsinks_h = -sum_i e^(sinks_h - lse_ih) D_ih
+ * dk_j and dv_j sum over the Hq / Hkv query heads of the KV head, and over
+ * prefix keys as well as new ones: the prefix takes its gradient too.  lse
+ * holds the sink or the smooth_softmax "+1" already, so the latter is no
+ * argument here.
+ *
+ *   q .. kv_indptr, scale, window   as the forward call had them
+ *   out, lse      what it returned: [total_q, Hq, d] and fp32 [total_q, Hq]
+ *   dout          [total_q, Hq, d]
+ *   dlse          fp32 [total_q, Hq], or NULL for none
+ *   sinks, dsinks fp32 [Hq], both or neither (a call may leave the sinks'
+ *                 gradient out)
+ *   dq, dk, dv    as q, k, v; overwritten, not added to.  Every row of a
+ *                 sequence is written (keys that no query sees get zeros),
+ *                 rows outside every sequence are left as they were.
+ *   workspace     device memory of the caller, 256-byte aligned, at least
+ *                 gqa_prefill_backward_workspace() bytes; its contents mean
+ *                 nothing before and after.  Calls that may run at the same
+ *                 time, captured graphs included, need one each.
+ *
+ * Rows of a sequence hold finite values; rows outside every sequence may hold
+ * anything.  16-bit tensors are 16-byte aligned.  Results share no memory with
+ * one another or with an argument (GQA_ERR_INVALID).  Hq / Hkv is a power of
+ * two up to 128; d is 64, 128 or 256.  Sums are fp32; p and ds are rounded once
+ * to the inputs' type for their products (in f16 they are scaled by powers of
+ * two first, so that small ones keep their bits).  The result is the same run
+ * to run.  Four kernels are enqueued on `stream`.  Metadata, waits and return
+ * codes as gqa_flash_prefill; a missing or small workspace is GQA_ERR_INVALID.
+ */
+GQA_API int gqa_prefill_backward(const void* q, const void* k, const void* v,
+                                 const int32_t* cu_seqlens_q, const int32_t* prefix_lens,
+                                 const int32_t* kv_indptr, int num_seqs, int total_q, int total_kv,
+                                 int Hq, int Hkv, int d, int dtype, float scale, int window,
+                                 const void* out, const float* lse, const void* dout,
+                                 const float* dlse, const float* sinks, void* dq, void* dk,
+                                 void* dv, float* dsinks, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of a gqa_prefill_backward call with these shapes (host only). */
+GQA_API int gqa_prefill_backward_workspace(int num_seqs, int total_q, int total_kv, int Hq,
+                                           int Hkv, int d, int dtype, size_t* bytes);
+
 /* num_splits value selecting the balanced split (see below). */
 #define GQA_SPLITS_BALANCED (-1)
 
