@@ -26,9 +26,11 @@ __all__ = ["load", "gqa_flash_prefill", "gqa_flash_prefill_debug", "prefill", "p
            "gqa_cache_read", "gqa_cache_attention", "cache_attention_workspace",
            "prepare_call", "PreparedOp", "cache_write", "cache_read", "cache_attention",
            "gqa_prefill_backward", "prefill_backward_workspace", "prefill_backward",
+           "gqa_rms_norm", "rms_norm", "gqa_rms_norm_backward", "rms_norm_backward_workspace",
+           "rms_norm_backward", "GQA_F32",
            "EXPORTED_SYMBOLS"]
 
-GQA_F16, GQA_BF16 = 0, 1
+GQA_F16, GQA_BF16, GQA_F32 = 0, 1, 2  # GQA_F32: residual streams and weights of the norm only
 GQA_OK, GQA_ERR_INVALID, GQA_ERR_UNSUPPORTED, GQA_ERR_CUDA = 0, -1, -2, -3
 GQA_DEV_TIMEOUT, GQA_DEV_BAD_METADATA = 1, 2
 SPLITS_BALANCED = -1  # num_splits of the balanced split (GQA_SPLITS_BALANCED)
@@ -47,6 +49,7 @@ EXPORTED_SYMBOLS = [
     "gqa_prefill_set_call_flags", "gqa_prefill_get_call_flags",
     "gqa_rope", "gqa_cache_write", "gqa_cache_read", "gqa_cache_attention",
     "gqa_cache_attention_workspace", "gqa_prefill_backward", "gqa_prefill_backward_workspace",
+    "gqa_rms_norm", "gqa_rms_norm_backward", "gqa_rms_norm_backward_workspace",
 ]
 NOALLOC_SCRATCH_BYTES = 32 << 20  # the library's file-scope split-KV scratch (gqa_prefill.h)
 
@@ -149,9 +152,15 @@ def load(path: Optional[str] = None):
     lib.gqa_prefill_backward.argtypes = [vp] * 6 + [i] * 7 + [ctypes.c_float, i] + [vp] * 10 + [
         ctypes.c_size_t, vp]
     lib.gqa_prefill_backward_workspace.argtypes = [i] * 7 + [ctypes.POINTER(ctypes.c_size_t)]
+    lib.gqa_rms_norm.argtypes = [vp, ll, vp, vp, i, vp, i, ctypes.c_float, ctypes.c_float] + [i] * 6 + [
+        vp, ll, vp, vp, vp]
+    lib.gqa_rms_norm_backward.argtypes = [vp, ll, vp, ll, i, vp, vp, i, ctypes.c_float, vp] + [i] * 4 + [
+        vp, ll, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.gqa_rms_norm_backward_workspace.argtypes = [i] * 4 + [ctypes.POINTER(ctypes.c_size_t)]
     for f in (lib.gqa_rope, lib.gqa_cache_write, lib.gqa_cache_read, lib.gqa_cache_attention,
               lib.gqa_cache_attention_workspace, lib.gqa_prefill_backward,
-              lib.gqa_prefill_backward_workspace):
+              lib.gqa_prefill_backward_workspace, lib.gqa_rms_norm, lib.gqa_rms_norm_backward,
+              lib.gqa_rms_norm_backward_workspace):
         f.restype = i
     if path is None:
         _lib = lib
@@ -489,11 +498,13 @@ class PreparedOp:
 def prepare_call(function, *args, **kwargs) -> PreparedOp:
     """The call ``function(*args, **kwargs)`` marshalled once, to be issued by
     calling the result.  For gqa_rope, gqa_cache_write, gqa_cache_read,
-    gqa_cache_attention and gqa_prefill_backward."""
+    gqa_cache_attention, gqa_prefill_backward, gqa_rms_norm and
+    gqa_rms_norm_backward."""
     marshal = _MARSHAL.get(function)
     if marshal is None:
         raise ValueError("prepare_call takes gqa_rope, gqa_cache_write, gqa_cache_read, "
-                         "gqa_cache_attention or gqa_prefill_backward")
+                         "gqa_cache_attention, gqa_prefill_backward, gqa_rms_norm or "
+                         "gqa_rms_norm_backward")
     return marshal(*args, **kwargs)
 
 
@@ -883,9 +894,193 @@ def prefill_backward(batch, out, lse, dout, dlse=None, workspace=None, stream=No
     return dq, dk, dv, dsinks
 
 
+# ------------------------------------------------------------------ the norm
+def _norm_rows(name, t, like=None):
+    """(rows, heads, n, row stride) of [rows, n] or [rows, heads, n] with
+    packed heads."""
+    if t.dim() == 2:
+        t = t.unsqueeze(1)
+    if like is not None and tuple(t.shape) != like:
+        raise ValueError(f"{name} must have the shape of the rows")
+    stride = _rows(name, t)
+    return (*(int(x) for x in t.shape), stride)
+
+
+def _norm_type(name, t, dtype) -> int:
+    """GQA_* code of a residual stream or a weight: the rows' type, or float32."""
+    import torch
+    if t.dtype == torch.float32:
+        return GQA_F32
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must have the rows' type or be float32, got {t.dtype}")
+    return _dtype_code(t)
+
+
+def _norm_weight(weight, n, dtype) -> int:
+    if weight.dim() != 1 or weight.numel() != n or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous vector of one value per column")
+    return _norm_type("weight", weight, dtype)
+
+
+def _norm_stream(name, t, shape):
+    if t is not None and (tuple(t.unsqueeze(1).shape if t.dim() == 2 else t.shape) != shape
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous and have the shape of the rows")
+
+
+def _norm_rstd(rstd, rows, heads):
+    import torch
+    if rstd is not None and (rstd.dtype != torch.float32 or rstd.numel() != rows * heads
+                             or not rstd.is_contiguous()):
+        raise ValueError("rstd must be a contiguous float32 tensor of one value per row and head")
+
+
+def _marshal_rms_norm(x, weight, out, eps=1e-5, offset=0.0, residual=None, residual_out=None,
+                      scales=None, rstd=None, stream=None):
+    import torch
+    _on_device(x=x, weight=weight, out=out, residual=residual, residual_out=residual_out,
+               scales=scales, rstd=rstd)
+    rows, heads, n, xs = _norm_rows("x", x)
+    shape = (rows, heads, n)
+    os_ = _norm_rows("out", out, shape)[3]
+    code, wtype = _dtype_code(x), _norm_weight(weight, n, x.dtype)
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out go together")
+    _norm_stream("residual", residual, shape)
+    _norm_stream("residual_out", residual_out, shape)
+    stype = code
+    if residual is not None:
+        stype = _norm_type("residual", residual, x.dtype)
+        if residual_out.dtype != residual.dtype:
+            raise ValueError("residual_out must have residual's type")
+    _norm_rstd(rstd, rows, heads)
+    kind, group = GQA_CACHE_16, 0
+    if scales is not None:
+        if out.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise TypeError(f"out with scales must be e4m3, got {out.dtype}")
+        groups = int(scales.shape[-1]) if scales.dim() == out.dim() else 0
+        if (groups <= 0 or n % groups != 0 or scales.element_size() != 1
+                or scales.shape[:-1] != out.shape[:-1] or not scales.is_contiguous()):
+            raise ValueError("scales must be a contiguous byte tensor [rows, heads, groups], as many "
+                             "dimensions as out, whose groups divide the columns")
+        kind, group = GQA_CACHE_E4M3, n // groups
+    elif out.dtype != x.dtype:
+        raise TypeError(f"out must have x's type, or be e4m3 with scales, got {out.dtype}")
+    return PreparedOp(load().gqa_rms_norm,
+                      (_ptr(x), xs, _ptr(residual), _ptr(residual_out), stype, _ptr(weight), wtype,
+                       float(offset), float(eps), rows, heads, n, code, kind, group, _ptr(out), os_,
+                       _ptr(scales), _ptr(rstd), _stream_handle(stream)), "gqa_rms_norm",
+                      (x, residual, residual_out, weight, out, scales, rstd))
+
+
+def gqa_rms_norm(x, weight, out, eps=1e-5, offset=0.0, residual=None, residual_out=None,
+                 scales=None, rstd=None, stream=None):
+    """Root-mean-square norm of each row's last dimension, x [rows, n] or
+    [rows, heads, n] (a slice of a packed projection will do), after the
+    addition of ``residual`` (into ``residual_out``), into ``out``: x's type, or
+    e4m3 with byte ``scales`` [.., n / group].  ``rstd`` is kept for the
+    gradient.  See gqa_prefill.h; returns ``out``."""
+    _marshal_rms_norm(x, weight, out, eps, offset, residual, residual_out, scales, rstd, stream)()
+    return out
+
+
+def rms_norm(x, weight, eps=1e-5, offset=0.0, residual=None, group=None, with_rstd=False,
+             stream=None):
+    """gqa_rms_norm into new tensors; ``group`` values share a scale of an e4m3
+    output (None: an output of x's type).  Returns (out, scales or None, h, rstd
+    or None) with h the sum with the residual, or x itself."""
+    import torch
+    dtype = x.dtype if group is None else torch.float8_e4m3fn
+    out = _result(x.shape, dtype, x.device, stream)
+    scales = h = rstd = None
+    if group is not None:
+        if group <= 0 or x.shape[-1] % group != 0:
+            raise ValueError("group must divide the columns")
+        scales = _result((*x.shape[:-1], x.shape[-1] // group), torch.uint8, x.device, stream)
+    if residual is not None:
+        h = _result(x.shape, residual.dtype, x.device, stream)
+    if with_rstd:
+        rstd = _result(x.shape[:-1], torch.float32, x.device, stream)
+    gqa_rms_norm(x, weight, out, eps, offset, residual, h, scales, rstd, stream)
+    return out, scales, x if h is None else h, rstd
+
+
+def rms_norm_backward_workspace(rows, heads, n, dtype):
+    """Workspace bytes of a gqa_rms_norm_backward call with these shapes."""
+    nbytes = ctypes.c_size_t(0)
+    rc = load().gqa_rms_norm_backward_workspace(int(rows), int(heads), int(n), _type_code(dtype),
+                                                ctypes.byref(nbytes))
+    if rc != GQA_OK:
+        raise GQAError(rc, "gqa_rms_norm_backward_workspace")
+    return nbytes.value
+
+
+def _marshal_rms_norm_backward(dy, h, weight, rstd, dx=None, dresidual=None, dweight=None,
+                               workspace=None, offset=0.0, dh=None, stream=None):
+    import torch
+    _on_device(dy=dy, h=h, weight=weight, rstd=rstd, dx=dx, dresidual=dresidual, dweight=dweight,
+               workspace=workspace, dh=dh)
+    if rstd is None:
+        raise ValueError("rstd is required")
+    rows, heads, n, ys = _norm_rows("dy", dy)
+    shape = (rows, heads, n)
+    hs = _norm_rows("h", h, shape)[3]
+    code, wtype = _dtype_code(dy), _norm_weight(weight, n, dy.dtype)
+    stype = _norm_type("h", h, dy.dtype)
+    xs = heads * n
+    if dx is not None:
+        xs = _norm_rows("dx", dx, shape)[3]
+        if dx.dtype != dy.dtype:
+            raise ValueError("dx must have dy's type")
+    for name, t in (("dh", dh), ("dresidual", dresidual)):
+        _norm_stream(name, t, shape)
+        if t is not None and t.dtype != h.dtype:
+            raise ValueError(f"{name} must have h's type")
+    _norm_rstd(rstd, rows, heads)
+    _float32((n,), dweight=dweight)
+    if dweight is not None and workspace is None and rows > 0:
+        raise ValueError("dweight needs a workspace")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return PreparedOp(load().gqa_rms_norm_backward,
+                      (_ptr(dy), ys, _ptr(h), hs, stype, _ptr(rstd), _ptr(weight), wtype,
+                       float(offset), _ptr(dh), rows, heads, n, code, _ptr(dx), xs,
+                       _ptr(dresidual), _ptr(dweight), _ptr(workspace), nbytes,
+                       _stream_handle(stream)), "gqa_rms_norm_backward",
+                      (dy, h, rstd, weight, dh, dx, dresidual, dweight, workspace))
+
+
+def gqa_rms_norm_backward(dy, h, weight, rstd, dx=None, dresidual=None, dweight=None,
+                          workspace=None, offset=0.0, dh=None, stream=None):
+    """The gradient of gqa_rms_norm (see gqa_prefill.h) into those of ``dx``,
+    ``dresidual`` and ``dweight`` that are given, from ``dy`` and ``dh``, the
+    gradient that reaches h another way; ``dweight`` needs a workspace of
+    ``rms_norm_backward_workspace(...)`` bytes.  Returns ``dx``."""
+    _marshal_rms_norm_backward(dy, h, weight, rstd, dx, dresidual, dweight, workspace, offset, dh,
+                               stream)()
+    return dx
+
+
+def rms_norm_backward(dy, h, weight, rstd, offset=0.0, dh=None, workspace=None, stream=None):
+    """gqa_rms_norm_backward into new tensors.  Returns (dx, dresidual,
+    dweight): dx in dy's type; dresidual is dx itself unless the stream h is
+    wider."""
+    import torch
+    rows, heads, n = (*dy.shape[:1], 1, *dy.shape[1:]) if dy.dim() == 2 else dy.shape
+    dx = _result(dy.shape, dy.dtype, dy.device, stream)
+    dresidual = None if h.dtype == dy.dtype else _result(h.shape, h.dtype, h.device, stream)
+    dweight = _result((n,), torch.float32, dy.device, stream)
+    if workspace is None:
+        with _allocating(stream):
+            workspace = torch.empty(rms_norm_backward_workspace(rows, heads, n, dy.dtype),
+                                    dtype=torch.uint8, device=dy.device)
+    gqa_rms_norm_backward(dy, h, weight, rstd, dx, dresidual, dweight, workspace, offset, dh, stream)
+    return dx, dx if dresidual is None else dresidual, dweight
+
+
 _MARSHAL = {gqa_rope: _marshal_rope, gqa_cache_write: _marshal_cache_write,
             gqa_cache_read: _marshal_cache_read, gqa_cache_attention: _marshal_cache_attention,
-            gqa_prefill_backward: _marshal_prefill_backward}
+            gqa_prefill_backward: _marshal_prefill_backward, gqa_rms_norm: _marshal_rms_norm,
+            gqa_rms_norm_backward: _marshal_rms_norm_backward}
 
 
 def cache_write(batch, cache, rope=None, stream=None):

@@ -23,7 +23,7 @@ SOURCES = ["host.cu", "inst_d64.cu", "inst_d64_pair.cu", "inst_d128.cu", "inst_d
            "noalloc.cu", "cache_rows.cu", "cache_attn.cu", "inst_cache_d64.cu",
            "inst_cache_d128.cu", "inst_cache_d256.cu",
            "inst_cache_tile.cu", "backward.cu", "inst_bwd_d64.cu", "inst_bwd_d128.cu",
-           "inst_bwd_d256.cu"]
+           "inst_bwd_d256.cu", "rms_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -79,6 +79,8 @@ extern "C" {
 
 /* Element type of q, k, v and out. */
 enum { GQA_F16 = 0, GQA_BF16 = 1 };
+/* 32 bits: only where a stream_type or weight_type says so. */
+enum { GQA_F32 = 2 };
 
 /* Host-side return codes. */
 enum {
@@ -412,6 +414,75 @@ GQA_API int gqa_prefill_backward(const void* q, const void* k, const void* v,
 /* Workspace bytes of a gqa_prefill_backward call with these shapes (host only). */
 GQA_API int gqa_prefill_backward_workspace(int num_seqs, int total_q, int total_kv, int Hq,
                                            int Hkv, int d, int dtype, size_t* bytes);
+
+/*
+ * gqa_rms_norm -- the root-mean-square norm in front of a layer's projections,
+ * or of each query and key head before its rotation, with the addition of the
+ * residual stream before it:
+ *     h = x + residual,  rounded to stream_type   (h = x without a residual)
+ *     rstd = (mean of h^2 over n + eps)^-1/2
+ *     out = h * rstd * (weight + offset)
+ *
+ *   x             [rows] of heads * n values (dtype), x_stride elements apart
+ *                 (a multiple of 8, at least heads * n): a slice of a packed
+ *                 projection will do.  The norm is over each n values; a hidden
+ *                 row has heads = 1.
+ *   residual, residual_out  [rows, heads, n] in stream_type, both or neither;
+ *                 residual_out receives h.  stream_type is dtype or GQA_F32.
+ *   weight        [n] in weight_type (dtype or GQA_F32); offset is added to it
+ *   eps           > 0
+ *   out_type      GQA_CACHE_16: out in dtype; GQA_CACHE_E4M3: out in e4m3 with
+ *                 one power-of-two scale for each `group` values (32, 64, 128,
+ *                 or n for one a row), in `scales`, bytes [rows, heads, n /
+ *                 group]: the format of gqa_cache_write's rows.
+ *   group         ignored with GQA_CACHE_16
+ *   out           [rows] of heads * n values, out_stride elements apart
+ *   rstd          fp32 [rows, heads] or NULL; the gradient needs it
+ *
+ * n is a multiple of 8 up to 32768 (else GQA_ERR_UNSUPPORTED); bases are 16-byte
+ * aligned.  Sums and products are fp32 (|h| below 2^56), each result is rounded
+ * once.  residual_out and a 16-bit out may be x or residual themselves (same
+ * base, stride and type); other overlaps are GQA_ERR_INVALID.  Returns as
+ * gqa_flash_prefill.
+ */
+GQA_API int gqa_rms_norm(const void* x, long long x_stride, const void* residual,
+                         void* residual_out, int stream_type, const void* weight, int weight_type,
+                         float offset, float eps, int rows, int heads, int n, int dtype,
+                         int out_type, int group, void* out, long long out_stride, void* scales,
+                         float* rstd, void* stream);
+
+/*
+ * gqa_rms_norm_backward -- its gradient.  With t = h * rstd and g = dy * (weight
+ * + offset),
+ *     dx = rstd * (g - t * mean of g t) + dh       dweight = sum of dy * t over rows
+ * dx is the gradient of h, so of x and of the residual alike; dh is what reaches
+ * h another way (the residual stream's gradient), or NULL.
+ *
+ *   dy            [rows] of heads * n values (dtype), dy_stride elements apart
+ *   h, rstd       gqa_rms_norm's residual_out (its x, h_stride elements apart,
+ *                 without a residual) and rstd; h in stream_type
+ *   dh            [rows, heads, n] in stream_type, or NULL
+ *   dx            [rows] of heads * n values (dtype), dx_stride apart, or NULL
+ *   dresidual     the same values [rows, heads, n] in stream_type, or NULL: for a
+ *                 stream of 32 bits beside a dx of 16
+ *   dweight       fp32 [n], overwritten, or NULL
+ *   workspace     for dweight: device memory of the caller, 256-byte aligned, at
+ *                 least gqa_rms_norm_backward_workspace() bytes, one for each
+ *                 call that may run at the same time; else ignored
+ *
+ * dx and dresidual may be dy, h or dh themselves (same base, stride and type).
+ * The result is the same run to run.  Otherwise as gqa_rms_norm; no result at
+ * all is GQA_ERR_INVALID.
+ */
+GQA_API int gqa_rms_norm_backward(const void* dy, long long dy_stride, const void* h,
+                                  long long h_stride, int stream_type, const float* rstd,
+                                  const void* weight, int weight_type, float offset,
+                                  const void* dh, int rows, int heads, int n, int dtype, void* dx,
+                                  long long dx_stride, void* dresidual, float* dweight,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of a gqa_rms_norm_backward call with these shapes (host only). */
+GQA_API int gqa_rms_norm_backward_workspace(int rows, int heads, int n, int dtype, size_t* bytes);
 
 /* num_splits value selecting the balanced split (see below). */
 #define GQA_SPLITS_BALANCED (-1)
