@@ -6,9 +6,9 @@
 // eps)^-1/2, y = h r (w + offset).  With t = h r, g = dy (w + offset):
 //   dh_row = r (g - t mean(g t)) + dh        dw = sum over rows of dy t.
 // Both are bound by memory: each value is read once and kept in registers
-// between the row's sum and its output.  A row of up to 1024 values belongs to
-// 8, 16 or 32 lanes of a warp, a longer one to a CTA; a thread holds V groups of
-// 8 neighbouring values.  Sums are fp32, in an order that depends on the shape
+// between the row's sum and its output.  A row of up to 256 values belongs to 8,
+// 16 or 32 lanes of a warp, a longer one to a CTA; a thread holds one or two
+// groups of 8 neighbouring values.  Sums are fp32, in an order that depends on the shape
 // alone, so results are the same run to run.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -35,7 +35,7 @@ struct NormParams {
   void* dresidual;
   uint8_t* scales;
   float* rstd;
-  float* part;  // [gridDim.x][n]
+  float* part;  // [CTAs of the gradient][n]
   float* dweight;
   long long x_stride, h_stride, out_stride;
   long long rows;  // rows x heads
@@ -43,8 +43,12 @@ struct NormParams {
   int group;       // values that share a scale (0: 16-bit output)
   int w32;
   int parts;
-  float offset, eps, inv_n;
+  int stages;
+  float offset, eps;
+  unsigned int* status;
+  unsigned long long timeout_ns;
 };
+constexpr int kMaxStages = 4;
 
 struct Vec8 {
   float v[8];
@@ -147,120 +151,216 @@ __device__ __forceinline__ void row_reduce(float& sum, float& most, int team, fl
   }
 }
 
-template <bool BF16, bool F32, bool OUT8, int V, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 1024 : 256) norm_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float s[64];
-  grid_dep_launch_dependents();
-  grid_dep_wait();
-  const int TS = WIDE ? (int)blockDim.x : p.team;
-  const int lane = WIDE ? (int)threadIdx.x : (int)threadIdx.x & (TS - 1);
-  const long long row = WIDE ? (long long)blockIdx.x
-                             : ((long long)blockIdx.x * 256 + threadIdx.x) / TS;
-  const bool live = row < p.rows;
-  const long long token = live ? row / p.heads : 0;
-  const int head = live ? (int)(row - token * p.heads) : 0;
-  const int nv = p.n / 8;
-  const size_t xat = (size_t)token * p.x_stride + (size_t)head * p.n;
-  const size_t hat = (size_t)row * p.n;
-  uint4 xr[V];
-  Raw<F32> rr[V];
-  const bool has = p.residual != nullptr;
+// (sum / n + eps)^-1/2 within an ulp: the reciprocal square root, and a step of
+// Newton's method with the residual in one rounding.
+__device__ __forceinline__ float rstd_of(float sum, int n, float eps) {
+  const float v = sum / (float)n + eps, r = rsqrtf(v), t = v * r;
+  return fmaf(0.5f * r, fmaf(-t, r, 1.f) - fmaf(v, r, -t) * r, r);
+}
+
+// Sum over 8 values of a b, in pairs.
+__device__ __forceinline__ float dot8(const Vec8& a, const Vec8& b) {
+  float s[4];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = v * TS + lane;
-    if (live && c < nv) {
-      xr[v] = load_raw<false>(p.x, xat + 8 * c).a[0];
-      if (has) rr[v] = load_raw<F32>(p.residual, hat + 8 * c);
+  for (int i = 0; i < 4; ++i) s[i] = fmaf(a.v[2 * i], b.v[2 * i], a.v[2 * i + 1] * b.v[2 * i + 1]);
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// One row's 8 values in a thread of its team, before and after the row's sums.
+template <bool BF16, bool F32, bool OUT8>
+struct NormVec {
+  Vec8 h;
+  bool in;
+  __device__ __forceinline__ void take(const NormParams& p, const uint4& x, const Raw<F32>& r,
+                                       size_t hat, int c, float& sum, float& most) {
+    if (!in) return;
+    h = widen<BF16>(x);
+    if (p.residual != nullptr) {
+      const Vec8 a = values<F32, BF16>(r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h.v[i] += a.v[i];
+      // The norm is of what the stream holds.
+      if constexpr (!F32) h = widen<BF16>(narrow<BF16>(h));
+      store8<F32, BF16>(p.h_out, hat + 8 * c, h);
+    }
+    sum += dot8(h, h);
+    if constexpr (OUT8) {
+      const Vec8 w = weight8<BF16>(p, 8 * c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(h.v[i] * w.v[i]));
     }
   }
-  Vec8 h[V];
-  float sum = 0.f, most = 0.f;
+  // All lanes of a warp call it together.
+  __device__ __forceinline__ void give(const NormParams& p, size_t row, size_t oat, int c, float rstd,
+                                       float most) {
+    Vec8 w;
+    if (in) {
+      w = weight8<BF16>(p, 8 * c);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = v * TS + lane;
-    if (live && c < nv) {
-      h[v] = widen<BF16>(xr[v]);
-      if (has) {
-        const Vec8 r = values<F32, BF16>(rr[v]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[v].v[i] += r.v[i];
-        // The norm is of what the stream holds.
-        if constexpr (!F32) h[v] = widen<BF16>(narrow<BF16>(h[v]));
-        store8<F32, BF16>(p.h_out, hat + 8 * c, h[v]);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(h[v].v[i], h[v].v[i], sum);
-      if constexpr (OUT8) {
-        const Vec8 w = weight8<BF16>(p, 8 * c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          h[v].v[i] *= w.v[i];
-          most = fmaxf(most, fabsf(h[v].v[i]));
-        }
-      }
+      for (int i = 0; i < 8; ++i) h.v[i] = h.v[i] * rstd * w.v[i];
     }
-  }
-  const bool whole = OUT8 && p.group == p.n;  // one scale a row
-  row_reduce<WIDE, OUT8>(sum, most, TS, s);
-  const float rstd = 1.f / sqrtf(fmaf(sum, p.inv_n, p.eps));
-  if (live && lane == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
-  const size_t oat = (size_t)token * p.out_stride + (size_t)head * p.n;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = v * TS + lane;
-    const bool in = live && c < nv;
     if constexpr (!OUT8) {
-      if (in) {
-        const Vec8 w = weight8<BF16>(p, 8 * c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[v].v[i] = h[v].v[i] * rstd * w.v[i];
-        store8<false, BF16>(p.out, oat + 8 * c, h[v]);
-      }
+      if (in) store8<false, BF16>(p.out, oat + 8 * c, h);
     } else {
-      float top = most;
+      const bool whole = p.group == p.n;  // one scale a row
+      float top = most * rstd;
       if (!whole) {
         top = 0.f;
         if (in) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(h[v].v[i]));
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(h.v[i]));
         }
         for (int o = 1; o < p.group / 8; o <<= 1)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       }
-      const int e = e4m3_scale_exponent(top * rstd);
-      if (in) {
-        const float m = pow2f(-e);
-        uint32_t w[2];
+      const int e = e4m3_scale_exponent(top);
+      if (!in) return;
+      const float m = pow2f(-e);
+      uint32_t b[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float* a = h[v].v + 4 * i;
-          w[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a[0] * rstd * m, a[1] * rstd * m),
-                                                    __NV_SATFINITE, __NV_E4M3) |
-                 (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a[2] * rstd * m, a[3] * rstd * m),
-                                                    __NV_SATFINITE, __NV_E4M3) << 16;
-        }
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + oat + 8 * c) = make_uint2(w[0], w[1]);
-        const int per = whole ? p.n : p.group;
-        if (8 * c % per == 0) p.scales[(size_t)row * (p.n / per) + 8 * c / per] = (uint8_t)(e + 127);
-      }
+      for (int i = 0; i < 2; ++i)
+        b[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(h.v[4 * i] * m, h.v[4 * i + 1] * m),
+                                                  __NV_SATFINITE, __NV_E4M3) |
+               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(h.v[4 * i + 2] * m, h.v[4 * i + 3] * m),
+                                                  __NV_SATFINITE, __NV_E4M3) << 16;
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + oat + 8 * c) = make_uint2(b[0], b[1]);
+      if (8 * c % p.group == 0) p.scales[row * (p.n / p.group) + 8 * c / p.group] = (uint8_t)(e + 127);
     }
+  }
+};
+
+// A CTA of up to T threads per row, V groups of 8 values a thread.
+template <bool BF16, bool F32, bool OUT8, int V, int T>
+__global__ void __launch_bounds__(T) norm_kernel(const __grid_constant__ NormParams p) {
+  __shared__ float s[64];
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  const int TS = blockDim.x, lane = threadIdx.x, nv = p.n / 8;
+  const size_t row = blockIdx.x, token = row / p.heads, head = row - token * p.heads;
+  const size_t xat = token * p.x_stride + head * p.n, hat = row * p.n, oat = token * p.out_stride + head * p.n;
+  uint4 x[V];
+  Raw<F32> r[V];
+  NormVec<BF16, F32, OUT8> n[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = v * TS + lane;
+    n[v].in = c < nv;
+    if (n[v].in) {
+      x[v] = load_raw<false>(p.x, xat + 8 * c).a[0];
+      if (p.residual != nullptr) r[v] = load_raw<F32>(p.residual, hat + 8 * c);
+    }
+  }
+  float sum = 0.f, most = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) n[v].take(p, x[v], r[v], hat, v * TS + lane, sum, most);
+  row_reduce<true, OUT8>(sum, most, 32, s);
+  const float rstd = rstd_of(sum, p.n, p.eps);
+  if (lane == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+#pragma unroll
+  for (int v = 0; v < V; ++v) n[v].give(p, row, oat, v * TS + lane, rstd, most);
+}
+
+// Rows of up to 256 values: a row in `team` lanes (8, 16 or 32), U rows a team,
+// all of whose loads are on their way at once.
+constexpr int kTeamRows = 4;
+template <bool BF16, bool F32, bool OUT8>
+__global__ void __launch_bounds__(256) norm_team_kernel(const __grid_constant__ NormParams p) {
+  constexpr int U = kTeamRows;
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  const int c = threadIdx.x & (p.team - 1), teams = 256 / p.team;
+  const long long row0 = (long long)blockIdx.x * teams * U + threadIdx.x / p.team;
+  uint4 x[U];
+  Raw<F32> r[U];
+  NormVec<BF16, F32, OUT8> n[U];
+  size_t oat[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const long long row = row0 + u * teams;
+    n[u].in = row < p.rows && c < p.n / 8;
+    if (n[u].in) {
+      const size_t token = (uint32_t)row / (uint32_t)p.heads, head = (size_t)row - token * p.heads;
+      x[u] = load_raw<false>(p.x, token * p.x_stride + head * p.n + 8 * c).a[0];
+      if (p.residual != nullptr) r[u] = load_raw<F32>(p.residual, (size_t)row * p.n + 8 * c);
+      oat[u] = token * p.out_stride + head * p.n;
+    }
+  }
+  float sum[U], most[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    sum[u] = most[u] = 0.f;
+    n[u].take(p, x[u], r[u], (size_t)(row0 + u * teams) * p.n, c, sum[u], most[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) row_reduce<false, OUT8>(sum[u], most[u], p.team, nullptr);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float rstd = rstd_of(sum[u], p.n, p.eps);
+    const long long row = row0 + u * teams;
+    if (n[u].in && c == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+    n[u].give(p, (size_t)row, oat[u], c, rstd, most[u]);
   }
 }
 
-// Each CTA walks rows blockIdx.x, + gridDim.x, ..., the next row's values on
-// their way while this one's are summed, and keeps its share of dw in registers.
-template <bool BF16, bool F32, int V, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 1024 : 256) norm_backward_kernel(const __grid_constant__ NormParams p) {
+// ------------------------------------------------------------------ gradient
+// dx of 8 values, and the thread's share of dw and of the row's sum.
+template <bool BF16, bool F32>
+__device__ __forceinline__ float grad_sum(const Vec8& d, const Vec8& h, const Vec8& w, float rstd, Vec8& acc) {
+  Vec8 t, g;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    t.v[i] = h.v[i] * rstd;
+    acc.v[i] = fmaf(d.v[i], t.v[i], acc.v[i]);
+    g.v[i] = d.v[i] * w.v[i];
+  }
+  return dot8(g, t);
+}
+template <bool BF16, bool F32>
+__device__ __forceinline__ void grad_store(const NormParams& p, const Vec8& d, const Vec8& h, const Vec8& w,
+                                           const Vec8& dh, float rstd, float mean, size_t oat, size_t sat) {
+  Vec8 o;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    o.v[i] = rstd * fmaf(d.v[i], w.v[i], -(h.v[i] * rstd) * mean) + dh.v[i];
+  if (p.out != nullptr) store8<false, BF16>(p.out, oat, o);
+  if (p.dresidual != nullptr) store8<F32, BF16>(p.dresidual, sat, o);
+}
+
+// A row in a CTA.  Each CTA walks rows blockIdx.x, + gridDim.x, ... through a
+// ring of `stages` rows in shared memory, filled by bulk copies that run ahead:
+// the bytes in flight that the memory's latency asks for would not fit in
+// registers beside the sums.  Its share of dw stays in registers.
+template <bool BF16, bool F32, int V, int T>
+__global__ void __launch_bounds__(T) norm_backward_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ __align__(8) uint64_t bars[kMaxStages];
+  __shared__ uint32_t abort_word;
   __shared__ float s[2][64];
-  __shared__ float s_acc[WIDE ? 1 : 256 * 8];
+  const int TS = blockDim.x, lane = threadIdx.x, nv = p.n / 8;
+  constexpr uint32_t es = F32 ? 4u : 2u;
+  const uint32_t off_h = 2u * p.n, off_dh = off_h + es * p.n, stage = off_dh + (p.dh != nullptr ? es * p.n : 0u);
+  const uint32_t sbar = smem_u32(bars), sring = smem_u32(ring);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) mbar_init(sbar + 8 * i, 1u);
+    abort_word = 0u;
+    fence_barrier_init();
+  }
+  __syncthreads();
   grid_dep_launch_dependents();
   grid_dep_wait();
-  const int TS = WIDE ? (int)blockDim.x : p.team;
-  const int lane = WIDE ? (int)threadIdx.x : (int)threadIdx.x & (TS - 1);
-  const int per_cta = WIDE ? 1 : 256 / TS;
-  const int nv = p.n / 8;
-  const long long step = (long long)gridDim.x * per_cta;
-  const bool has = p.dh != nullptr;
+  // Copies row number k of this CTA into its stage.
+  auto fill = [&](long long k) {
+    const long long row = blockIdx.x + k * gridDim.x;
+    if (row >= p.rows) return;
+    const size_t token = (size_t)row / p.heads, head = (size_t)row - token * p.heads;
+    const uint32_t st = (uint32_t)(k % p.stages), bar = sbar + 8 * st, dst = sring + st * stage;
+    mbar_arrive_expect_tx(bar, stage);
+    bulk_load(dst, static_cast<const uint16_t*>(p.x) + token * p.x_stride + head * p.n, 2u * p.n, bar);
+    bulk_load(dst + off_h, static_cast<const uint8_t*>(p.residual) + es * (token * p.h_stride + head * p.n), es * p.n, bar);
+    if (p.dh != nullptr) bulk_load(dst + off_dh, static_cast<const uint8_t*>(p.dh) + es * ((size_t)row * p.n), es * p.n, bar);
+  };
+  if (threadIdx.x == 0)
+    for (int k = 0; k < p.stages; ++k) fill(k);
   Vec8 w[V], acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -269,96 +369,126 @@ __global__ void __launch_bounds__(WIDE ? 1024 : 256) norm_backward_kernel(const 
     for (int i = 0; i < 8; ++i) acc[v].v[i] = 0.f;
     if (c < nv) w[v] = weight8<BF16>(p, 8 * c);
   }
-  uint4 dy[V];
-  Raw<F32> h[V], dh[V];
-  float r = 0.f;
-  auto fetch = [&](long long row) {
-    if (row >= p.rows) return;
-    const long long token = row / p.heads;
-    const int head = (int)(row - token * p.heads);
-    const size_t yat = (size_t)token * p.x_stride + (size_t)head * p.n;
-    const size_t hat = (size_t)token * p.h_stride + (size_t)head * p.n;
-    r = __ldg(p.rstd_in + row);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = v * TS + lane;
-      if (c < nv) {
-        dy[v] = load_raw<false>(p.x, yat + 8 * c).a[0];
-        h[v] = load_raw<F32>(p.residual, hat + 8 * c);
-        if (has) dh[v] = load_raw<F32>(p.dh, (size_t)row * p.n + 8 * c);
-      }
-    }
-  };
-  const long long row0 = (long long)blockIdx.x * per_cta;  // the first team's row
-  const int mine = WIDE ? 0 : (int)threadIdx.x / TS;
-  fetch(row0 + mine);
-  int buf = 0;
-  for (long long base = row0; base < p.rows; base += step, buf ^= 1) {
-    const long long row = base + mine;
-    const bool live = row < p.rows;
-    const float rstd = r;
-    Vec8 t[V], g[V];
-    Raw<F32> old[V];
+  const float inv_n = 1.f / (float)p.n;
+  long long k = 0;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, ++k) {
+    const uint32_t st = (uint32_t)(k % p.stages);
+    const float rstd = __ldg(p.rstd_in + row);
+    // A wait that runs out raises the status; the sums below are then of
+    // whatever the stage holds, and the rows still end.
+    (void)wait_bounded(sbar + 8 * st, (uint32_t)(k / p.stages) & 1u, &abort_word, p.status, p.timeout_ns);
+    const uint8_t* at = ring + st * stage;
     float sum = 0.f, none = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = v * TS + lane;
-      if (live && c < nv) {
-        const Vec8 d = widen<BF16>(dy[v]);
-        t[v] = values<F32, BF16>(h[v]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          t[v].v[i] *= rstd;
-          acc[v].v[i] = fmaf(d.v[i], t[v].v[i], acc[v].v[i]);
-          g[v].v[i] = d.v[i] * w[v].v[i];
-          sum = fmaf(g[v].v[i], t[v].v[i], sum);
-        }
-        if (has) old[v] = dh[v];
-      }
+      if (c < nv)
+        sum += grad_sum<BF16, F32>(widen<BF16>(load_raw<false>(at, 8 * c).a[0]),
+                                   values<F32, BF16>(load_raw<F32>(at + off_h, 8 * c)), w[v], rstd, acc[v]);
     }
-    fetch(row + step);
-    row_reduce<WIDE, false>(sum, none, TS, s[buf]);
-    const float mean = sum * p.inv_n;
-    const long long token = live ? row / p.heads : 0;
-    const size_t oat = (size_t)token * p.out_stride + (size_t)(live ? row - token * p.heads : 0) * p.n;
+    row_reduce<true, false>(sum, none, 32, s[k & 1]);
+    // Every thread is past the row before: its stage is free.
+    if (threadIdx.x == 0 && k > 0 && p.stages > 1) fill(k - 1 + p.stages);
+    const float mean = sum * inv_n;
+    const size_t token = (size_t)row / p.heads, head = (size_t)row - token * p.heads;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = v * TS + lane;
-      if (live && c < nv) {
+      if (c < nv) {
+        Vec8 o;
+        if (p.dh != nullptr) {
+          o = values<F32, BF16>(load_raw<F32>(at + off_dh, 8 * c));
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[v].v[i] = rstd * (g[v].v[i] - t[v].v[i] * mean);
-        if (has) {
-          const Vec8 o = values<F32, BF16>(old[v]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) g[v].v[i] += o.v[i];
+          for (int i = 0; i < 8; ++i) o.v[i] = 0.f;
         }
-        if (p.out != nullptr) store8<false, BF16>(p.out, oat + 8 * c, g[v]);
-        if (p.dresidual != nullptr) store8<F32, BF16>(p.dresidual, (size_t)row * p.n + 8 * c, g[v]);
+        grad_store<BF16, F32>(p, widen<BF16>(load_raw<false>(at, 8 * c).a[0]),
+                              values<F32, BF16>(load_raw<F32>(at + off_h, 8 * c)), w[v], o, rstd, mean,
+                              token * p.out_stride + head * p.n + 8 * c, (size_t)row * p.n + 8 * c);
+      }
+    }
+    if (p.stages == 1) {  // rows so wide that one fits
+      __syncthreads();
+      if (threadIdx.x == 0) fill(k + 1);
+    }
+  }
+  if (abort_word != 0u && threadIdx.x == 0)  // let the copies in flight land
+    for (long long j = k > p.stages ? k - p.stages : 0; j < k + p.stages; ++j)
+      if (blockIdx.x + j * gridDim.x < p.rows)
+        wait_drain(sbar + 8 * (uint32_t)(j % p.stages), (uint32_t)(j / p.stages) & 1u, p.timeout_ns);
+  if (p.part == nullptr) return;
+  float* part = p.part + (size_t)blockIdx.x * p.n;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = v * TS + lane;
+    if (c < nv) store8<true, BF16>(part, (size_t)8 * c, acc[v]);
+  }
+}
+
+// Rows of up to 256 values: a row in `team` lanes, U rows a team at a time.
+template <bool BF16, bool F32>
+__global__ void __launch_bounds__(256, 2) norm_backward_team_kernel(const __grid_constant__ NormParams p) {
+  constexpr int U = kTeamRows;
+  __shared__ float s_acc[256 * 8];
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  const int c = threadIdx.x & (p.team - 1), teams = 256 / p.team, mine = threadIdx.x / p.team;
+  const bool col = c < p.n / 8, has = p.dh != nullptr;
+  Vec8 w, acc;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc.v[i] = 0.f;
+  if (col) w = weight8<BF16>(p, 8 * c);
+  const float inv_n = 1.f / (float)p.n;
+  const long long per = (long long)teams * U;
+  for (long long base = blockIdx.x * per; base < p.rows; base += gridDim.x * per) {
+    uint4 dy[U];
+    Raw<F32> h[U], dh[U];
+    float rstd[U], sum[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long row = base + u * teams + mine;
+      if (col && row < p.rows) {
+        const size_t token = (uint32_t)row / (uint32_t)p.heads, head = (size_t)row - token * p.heads;
+        dy[u] = load_raw<false>(p.x, token * p.x_stride + head * p.n + 8 * c).a[0];
+        h[u] = load_raw<F32>(p.residual, token * p.h_stride + head * p.n + 8 * c);
+        if (has) dh[u] = load_raw<F32>(p.dh, (size_t)row * p.n + 8 * c);
+        rstd[u] = __ldg(p.rstd_in + row);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      sum[u] = 0.f;
+      if (col && base + u * teams + mine < p.rows)
+        sum[u] = grad_sum<BF16, F32>(widen<BF16>(dy[u]), values<F32, BF16>(h[u]), w, rstd[u], acc);
+    }
+    float none = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) row_reduce<false, false>(sum[u], none, p.team, nullptr);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long row = base + u * teams + mine;
+      if (col && row < p.rows) {
+        const size_t token = (uint32_t)row / (uint32_t)p.heads, head = (size_t)row - token * p.heads;
+        Vec8 o;
+        if (has) {
+          o = values<F32, BF16>(dh[u]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o.v[i] = 0.f;
+        }
+        grad_store<BF16, F32>(p, widen<BF16>(dy[u]), values<F32, BF16>(h[u]), w, o, rstd[u], sum[u] * inv_n,
+                              token * p.out_stride + head * p.n + 8 * c, (size_t)row * p.n + 8 * c);
       }
     }
   }
   if (p.part == nullptr) return;
-  float* part = p.part + (size_t)blockIdx.x * p.n;
-  if constexpr (WIDE) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = v * TS + lane;
-      if (c < nv) store8<true, BF16>(part, (size_t)8 * c, acc[v]);
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s_acc[threadIdx.x * 8 + i] = acc[v].v[i];
-      __syncthreads();
-      const int at = v * TS * 8 + (int)threadIdx.x;  // the column
-      if ((int)threadIdx.x < TS * 8 && at < p.n) {
-        float a = 0.f;
-        for (int k = 0; k < per_cta; ++k) a += s_acc[k * TS * 8 + threadIdx.x];
-        part[at] = a;
-      }
-    }
+  for (int i = 0; i < 8; ++i) s_acc[threadIdx.x * 8 + i] = acc.v[i];
+  __syncthreads();
+  if ((int)threadIdx.x < p.n) {  // at most 256 columns
+    float a = 0.f;
+    for (int k = 0; k < teams; ++k) a += s_acc[k * p.team * 8 + threadIdx.x];
+    p.part[(size_t)blockIdx.x * p.n + threadIdx.x] = a;
   }
 }
 
@@ -381,28 +511,26 @@ __global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ host
-constexpr int kMaxN = 32768;
+constexpr int kMaxN = 16384;
+constexpr unsigned kRingBytes = 220u * 1024u;  // of an SM's shared memory, for the gradient's rows
 
 struct NormShape {
-  int team, v, threads;  // team 0: a row per CTA
+  int team;     // lanes of a row, 0: a CTA
+  int v, t;     // groups of 8 values a thread, and the threads it is compiled for
+  int threads;
 };
 NormShape norm_shape(int n) {
   const int nv = n / 8;
-  NormShape s{0, 1, 256};
-  if (nv <= 128) {
-    s.team = 8;
-    while (s.team < 32 && s.team < nv) s.team *= 2;
-    const int v = (nv + s.team - 1) / s.team;
-    s.v = v <= 1 ? 1 : v <= 2 ? 2 : 4;
-    return s;
-  }
-  s.v = nv <= 256 ? 1 : nv <= 1024 ? 2 : 4;
+  if (nv <= 32) return {nv <= 8 ? 8 : nv <= 16 ? 16 : 32, 1, 256, 256};
+  NormShape s{0, nv <= 256 ? 1 : 2, nv <= 256 ? 256 : nv <= 1024 ? 512 : 1024, 0};
   s.threads = ((nv + s.v - 1) / s.v + 31) / 32 * 32;
   return s;
 }
-// CTAs of the gradient's persistent grid.
-int backward_ctas(int sms, const NormShape& s) {
-  return s.team > 0 ? 4 * sms : sms * (s.threads <= 256 ? 2 : 1);
+// CTAs per SM of the gradient's persistent grid.
+int backward_per_sm(const NormShape& s) {
+  if (s.team > 0) return 2;
+  const int c = 512 / s.threads;
+  return c < 1 ? 1 : c > 4 ? 4 : c;
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -435,30 +563,43 @@ int norm_check(int rows, int heads, int n, int dtype, int stream_type, int weigh
 }
 bool bad_stride(long long stride, long long row) { return stride < row || stride % 8 != 0; }
 
-template <bool BF16, bool F32, bool OUT8, bool WIDE>
-cudaError_t launch_norm_v(const NormParams& p, const NormShape& s, int grid, cudaStream_t st) {
-  return s.v == 1   ? launch_pdl(norm_kernel<BF16, F32, OUT8, 1, WIDE>, p, grid, s.threads, 0, st)
-         : s.v == 2 ? launch_pdl(norm_kernel<BF16, F32, OUT8, 2, WIDE>, p, grid, s.threads, 0, st)
-                    : launch_pdl(norm_kernel<BF16, F32, OUT8, 4, WIDE>, p, grid, s.threads, 0, st);
+template <bool BF16, bool F32, bool OUT8>
+cudaError_t launch_norm_as(const NormParams& p, const NormShape& s, cudaStream_t st) {
+  if (s.team > 0) {
+    const long long per = (long long)kTeamRows * 256 / s.team;
+    return launch_pdl(norm_team_kernel<BF16, F32, OUT8>, p, (int)((p.rows + per - 1) / per), 256, 0, st);
+  }
+  const int grid = (int)p.rows;
+  return s.v == 1     ? launch_pdl(norm_kernel<BF16, F32, OUT8, 1, 256>, p, grid, s.threads, 0, st)
+         : s.t == 512 ? launch_pdl(norm_kernel<BF16, F32, OUT8, 2, 512>, p, grid, s.threads, 0, st)
+                      : launch_pdl(norm_kernel<BF16, F32, OUT8, 2, 1024>, p, grid, s.threads, 0, st);
 }
 template <bool BF16, bool F32>
-cudaError_t launch_norm(const NormParams& p, const NormShape& s, int grid, cudaStream_t st) {
-  if (p.group > 0)
-    return s.team > 0 ? launch_norm_v<BF16, F32, true, false>(p, s, grid, st)
-                      : launch_norm_v<BF16, F32, true, true>(p, s, grid, st);
-  return s.team > 0 ? launch_norm_v<BF16, F32, false, false>(p, s, grid, st)
-                    : launch_norm_v<BF16, F32, false, true>(p, s, grid, st);
+cudaError_t launch_norm(const NormParams& p, const NormShape& s, cudaStream_t st) {
+  return p.group > 0 ? launch_norm_as<BF16, F32, true>(p, s, st) : launch_norm_as<BF16, F32, false>(p, s, st);
 }
-template <bool BF16, bool F32, bool WIDE>
-cudaError_t launch_back_v(const NormParams& p, const NormShape& s, int grid, cudaStream_t st) {
-  return s.v == 1   ? launch_pdl(norm_backward_kernel<BF16, F32, 1, WIDE>, p, grid, s.threads, 0, st)
-         : s.v == 2 ? launch_pdl(norm_backward_kernel<BF16, F32, 2, WIDE>, p, grid, s.threads, 0, st)
-                    : launch_pdl(norm_backward_kernel<BF16, F32, 4, WIDE>, p, grid, s.threads, 0, st);
+
+template <bool BF16, bool F32, int V, int T>
+cudaError_t launch_ring(const NormParams& p, const NormShape& s, int grid, unsigned smem, cudaStream_t st) {
+  auto kern = norm_backward_kernel<BF16, F32, V, T>;
+  static SmemAttr attr{};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (attr.allowed[dev].load(std::memory_order_acquire) < kRingBytes) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (e != cudaSuccess) return e;
+    attr.allowed[dev].store(kRingBytes, std::memory_order_release);
+  }
+  return launch_pdl(kern, p, grid, s.threads, smem, st);
 }
 template <bool BF16, bool F32>
-cudaError_t launch_back(const NormParams& p, const NormShape& s, int grid, cudaStream_t st) {
-  return s.team > 0 ? launch_back_v<BF16, F32, false>(p, s, grid, st)
-                    : launch_back_v<BF16, F32, true>(p, s, grid, st);
+cudaError_t launch_back(const NormParams& p, const NormShape& s, int grid, unsigned smem, cudaStream_t st) {
+  return s.team > 0   ? launch_pdl(norm_backward_team_kernel<BF16, F32>, p, grid, 256, 0, st)
+         : s.v == 1   ? launch_ring<BF16, F32, 1, 256>(p, s, grid, smem, st)
+         : s.t == 512 ? launch_ring<BF16, F32, 2, 512>(p, s, grid, smem, st)
+                      : launch_ring<BF16, F32, 2, 1024>(p, s, grid, smem, st);
 }
 
 int run_norm(const void* x, long long x_stride, const void* residual, void* residual_out,
@@ -518,23 +659,20 @@ int run_norm(const void* x, long long x_stride, const void* residual, void* resi
   p.w32 = weight_type == GQA_F32;
   p.offset = offset;
   p.eps = eps;
-  p.inv_n = 1.f / (float)n;
   const NormShape s = norm_shape(n);
   p.team = s.team;
-  const long long per = s.team > 0 ? 256 / s.team : 1;
-  const int grid = (int)((p.rows + per - 1) / per);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf = dtype == GQA_BF16, f32 = stream_type == GQA_F32;
-  const cudaError_t e = bf ? (f32 ? launch_norm<true, true>(p, s, grid, st) : launch_norm<true, false>(p, s, grid, st))
-                           : (f32 ? launch_norm<false, true>(p, s, grid, st) : launch_norm<false, false>(p, s, grid, st));
+  const cudaError_t e = bf ? (f32 ? launch_norm<true, true>(p, s, st) : launch_norm<true, false>(p, s, st))
+                           : (f32 ? launch_norm<false, true>(p, s, st) : launch_norm<false, false>(p, s, st));
   return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
-int sm_count() {
+size_t backward_bytes(const NormShape& s, int n) {
   int sms = 152;
   unsigned int* status = nullptr;
   if (call_device(&sms, &status) != GQA_OK) sms = 152;
-  return sms;
+  return 4u * (size_t)sms * backward_per_sm(s) * n;
 }
 
 int run_norm_backward(const void* dy, long long dy_stride, const void* h, long long h_stride,
@@ -562,8 +700,7 @@ int run_norm_backward(const void* dy, long long dy_stride, const void* h, long l
   if (bad_stride(dy_stride, wide) || bad_stride(h_stride, wide) || bad_stride(dx_stride, wide))
     return GQA_ERR_INVALID;
   const NormShape s = norm_shape(n);
-  const int sms = sm_count();
-  const size_t need = 4u * (size_t)backward_ctas(sms, s) * n;
+  const size_t need = backward_bytes(s, n);
   if (dweight != nullptr && (workspace == nullptr || workspace_bytes < need ||
                              (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
     return GQA_ERR_INVALID;
@@ -606,14 +743,26 @@ int run_norm_backward(const void* dy, long long dy_stride, const void* h, long l
   p.team = s.team;
   p.w32 = weight_type == GQA_F32;
   p.offset = offset;
-  p.inv_n = 1.f / (float)n;
-  const long long per = s.team > 0 ? 256 / s.team : 1, all = (p.rows + per - 1) / per;
-  const int most = backward_ctas(sms, s);
+  int sms = 0;
+  if (call_device(&sms, &p.status) != GQA_OK) return GQA_ERR_CUDA;
+  p.timeout_ns = wait_limit_ns();
+  // Rows of the ring: as many as fit beside the SM's other CTAs, four at most;
+  // a CTA has the SM to itself where two rows would not fit otherwise.
+  int per_sm = backward_per_sm(s);
+  const size_t stage = (size_t)n * (2 + es * (dh != nullptr ? 2 : 1));
+  if (s.team == 0) {
+    while (per_sm > 1 && 2 * stage > kRingBytes / per_sm - 2048) --per_sm;
+    const size_t fit = (per_sm > 1 ? kRingBytes / per_sm - 2048 : kRingBytes) / stage;
+    p.stages = (int)(fit < kMaxStages ? fit : kMaxStages);
+  }
+  const long long per = s.team > 0 ? (long long)kTeamRows * 256 / s.team : 1, all = (p.rows + per - 1) / per;
+  const long long most = (long long)sms * per_sm;
   const int grid = (int)(all < most ? all : most);
+  const unsigned smem = (unsigned)(p.stages * stage);
   p.parts = grid;
   const bool bf = dtype == GQA_BF16, f32 = stream_type == GQA_F32;
-  cudaError_t e = bf ? (f32 ? launch_back<true, true>(p, s, grid, st) : launch_back<true, false>(p, s, grid, st))
-                     : (f32 ? launch_back<false, true>(p, s, grid, st) : launch_back<false, false>(p, s, grid, st));
+  cudaError_t e = bf ? (f32 ? launch_back<true, true>(p, s, grid, smem, st) : launch_back<true, false>(p, s, grid, smem, st))
+                     : (f32 ? launch_back<false, true>(p, s, grid, smem, st) : launch_back<false, false>(p, s, grid, smem, st));
   if (e == cudaSuccess && dweight != nullptr) e = launch_pdl(norm_join_kernel, p, (n + 31) / 32, 256, 0, st);
   return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
@@ -645,7 +794,7 @@ int gqa_rms_norm_backward(const void* dy, long long dy_stride, const void* h, lo
 int gqa_rms_norm_backward_workspace(int rows, int heads, int n, int dtype, size_t* bytes) {
   if (bytes == nullptr) return GQA_ERR_INVALID;
   const int rc = gqa::norm_check(rows, heads, n, dtype, dtype, dtype, 0.f);
-  if (rc == GQA_OK) *bytes = 4u * (size_t)gqa::backward_ctas(gqa::sm_count(), gqa::norm_shape(n)) * n;
+  if (rc == GQA_OK) *bytes = gqa::backward_bytes(gqa::norm_shape(n), n);
   return rc;
 }
 

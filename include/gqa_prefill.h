@@ -439,7 +439,7 @@ GQA_API int gqa_prefill_backward_workspace(int num_seqs, int total_q, int total_
  *   out           [rows] of heads * n values, out_stride elements apart
  *   rstd          fp32 [rows, heads] or NULL; the gradient needs it
  *
- * n is a multiple of 8 up to 32768 (else GQA_ERR_UNSUPPORTED); bases are 16-byte
+ * n is a multiple of 8 up to 16384 (else GQA_ERR_UNSUPPORTED); bases are 16-byte
  * aligned.  Sums and products are fp32 (|h| below 2^56), each result is rounded
  * once.  residual_out and a 16-bit out may be x or residual themselves (same
  * base, stride and type); other overlaps are GQA_ERR_INVALID.  Returns as

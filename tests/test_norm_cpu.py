@@ -35,7 +35,7 @@ E4 = dict(kind=1, group=32, scales=FAKE + 6 * STEP)
     (dict(out=FAKE + 16), -1), (dict(out=FAKE, os=512), -1), (dict(h=FAKE + 16), -1), (dict(out=FAKE + 2 * STEP), -1),
     (dict(st=2, h=FAKE), -1), (dict(E4, out=FAKE), -1), (dict(E4, scales=FAKE + STEP), -1), (dict(rstd=FAKE + 4 * STEP), -1),
     (dict(out=FAKE + 3 * STEP), -1),
-    (dict(n=12, xs=16, os=16), -2), (dict(n=32776, xs=32776, os=32776), -2), (dict(E4, group=16), -2), (dict(E4, group=8), -2),
+    (dict(n=12, xs=16, os=16), -2), (dict(n=16392, xs=16392, os=16392), -2), (dict(E4, group=16), -2), (dict(E4, group=8), -2),
     (dict(rows=1 << 30, heads=4, n=8, xs=32, os=32), -2),
     (dict(rows=0, x=None, w=None, out=None), 0)])
 def test_norm_refusals(lib, over, code):
@@ -57,7 +57,7 @@ def gradient(lib, **over):
     (dict(dh=FAKE + 4 * STEP + 8), -1), (dict(dw=FAKE + 6 * STEP + 2), -1), (dict(ws=None), -1), (dict(ws=FAKE + 7 * STEP + 64), -1),
     (dict(size=256), -1), (dict(dx=FAKE + 32), -1), (dict(dx=FAKE, xs=512), -1), (dict(dres=FAKE + 5 * STEP), -1),
     (dict(dw=FAKE + 2 * STEP), -1), (dict(st=2, dx=FAKE + STEP), -1), (dict(ws=FAKE + 4 * STEP), -1),
-    (dict(n=20, ys=24, hs=24, xs=24), -2), (dict(n=40000, ys=40000, hs=40000, xs=40000), -2),
+    (dict(n=20, ys=24, hs=24, xs=24), -2), (dict(n=20000, ys=20000, hs=20000, xs=20000), -2),
     (dict(rows=0, dy=None, dw=None), 0)])
 def test_gradient_refusals(lib, over, code):
     assert gradient(lib, **over) == code
