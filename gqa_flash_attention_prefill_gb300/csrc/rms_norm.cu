@@ -24,6 +24,18 @@ namespace gqa {
 
 namespace {
 
+// n / d for 0 <= n < 2^31: the high half of a product, and a shift.
+struct Div {
+  uint32_t m;
+  int l;
+  __host__ void set(uint32_t d) {
+    l = 0;
+    while ((1ull << l) < d) ++l;
+    m = (uint32_t)(((1ull << (32 + l)) + d - 1) / d - (1ull << 32));
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, m) + n) >> l; }
+};
+
 struct NormParams {
   const void* x;  // backward: dy
   const void* residual;  // backward: h
@@ -38,20 +50,51 @@ struct NormParams {
   float* part;  // [CTAs of the gradient][n]
   float* dweight;
   long long x_stride, h_stride, out_stride;
-  long long rows;  // rows x heads
+  uint32_t rows;  // rows x heads
+  Div div_heads;
   int heads, n, team;  // team: lanes of a row (0: the CTA)
   int group;       // values that share a scale (0: 16-bit output)
   int w32;
   int parts;
   int stages;
-  float offset, eps;
+  float offset, eps, inv_n;
   unsigned int* status;
   unsigned long long timeout_ns;
 };
 constexpr int kMaxStages = 4;
 
-struct Vec8 {
-  float v[8];
+// Row r of [rows, heads]: where its values start in a tensor of that row stride.
+__device__ __forceinline__ size_t start(const NormParams& p, uint32_t row, long long stride) {
+  const uint32_t token = p.div_heads(row), head = row - token * p.heads;
+  return (size_t)token * stride + (size_t)head * p.n;
+}
+
+// Two fp32 values in one register pair, two lanes an instruction (subnormals
+// kept): at 6.8 TB/s an SM has some 100 instructions for 8 values and their
+// gradient, so their count matters.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float sum2(uint64_t a) {
+  float x, y;
+  unf2(a, x, y);
+  return x + y;
+}
+
+struct Vec8 {  // 8 values
+  uint64_t v[4];
 };
 
 template <bool BF16>
@@ -59,16 +102,19 @@ __device__ __forceinline__ Vec8 widen(const uint4& u) {
   Vec8 r;
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = unpack_lo<BF16>(w[i]);
-    r.v[2 * i + 1] = unpack_hi<BF16>(w[i]);
-  }
+  for (int i = 0; i < 4; ++i) r.v[i] = f2(unpack_lo<BF16>(w[i]), unpack_hi<BF16>(w[i]));
   return r;
 }
 template <bool BF16>
 __device__ __forceinline__ uint4 narrow(const Vec8& a) {
-  return make_uint4(pack2<BF16>(a.v[0], a.v[1]), pack2<BF16>(a.v[2], a.v[3]),
-                    pack2<BF16>(a.v[4], a.v[5]), pack2<BF16>(a.v[6], a.v[7]));
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    unf2(a.v[i], lo, hi);
+    w[i] = pack2<BF16>(lo, hi);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // 8 values as they lie in memory: 16 bytes, or 32.
@@ -96,10 +142,8 @@ __device__ __forceinline__ Vec8 values(const Raw<F32>& r) {
     Vec8 v;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      v.v[4 * i] = __uint_as_float(r.a[i].x);
-      v.v[4 * i + 1] = __uint_as_float(r.a[i].y);
-      v.v[4 * i + 2] = __uint_as_float(r.a[i].z);
-      v.v[4 * i + 3] = __uint_as_float(r.a[i].w);
+      v.v[2 * i] = (uint64_t)r.a[i].y << 32 | r.a[i].x;
+      v.v[2 * i + 1] = (uint64_t)r.a[i].w << 32 | r.a[i].z;
     }
     return v;
   }
@@ -107,9 +151,9 @@ __device__ __forceinline__ Vec8 values(const Raw<F32>& r) {
 template <bool F32, bool BF16>
 __device__ __forceinline__ void store8(void* base, size_t at, const Vec8& v) {
   if constexpr (F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-    p[0] = make_float4(v.v[0], v.v[1], v.v[2], v.v[3]);
-    p[1] = make_float4(v.v[4], v.v[5], v.v[6], v.v[7]);
+    ulonglong2* p = reinterpret_cast<ulonglong2*>(static_cast<float*>(base) + at);
+    p[0] = make_ulonglong2(v.v[0], v.v[1]);
+    p[1] = make_ulonglong2(v.v[2], v.v[3]);
   } else {
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = narrow<BF16>(v);
   }
@@ -120,8 +164,9 @@ template <bool BF16>
 __device__ __forceinline__ Vec8 weight8(const NormParams& p, int col) {
   Vec8 w = p.w32 ? values<true, BF16>(load_raw<true>(p.weight, (size_t)col))
                  : values<false, BF16>(load_raw<false>(p.weight, (size_t)col));
+  const uint64_t o = f2(p.offset, p.offset);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w.v[i] += p.offset;
+  for (int i = 0; i < 4; ++i) w.v[i] = add2(w.v[i], o);
   return w;
 }
 
@@ -151,95 +196,107 @@ __device__ __forceinline__ void row_reduce(float& sum, float& most, int team, fl
   }
 }
 
-// (sum / n + eps)^-1/2 within an ulp: the reciprocal square root, and a step of
-// Newton's method with the residual in one rounding.
-__device__ __forceinline__ float rstd_of(float sum, int n, float eps) {
-  const float v = sum / (float)n + eps, r = rsqrtf(v), t = v * r;
+// (sum / n + eps)^-1/2: the reciprocal square root, and a step of Newton's method
+// whose residual 1 - v r^2 has the rounding of v r in it.
+__device__ __forceinline__ float rstd_of(const NormParams& p, float sum) {
+  const float v = fmaf(sum, p.inv_n, p.eps), r = rsqrtf(v), t = v * r;
   return fmaf(0.5f * r, fmaf(-t, r, 1.f) - fmaf(v, r, -t) * r, r);
 }
 
-// Sum over 8 values of a b, in pairs.
+// The sum of 8 products.
 __device__ __forceinline__ float dot8(const Vec8& a, const Vec8& b) {
-  float s[4];
+  return sum2(add2(fma2(a.v[0], b.v[0], mul2(a.v[1], b.v[1])), fma2(a.v[2], b.v[2], mul2(a.v[3], b.v[3]))));
+}
+__device__ __forceinline__ float most8(const Vec8& a) {
+  float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s[i] = fmaf(a.v[2 * i], b.v[2 * i], a.v[2 * i + 1] * b.v[2 * i + 1]);
-  return (s[0] + s[1]) + (s[2] + s[3]);
+  for (int i = 0; i < 4; ++i) {
+    float x, y;
+    unf2(a.v[i], x, y);
+    m = max3(m, fabsf(x), fabsf(y));
+  }
+  return m;
 }
 
 // One row's 8 values in a thread of its team, before and after the row's sums.
 template <bool BF16, bool F32, bool OUT8>
 struct NormVec {
-  Vec8 h;
+  Vec8 h;      // with OUT8, from take() on times the weight
+  float top;   // OUT8: the largest magnitude of them
   bool in;
-  __device__ __forceinline__ void take(const NormParams& p, const uint4& x, const Raw<F32>& r,
-                                       size_t hat, int c, float& sum, float& most) {
+  // w: the weight of the columns (OUT8 alone uses it here).
+  __device__ __forceinline__ void take(const NormParams& p, const uint4& x, const Raw<F32>& r, const Vec8& w,
+                                       size_t hat, float& sum, float& most) {
+    top = 0.f;
     if (!in) return;
     h = widen<BF16>(x);
     if (p.residual != nullptr) {
       const Vec8 a = values<F32, BF16>(r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h.v[i] += a.v[i];
+      for (int i = 0; i < 4; ++i) h.v[i] = add2(h.v[i], a.v[i]);
       // The norm is of what the stream holds.
-      if constexpr (!F32) h = widen<BF16>(narrow<BF16>(h));
-      store8<F32, BF16>(p.h_out, hat + 8 * c, h);
+      if constexpr (!F32) {
+        const uint4 n = narrow<BF16>(h);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.h_out) + hat) = n;
+        h = widen<BF16>(n);
+      } else {
+        store8<true, BF16>(p.h_out, hat, h);
+      }
     }
     sum += dot8(h, h);
     if constexpr (OUT8) {
-      const Vec8 w = weight8<BF16>(p, 8 * c);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(h.v[i] * w.v[i]));
+      for (int i = 0; i < 4; ++i) h.v[i] = mul2(h.v[i], w.v[i]);
+      top = most8(h);
+      most = fmaxf(most, top);
     }
   }
   // All lanes of a warp call it together.
-  __device__ __forceinline__ void give(const NormParams& p, size_t row, size_t oat, int c, float rstd,
-                                       float most) {
-    Vec8 w;
-    if (in) {
-      w = weight8<BF16>(p, 8 * c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h.v[i] = h.v[i] * rstd * w.v[i];
-    }
+  __device__ __forceinline__ void give(const NormParams& p, size_t row, size_t oat, int c, const Vec8& w,
+                                       float rstd, float most) {
     if constexpr (!OUT8) {
-      if (in) store8<false, BF16>(p.out, oat + 8 * c, h);
-    } else {
-      const bool whole = p.group == p.n;  // one scale a row
-      float top = most * rstd;
-      if (!whole) {
-        top = 0.f;
-        if (in) {
+      if (!in) return;
+      const uint64_t r = f2(rstd, rstd);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(h.v[i]));
-        }
+      for (int i = 0; i < 4; ++i) h.v[i] = mul2(mul2(h.v[i], r), w.v[i]);
+      store8<false, BF16>(p.out, oat + 8 * c, h);
+    } else {
+      if (p.group == p.n) {  // one scale a row
+        top = most;
+      } else {
         for (int o = 1; o < p.group / 8; o <<= 1)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       }
-      const int e = e4m3_scale_exponent(top);
       if (!in) return;
-      const float m = pow2f(-e);
-      uint32_t b[2];
+      const int e = e4m3_scale_exponent(top * rstd);
+      const float m = rstd * pow2f(-e);  // exact: one rounding of h w rstd, then e4m3's
+      const uint64_t mm = f2(m, m);
+      uint32_t b[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        b[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(h.v[4 * i] * m, h.v[4 * i + 1] * m),
-                                                  __NV_SATFINITE, __NV_E4M3) |
-               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(h.v[4 * i + 2] * m, h.v[4 * i + 3] * m),
-                                                  __NV_SATFINITE, __NV_E4M3) << 16;
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + oat + 8 * c) = make_uint2(b[0], b[1]);
+      for (int i = 0; i < 4; ++i) {
+        float x, y;
+        unf2(mul2(h.v[i], mm), x, y);
+        b[i] = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + oat + 8 * c) =
+          make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
       if (8 * c % p.group == 0) p.scales[row * (p.n / p.group) + 8 * c / p.group] = (uint8_t)(e + 127);
     }
   }
 };
 
-// A CTA of up to T threads per row, V groups of 8 values a thread.
-template <bool BF16, bool F32, bool OUT8, int V, int T>
-__global__ void __launch_bounds__(T) norm_kernel(const __grid_constant__ NormParams p) {
+// A CTA of up to T threads per row, V groups of 8 values a thread; B CTAs an SM.
+template <bool BF16, bool F32, bool OUT8, int V, int T, int B>
+__global__ void __launch_bounds__(T, B) norm_kernel(const __grid_constant__ NormParams p) {
   __shared__ float s[64];
   grid_dep_launch_dependents();
   grid_dep_wait();
   const int TS = blockDim.x, lane = threadIdx.x, nv = p.n / 8;
-  const size_t row = blockIdx.x, token = row / p.heads, head = row - token * p.heads;
-  const size_t xat = token * p.x_stride + head * p.n, hat = row * p.n, oat = token * p.out_stride + head * p.n;
+  const uint32_t row = blockIdx.x;
+  const size_t xat = start(p, row, p.x_stride), hat = (size_t)row * p.n;
   uint4 x[V];
   Raw<F32> r[V];
+  Vec8 w[V];
   NormVec<BF16, F32, OUT8> n[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -248,82 +305,96 @@ __global__ void __launch_bounds__(T) norm_kernel(const __grid_constant__ NormPar
     if (n[v].in) {
       x[v] = load_raw<false>(p.x, xat + 8 * c).a[0];
       if (p.residual != nullptr) r[v] = load_raw<F32>(p.residual, hat + 8 * c);
+      if constexpr (OUT8) w[v] = weight8<BF16>(p, 8 * c);
     }
   }
   float sum = 0.f, most = 0.f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) n[v].take(p, x[v], r[v], hat, v * TS + lane, sum, most);
+  for (int v = 0; v < V; ++v) n[v].take(p, x[v], r[v], w[v], hat + 8 * (v * TS + lane), sum, most);
   row_reduce<true, OUT8>(sum, most, 32, s);
-  const float rstd = rstd_of(sum, p.n, p.eps);
+  const float rstd = rstd_of(p, sum);
   if (lane == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+  const size_t oat = start(p, row, p.out_stride);
 #pragma unroll
-  for (int v = 0; v < V; ++v) n[v].give(p, row, oat, v * TS + lane, rstd, most);
+  for (int v = 0; v < V; ++v) {
+    const int c = v * TS + lane;
+    if (!OUT8 && n[v].in) w[v] = weight8<BF16>(p, 8 * c);
+    n[v].give(p, row, oat, c, w[v], rstd, most);
+  }
 }
 
 // Rows of up to 256 values: a row in `team` lanes (8, 16 or 32), U rows a team,
-// all of whose loads are on their way at once.
+// all of whose loads are on their way at once, and one weight for all of them.
 constexpr int kTeamRows = 4;
 template <bool BF16, bool F32, bool OUT8>
-__global__ void __launch_bounds__(256) norm_team_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(256, 4) norm_team_kernel(const __grid_constant__ NormParams p) {
   constexpr int U = kTeamRows;
   grid_dep_launch_dependents();
   grid_dep_wait();
   const int c = threadIdx.x & (p.team - 1), teams = 256 / p.team;
-  const long long row0 = (long long)blockIdx.x * teams * U + threadIdx.x / p.team;
+  const uint32_t row0 = blockIdx.x * teams * U + threadIdx.x / p.team;
+  const bool col = c < p.n / 8;
   uint4 x[U];
   Raw<F32> r[U];
   NormVec<BF16, F32, OUT8> n[U];
-  size_t oat[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const long long row = row0 + u * teams;
-    n[u].in = row < p.rows && c < p.n / 8;
+    const uint32_t row = row0 + u * teams;
+    n[u].in = row < p.rows && col;
     if (n[u].in) {
-      const size_t token = (uint32_t)row / (uint32_t)p.heads, head = (size_t)row - token * p.heads;
-      x[u] = load_raw<false>(p.x, token * p.x_stride + head * p.n + 8 * c).a[0];
+      x[u] = load_raw<false>(p.x, start(p, row, p.x_stride) + 8 * c).a[0];
       if (p.residual != nullptr) r[u] = load_raw<F32>(p.residual, (size_t)row * p.n + 8 * c);
-      oat[u] = token * p.out_stride + head * p.n;
     }
   }
+  Vec8 w;
+  if (col) w = weight8<BF16>(p, 8 * c);
   float sum[U], most[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     sum[u] = most[u] = 0.f;
-    n[u].take(p, x[u], r[u], (size_t)(row0 + u * teams) * p.n, c, sum[u], most[u]);
+    n[u].take(p, x[u], r[u], w, (size_t)(row0 + u * teams) * p.n + 8 * c, sum[u], most[u]);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) row_reduce<false, OUT8>(sum[u], most[u], p.team, nullptr);
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const float rstd = rstd_of(sum[u], p.n, p.eps);
-    const long long row = row0 + u * teams;
+    const float rstd = rstd_of(p, sum[u]);
+    const uint32_t row = row0 + u * teams;
     if (n[u].in && c == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
-    n[u].give(p, (size_t)row, oat[u], c, rstd, most[u]);
+    n[u].give(p, row, start(p, row, p.out_stride), c, w, rstd, most[u]);
   }
 }
 
 // ------------------------------------------------------------------ gradient
-// dx of 8 values, and the thread's share of dw and of the row's sum.
-template <bool BF16, bool F32>
+// The thread's share of dw and of the row's sum of g t, from 8 values.
 __device__ __forceinline__ float grad_sum(const Vec8& d, const Vec8& h, const Vec8& w, float rstd, Vec8& acc) {
+  const uint64_t r = f2(rstd, rstd);
   Vec8 t, g;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    t.v[i] = h.v[i] * rstd;
-    acc.v[i] = fmaf(d.v[i], t.v[i], acc.v[i]);
-    g.v[i] = d.v[i] * w.v[i];
+  for (int i = 0; i < 4; ++i) {
+    t.v[i] = mul2(h.v[i], r);
+    acc.v[i] = fma2(d.v[i], t.v[i], acc.v[i]);
+    g.v[i] = mul2(d.v[i], w.v[i]);
   }
   return dot8(g, t);
 }
+// dx = rstd g + (dh - h rstd^2 mean(g t)) of 8 values; k = rstd^2 mean(g t).
 template <bool BF16, bool F32>
 __device__ __forceinline__ void grad_store(const NormParams& p, const Vec8& d, const Vec8& h, const Vec8& w,
-                                           const Vec8& dh, float rstd, float mean, size_t oat, size_t sat) {
+                                           const Vec8& dh, float rstd, float k, size_t oat, size_t sat) {
+  const uint64_t r = f2(rstd, rstd), kk = f2(-k, -k);
   Vec8 o;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    o.v[i] = rstd * fmaf(d.v[i], w.v[i], -(h.v[i] * rstd) * mean) + dh.v[i];
+  for (int i = 0; i < 4; ++i)
+    o.v[i] = fma2(mul2(d.v[i], w.v[i]), r, fma2(h.v[i], kk, dh.v[i]));
   if (p.out != nullptr) store8<false, BF16>(p.out, oat, o);
   if (p.dresidual != nullptr) store8<F32, BF16>(p.dresidual, sat, o);
+}
+__device__ __forceinline__ Vec8 zero8() {
+  Vec8 z;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z.v[i] = 0ull;
+  return z;
 }
 
 // A row in a CTA.  Each CTA walks rows blockIdx.x, + gridDim.x, ... through a
@@ -349,72 +420,67 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const __grid_constant_
   grid_dep_launch_dependents();
   grid_dep_wait();
   // Copies row number k of this CTA into its stage.
-  auto fill = [&](long long k) {
-    const long long row = blockIdx.x + k * gridDim.x;
-    if (row >= p.rows) return;
-    const size_t token = (size_t)row / p.heads, head = (size_t)row - token * p.heads;
-    const uint32_t st = (uint32_t)(k % p.stages), bar = sbar + 8 * st, dst = sring + st * stage;
+  auto fill = [&](uint32_t k, uint32_t st) {
+    const unsigned long long at = blockIdx.x + (unsigned long long)k * gridDim.x;
+    if (at >= p.rows) return;
+    const uint32_t row = (uint32_t)at, bar = sbar + 8 * st, dst = sring + st * stage;
     mbar_arrive_expect_tx(bar, stage);
-    bulk_load(dst, static_cast<const uint16_t*>(p.x) + token * p.x_stride + head * p.n, 2u * p.n, bar);
-    bulk_load(dst + off_h, static_cast<const uint8_t*>(p.residual) + es * (token * p.h_stride + head * p.n), es * p.n, bar);
+    bulk_load(dst, static_cast<const uint16_t*>(p.x) + start(p, row, p.x_stride), 2u * p.n, bar);
+    bulk_load(dst + off_h, static_cast<const uint8_t*>(p.residual) + es * start(p, row, p.h_stride), es * p.n, bar);
     if (p.dh != nullptr) bulk_load(dst + off_dh, static_cast<const uint8_t*>(p.dh) + es * ((size_t)row * p.n), es * p.n, bar);
   };
   if (threadIdx.x == 0)
-    for (int k = 0; k < p.stages; ++k) fill(k);
+    for (int k = 0; k < p.stages; ++k) fill(k, k);
   Vec8 w[V], acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = v * TS + lane;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc[v].v[i] = 0.f;
+    acc[v] = zero8();
     if (c < nv) w[v] = weight8<BF16>(p, 8 * c);
   }
-  const float inv_n = 1.f / (float)p.n;
-  long long k = 0;
-  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, ++k) {
-    const uint32_t st = (uint32_t)(k % p.stages);
+  uint32_t k = 0, st = 0, par = 0;  // the row's number, its stage, the stage's parity
+  for (unsigned long long at_row = blockIdx.x; at_row < p.rows; at_row += gridDim.x, ++k) {
+    const uint32_t row = (uint32_t)at_row;
     const float rstd = __ldg(p.rstd_in + row);
     // A wait that runs out raises the status; the sums below are then of
     // whatever the stage holds, and the rows still end.
-    (void)wait_bounded(sbar + 8 * st, (uint32_t)(k / p.stages) & 1u, &abort_word, p.status, p.timeout_ns);
+    (void)wait_bounded(sbar + 8 * st, par, &abort_word, p.status, p.timeout_ns);
     const uint8_t* at = ring + st * stage;
     float sum = 0.f, none = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = v * TS + lane;
       if (c < nv)
-        sum += grad_sum<BF16, F32>(widen<BF16>(load_raw<false>(at, 8 * c).a[0]),
-                                   values<F32, BF16>(load_raw<F32>(at + off_h, 8 * c)), w[v], rstd, acc[v]);
+        sum += grad_sum(widen<BF16>(load_raw<false>(at, 8 * c).a[0]),
+                        values<F32, BF16>(load_raw<F32>(at + off_h, 8 * c)), w[v], rstd, acc[v]);
     }
     row_reduce<true, false>(sum, none, 32, s[k & 1]);
     // Every thread is past the row before: its stage is free.
-    if (threadIdx.x == 0 && k > 0 && p.stages > 1) fill(k - 1 + p.stages);
-    const float mean = sum * inv_n;
-    const size_t token = (size_t)row / p.heads, head = (size_t)row - token * p.heads;
+    if (threadIdx.x == 0 && k > 0 && p.stages > 1)
+      fill(k - 1 + p.stages, (st == 0 ? p.stages : st) - 1);
+    const float mean = rstd * rstd * (sum * p.inv_n);
+    const size_t oat = start(p, row, p.out_stride), sat = (size_t)row * p.n;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = v * TS + lane;
       if (c < nv) {
-        Vec8 o;
-        if (p.dh != nullptr) {
-          o = values<F32, BF16>(load_raw<F32>(at + off_dh, 8 * c));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o.v[i] = 0.f;
-        }
+        const Vec8 o = p.dh != nullptr ? values<F32, BF16>(load_raw<F32>(at + off_dh, 8 * c)) : zero8();
         grad_store<BF16, F32>(p, widen<BF16>(load_raw<false>(at, 8 * c).a[0]),
                               values<F32, BF16>(load_raw<F32>(at + off_h, 8 * c)), w[v], o, rstd, mean,
-                              token * p.out_stride + head * p.n + 8 * c, (size_t)row * p.n + 8 * c);
+                              oat + 8 * c, sat + 8 * c);
       }
     }
     if (p.stages == 1) {  // rows so wide that one fits
       __syncthreads();
-      if (threadIdx.x == 0) fill(k + 1);
+      if (threadIdx.x == 0) fill(k + 1, 0);
+    }
+    if (++st == (uint32_t)p.stages) {
+      st = 0;
+      par ^= 1u;
     }
   }
   if (abort_word != 0u && threadIdx.x == 0)  // let the copies in flight land
-    for (long long j = k > p.stages ? k - p.stages : 0; j < k + p.stages; ++j)
-      if (blockIdx.x + j * gridDim.x < p.rows)
+    for (unsigned long long j = k > (uint32_t)p.stages ? k - p.stages : 0; j < k; ++j)
         wait_drain(sbar + 8 * (uint32_t)(j % p.stages), (uint32_t)(j / p.stages) & 1u, p.timeout_ns);
   if (p.part == nullptr) return;
   float* part = p.part + (size_t)blockIdx.x * p.n;
@@ -425,32 +491,33 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const __grid_constant_
   }
 }
 
-// Rows of up to 256 values: a row in `team` lanes, U rows a team at a time.
+// Rows of up to 256 values: a row in `team` lanes, U rows a team at a time (two,
+// in 64 registers, and four CTAs an SM: 4095 x 32 rows of 128 in 23.1 us; four in
+// 116 registers and two CTAs 25.3).
+constexpr int kTeamRowsBack = 2;
 template <bool BF16, bool F32>
-__global__ void __launch_bounds__(256, 2) norm_backward_team_kernel(const __grid_constant__ NormParams p) {
-  constexpr int U = kTeamRows;
-  __shared__ float s_acc[256 * 8];
+__global__ void __launch_bounds__(256, 4) norm_backward_team_kernel(const __grid_constant__ NormParams p) {
+  constexpr int U = kTeamRowsBack;
+  __shared__ __align__(16) float s_acc[256 * 8];
   grid_dep_launch_dependents();
   grid_dep_wait();
   const int c = threadIdx.x & (p.team - 1), teams = 256 / p.team, mine = threadIdx.x / p.team;
   const bool col = c < p.n / 8, has = p.dh != nullptr;
-  Vec8 w, acc;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) acc.v[i] = 0.f;
+  Vec8 w, acc = zero8();
   if (col) w = weight8<BF16>(p, 8 * c);
-  const float inv_n = 1.f / (float)p.n;
-  const long long per = (long long)teams * U;
-  for (long long base = blockIdx.x * per; base < p.rows; base += gridDim.x * per) {
+  const uint32_t per = teams * U;
+  for (unsigned long long base = (unsigned long long)blockIdx.x * per; base < p.rows;
+       base += (unsigned long long)gridDim.x * per) {
     uint4 dy[U];
     Raw<F32> h[U], dh[U];
     float rstd[U], sum[U];
+    const uint32_t row0 = (uint32_t)base + mine;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long row = base + u * teams + mine;
+      const uint32_t row = row0 + u * teams;
       if (col && row < p.rows) {
-        const size_t token = (uint32_t)row / (uint32_t)p.heads, head = (size_t)row - token * p.heads;
-        dy[u] = load_raw<false>(p.x, token * p.x_stride + head * p.n + 8 * c).a[0];
-        h[u] = load_raw<F32>(p.residual, token * p.h_stride + head * p.n + 8 * c);
+        dy[u] = load_raw<false>(p.x, start(p, row, p.x_stride) + 8 * c).a[0];
+        h[u] = load_raw<F32>(p.residual, start(p, row, p.h_stride) + 8 * c);
         if (has) dh[u] = load_raw<F32>(p.dh, (size_t)row * p.n + 8 * c);
         rstd[u] = __ldg(p.rstd_in + row);
       }
@@ -458,32 +525,25 @@ __global__ void __launch_bounds__(256, 2) norm_backward_team_kernel(const __grid
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       sum[u] = 0.f;
-      if (col && base + u * teams + mine < p.rows)
-        sum[u] = grad_sum<BF16, F32>(widen<BF16>(dy[u]), values<F32, BF16>(h[u]), w, rstd[u], acc);
+      if (col && row0 + u * teams < p.rows)
+        sum[u] = grad_sum(widen<BF16>(dy[u]), values<F32, BF16>(h[u]), w, rstd[u], acc);
     }
     float none = 0.f;
 #pragma unroll
     for (int u = 0; u < U; ++u) row_reduce<false, false>(sum[u], none, p.team, nullptr);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long row = base + u * teams + mine;
+      const uint32_t row = row0 + u * teams;
       if (col && row < p.rows) {
-        const size_t token = (uint32_t)row / (uint32_t)p.heads, head = (size_t)row - token * p.heads;
-        Vec8 o;
-        if (has) {
-          o = values<F32, BF16>(dh[u]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o.v[i] = 0.f;
-        }
-        grad_store<BF16, F32>(p, widen<BF16>(dy[u]), values<F32, BF16>(h[u]), w, o, rstd[u], sum[u] * inv_n,
-                              token * p.out_stride + head * p.n + 8 * c, (size_t)row * p.n + 8 * c);
+        const Vec8 o = has ? values<F32, BF16>(dh[u]) : zero8();
+        grad_store<BF16, F32>(p, widen<BF16>(dy[u]), values<F32, BF16>(h[u]), w, o, rstd[u],
+                              rstd[u] * rstd[u] * (sum[u] * p.inv_n), start(p, row, p.out_stride) + 8 * c,
+                              (size_t)row * p.n + 8 * c);
       }
     }
   }
   if (p.part == nullptr) return;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s_acc[threadIdx.x * 8 + i] = acc.v[i];
+  store8<true, BF16>(s_acc, (size_t)threadIdx.x * 8, acc);
   __syncthreads();
   if ((int)threadIdx.x < p.n) {  // at most 256 columns
     float a = 0.f;
@@ -492,22 +552,31 @@ __global__ void __launch_bounds__(256, 2) norm_backward_team_kernel(const __grid
   }
 }
 
-// dw: the sum of the CTAs' shares.  32 columns a block, 8 shares at a time.
-__global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ NormParams p) {
-  __shared__ float s[8][32];
+// dw: the sum of the CTAs' shares.  32 columns a block, a share a warp; up to ten
+// of a warp's loads on their way at once.
+__global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__ NormParams p) {
+  constexpr int U = 10;
+  __shared__ float s[32][33];
   grid_dep_launch_dependents();
   grid_dep_wait();
   const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float a = 0.f;
-  if (c < p.n)
-    for (int b = y; b < p.parts; b += 8) a += __ldcg(p.part + (size_t)b * p.n + c);
+  for (int b0 = y; b0 < p.parts; b0 += 32 * U) {
+    float v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + 32 * u;
+      v[u] = b < p.parts && c < p.n ? __ldcg(p.part + (size_t)b * p.n + c) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) a += v[u];
+  }
   s[y][lane] = a;
   __syncthreads();
-  if (y == 0 && c < p.n) {
+  a = s[lane][y];  // column y of the block, share `lane`
 #pragma unroll
-    for (int k = 1; k < 8; ++k) a += s[k][lane];
-    p.dweight[c] = a;
-  }
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if (lane == 0 && blockIdx.x * 32 + y < p.n) p.dweight[blockIdx.x * 32 + y] = a;
 }
 
 // ------------------------------------------------------------------ host
@@ -528,7 +597,7 @@ NormShape norm_shape(int n) {
 }
 // CTAs per SM of the gradient's persistent grid.
 int backward_per_sm(const NormShape& s) {
-  if (s.team > 0) return 2;
+  if (s.team > 0) return 4;
   const int c = 512 / s.threads;
   return c < 1 ? 1 : c > 4 ? 4 : c;
 }
@@ -567,12 +636,12 @@ template <bool BF16, bool F32, bool OUT8>
 cudaError_t launch_norm_as(const NormParams& p, const NormShape& s, cudaStream_t st) {
   if (s.team > 0) {
     const long long per = (long long)kTeamRows * 256 / s.team;
-    return launch_pdl(norm_team_kernel<BF16, F32, OUT8>, p, (int)((p.rows + per - 1) / per), 256, 0, st);
+    return launch_pdl(norm_team_kernel<BF16, F32, OUT8>, p, (int)(((long long)p.rows + per - 1) / per), 256, 0, st);
   }
   const int grid = (int)p.rows;
-  return s.v == 1     ? launch_pdl(norm_kernel<BF16, F32, OUT8, 1, 256>, p, grid, s.threads, 0, st)
-         : s.t == 512 ? launch_pdl(norm_kernel<BF16, F32, OUT8, 2, 512>, p, grid, s.threads, 0, st)
-                      : launch_pdl(norm_kernel<BF16, F32, OUT8, 2, 1024>, p, grid, s.threads, 0, st);
+  return s.v == 1     ? launch_pdl(norm_kernel<BF16, F32, OUT8, 1, 256, 6>, p, grid, s.threads, 0, st)
+         : s.t == 512 ? launch_pdl(norm_kernel<BF16, F32, OUT8, 2, 512, 2>, p, grid, s.threads, 0, st)
+                      : launch_pdl(norm_kernel<BF16, F32, OUT8, 2, 1024, 1>, p, grid, s.threads, 0, st);
 }
 template <bool BF16, bool F32>
 cudaError_t launch_norm(const NormParams& p, const NormShape& s, cudaStream_t st) {
@@ -652,7 +721,9 @@ int run_norm(const void* x, long long x_stride, const void* residual, void* resi
   p.rstd = rstd;
   p.x_stride = x_stride;
   p.out_stride = out_stride;
-  p.rows = (long long)rows * heads;
+  p.rows = (uint32_t)rows * (uint32_t)heads;
+  p.div_heads.set((uint32_t)heads);
+  p.inv_n = 1.f / (float)n;
   p.heads = heads;
   p.n = n;
   p.group = e4 ? group : 0;
@@ -737,7 +808,9 @@ int run_norm_backward(const void* dy, long long dy_stride, const void* h, long l
   p.x_stride = dy_stride;
   p.h_stride = h_stride;
   p.out_stride = dx_stride;
-  p.rows = (long long)rows * heads;
+  p.rows = (uint32_t)rows * (uint32_t)heads;
+  p.div_heads.set((uint32_t)heads);
+  p.inv_n = 1.f / (float)n;
   p.heads = heads;
   p.n = n;
   p.team = s.team;
@@ -755,7 +828,7 @@ int run_norm_backward(const void* dy, long long dy_stride, const void* h, long l
     const size_t fit = (per_sm > 1 ? kRingBytes / per_sm - 2048 : kRingBytes) / stage;
     p.stages = (int)(fit < kMaxStages ? fit : kMaxStages);
   }
-  const long long per = s.team > 0 ? (long long)kTeamRows * 256 / s.team : 1, all = (p.rows + per - 1) / per;
+  const long long per = s.team > 0 ? (long long)kTeamRowsBack * 256 / s.team : 1, all = ((long long)p.rows + per - 1) / per;
   const long long most = (long long)sms * per_sm;
   const int grid = (int)(all < most ? all : most);
   const unsigned smem = (unsigned)(p.stages * stage);
@@ -763,7 +836,7 @@ int run_norm_backward(const void* dy, long long dy_stride, const void* h, long l
   const bool bf = dtype == GQA_BF16, f32 = stream_type == GQA_F32;
   cudaError_t e = bf ? (f32 ? launch_back<true, true>(p, s, grid, smem, st) : launch_back<true, false>(p, s, grid, smem, st))
                      : (f32 ? launch_back<false, true>(p, s, grid, smem, st) : launch_back<false, false>(p, s, grid, smem, st));
-  if (e == cudaSuccess && dweight != nullptr) e = launch_pdl(norm_join_kernel, p, (n + 31) / 32, 256, 0, st);
+  if (e == cudaSuccess && dweight != nullptr) e = launch_pdl(norm_join_kernel, p, (n + 31) / 32, 1024, 0, st);
   return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
