@@ -21,7 +21,7 @@ constexpr int kPlanBins = 64;
 // Shares of the work that a CTA gets at the least: a unit is cut when it costs
 // more than 1 / kShares of a CTA's part of the whole.  Tiles below which a
 // unit is not cut.
-constexpr int kShares = 3;
+constexpr int kShares = 1;
 constexpr int kMinTiles = 8;
 
 // Relative cost of a streamed tile: its products.
@@ -81,14 +81,13 @@ __device__ __forceinline__ BwdUnit plan_unit(const BwdParams& p, int x, int nq, 
   return u;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) bwd_plan_kernel(const __grid_constant__ BwdParams p) {
-  __shared__ long long s_total;
-  __shared__ int s_bad, s_slots, s_joins, s_carry[2], s_warp[2][32], s_bins[kPlanBins];
+// Metadata checks, and the tiles of the sequences before each one.
+__global__ void __launch_bounds__(kPlanThreads) bwd_scan_kernel(const __grid_constant__ BwdParams p) {
+  __shared__ int s_bad, s_carry[2], s_warp[2][32];
   grid_dep_launch_dependents();
   grid_dep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    s_total = 0;
     s_bad = __ldg(p.cu) != 0;
     s_carry[0] = s_carry[1] = 0;
   }
@@ -140,8 +139,7 @@ __global__ void __launch_bounds__(kPlanThreads) bwd_plan_kernel(const __grid_con
   if (s_bad) {  // nothing is written
     if (tid == 0) {
       atomicOr(p.status, 2u);  // GQA_DEV_BAD_METADATA
-      p.hdr[kBwdUnits] = p.hdr[kBwdJoins] = p.hdr[kBwdQTiles] = p.hdr[kBwdKTiles] = 0;
-      p.hdr[kBwdNext] = 0;
+      p.hdr[kBwdQTiles] = p.hdr[kBwdKTiles] = 0;
       p.hdr[kBwdFailed] = 1;
     }
     return;
@@ -149,40 +147,57 @@ __global__ void __launch_bounds__(kPlanThreads) bwd_plan_kernel(const __grid_con
   if (tid == 0) {
     p.qtile0[p.num_seqs] = nq;
     p.ktile0[p.num_seqs] = nk;
+    p.hdr[kBwdFailed] = 0;
+    p.hdr[kBwdQTiles] = nq;
+    p.hdr[kBwdKTiles] = nk;
   }
   if (p.most != nullptr)
     for (long long i = tid; i < 4ll * p.num_seqs * p.Hkv; i += kPlanThreads) p.most[i] = 0u;
-  __syncthreads();
+}
+
+// The list of units, by one CTA: their costs are summed, costly ones are cut, and
+// the parts are sorted by cost, in bins (which CTA takes which unit changes no
+// result, so the order inside a bin may be any).
+__device__ __forceinline__ void bwd_plan(const BwdParams& p) {
+  constexpr int kKept = 2048;
+  __shared__ unsigned long long s_total;
+  __shared__ int s_slots, s_joins, s_bins[kPlanBins], s_n[kKept];
+  const int tid = threadIdx.x, lane = tid & 31, threads = blockDim.x;
+  const int nq = p.hdr[kBwdQTiles], nk = p.hdr[kBwdKTiles];
   const int total = nq + (p.d == 256 ? 2 : 1) * nk;
-  long long sum = 0;
-  for (int x = tid; x < total; x += kPlanThreads) {
-    const BwdUnit u = plan_unit(p, x, nq, nk);
-    sum += (long long)u.n * tile_cost(u.kind);
+  auto kind_of = [&](int x) { return x < nq ? kBwdQ : p.d != 256 ? kBwdKV : x < nq + nk ? kBwdK : kBwdV; };
+  auto tiles_of = [&](int x) { return x < kKept ? s_n[x] : plan_unit(p, x, nq, nk).n; };
+  if (tid == 0) s_total = 0;
+  __syncthreads();
+  unsigned long long sum = 0;
+  for (int x = tid; x < total; x += threads) {
+    const int n = plan_unit(p, x, nq, nk).n;
+    if (x < kKept) s_n[x] = n;
+    sum += (unsigned long long)n * tile_cost(kind_of(x));
   }
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) atomicAdd(reinterpret_cast<unsigned long long*>(&s_total), (unsigned long long)sum);
+  if (lane == 0) atomicAdd(&s_total, sum);
   __syncthreads();
   // The cost above which a unit is cut.  At most 2 sum / cap parts come of it;
   // should they not fit the workspace, the cap is doubled.
-  long long cap = (s_total * p.Hkv + (long long)p.ctas * kShares - 1) / ((long long)p.ctas * kShares);
+  long long cap = ((long long)s_total * p.Hkv + (long long)p.ctas * kShares - 1) / ((long long)p.ctas * kShares);
   if (cap < 4 * kMinTiles) cap = 4 * kMinTiles;
-  auto parts_of = [&](const BwdUnit& u) {
-    const long long n = ((long long)u.n * tile_cost(u.kind) + cap - 1) / cap;
-    return (int)(n < 1 ? 1 : n < u.n ? n : u.n);
+  auto parts_of = [&](int kind, int n) {
+    const long long k = ((long long)n * tile_cost(kind) + cap - 1) / cap;
+    return (int)(k < 1 ? 1 : k < n ? k : n);
   };
   auto bin_of = [&](int kind, int n) {  // 0: the costliest
     const long long k = n == 0 ? 0 : 1 + (long long)n * tile_cost(kind) * (kPlanBins - 2) / cap;
     return kPlanBins - 1 - (int)(k < kPlanBins - 1 ? k : kPlanBins - 1);
   };
   for (;;) {
-    for (int i = tid; i < kPlanBins; i += kPlanThreads) s_bins[i] = 0;
+    for (int i = tid; i < kPlanBins; i += threads) s_bins[i] = 0;
     if (tid == 0) s_slots = s_joins = 0;
     __syncthreads();
-    for (int x = tid; x < total; x += kPlanThreads) {
-      const BwdUnit u = plan_unit(p, x, nq, nk);
-      const int parts = parts_of(u);
+    for (int x = tid; x < total; x += threads) {
+      const int kind = kind_of(x), n = tiles_of(x), parts = parts_of(kind, n);
       for (int i = 0; i < parts; ++i)
-        atomicAdd(&s_bins[bin_of(u.kind, (int)((i + 1ll) * u.n / parts - (long long)i * u.n / parts))], 1);
+        atomicAdd(&s_bins[bin_of(kind, (int)((i + 1ll) * n / parts - (long long)i * n / parts))], 1);
       if (parts > 1) {
         atomicAdd(&s_slots, parts);
         atomicAdd(&s_joins, 1);
@@ -193,25 +208,27 @@ __global__ void __launch_bounds__(kPlanThreads) bwd_plan_kernel(const __grid_con
     cap *= 2;
     __syncthreads();
   }
-  if (tid == 0) {
-    int acc = 0;
-    for (int i = 0; i < kPlanBins; ++i) {
-      const int v = s_bins[i];
-      s_bins[i] = acc;
-      acc += v;
+  if (tid < 32) {  // the bins' first places: two bins a lane
+    static_assert(kPlanBins == 64, "two bins a lane");
+    const int n0 = s_bins[2 * lane], n1 = s_bins[2 * lane + 1];
+    int v = n0 + n1;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += w;
     }
-    p.hdr[kBwdUnits] = acc;
-    p.hdr[kBwdJoins] = s_joins;
-    p.hdr[kBwdNext] = 0;
-    p.hdr[kBwdFailed] = 0;
-    p.hdr[kBwdQTiles] = nq;
-    p.hdr[kBwdKTiles] = nk;
-    s_slots = s_joins = 0;
+    s_bins[2 * lane] = v - n0 - n1;
+    s_bins[2 * lane + 1] = v - n1;
+    if (lane == 31) {
+      p.hdr[kBwdUnits] = v;
+      p.hdr[kBwdJoins] = s_joins;
+      p.hdr[kBwdNext] = 0;
+      s_slots = s_joins = 0;
+    }
   }
   __syncthreads();
-  for (int x = tid; x < total; x += kPlanThreads) {
+  for (int x = tid; x < total; x += threads) {
     BwdUnit u = plan_unit(p, x, nq, nk);
-    const int parts = parts_of(u), n = u.n, off = u.b_off;
+    const int n = u.n, off = u.b_off, parts = parts_of(u.kind, n);
     int slot = -1;
     if (parts > 1) {
       slot = atomicAdd(&s_slots, parts);
@@ -230,7 +247,7 @@ __global__ void __launch_bounds__(kPlanThreads) bwd_plan_kernel(const __grid_con
 
 // ------------------------------------------------------------------ the rows' statistics
 // Bound by memory: out and dout are read once, 8 values a lane, a row in d / 8
-// neighbouring lanes.
+// neighbouring lanes.  The last CTA lists the units meanwhile.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ BwdParams p) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, ROUNDS = 16 / RPW;  // 16 rows a warp
@@ -239,8 +256,13 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ B
   grid_dep_launch_dependents();
   grid_dep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ctas = gridDim.x - 1;
+  if ((int)blockIdx.x == ctas) {
+    bwd_plan(p);
+    return;
+  }
   const int nq = p.hdr[kBwdQTiles] * p.Hkv, nk = BF16 ? 0 : p.hdr[kBwdKTiles] * p.Hkv;
-  for (int x = blockIdx.x; x < nq + nk; x += gridDim.x) {
+  for (int x = blockIdx.x; x < nq + nk; x += ctas) {
     const bool keys = x >= nq;
     const int y = keys ? x - nq : x, tile = y / p.Hkv, g = y - tile * p.Hkv;
     const int32_t* first = keys ? p.ktile0 : p.qtile0;
@@ -340,15 +362,17 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ B
 }
 
 // ------------------------------------------------------------------ join
-// Sums of the parts of cut units, in their order, and the sinks' gradient: one
-// block for 128 rows of one accumulator, or for one head's sink.
+// Sums of the parts of cut units, in their order: a thread per row and 16 of its
+// columns, all loads of two parts on their way at once; and the sinks' gradient,
+// one block a head.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ BwdParams p) {
+  constexpr int A = bwd_accs(D), kPieces = D / 32;  // blocks for 128 rows of one accumulator
   grid_dep_launch_dependents();
   grid_dep_wait();
   if (p.hdr[kBwdFailed] != 0) return;
   const int tid = threadIdx.x;
-  const int nj = p.hdr[kBwdJoins] * p.Hkv, tiles = p.hdr[kBwdQTiles];
+  const int nj = p.hdr[kBwdJoins] * p.Hkv * A * kPieces, tiles = p.hdr[kBwdQTiles];
   const int ns = p.dsinks != nullptr ? p.Hq : 0;
   for (int x = blockIdx.x; x < nj + ns; x += gridDim.x) {
     if (x >= nj) {
@@ -367,33 +391,39 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ B
       __syncthreads();
       continue;
     }
-    const BwdJoin j = p.joins[x / p.Hkv];
-    const int g = x % p.Hkv;
-    constexpr int A = bwd_accs(D);
+    const int a = x / kPieces % A, y = x / (kPieces * A), g = y % p.Hkv;
+    const BwdJoin j = p.joins[y / p.Hkv];
+    const int r = tid & 127, c = (x % kPieces) * 2 + (tid >> 7);  // columns [16 c, 16 c + 16)
+    if ((a > 0 && j.kind != kBwdKV) || r >= j.a_valid) continue;
     const size_t stride = (size_t)p.Hkv * A * (D / 4) * 128;  // float4 between slots
-    for (int a = 0; a < (j.kind == kBwdKV ? 2 : 1); ++a) {
-      const float4* src = reinterpret_cast<const float4*>(p.part) +
-                          (((size_t)j.slot * p.Hkv + g) * A + a) * (D / 4) * 128;
-      void* dst = j.kind == kBwdQ ? p.dq : (j.kind == kBwdV || (j.kind == kBwdKV && a == 0)) ? p.dv : p.dk;
-      for (int i = tid; i < 128 * D / 8; i += 256) {
-        const int r = i & 127, c = i >> 7;
-        if (r >= j.a_valid) continue;
-        float4 s0 = make_float4(0.f, 0.f, 0.f, 0.f), s1 = s0;
-        for (int k = 0; k < j.parts; ++k) {
-          const float4 v0 = __ldcg(src + k * stride + (size_t)(2 * c) * 128 + r);
-          const float4 v1 = __ldcg(src + k * stride + (size_t)(2 * c + 1) * 128 + r);
-          s0.x += v0.x; s0.y += v0.y; s0.z += v0.z; s0.w += v0.w;
-          s1.x += v1.x; s1.y += v1.y; s1.z += v1.z; s1.w += v1.w;
-        }
-        const int ar = j.a_off + r;
-        const size_t row = j.kind == kBwdQ
-                               ? (size_t)(j.a_base + (ar >> p.log_G)) * p.Hq + g * p.G + (ar & (p.G - 1))
-                               : (size_t)(j.a_base + ar) * p.Hkv + g;
-        reinterpret_cast<uint4*>(dst)[row * (D / 8) + c] =
-            make_uint4(pack2<BF16>(s0.x, s0.y), pack2<BF16>(s0.z, s0.w), pack2<BF16>(s1.x, s1.y),
-                       pack2<BF16>(s1.z, s1.w));
+    const float4* src = reinterpret_cast<const float4*>(p.part) +
+                        (((size_t)j.slot * p.Hkv + g) * A + a) * (D / 4) * 128 + (size_t)(4 * c) * 128 + r;
+    float4 s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = 0; k < j.parts; ++k) {
+      float4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __ldcg(src + k * stride + (size_t)i * 128);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[i].x += v[i].x;
+        s[i].y += v[i].y;
+        s[i].z += v[i].z;
+        s[i].w += v[i].w;
       }
     }
+    void* dst = j.kind == kBwdQ ? p.dq : (j.kind == kBwdV || (j.kind == kBwdKV && a == 0)) ? p.dv : p.dk;
+    const int ar = j.a_off + r;
+    const size_t row = j.kind == kBwdQ
+                           ? (size_t)(j.a_base + (ar >> p.log_G)) * p.Hq + g * p.G + (ar & (p.G - 1))
+                           : (size_t)(j.a_base + ar) * p.Hkv + g;
+    uint4* to = reinterpret_cast<uint4*>(dst) + row * (D / 8) + 2 * c;
+    to[0] = make_uint4(pack2<BF16>(s[0].x, s[0].y), pack2<BF16>(s[0].z, s[0].w), pack2<BF16>(s[1].x, s[1].y),
+                       pack2<BF16>(s[1].z, s[1].w));
+    to[1] = make_uint4(pack2<BF16>(s[2].x, s[2].y), pack2<BF16>(s[2].z, s[2].w), pack2<BF16>(s[3].x, s[3].y),
+                       pack2<BF16>(s[3].z, s[3].w));
   }
 }
 
@@ -404,7 +434,7 @@ struct BwdPlan {
   size_t units, joins, qt, kt, nlse, nd, sink, most, part, bytes;
 };
 
-int bwd_plan(int num_seqs, int total_q, int total_kv, int Hq, int Hkv, int d, int dtype, BwdPlan* pl) {
+int bwd_layout(int num_seqs, int total_q, int total_kv, int Hq, int Hkv, int d, int dtype, BwdPlan* pl) {
   if (num_seqs < 0 || total_q < 0 || total_kv < 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv != 0)
     return GQA_ERR_INVALID;
   if (dtype != GQA_F16 && dtype != GQA_BF16) return GQA_ERR_INVALID;
@@ -419,6 +449,7 @@ int bwd_plan(int num_seqs, int total_q, int total_kv, int Hq, int Hkv, int d, in
   int sms = 152;
   unsigned int* status = nullptr;
   if (call_device(&sms, &status) != GQA_OK) sms = 152;
+  sms *= bwd_per_sm(d);
   pl->ctas = sms;
   pl->max_qtiles = (int)qt;
   pl->max_ktiles = (int)kt;
@@ -461,11 +492,11 @@ bool overlap(const Range& a, const Range& b) {
 
 template <int D, bool BF16>
 cudaError_t launch_around(const BwdParams& p, cudaStream_t st) {
-  cudaError_t e = launch_pdl(bwd_plan_kernel, p, 1, kPlanThreads, 0, st);
+  cudaError_t e = launch_pdl(bwd_scan_kernel, p, 1, kPlanThreads, 0, st);
   if (e != cudaSuccess) return e;
   const long long items = ((long long)p.max_qtiles + (BF16 ? 0 : p.total_kv / 128 + p.num_seqs)) * p.Hkv;
   const long long room = 8ll * p.ctas;
-  e = launch_pdl(bwd_prep_kernel<D, BF16>, p, (int)(items < 1 ? 1 : items < room ? items : room), 256, 0, st);
+  e = launch_pdl(bwd_prep_kernel<D, BF16>, p, 1 + (int)(items < room ? items : room), 256, 0, st);
   if (e != cudaSuccess) return e;
   e = D == 64 ? launch_bwd_d64(p, BF16, st) : D == 128 ? launch_bwd_d128(p, BF16, st) : launch_bwd_d256(p, BF16, st);
   if (e != cudaSuccess) return e;
@@ -478,7 +509,7 @@ int run_backward(const void* q, const void* k, const void* v, const int32_t* cu,
                  const void* dout, const float* dlse, const float* sinks, void* dq, void* dk,
                  void* dv, float* dsinks, void* workspace, size_t workspace_bytes, void* stream) {
   BwdPlan pl;
-  const int rc = bwd_plan(num_seqs, total_q, total_kv, Hq, Hkv, d, dtype, &pl);
+  const int rc = bwd_layout(num_seqs, total_q, total_kv, Hq, Hkv, d, dtype, &pl);
   if (rc == GQA_ERR_INVALID) return rc;
   if (!(scale > 0.f) || !std::isfinite(scale)) return GQA_ERR_INVALID;
   if ((sinks == nullptr) != (dsinks == nullptr) || !al4(sinks) || !al4(dsinks)) return GQA_ERR_INVALID;
@@ -608,7 +639,7 @@ int gqa_prefill_backward_workspace(int num_seqs, int total_q, int total_kv, int 
                                    int dtype, size_t* bytes) {
   if (bytes == nullptr) return GQA_ERR_INVALID;
   gqa::BwdPlan pl;
-  const int rc = gqa::bwd_plan(num_seqs, total_q, total_kv, Hq, Hkv, d, dtype, &pl);
+  const int rc = gqa::bwd_layout(num_seqs, total_q, total_kv, Hq, Hkv, d, dtype, &pl);
   if (rc == GQA_OK) *bytes = pl.bytes;
   return rc;
 }

@@ -6,8 +6,9 @@
 //   dv_j = sum_i p_ij dout_i           dk_j = scale sum_i ds_ij q_i
 //   dq_i = scale sum_j ds_ij k_j       dsink_h = -sum_i e^(sink_h - lse_ih) D_ih
 // Four kernels in stream order:
-//   plan  (1 CTA)  checks the metadata and lists the work units;
-//   prep           D and -lse log2(e) per query row, the sinks' partial sums;
+//   scan  (1 CTA)  checks the metadata and counts the sequences' tiles;
+//   prep           D and -lse log2(e) per query row, the sinks' partial sums; one
+//                  more CTA lists the work units;
 //   main           the products (backward_kernel.cuh);
 //   join           sums of cut units, and the sinks' gradient.
 #pragma once
@@ -85,8 +86,10 @@ struct BwdParams {
 
 constexpr float kBwdBias = 15.f;  // f16: p is held times 2^15, so that it keeps its bits down to 2^-29
 
-// Rows of a streamed tile: 64 at d = 256, where 128 would not fit in shared memory.
-__host__ __device__ constexpr int bwd_n(int D) { return D == 256 ? 64 : 128; }
+// Rows of a streamed tile: 64 at d = 256, where 128 would not fit in shared memory,
+// and at d = 64, where two CTAs an SM overlap each other's waits.
+__host__ __device__ constexpr int bwd_n(int D) { return D == 128 ? 128 : 64; }
+__host__ __device__ constexpr int bwd_per_sm(int D) { return D == 64 ? 2 : 1; }
 __host__ __device__ constexpr int bwd_accs(int D) { return D == 256 ? 1 : 2; }
 
 cudaError_t launch_bwd_d64(const BwdParams& p, bool bf16, cudaStream_t st);

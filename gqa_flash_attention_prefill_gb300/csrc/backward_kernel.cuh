@@ -14,8 +14,8 @@
 // the result has one writer: no atomics, the same bits run to run.  (The price
 // is that S and T are computed for both kinds of unit: 7 products, not 5.)
 //
-// CTA: 8 softmax warps (warpgroup w takes the columns of half w), a loading
-// warp, a warp that issues the products.  Persistent: units are taken from a
+// CTA: 8 or 16 softmax warps (each warpgroup takes a share of the columns), a
+// loading warp, a warp that issues the products.  Persistent: units are taken from a
 // list sorted by cost with an atomic counter.
 #pragma once
 #include "backward.h"
@@ -25,13 +25,13 @@
 
 namespace gqa {
 
-constexpr int kBwdSoftWarps = 8;
-constexpr int kBwdThreads = 32 * (kBwdSoftWarps + 2);
+constexpr int bwd_warps(int D) { return D == 64 ? 8 : 16; }  // softmax warps
+constexpr int bwd_threads(int D) { return 32 * (bwd_warps(D) + 2); }
 constexpr int kBwdRecs = 4;  // unit records in flight
 
-constexpr int bwd_a_buffers(int D) { return D == 64 ? 2 : 1; }
+constexpr int bwd_a_buffers(int D) { return 1; }
 constexpr int bwd_stages(int D) { return D == 64 ? 4 : D == 128 ? 2 : 1; }
-constexpr int bwd_s_buffers(int D) { return D == 64 ? 2 : 1; }
+constexpr int bwd_s_buffers(int D) { return 1; }
 constexpr uint32_t bwd_a_bytes(int D) { return 128u * D * 2u; }            // one tile
 constexpr uint32_t bwd_b_bytes(int D) { return (uint32_t)bwd_n(D) * D * 2u; }
 constexpr uint32_t bwd_stat_bytes(int D) { return 8u * bwd_n(D); }         // -lse, -D of a tile
@@ -50,59 +50,87 @@ struct BwdBar {
 template <int D, bool BF16>
 struct Bwd {
   static constexpr int N = bwd_n(D), NS = bwd_stages(D), NA = bwd_a_buffers(D),
-                       NSB = bwd_s_buffers(D), NCH = D / 64, CW = N / 2;
+                       NSB = bwd_s_buffers(D), NCH = D / 64,
+                       WARPS = bwd_warps(D), PG = WARPS / 4, CW = N / PG;
   static constexpr uint32_t kABytes = bwd_a_bytes(D), kBBytes = bwd_b_bytes(D),
                             kStat = bwd_stat_bytes(D);
   static constexpr uint32_t kAChunk = 128u * 128u, kBChunk = N * 128u;
-  static constexpr uint32_t kColT = NSB * N, kColAcc0 = D == 64 ? 384 : 256,
-                            kColAcc1 = D == 64 ? 448 : D == 128 ? 384 : 256;
-  static_assert(kColT + N <= kColAcc0 && kColAcc1 + D <= 512, "tensor memory");
+  static constexpr uint32_t kColT = NSB * N, kColAcc0 = D == 64 ? 128 : 256,
+                            kColAcc1 = D == 64 ? 192 : D == 128 ? 384 : 256, kCols = 512 / bwd_per_sm(D);
+  static_assert(kColT + N <= kColAcc0 && kColAcc1 + D <= kCols, "tensor memory");
 };
 
 // One tile of one unit in the hands of a softmax thread: lane row `r` of A,
-// columns [col0, col0 + CW) of the tile.  lo, hi: the columns the row keeps.
+// CW neighbouring columns of the tile.  lo, hi: the columns the row keeps.
 struct BwdTile {
   uint32_t t_s, t_t;  // tensor-memory addresses of the thread's columns of S and T
-  uint32_t stats;     // shared memory: -lse of the tile's columns, then -D (dk, dv units)
+  uint32_t stats;     // shared memory: -lse of the thread's columns; N floats on, -D (dk, dv units)
   float row_nlse, row_nd;
   int lo, hi;
-  bool masked;
+  bool mask_lo, mask_hi;  // whether some row of the tile has such an edge
 };
+
+template <int CW>
+__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[CW]) {
+  if constexpr (CW == 32)
+    tmem_ld32(at, r);
+  else
+    tmem_ld16(at, r);
+}
+template <int W>
+__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[W]) {
+  if constexpr (W == 16)
+    tmem_st16(at, r);
+  else
+    tmem_st8(at, r);
+}
+__device__ __forceinline__ void ld_shared_f4(uint32_t at, float (&v)[4]) {
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(at));
+}
+// What this warp wrote to, or read from, tensor memory is done: one arrival.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 
 template <int KIND, int D, bool BF16>
 __device__ __forceinline__ bool bwd_tile(const BwdTile& t, float sl2, float mul, uint32_t bar_s,
                                          uint32_t par_s, uint32_t bar_p, uint32_t bar_t,
                                          uint32_t par_t, uint32_t bar_d,
                                          volatile uint32_t* abort_flag, const BwdParams& p) {
-  constexpr int CW = Bwd<D, BF16>::CW;
+  using K = Bwd<D, BF16>;
+  constexpr int CW = K::CW;
   auto wait = [&](uint32_t bar, uint32_t par) {
     return __all_sync(0xffffffffu, wait_bounded(bar, par, abort_flag, p.status, p.timeout_ns));
   };
   if (!wait(bar_s, par_s)) return false;
   tc_fence_after();
   float x[CW];
-#pragma unroll
-  for (int c = 0; c < CW; c += 32)
-    tmem_ld32(t.t_s + c, *reinterpret_cast<uint32_t(*)[32]>(x + c));
+  tmem_load<CW>(t.t_s, *reinterpret_cast<uint32_t(*)[CW]>(x));
   tmem_wait_ld();
   const uint64_t sc = f2(sl2, sl2);
 #pragma unroll
   for (int c = 0; c < CW; c += 4) {
     float l[4];
-    if constexpr (KIND == kBwdQ) {
+    if constexpr (KIND == kBwdQ)
       l[0] = l[1] = l[2] = l[3] = t.row_nlse;
-    } else {
-      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                   : "=f"(l[0]), "=f"(l[1]), "=f"(l[2]), "=f"(l[3])
-                   : "r"(t.stats + 4u * c));
-    }
+    else
+      ld_shared_f4(t.stats + 4u * c, l);
     unf2(ffma2(f2(x[c], x[c + 1]), sc, f2(l[0], l[1])), x[c], x[c + 1]);
     unf2(ffma2(f2(x[c + 2], x[c + 3]), sc, f2(l[2], l[3])), x[c + 2], x[c + 3]);
   }
-  if (t.masked) {
+  if (t.mask_hi) {
 #pragma unroll
     for (int c = 0; c < CW; ++c)
-      if (c < t.lo || c > t.hi) x[c] = -INFINITY;
+      if (c > t.hi) x[c] = -INFINITY;
+  }
+  if (t.mask_lo) {
+#pragma unroll
+    for (int c = 0; c < CW; ++c)
+      if (c < t.lo) x[c] = -INFINITY;
   }
 #pragma unroll
   for (int c = 0; c < CW; ++c) x[c] = ex2(x[c]);
@@ -111,87 +139,73 @@ __device__ __forceinline__ bool bwd_tile(const BwdTile& t, float sl2, float mul,
     uint32_t pk[CW / 2];
 #pragma unroll
     for (int c = 0; c < CW; c += 2) pk[c / 2] = pack2<BF16>(x[c], x[c + 1]);
-    if constexpr (CW == 64)
-      tmem_st32(t.t_s, *reinterpret_cast<uint32_t(*)[32]>(pk));
-    else
-      tmem_st16(t.t_s, *reinterpret_cast<uint32_t(*)[16]>(pk));
+    tmem_store<CW / 2>(t.t_s, pk);
     tmem_wait_st();
   }
-  tc_fence_before();
-  mbar_arrive(bar_p);  // S is read (and P written)
+  warp_arrive(bar_p);  // S is read (and P written)
   if constexpr (KIND == kBwdV) return true;
 
   if (!wait(bar_t, par_t)) return false;
   tc_fence_after();
-  uint32_t dk[CW / 2];
+  uint32_t y[CW], dk[CW / 2];
+  tmem_load<CW>(t.t_t, y);
+  tmem_wait_ld();
   const uint64_t rnd = f2(t.row_nd, t.row_nd), mm = f2(mul, mul);
 #pragma unroll
-  for (int h = 0; h < CW; h += 32) {
-    uint32_t y[32];
-    tmem_ld32(t.t_t + h, y);
-    tmem_wait_ld();
-#pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-      uint64_t n0 = rnd, n1 = rnd;
-      if constexpr (KIND != kBwdQ) {
-        float l[4];
-        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(l[0]), "=f"(l[1]), "=f"(l[2]), "=f"(l[3])
-                     : "r"(t.stats + 4u * (uint32_t)Bwd<D, BF16>::N + 4u * (h + c)));
-        n0 = f2(l[0], l[1]);
-        n1 = f2(l[2], l[3]);
-      }
-      uint64_t a = fadd2(f2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), n0);
-      uint64_t b = fadd2(f2(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), n1);
-      if constexpr (!BF16) {  // f16: times a power of two, so that dS keeps its bits
-        a = fmul2(a, mm);
-        b = fmul2(b, mm);
-      }
-      float d0, d1, d2, d3;
-      unf2(fmul2(a, f2(x[h + c], x[h + c + 1])), d0, d1);
-      unf2(fmul2(b, f2(x[h + c + 2], x[h + c + 3])), d2, d3);
-      dk[(h + c) / 2] = pack2<BF16>(d0, d1);
-      dk[(h + c) / 2 + 1] = pack2<BF16>(d2, d3);
+  for (int c = 0; c < CW; c += 4) {
+    uint64_t n0 = rnd, n1 = rnd;
+    if constexpr (KIND != kBwdQ) {
+      float l[4];
+      ld_shared_f4(t.stats + 4u * (uint32_t)K::N + 4u * c, l);
+      n0 = f2(l[0], l[1]);
+      n1 = f2(l[2], l[3]);
     }
+    uint64_t a = fadd2(f2(__uint_as_float(y[c]), __uint_as_float(y[c + 1])), n0);
+    uint64_t b = fadd2(f2(__uint_as_float(y[c + 2]), __uint_as_float(y[c + 3])), n1);
+    if constexpr (!BF16) {  // f16: times a power of two, so that dS keeps its bits
+      a = fmul2(a, mm);
+      b = fmul2(b, mm);
+    }
+    float d0, d1, d2, d3;
+    unf2(fmul2(a, f2(x[c], x[c + 1])), d0, d1);
+    unf2(fmul2(b, f2(x[c + 2], x[c + 3])), d2, d3);
+    dk[c / 2] = pack2<BF16>(d0, d1);
+    dk[c / 2 + 1] = pack2<BF16>(d2, d3);
   }
-  if constexpr (CW == 64)
-    tmem_st32(t.t_t, *reinterpret_cast<uint32_t(*)[32]>(dk));
-  else
-    tmem_st16(t.t_t, *reinterpret_cast<uint32_t(*)[16]>(dk));
+  tmem_store<CW / 2>(t.t_t, dk);
   tmem_wait_st();
-  tc_fence_before();
-  mbar_arrive(bar_d);
+  warp_arrive(bar_d);
   return true;
 }
 
 // `cols` accumulator columns of this lane's row, times `mul`, to a row of the
-// result or to a partial ([d / 4][128][4], from its column `col0`).
+// result or to a partial ([d / 4][128][4]), both from column `col0`.
 template <int D, bool BF16>
 __device__ __forceinline__ void bwd_store(uint32_t t_acc, int cols, int col0, float mul,
                                           uint16_t* row, float4* part, int r, bool zero) {
 #pragma unroll 1
-  for (int c = 0; c < cols; c += 32) {
-    uint32_t o[32];
+  for (int c = 0; c < cols; c += 16) {
+    uint32_t o[16];
     if (!zero) {
-      tmem_ld32(t_acc + c, o);
+      tmem_ld16(t_acc + c, o);
       tmem_wait_ld();
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = 0u;
+      for (int i = 0; i < 16; ++i) o[i] = 0u;
     }
     if (part != nullptr) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 4; ++i)
         part[(size_t)((col0 + c) / 4 + i) * 128 + r] =
             make_float4(__uint_as_float(o[4 * i]) * mul, __uint_as_float(o[4 * i + 1]) * mul,
                         __uint_as_float(o[4 * i + 2]) * mul, __uint_as_float(o[4 * i + 3]) * mul);
     } else if (row != nullptr) {
-      uint32_t w[16];
+      uint32_t w[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < 8; ++i)
         w[i] = pack2<BF16>(__uint_as_float(o[2 * i]) * mul, __uint_as_float(o[2 * i + 1]) * mul);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 2; ++i)
         reinterpret_cast<uint4*>(row + col0 + c)[i] =
             make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
@@ -199,12 +213,12 @@ __device__ __forceinline__ void bwd_store(uint32_t t_acc, int cols, int col0, fl
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
     backward_kernel(const __grid_constant__ BwdParams p) {
   using K = Bwd<D, BF16>;
   using B = BwdBar;
   constexpr int N = K::N, NS = K::NS, NA = K::NA, NSB = K::NSB, NCH = K::NCH, CW = K::CW;
-  constexpr int kLoadWarp = kBwdSoftWarps, kMmaWarp = kBwdSoftWarps + 1;
+  constexpr int WARPS = K::WARPS, kLoadWarp = WARPS, kMmaWarp = WARPS + 1;
   constexpr uint32_t kIdescS = idesc_f16(BF16, 128, N, false);
   constexpr uint32_t kIdescO = idesc_f16(BF16, 128, D, true);
 
@@ -226,16 +240,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < B::kCount; ++i) {
       uint32_t cnt = 1u;
-      if (i >= B::kRecEmpty && i < B::kRecEmpty + kBwdRecs) cnt = kBwdSoftWarps + 1u;
+      if (i >= B::kRecEmpty && i < B::kRecEmpty + kBwdRecs) cnt = WARPS + 1u;
       if (i == B::kPFull || i == B::kPFull + 1 || i == B::kDFull || i == B::kAccFree)
-        cnt = 32u * kBwdSoftWarps;
+        cnt = WARPS;
       mbar_init(bar(i), cnt);
     }
     misc[1] = 0u;
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(misc), 512u);
+    tmem_alloc(smem_u32(misc), K::kCols);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -386,21 +400,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         mma_commit(bar(B::kSFull + t % NSB));
         return true;
       };
-      // acc (+)= (the 16-bit tile at `src`) B: the tile's two halves stand
-      // each at the start of their fp32 columns.
+      // acc (+)= (the 16-bit tile at `src`) B: each warpgroup's columns stand at
+      // the start of its fp32 ones.
       auto issue_acc = [&](uint32_t acc, uint32_t src, uint64_t b, bool first) {
 #pragma unroll
         for (int kk = 0; kk < N / 16; ++kk)
-          mma_ts(acc, src + (kk / (N / 32)) * (N / 2) + (kk % (N / 32)) * 8,
+          mma_ts(acc, src + (kk / (CW / 16)) * CW + (kk % (CW / 16)) * 8,
                  b + (uint64_t)(kk * 128), kIdescO, (first && kk == 0) ? 0u : 1u);
       };
       if constexpr (NS > 1) {
-        if (!(ok = issue_s(it))) break;
+        ok = issue_s(it);
+        if (!ok) break;
       }
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t s = it % NS, sb = it % NSB;
         if constexpr (NS == 1) {
-          if (!(ok = issue_s(it))) break;
+          ok = issue_s(it);
+          if (!ok) break;
         }
         const uint64_t dB = dB0 + s * 2u * (K::kBBytes >> 4), dBt = dBt0 + s * 2u * (K::kBBytes >> 4);
         if (has_t) {
@@ -413,7 +429,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
         if (j == n - 1) mma_commit(bar(B::kAEmpty + ab));
         if constexpr (NSB == 2) {
-          if (j + 1 < n && !(ok = issue_s(it + 1))) break;
+          if (j + 1 < n) ok = issue_s(it + 1);
+          if (!ok) break;
         }
         if (!(ok = wait(B::kPFull + (it & 1u), (it >> 1) & 1u))) break;
         if (j == 0 && uc > 0 && !(ok = wait(B::kAccFree, (uc - 1u) & 1u))) break;
@@ -421,7 +438,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (has_p)
           issue_acc(tmem + K::kColAcc0, tmem + sb * N, dBt + (K::kBBytes >> 4), j == 0);
         if constexpr (NS > 1 && NSB == 1) {
-          if (j + 1 < n && !(ok = issue_s(it + 1))) break;
+          if (j + 1 < n) ok = issue_s(it + 1);
+          if (!ok) break;
         }
         if (has_t) {
           if (!(ok = wait(B::kDFull, td & 1u))) break;
@@ -441,8 +459,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 
   // ---------------------------------------------------------------- softmax, results
-  if (warp < kBwdSoftWarps) {
-    const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+  if (warp < WARPS) {
+    constexpr int PG = K::PG;
+    const int part = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float sl2 = p.scale_log2;
     auto wait = [&](int b, uint32_t par) {
@@ -495,18 +514,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         bounds(a_off + r, lo0, hi0);
         bounds(last, lo_max, x);
         bounds(a_off, x, hi_min);
-        lo0 -= half * CW;
-        hi0 -= half * CW;
+        lo0 -= part * CW;
+        hi0 -= part * CW;
       }
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t s = it % NS, sb = it % NSB;
         const int off = b_off + j * N;
-        t.t_s = t_lane + sb * N + half * CW;
-        t.t_t = t_lane + K::kColT + half * CW;
-        t.stats = sStat + s * K::kStat + (uint32_t)half * CW * 4u;
+        t.t_s = t_lane + sb * N + part * CW;
+        t.t_t = t_lane + K::kColT + part * CW;
+        t.stats = sStat + s * K::kStat + (uint32_t)part * CW * 4u;
         t.lo = lo0 - off;
         t.hi = hi0 - off;
-        t.masked = lo_max > off || hi_min < off + N - 1;
+        t.mask_lo = lo_max > off;
+        t.mask_hi = hi_min < off + N - 1;
         const uint32_t bs = bar(B::kSFull + sb), ps = (it / NSB) & 1u, bp = bar(B::kPFull + (it & 1u)),
                        bt = bar(B::kTFull), bd = bar(B::kDFull);
         if (qa) {
@@ -529,18 +549,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (!(ok = wait(B::kAccDone, uc & 1u))) break;
         tc_fence_after();
       }
-      // Warpgroup `half` takes dv (0) or dk (1) of a unit with both, else half
-      // of the columns of its one result.
+      // Half of the warpgroups take dv and half dk of a unit with both, else each
+      // an equal share of the columns of its one result.
       const bool both = kind == kBwdKV;
-      const bool is_v = kind == kBwdV || (both && half == 0);
+      const bool is_v = kind == kBwdV || (both && part < PG / 2);
       const float out_mul = is_v ? (BF16 ? 1.f : 1.f / 32768.f) : p.scale * undo;
       const uint32_t acc = is_v ? K::kColAcc0 : K::kColAcc1;
-      const int cols = both ? D : D / 2, col0 = both ? 0 : half * (D / 2);
+      const int cols = both ? D / (PG / 2) : D / PG, col0 = (both ? part % (PG / 2) : part) * cols;
       uint16_t* row = nullptr;
-      float4* part = nullptr;
+      float4* to_part = nullptr;
       if (slot >= 0) {
-        part = reinterpret_cast<float4*>(p.part) +
-               (((size_t)slot * p.Hkv + g) * bwd_accs(D) + (both && half == 1 ? 1 : 0)) * (D / 4) * 128;
+        to_part = reinterpret_cast<float4*>(p.part) +
+               (((size_t)slot * p.Hkv + g) * bwd_accs(D) + (both && !is_v ? 1 : 0)) * (D / 4) * 128;
       } else if (r < a_valid) {
         if (qa) {
           const int a = a_off + r;
@@ -550,10 +570,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           row = static_cast<uint16_t*>(is_v ? p.dv : p.dk) + ((size_t)(a_base + a_off + r) * p.Hkv + g) * D;
         }
       }
-      bwd_store<D, BF16>(t_lane + acc + col0, cols, col0, out_mul, row, part, r, n == 0);
+      bwd_store<D, BF16>(t_lane + acc + col0, cols, col0, out_mul, row, to_part, r, n == 0);
       if (n > 0) {
-        tc_fence_before();
-        mbar_arrive(bar(B::kAccFree));
+        warp_arrive(bar(B::kAccFree));
         ++uc;
       }
     }
@@ -563,7 +582,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (tid == 0 && *abort_flag) p.hdr[kBwdFailed] = 1;  // nothing is joined
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512u);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, K::kCols);
 }
 
 namespace {
@@ -583,7 +602,7 @@ cudaError_t launch_backward(const BwdParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attr.allowed[dev].store(smem, std::memory_order_release);
   }
-  return launch_pdl(kern, p, p.ctas, kBwdThreads, smem, st);
+  return launch_pdl(kern, p, p.ctas, bwd_threads(D), smem, st);
 }
 
 }  // namespace
