@@ -247,7 +247,7 @@ __device__ __forceinline__ void bwd_plan(const BwdParams& p) {
 
 // ------------------------------------------------------------------ the rows' statistics
 // Bound by memory: out and dout are read once, 8 values a lane, a row in d / 8
-// neighbouring lanes.  The last CTA lists the units meanwhile.
+// neighbouring lanes.  The first CTA lists the units meanwhile.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ BwdParams p) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, ROUNDS = 16 / RPW;  // 16 rows a warp
@@ -257,12 +257,12 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ B
   grid_dep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int ctas = gridDim.x - 1;
-  if ((int)blockIdx.x == ctas) {
+  if (blockIdx.x == 0) {
     bwd_plan(p);
     return;
   }
   const int nq = p.hdr[kBwdQTiles] * p.Hkv, nk = BF16 ? 0 : p.hdr[kBwdKTiles] * p.Hkv;
-  for (int x = blockIdx.x; x < nq + nk; x += ctas) {
+  for (int x = blockIdx.x - 1; x < nq + nk; x += ctas) {
     const bool keys = x >= nq;
     const int y = keys ? x - nq : x, tile = y / p.Hkv, g = y - tile * p.Hkv;
     const int32_t* first = keys ? p.ktile0 : p.qtile0;
@@ -273,19 +273,23 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ B
     if (!BF16 && tid < 2) s_most[tid] = 0u;
     if (!BF16) __syncthreads();
     uint4 o[ROUNDS], dn[ROUNDS];
+    float ls[ROUNDS], dl[ROUNDS];  // lse and dlse of the row: one address for its lanes
 #pragma unroll
     for (int i = 0; i < ROUNDS; ++i) {
       const int r = warp * 16 + i * RPW + lane / LPR;
       o[i] = dn[i] = make_uint4(0u, 0u, 0u, 0u);
+      ls[i] = -INFINITY;
+      dl[i] = 0.f;
       if (r < valid) {
         if (keys) {
           dn[i] = __ldg(reinterpret_cast<const uint4*>(p.v) +
                         ((size_t)(base + r0 + r) * p.Hkv + g) * LPR + lane % LPR);
         } else {
-          const size_t at = ((size_t)(base + ((r0 + r) >> p.log_G)) * p.Hq + g * p.G +
-                             ((r0 + r) & (p.G - 1))) * LPR + lane % LPR;
-          o[i] = __ldg(reinterpret_cast<const uint4*>(p.out) + at);
-          dn[i] = __ldg(reinterpret_cast<const uint4*>(p.dout) + at);
+          const size_t row = (size_t)(base + ((r0 + r) >> p.log_G)) * p.Hq + g * p.G + ((r0 + r) & (p.G - 1));
+          o[i] = __ldg(reinterpret_cast<const uint4*>(p.out) + row * LPR + lane % LPR);
+          dn[i] = __ldg(reinterpret_cast<const uint4*>(p.dout) + row * LPR + lane % LPR);
+          ls[i] = __ldg(p.lse + row);
+          if (p.dlse != nullptr) dl[i] = __ldg(p.dlse + row);
         }
       }
     }
@@ -312,14 +316,11 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ B
       if (!keys && lane % LPR == 0) {
         float nl = -INFINITY, nd = 0.f, w = 0.f;
         if (r < valid) {
-          const int h = g * p.G + ((r0 + r) & (p.G - 1));
-          const size_t at = (size_t)(base + ((r0 + r) >> p.log_G)) * p.Hq + h;
-          const float lse = __ldg(p.lse + at);
-          const float dlt = dot - (p.dlse != nullptr ? __ldg(p.dlse + at) : 0.f);
+          const float lse = ls[i], dlt = dot - dl[i];
           nd = -dlt;
           if (lse != -INFINITY) {  // else: no key, no probability
             nl = -lse * kLog2e + (BF16 ? 0.f : kBwdBias);
-            if (p.sinks != nullptr) w = expf(__ldg(p.sinks + h) - lse) * dlt;
+            if (p.sinks != nullptr) w = expf(__ldg(p.sinks + g * p.G + ((r0 + r) & (p.G - 1))) - lse) * dlt;
           }
           if (!BF16) md = fmaxf(md, fabsf(dlt));
         }
