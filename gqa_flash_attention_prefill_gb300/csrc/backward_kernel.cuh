@@ -67,7 +67,7 @@ struct BwdTile {
   uint32_t stats;     // shared memory: -lse of the thread's columns; N floats on, -D (dk, dv units)
   float row_nlse, row_nd;
   int lo, hi;
-  bool mask_lo, mask_hi;  // whether some row of the tile has such an edge
+  bool masked;  // whether some row of the tile has such an edge
 };
 
 template <int CW>
@@ -122,15 +122,13 @@ __device__ __forceinline__ bool bwd_tile(const BwdTile& t, float sl2, float mul,
     unf2(ffma2(f2(x[c], x[c + 1]), sc, f2(l[0], l[1])), x[c], x[c + 1]);
     unf2(ffma2(f2(x[c + 2], x[c + 3]), sc, f2(l[2], l[3])), x[c + 2], x[c + 3]);
   }
-  if (t.mask_hi) {
+  if (t.masked) {
+    // A bit per column: constant bits become predicates several at a time.
+    const uint32_t below = t.hi >= 31 ? ~0u : t.hi < 0 ? 0u : (2u << t.hi) - 1u,
+                   above = t.lo <= 0 ? ~0u : t.lo > 31 ? 0u : ~0u << t.lo, keep = below & above;
 #pragma unroll
     for (int c = 0; c < CW; ++c)
-      if (c > t.hi) x[c] = -INFINITY;
-  }
-  if (t.mask_lo) {
-#pragma unroll
-    for (int c = 0; c < CW; ++c)
-      if (c < t.lo) x[c] = -INFINITY;
+      if ((keep & (1u << c)) == 0u) x[c] = -INFINITY;
   }
 #pragma unroll
   for (int c = 0; c < CW; ++c) x[c] = ex2(x[c]);
@@ -525,8 +523,7 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
         t.stats = sStat + s * K::kStat + (uint32_t)part * CW * 4u;
         t.lo = lo0 - off;
         t.hi = hi0 - off;
-        t.mask_lo = lo_max > off;
-        t.mask_hi = hi_min < off + N - 1;
+        t.masked = lo_max > off || hi_min < off + N - 1;
         const uint32_t bs = bar(B::kSFull + sb), ps = (it / NSB) & 1u, bp = bar(B::kPFull + (it & 1u)),
                        bt = bar(B::kTFull), bd = bar(B::kDFull);
         if (qa) {
