@@ -467,50 +467,58 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
                         wait_bounded(bar(b), par, abort_flag, p.status, p.timeout_ns));
     };
     uint32_t it = 0, td = 0, uc = 0;
-    bool ok = true;
-    for (uint32_t un = 0; ok; ++un) {
+    // The next unit's record, and what of global memory it needs: on its way while
+    // this unit's results are stored.
+    int next = -1, next_k = 0;
+    float next_nlse = 0.f, next_nd = 0.f;
+    auto fetch = [&](uint32_t un) -> bool {
       const uint32_t rs = un % kBwdRecs;
-      if (!(ok = wait(B::kRecFull + rs, (un / kBwdRecs) & 1u))) break;
+      if (!wait(B::kRecFull + rs, (un / kBwdRecs) & 1u)) return false;
       const int32_t* rec = recs + rs * 16;
-      const int kind = rec[0], n = rec[1], a_base = rec[2], a_off = rec[3], a_valid = rec[4],
-                b_off = rec[6], P = rec[8], E = rec[9], slot = rec[10], stat = rec[11],
-                seq = rec[12], g = rec[13];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B::kRecEmpty + rs));
-      if (kind < 0) break;
+      next = rec[0];
+      if (next < 0) return true;
+      if (next == kBwdQ) {
+        const size_t at = (size_t)rec[13] * p.stat_rows + rec[11] + rec[3] + r;
+        next_nlse = __ldcg(p.nlse + at);
+        next_nd = __ldcg(p.nd + at);
+      }
+      if constexpr (!BF16) next_k = bwd_exponent(p.most + ((size_t)rec[12] * p.Hkv + rec[13]) * 4);
+      return true;
+    };
+    bool ok = fetch(0);
+    for (uint32_t un = 0; ok && next >= 0; ++un) {
+      const uint32_t rs = un % kBwdRecs;
+      const int32_t* rec = recs + rs * 16;
+      const int kind = next, n = rec[1];
       const bool qa = kind == kBwdQ;
       BwdTile t;
-      t.row_nlse = t.row_nd = 0.f;
-      if (qa) {
-        const size_t at = (size_t)g * p.stat_rows + stat + a_off + r;
-        t.row_nlse = __ldcg(p.nlse + at);
-        t.row_nd = __ldcg(p.nd + at);
-      }
+      t.row_nlse = next_nlse;
+      t.row_nd = next_nd;
       float mul = 1.f, undo = 1.f;  // of dS, and of the results it enters
       if constexpr (!BF16) {
-        const int k = bwd_exponent(p.most + ((size_t)seq * p.Hkv + g) * 4);
-        mul = ldexpf(1.f, k - (int)kBwdBias);
-        undo = ldexpf(1.f, -k);
+        mul = ldexpf(1.f, next_k - (int)kBwdBias);
+        undo = ldexpf(1.f, -next_k);
       }
+      const int a_off = rec[3], b_off = rec[6];
       // Columns the row keeps, counted from B's first row: key or packed row
       // c of tile j is kept iff lo0 <= b_off + j N + c <= hi0.
-      const int last = a_off + a_valid - 1;
       int lo0, hi0, lo_max, hi_min;  // this row's; over the rows: the largest lo0, the least hi0
-      auto bounds = [&](int a, int& lo, int& hi) {
-        if (qa) {
-          const int pos = P + (a >> p.log_G);
-          hi = pos;
-          lo = p.window > 0 ? pos - p.window + 1 : 0;
-        } else {
-          lo = max(a - P, 0) * p.G;
-          const long long i = p.window > 0 ? (long long)a + p.window - P : (long long)E;
-          hi = (int)(i < 0 ? 0 : i < (long long)E ? i : (long long)E) * p.G - 1;
-        }
-      };
       {
+        const int P = rec[8], E = rec[9];
+        auto bounds = [&](int a, int& lo, int& hi) {
+          if (qa) {
+            const int pos = P + (a >> p.log_G);
+            hi = pos;
+            lo = p.window > 0 ? pos - p.window + 1 : 0;
+          } else {
+            lo = max(a - P, 0) * p.G;
+            const long long i = p.window > 0 ? (long long)a + p.window - P : (long long)E;
+            hi = (int)(i < 0 ? 0 : i < (long long)E ? i : (long long)E) * p.G - 1;
+          }
+        };
         int x;
         bounds(a_off + r, lo0, hi0);
-        bounds(last, lo_max, x);
+        bounds(a_off + rec[4] - 1, lo_max, x);
         bounds(a_off, x, hi_min);
         lo0 -= part * CW;
         hi0 -= part * CW;
@@ -541,7 +549,7 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
         if (!ok) break;
         if (kind != kBwdV) ++td;
       }
-      if (!ok) break;
+      if (!ok || !(ok = fetch(un + 1u))) break;
       if (n > 0) {
         if (!(ok = wait(B::kAccDone, uc & 1u))) break;
         tc_fence_after();
@@ -553,12 +561,13 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
       const float out_mul = is_v ? (BF16 ? 1.f : 1.f / 32768.f) : p.scale * undo;
       const uint32_t acc = is_v ? K::kColAcc0 : K::kColAcc1;
       const int cols = both ? D / (PG / 2) : D / PG, col0 = (both ? part % (PG / 2) : part) * cols;
+      const int a_base = rec[2], slot = rec[10], g = rec[13];
       uint16_t* row = nullptr;
       float4* to_part = nullptr;
       if (slot >= 0) {
         to_part = reinterpret_cast<float4*>(p.part) +
                (((size_t)slot * p.Hkv + g) * bwd_accs(D) + (both && !is_v ? 1 : 0)) * (D / 4) * 128;
-      } else if (r < a_valid) {
+      } else if (r < rec[4]) {
         if (qa) {
           const int a = a_off + r;
           row = static_cast<uint16_t*>(p.dq) +
@@ -568,6 +577,8 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
         }
       }
       bwd_store<D, BF16>(t_lane + acc + col0, cols, col0, out_mul, row, to_part, r, n == 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B::kRecEmpty + rs));
       if (n > 0) {
         warp_arrive(bar(B::kAccFree));
         ++uc;
