@@ -182,30 +182,52 @@ template <int D, bool BF16>
 __device__ __forceinline__ void bwd_store(uint32_t t_acc, int cols, int col0, float mul,
                                           uint16_t* row, float4* part, int r, bool zero) {
 #pragma unroll 1
-  for (int c = 0; c < cols; c += 16) {
-    uint32_t o[16];
+  for (int c = 0; c < cols; c += 32) {
+    uint32_t o[32];
     if (!zero) {
-      tmem_ld16(t_acc + c, o);
+      tmem_ld32(t_acc + c, o);
       tmem_wait_ld();
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = 0u;
+      for (int i = 0; i < 32; ++i) o[i] = 0u;
     }
     if (part != nullptr) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 8; ++i)
         part[(size_t)((col0 + c) / 4 + i) * 128 + r] =
             make_float4(__uint_as_float(o[4 * i]) * mul, __uint_as_float(o[4 * i + 1]) * mul,
                         __uint_as_float(o[4 * i + 2]) * mul, __uint_as_float(o[4 * i + 3]) * mul);
-    } else if (row != nullptr) {
-      uint32_t w[8];
+    } else {
+      // Four lanes exchange their rows' 16-byte pieces, so that a store writes 64
+      // bytes a row: 8 lines an instruction instead of 32.
+      uint32_t w[4][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        w[i] = pack2<BF16>(__uint_as_float(o[2 * i]) * mul, __uint_as_float(o[2 * i + 1]) * mul);
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        reinterpret_cast<uint4*>(row + col0 + c)[i] =
-            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int k = 0; k < 4; ++k)
+          w[i][k] = pack2<BF16>(__uint_as_float(o[8 * i + 2 * k]) * mul, __uint_as_float(o[8 * i + 2 * k + 1]) * mul);
+      const int lane = r & 31;
+#pragma unroll
+      for (int step = 1; step <= 2; ++step) {
+        const bool up = (lane & step) != 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int a = step == 1 ? 2 * i : i, b = a + step;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[a][k] : w[b][k], step);
+            w[a][k] = up ? got : w[a][k];
+            w[b][k] = up ? w[b][k] : got;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint16_t* to = reinterpret_cast<uint16_t*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), (lane & ~3) + i));
+        if (to != nullptr)
+          reinterpret_cast<uint4*>(to + col0 + c)[lane & 3] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+      }
     }
   }
 }
@@ -550,10 +572,6 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
         if (kind != kBwdV) ++td;
       }
       if (!ok || !(ok = fetch(un + 1u))) break;
-      if (n > 0) {
-        if (!(ok = wait(B::kAccDone, uc & 1u))) break;
-        tc_fence_after();
-      }
       // Half of the warpgroups take dv and half dk of a unit with both, else each
       // an equal share of the columns of its one result.
       const bool both = kind == kBwdKV;
@@ -575,6 +593,10 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
         } else {
           row = static_cast<uint16_t*>(is_v ? p.dv : p.dk) + ((size_t)(a_base + a_off + r) * p.Hkv + g) * D;
         }
+      }
+      if (n > 0) {
+        if (!(ok = wait(B::kAccDone, uc & 1u))) break;
+        tc_fence_after();
       }
       bwd_store<D, BF16>(t_lane + acc + col0, cols, col0, out_mul, row, to_part, r, n == 0);
       __syncwarp();
