@@ -57,27 +57,24 @@ __device__ __forceinline__ BwdUnit plan_unit(const BwdParams& p, int x, int nq, 
   u.a_off = (t - first[b]) * 128;
   u.slot = -1;
   u.stat = p.qtile0[b] * 128;
-  long long lo, hi;  // what B's rows [lo, hi) the unit streams
+  int lo, hi;  // B's rows [lo, hi) that the unit streams
   if (qa) {
     u.a_base = c0;
     u.a_valid = min(128, E * p.G - u.a_off);
     u.b_base = k0;
     u.b_len = P + E;
-    const int i0 = u.a_off >> p.log_G, i1 = (u.a_off + u.a_valid - 1) >> p.log_G;
-    lo = p.window > 0 ? (long long)P + i0 - p.window + 1 : 0;
-    hi = P + i1 + 1;
   } else {
     u.a_base = k0;
     u.a_valid = min(128, P + E - u.a_off);
     u.b_base = c0;
     u.b_len = E * p.G;
-    const long long last = (long long)u.a_off + u.a_valid - 1 - P;
-    lo = (long long)max(u.a_off - P, 0) * p.G;
-    hi = (p.window > 0 && last + p.window < E ? last + p.window : E) * p.G;
   }
+  bwd_bounds(qa, u.a_off, P, E, p.log_G, p.reach, lo, u.hi_min);
+  bwd_bounds(qa, u.a_off + u.a_valid - 1, P, E, p.log_G, p.reach, u.lo_max, hi);
+  ++hi;
   if (lo < 0) lo = 0;
-  u.b_off = (int)(lo / N) * N;
-  u.n = hi > lo ? (int)((hi - u.b_off + N - 1) / N) : 0;
+  u.b_off = lo / N * N;
+  u.n = hi > lo ? (hi - u.b_off + N - 1) / N : 0;
   return u;
 }
 
@@ -606,7 +603,7 @@ int run_backward(const void* q, const void* k, const void* v, const int32_t* cu,
   while ((1 << p.log_G) < G) ++p.log_G;
   p.d = d;
   p.N = N;
-  p.window = window > 0 ? window : 0;
+  p.reach = window > 0 && window < (1 << 30) ? window : 1 << 30;
   p.ctas = pl.ctas;
   p.scale = scale;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);

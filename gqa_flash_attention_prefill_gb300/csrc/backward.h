@@ -34,7 +34,8 @@ struct BwdUnit {      // one record of the plan, the same for every KV head
   int slot;           // -1: writes the result; else fp32 partial `slot`
   int stat;           // the sequence's first row in the arrays of row statistics
   int seq;
-  int pad[3];
+  int g;              // the KV head, once a CTA takes the record
+  int lo_max, hi_min; // of the columns that A's rows keep: the last first one, the first last one
 };
 static_assert(sizeof(BwdUnit) == 64, "copied as 16 words");
 
@@ -78,7 +79,7 @@ struct BwdParams {
   int num_seqs, total_q, total_kv;
   int Hq, Hkv, G, log_G;
   int d, N;             // N: rows of a streamed tile
-  int window;           // 0: none
+  int reach;            // the window, or 2^30: more than any length
   int ctas;
   float scale, scale_log2;
   unsigned long long timeout_ns;
@@ -95,6 +96,20 @@ __host__ __device__ constexpr int bwd_accs(int D) { return D == 256 ? 1 : 2; }
 cudaError_t launch_bwd_d64(const BwdParams& p, bool bf16, cudaStream_t st);
 cudaError_t launch_bwd_d128(const BwdParams& p, bool bf16, cudaStream_t st);
 cudaError_t launch_bwd_d256(const BwdParams& p, bool bf16, cudaStream_t st);
+
+// Rows of B that row `a` of a sequence on A's side keeps, both counted in their
+// sequence: keys of a packed query row, or packed query rows of a key.
+__device__ __forceinline__ void bwd_bounds(bool queries, int a, int P, int E, int log_G, int reach, int& lo,
+                                           int& hi) {
+  if (queries) {
+    hi = P + (a >> log_G);
+    lo = hi - reach + 1;
+  } else {
+    lo = max(a - P, 0) << log_G;
+    const int i = a - P;  // key a's token, if it is a new one
+    hi = ((i >= E - reach ? E : max(i + reach, 0)) << log_G) - 1;
+  }
+}
 
 // dS = P (dP - D) is held in f16 times 2^k, with k from a bound of |dP - D| that
 // leaves a factor of two to the largest f16: |dP_ij| <= |dout_i| |v_j|.

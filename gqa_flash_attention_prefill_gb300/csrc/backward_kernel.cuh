@@ -524,24 +524,10 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
       const int a_off = rec[3], b_off = rec[6];
       // Columns the row keeps, counted from B's first row: key or packed row
       // c of tile j is kept iff lo0 <= b_off + j N + c <= hi0.
-      int lo0, hi0, lo_max, hi_min;  // this row's; over the rows: the largest lo0, the least hi0
+      int lo0, hi0;
+      const int lo_max = rec[14], hi_min = rec[15];  // over A's rows: the largest lo0, the least hi0
       {
-        const int P = rec[8], E = rec[9];
-        auto bounds = [&](int a, int& lo, int& hi) {
-          if (qa) {
-            const int pos = P + (a >> p.log_G);
-            hi = pos;
-            lo = p.window > 0 ? pos - p.window + 1 : 0;
-          } else {
-            lo = max(a - P, 0) * p.G;
-            const long long i = p.window > 0 ? (long long)a + p.window - P : (long long)E;
-            hi = (int)(i < 0 ? 0 : i < (long long)E ? i : (long long)E) * p.G - 1;
-          }
-        };
-        int x;
-        bounds(a_off + r, lo0, hi0);
-        bounds(a_off + rec[4] - 1, lo_max, x);
-        bounds(a_off, x, hi_min);
+        bwd_bounds(qa, a_off + r, rec[8], rec[9], p.log_G, p.reach, lo0, hi0);
         lo0 -= part * CW;
         hi0 -= part * CW;
       }
