@@ -269,61 +269,66 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ B
     const int valid = keys ? min(128, p.kvi[b + 1] - base - r0) : min(128, (p.cu[b + 1] - base) * p.G - r0);
     if (!BF16 && tid < 2) s_most[tid] = 0u;
     if (!BF16) __syncthreads();
-    uint4 o[ROUNDS], dn[ROUNDS];
-    float ls[ROUNDS], dl[ROUNDS];  // lse and dlse of the row: one address for its lanes
-#pragma unroll
-    for (int i = 0; i < ROUNDS; ++i) {
-      const int r = warp * 16 + i * RPW + lane / LPR;
-      o[i] = dn[i] = make_uint4(0u, 0u, 0u, 0u);
-      ls[i] = -INFINITY;
-      dl[i] = 0.f;
-      if (r < valid) {
-        if (keys) {
-          dn[i] = __ldg(reinterpret_cast<const uint4*>(p.v) +
-                        ((size_t)(base + r0 + r) * p.Hkv + g) * LPR + lane % LPR);
-        } else {
-          const size_t row = (size_t)(base + ((r0 + r) >> p.log_G)) * p.Hq + g * p.G + ((r0 + r) & (p.G - 1));
-          o[i] = __ldg(reinterpret_cast<const uint4*>(p.out) + row * LPR + lane % LPR);
-          dn[i] = __ldg(reinterpret_cast<const uint4*>(p.dout) + row * LPR + lane % LPR);
-          ls[i] = __ldg(p.lse + row);
-          if (p.dlse != nullptr) dl[i] = __ldg(p.dlse + row);
-        }
-      }
-    }
     float m2 = 0.f, md = 0.f;
+    // Four rounds' loads at once, so that four CTAs fit an SM at any d (all rounds at
+    // once took 116 registers at d = 128: 3598 f16 tokens, the whole gradient 162 us, now 159).
+#pragma unroll 1
+    for (int at = 0; at < ROUNDS; at += 4) {
+      uint4 o[4], dn[4];
+      float ls[4], dl[4];  // lse and dlse of the row: one address for its lanes
 #pragma unroll
-    for (int i = 0; i < ROUNDS; ++i) {
-      const int r = warp * 16 + i * RPW + lane / LPR;
-      const uint32_t a[4] = {o[i].x, o[i].y, o[i].z, o[i].w},
-                     e[4] = {dn[i].x, dn[i].y, dn[i].z, dn[i].w};
-      float dot = 0.f, sq = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float el = unpack_lo<BF16>(e[k]), eh = unpack_hi<BF16>(e[k]);
-        dot = fmaf(unpack_lo<BF16>(a[k]), el, dot);
-        dot = fmaf(unpack_hi<BF16>(a[k]), eh, dot);
-        if (!BF16) sq = fmaf(el, el, fmaf(eh, eh, sq));
-      }
-#pragma unroll
-      for (int s = 1; s < LPR; s <<= 1) {
-        dot += __shfl_xor_sync(0xffffffffu, dot, s);
-        if (!BF16) sq += __shfl_xor_sync(0xffffffffu, sq, s);
-      }
-      if (!BF16) m2 = fmaxf(m2, sq);
-      if (!keys && lane % LPR == 0) {
-        float nl = -INFINITY, nd = 0.f, w = 0.f;
+      for (int i = 0; i < 4; ++i) {
+        const int r = warp * 16 + (at + i) * RPW + lane / LPR;
+        o[i] = dn[i] = make_uint4(0u, 0u, 0u, 0u);
+        ls[i] = -INFINITY;
+        dl[i] = 0.f;
         if (r < valid) {
-          const float lse = ls[i], dlt = dot - dl[i];
-          nd = -dlt;
-          if (lse != -INFINITY) {  // else: no key, no probability
-            nl = -lse * kLog2e + (BF16 ? 0.f : kBwdBias);
-            if (p.sinks != nullptr) w = expf(__ldg(p.sinks + g * p.G + ((r0 + r) & (p.G - 1))) - lse) * dlt;
+          if (keys) {
+            dn[i] = __ldg(reinterpret_cast<const uint4*>(p.v) +
+                          ((size_t)(base + r0 + r) * p.Hkv + g) * LPR + lane % LPR);
+          } else {
+            const size_t row = (size_t)(base + ((r0 + r) >> p.log_G)) * p.Hq + g * p.G + ((r0 + r) & (p.G - 1));
+            o[i] = __ldg(reinterpret_cast<const uint4*>(p.out) + row * LPR + lane % LPR);
+            dn[i] = __ldg(reinterpret_cast<const uint4*>(p.dout) + row * LPR + lane % LPR);
+            ls[i] = __ldg(p.lse + row);
+            if (p.dlse != nullptr) dl[i] = __ldg(p.dlse + row);
           }
-          if (!BF16) md = fmaxf(md, fabsf(dlt));
         }
-        s_nl[r] = nl;
-        s_nd[r] = nd;
-        s_w[r] = w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = warp * 16 + (at + i) * RPW + lane / LPR;
+        const uint32_t a[4] = {o[i].x, o[i].y, o[i].z, o[i].w},
+                       e[4] = {dn[i].x, dn[i].y, dn[i].z, dn[i].w};
+        float dot = 0.f, sq = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float el = unpack_lo<BF16>(e[k]), eh = unpack_hi<BF16>(e[k]);
+          dot = fmaf(unpack_lo<BF16>(a[k]), el, dot);
+          dot = fmaf(unpack_hi<BF16>(a[k]), eh, dot);
+          if (!BF16) sq = fmaf(el, el, fmaf(eh, eh, sq));
+        }
+#pragma unroll
+        for (int s = 1; s < LPR; s <<= 1) {
+          dot += __shfl_xor_sync(0xffffffffu, dot, s);
+          if (!BF16) sq += __shfl_xor_sync(0xffffffffu, sq, s);
+        }
+        if (!BF16) m2 = fmaxf(m2, sq);
+        if (!keys && lane % LPR == 0) {
+          float nl = -INFINITY, nd = 0.f, w = 0.f;
+          if (r < valid) {
+            const float lse = ls[i], dlt = dot - dl[i];
+            nd = -dlt;
+            if (lse != -INFINITY) {  // else: no key, no probability
+              nl = -lse * kLog2e + (BF16 ? 0.f : kBwdBias);
+              if (p.sinks != nullptr) w = expf(__ldg(p.sinks + g * p.G + ((r0 + r) & (p.G - 1))) - lse) * dlt;
+            }
+            if (!BF16) md = fmaxf(md, fabsf(dlt));
+          }
+          s_nl[r] = nl;
+          s_nd[r] = nd;
+          s_w[r] = w;
+        }
       }
     }
     if (!BF16) {
@@ -347,12 +352,19 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ B
       if (tid < 128) p.nlse[at + tid] = s_nl[tid];
       else p.nd[at + tid - 128] = s_nd[tid - 128];
       if (p.sinks != nullptr) {
-        // Rows of one head are G apart: halves are added until G sums are left.
-        for (int s = 64; s >= p.G; s >>= 1) {
-          if (tid < s) s_w[tid] += s_w[tid + s];
-          __syncthreads();
+        // Rows of one head are G apart: sums of pairs, in a warp and then over four.
+        if (tid < 128) {
+          float w = s_w[tid];
+          for (int s = 16; s >= p.G; s >>= 1) w += __shfl_xor_sync(0xffffffffu, w, s);
+          s_w[tid] = w;
         }
-        if (tid < p.G) p.sink_part[(size_t)(g * p.G + tid) * p.max_qtiles + tile] = s_w[tid];
+        __syncthreads();
+        if (tid < p.G) {
+          float w = s_w[tid];
+          if (p.G <= 32) w = (w + s_w[tid + 32]) + (s_w[tid + 64] + s_w[tid + 96]);
+          if (p.G == 64) w += s_w[tid + 64];
+          p.sink_part[(size_t)(g * p.G + tid) * p.max_qtiles + tile] = w;
+        }
       }
     }
     __syncthreads();
