@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ B
       if (tid == 0) {
         double a = 0.0;
         for (int w = 0; w < 8; ++w) a += s_sum[w];
-        p.dsinks[h] = (float)-a;
+        p.dsinks[h] = (float)(0.0 - a);
       }
       __syncthreads();
       continue;

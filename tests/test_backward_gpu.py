@@ -220,3 +220,21 @@ def test_memory_of_a_call_on_another_stream(pkg):  # noqa: F811
     other.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
     assert all(bool((x == 255).all()) for x in blocks)
+
+
+def test_offsets_past_32_bits(pkg):  # noqa: F811
+    """A short sequence behind a long one, past 2^31 values of q: the rows of a call of its own."""
+    long, pre, new, hq, hkv, d = 2 ** 18, 30, 90, 64, 2, 128
+    b = W.make_batch([0, pre], [long, new], hq, hkv, d, "bf16", window=40, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    dout = torch.randn(b.q.shape, generator=gen, device="cuda", dtype=torch.bfloat16)
+    out, lse = pkg.prefill(b)
+    got = pkg.prefill_backward(b, out, lse, dout)
+    tail = batch([pre], [new], hq, hkv, d, "bf16", window=40, sink="head")
+    tail.q, tail.k, tail.v, tail.sinks = b.q[long:].clone(), b.k[long:].clone(), b.v[long:].clone(), b.sinks
+    assert long * hq * d >= 2 ** 31 and len(tail.k) == pre + new
+    want, bounds = R.gradients(tail, out[long:], lse[long:], dout[long:])
+    torch.cuda.synchronize()
+    assert pkg.get_device_status() == 0
+    R.check([got[0][long:], got[1][long:], got[2][long:]], want[:3], bounds[:3])
+    assert bool(torch.stack([x.isfinite().all() for x in got]).all())

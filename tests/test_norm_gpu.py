@@ -223,3 +223,21 @@ def test_graph_and_stream(pkg):  # noqa: F811
         other.synchronize()
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
         assert all(bool((b == 255).all()) for b in blocks)
+
+
+def test_offsets_past_32_bits(pkg):  # noqa: F811
+    """Rows past 2^31 values, forward and back."""
+    rows, n = 2 ** 19 + 3, 4096
+    x = torch.zeros(rows, n, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = randn(3, n, seed=1, dtype=torch.bfloat16)
+    weight = randn(n, seed=2)
+    out, _, _, rstd = pkg.rms_norm(x, weight, EPS, with_rstd=True)
+    check_out(out[-3:, None], None, rstd[-3:, None], x[-3:, None], weight, 0.0, EPS, torch.bfloat16)
+    assert not bool(out[:-3].any())
+    dx, _, dweight = pkg.rms_norm_backward(x, x, weight, rstd)
+    few = pkg.rms_norm_backward(x[-3:].clone(), x[-3:].clone(), weight, rstd[-3:].clone())
+    assert torch.equal(dx[-3:], few[0]) and not bool(dx[:-3].any())
+    # Three rows' products, in another order at most: 3 f of the sum of magnitudes.
+    t = x[-3:].double() * rstd[-3:, None].double()
+    room = 2.0 ** -22 * (x[-3:].double() * t).abs().sum(0)
+    assert bool(((dweight - few[2]).abs().double() <= room).all())
