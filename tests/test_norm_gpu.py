@@ -241,3 +241,18 @@ def test_offsets_past_32_bits(pkg):  # noqa: F811
     t = x[-3:].double() * rstd[-3:, None].double()
     room = 2.0 ** -22 * (x[-3:].double() * t).abs().sum(0)
     assert bool(((dweight - few[2]).abs().double() <= room).all())
+
+
+@pytest.mark.parametrize("dtype,stream,weight", [("bf16", "bf16", "f32"), ("f16", "f32", "f16")])
+@pytest.mark.parametrize("rows", [1, 37, 311])
+@pytest.mark.parametrize("n", [264, 504, 512, 520, 768, 1016, 1024, 1032, 1536, 2040, 2048])
+def test_widths(pkg, rows, n, dtype, stream, weight):  # noqa: F811
+    """A row in a warp of one, two or four groups a lane, or in a CTA of one or two a thread; teams with rows missing."""
+    x, w = randn(rows, n, seed=1, dtype=DT[dtype]), randn(n, seed=2, dtype=DT[weight])
+    res = randn(rows, n, seed=3, dtype=DT[stream], scale=3.0)
+    out, _, h, rstd = pkg.rms_norm(x, w, EPS, 1.0, res, with_rstd=True)
+    check_out(out[:, None], None, rstd[:, None], h[:, None], w, 1.0, EPS, x.dtype)
+    for group in [g for g in (32, 128, n) if n % g == 0]:
+        out, scales, h, rstd = pkg.rms_norm(x, w, EPS, 0.0, res, group, True)
+        check_out(out[:, None], scales[:, None], rstd[:, None], h[:, None], w, 0.0, EPS, x.dtype)
+    check_gradient(pkg, rows, 1, n, dtype, stream, weight, 1.0, rows != 37, strided=rows == 37)
