@@ -797,7 +797,11 @@ def gqa_cache_attention(q, k_pages, v_pages, cu_seqlens_q, prefix_lens, kv_page_
 def _type_code(dtype) -> int:
     if isinstance(dtype, int):
         return dtype
-    return GQA_BF16 if "bf16" in str(dtype) or "bfloat16" in str(dtype) else GQA_F16
+    codes = {"bf16": GQA_BF16, "bfloat16": GQA_BF16, "f16": GQA_F16, "float16": GQA_F16}
+    name = str(dtype).replace("torch.", "")
+    if name not in codes:
+        raise TypeError(f"dtype must be float16 or bfloat16, got {dtype}")
+    return codes[name]
 
 
 def prefill_backward_workspace(num_seqs, total_q, total_kv, hq, hkv, d, dtype):

@@ -93,3 +93,14 @@ def test_binding_refusals():
         pkg._norm_rstd(w, 3, 1)
     # a slice of a packed projection: its stride is what is passed on
     assert pkg._norm_rows("x", torch.zeros(5, 8, 64)[:, 2:4]) == (5, 2, 64, 512)
+
+
+def test_workspaces_refuse_other_types():
+    import gqa_flash_attention_prefill_gb300 as pkg
+    for dtype in (torch.float32, "f32", "float64"):
+        with pytest.raises(TypeError, match="float16 or bfloat16"):
+            pkg.rms_norm_backward_workspace(4, 1, 64, dtype)
+        with pytest.raises(TypeError, match="float16 or bfloat16"):
+            pkg.prefill_backward_workspace(1, 4, 4, 2, 1, 64, dtype)
+    for names in (("bf16", torch.bfloat16), ("f16", torch.float16)):
+        assert len({pkg.prefill_backward_workspace(1, 400, 400, 2, 1, 64, dtype) for dtype in names}) == 1
