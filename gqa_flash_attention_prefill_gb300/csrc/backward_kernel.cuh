@@ -47,33 +47,30 @@ constexpr int bwd_warps(int D) { return D == 64 ? 8 : 16; }  // softmax warps
 constexpr int bwd_threads(int D) { return 32 * (bwd_warps(D) + 2); }
 constexpr int kBwdRecs = 4;  // unit records in flight
 
-constexpr int bwd_a_buffers(int D) { return 1; }
 constexpr int bwd_stages(int D) { return D == 64 ? 4 : D == 128 ? 2 : 1; }
-constexpr int bwd_s_buffers(int D) { return 1; }
 constexpr uint32_t bwd_a_bytes(int D) { return 128u * D * 2u; }            // one tile
 constexpr uint32_t bwd_b_bytes(int D) { return (uint32_t)bwd_n(D) * D * 2u; }
 constexpr uint32_t bwd_stat_bytes(int D) { return 8u * bwd_n(D); }         // -lse, -D of a tile
 constexpr uint32_t bwd_smem(int D) {
-  return 1024u + bwd_a_buffers(D) * 2u * bwd_a_bytes(D) +
+  return 1024u + 2u * bwd_a_bytes(D) +
          bwd_stages(D) * (2u * bwd_b_bytes(D) + bwd_stat_bytes(D)) + 64u * 8u + 16u +
          kBwdRecs * 64u;
 }
 
 struct BwdBar {
-  static constexpr int kRecFull = 0, kRecEmpty = 4, kAFull = 8, kAEmpty = 10, kBFull = 12,
-                       kBEmpty = 16, kLand = 20, kSFull = 21, kPFull = 23, kTFull = 25, kDFull = 26,
-                       kAccDone = 27, kAccFree = 28, kDrain = 29, kCount = 30;
+  static constexpr int kRecFull = 0, kRecEmpty = 4, kAFull = 8, kAEmpty = 9, kBFull = 10,
+                       kBEmpty = 14, kLand = 18, kSFull = 19, kPFull = 20, kTFull = 22, kDFull = 23,
+                       kAccDone = 24, kAccFree = 25, kDrain = 26, kCount = 27;
 };
 
 template <int D, bool BF16>
 struct Bwd {
-  static constexpr int N = bwd_n(D), NS = bwd_stages(D), NA = bwd_a_buffers(D),
-                       NSB = bwd_s_buffers(D), NCH = D / 64,
+  static constexpr int N = bwd_n(D), NS = bwd_stages(D), NCH = D / 64,
                        WARPS = bwd_warps(D), PG = WARPS / 4, CW = N / PG;
   static constexpr uint32_t kABytes = bwd_a_bytes(D), kBBytes = bwd_b_bytes(D),
                             kStat = bwd_stat_bytes(D);
   static constexpr uint32_t kAChunk = 128u * 128u, kBChunk = N * 128u;
-  static constexpr uint32_t kColT = NSB * N, kColAcc0 = D == 64 ? 128 : 256,
+  static constexpr uint32_t kColT = N, kColAcc0 = D == 64 ? 128 : 256,
                             kColAcc1 = D == 64 ? 192 : D == 128 ? 384 : 256, kCols = 512 / bwd_per_sm(D);
   static_assert(kColT + N <= kColAcc0 && kColAcc1 + D <= kCols, "tensor memory");
 };
@@ -255,7 +252,7 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
     backward_kernel(const __grid_constant__ BwdParams p) {
   using K = Bwd<D, BF16>;
   using B = BwdBar;
-  constexpr int N = K::N, NS = K::NS, NA = K::NA, NSB = K::NSB, NCH = K::NCH, CW = K::CW;
+  constexpr int N = K::N, NS = K::NS, NCH = K::NCH, CW = K::CW;
   constexpr int WARPS = K::WARPS, kLoadWarp = WARPS, kMmaWarp = WARPS + 1;
   constexpr uint32_t kIdescS = idesc_f16(BF16, 128, N, false);
   constexpr uint32_t kIdescO = idesc_f16(BF16, 128, D, true);
@@ -263,10 +260,10 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  const uint32_t sA = smem_u32(smem);                      // [NA][2] tiles
-  const uint32_t sB = sA + NA * 2u * K::kABytes;           // [NS][2] tiles
+  const uint32_t sA = smem_u32(smem);                      // [2] tiles
+  const uint32_t sB = sA + 2u * K::kABytes;           // [NS][2] tiles
   const uint32_t sStat = sB + NS * 2u * K::kBBytes;        // [NS] -lse, -D
-  uint8_t* tail = smem + NA * 2u * K::kABytes + NS * (2u * K::kBBytes + K::kStat);
+  uint8_t* tail = smem + 2u * K::kABytes + NS * (2u * K::kBBytes + K::kStat);
   uint64_t* bars = reinterpret_cast<uint64_t*>(tail);
   const uint32_t sBar = smem_u32(bars);
   uint32_t* misc = reinterpret_cast<uint32_t*>(bars + 64);  // [0] tensor memory, [1] abort
@@ -329,10 +326,9 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
                 b_base = field(5), b_off = field(6), b_len = field(7), stat = field(11);
       if (n == 0) continue;
       const bool qa = kind == kBwdQ;
-      const uint32_t ab = ua % NA;
-      if (!wait(B::kAEmpty + ab, ((ua / NA) & 1u) ^ 1u)) break;
+      if (!wait(B::kAEmpty, (ua & 1u) ^ 1u)) break;
       if (lane == 0) {
-        const uint32_t full = bar(B::kAFull + ab), dst = sA + ab * 2u * K::kABytes;
+        const uint32_t full = bar(B::kAFull), dst = sA;
         mbar_arrive_expect_tx(full, 2u * K::kABytes);
         // Queries are counted in packed rows, token by token: the G heads of a
         // KV head, one after the other.  A tile of 128 starts at a token.
@@ -388,9 +384,7 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
     }
     // Let every copy issued land before the CTA can exit.
     if (*abort_flag) {
-      for (uint32_t b = 0; b < NA; ++b)
-        if (ua > b)
-          wait_drain(bar(B::kAFull + (ua - 1u - b) % NA), ((ua - 1u - b) / NA) & 1u, p.timeout_ns);
+      if (ua > 0) wait_drain(bar(B::kAFull), (ua - 1u) & 1u, p.timeout_ns);
       if (lands > 0) wait_drain(bar(B::kLand), (lands - 1u) & 1u, p.timeout_ns);
       for (uint32_t b = 0; b < NS; ++b)
         if (it > b)
@@ -401,7 +395,7 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
 
   // ---------------------------------------------------------------- products
   if (warp == kMmaWarp) {
-    const uint64_t dA0 = smem_desc_sw128(sA, 16, 1024);
+    const uint64_t dA1 = smem_desc_sw128(sA, 16, 1024), dA2 = dA1 + (K::kABytes >> 4);
     const uint64_t dB0 = smem_desc_sw128(sB, 16, 1024);           // rows are N
     const uint64_t dBt0 = smem_desc_sw128(sB, K::kBChunk, 1024);  // rows are the contraction
     auto kstep = [](int kk, uint32_t chunk) -> uint64_t {
@@ -423,9 +417,7 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
       if (kind < 0) break;
       if (n == 0) continue;
       const bool has_t = kind != kBwdV, has_p = kind == kBwdKV || kind == kBwdV;
-      const uint32_t ab = uc % NA;
-      if (!(ok = wait(B::kAFull + ab, (uc / NA) & 1u))) break;
-      const uint64_t dA1 = dA0 + ab * 2u * (K::kABytes >> 4), dA2 = dA1 + (K::kABytes >> 4);
+      if (!(ok = wait(B::kAFull, uc & 1u))) break;
       auto issue_s = [&](uint32_t t) -> bool {  // S of tile t, once it is in
         const uint32_t s = t % NS;
         if (!wait(B::kBFull + s, (t / NS) & 1u)) return false;
@@ -433,9 +425,9 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
         const uint64_t b1 = dB0 + s * 2u * (K::kBBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + (t % NSB) * N, dA1 + kstep(kk, K::kAChunk), b1 + kstep(kk, K::kBChunk),
+          mma_ss(tmem, dA1 + kstep(kk, K::kAChunk), b1 + kstep(kk, K::kBChunk),
                  kIdescS, kk > 0 ? 1u : 0u);
-        mma_commit(bar(B::kSFull + t % NSB));
+        mma_commit(bar(B::kSFull));
         return true;
       };
       // acc (+)= (the 16-bit tile at `src`) B: each warpgroup's columns stand at
@@ -451,7 +443,7 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
         if (!ok) break;
       }
       for (int j = 0; j < n; ++j, ++it) {
-        const uint32_t s = it % NS, sb = it % NSB;
+        const uint32_t s = it % NS;
         if constexpr (NS == 1) {
           ok = issue_s(it);
           if (!ok) break;
@@ -465,17 +457,13 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
                    kk > 0 ? 1u : 0u);
           mma_commit(bar(B::kTFull));
         }
-        if (j == n - 1) mma_commit(bar(B::kAEmpty + ab));
-        if constexpr (NSB == 2) {
-          if (j + 1 < n) ok = issue_s(it + 1);
-          if (!ok) break;
-        }
+        if (j == n - 1) mma_commit(bar(B::kAEmpty));
         if (!(ok = wait(B::kPFull + (it & 1u), (it >> 1) & 1u))) break;
         if (j == 0 && uc > 0 && !(ok = wait(B::kAccFree, (uc - 1u) & 1u))) break;
         tc_fence_after();
         if (has_p)
-          issue_acc(tmem + K::kColAcc0, tmem + sb * N, dBt + (K::kBBytes >> 4), j == 0);
-        if constexpr (NS > 1 && NSB == 1) {
+          issue_acc(tmem + K::kColAcc0, tmem, dBt + (K::kBBytes >> 4), j == 0);
+        if constexpr (NS > 1) {
           if (j + 1 < n) ok = issue_s(it + 1);
           if (!ok) break;
         }
@@ -550,15 +538,15 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
         hi0 -= part * CW;
       }
       for (int j = 0; j < n; ++j, ++it) {
-        const uint32_t s = it % NS, sb = it % NSB;
+        const uint32_t s = it % NS;
         const int off = b_off + j * N;
-        t.t_s = t_lane + sb * N + part * CW;
+        t.t_s = t_lane + part * CW;
         t.t_t = t_lane + K::kColT + part * CW;
         t.stats = sStat + s * K::kStat + (uint32_t)part * CW * 4u;
         t.lo = lo0 - off;
         t.hi = hi0 - off;
         t.masked = lo_max > off || hi_min < off + N - 1;
-        const uint32_t bs = bar(B::kSFull + sb), ps = (it / NSB) & 1u, bp = bar(B::kPFull + (it & 1u)),
+        const uint32_t bs = bar(B::kSFull), ps = it & 1u, bp = bar(B::kPFull + (it & 1u)),
                        bt = bar(B::kTFull), bd = bar(B::kDFull);
         if (qa) {
           ok = bwd_tile<kBwdQ, D, BF16>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
@@ -582,6 +570,7 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
       const bool is_v = kind == kBwdV || (both && part < PG / 2);
       const float out_mul = is_v ? (BF16 ? 1.f : 1.f / 32768.f) : p.scale * undo;
       const uint32_t acc = is_v ? K::kColAcc0 : K::kColAcc1;
+      static_assert(D / PG % 32 == 0, "bwd_store takes 32 columns at a time");
       const int cols = both ? D / (PG / 2) : D / PG, col0 = (both ? part % (PG / 2) : part) * cols;
       const int a_base = rec[2], slot = rec[10], g = rec[13];
       uint16_t* row = nullptr;
