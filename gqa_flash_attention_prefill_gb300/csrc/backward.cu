@@ -275,13 +275,13 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ B
 #pragma unroll 1
     for (int at = 0; at < ROUNDS; at += 4) {
       uint4 o[4], dn[4];
-      float ls[4], dl[4];  // lse and dlse of the row: one address for its lanes
+      float ls[4], dl[4], sk[4];  // the row's lse, dlse and sink: one address for its lanes
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = warp * 16 + (at + i) * RPW + lane / LPR;
         o[i] = dn[i] = make_uint4(0u, 0u, 0u, 0u);
         ls[i] = -INFINITY;
-        dl[i] = 0.f;
+        dl[i] = sk[i] = 0.f;
         if (r < valid) {
           if (keys) {
             dn[i] = __ldg(reinterpret_cast<const uint4*>(p.v) +
@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ B
             dn[i] = __ldg(reinterpret_cast<const uint4*>(p.dout) + row * LPR + lane % LPR);
             ls[i] = __ldg(p.lse + row);
             if (p.dlse != nullptr) dl[i] = __ldg(p.dlse + row);
+            if (p.sinks != nullptr) sk[i] = __ldg(p.sinks + g * p.G + ((r0 + r) & (p.G - 1)));
           }
         }
       }
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ B
             nd = -dlt;
             if (lse != -INFINITY) {  // else: no key, no probability
               nl = -lse * kLog2e + (BF16 ? 0.f : kBwdBias);
-              if (p.sinks != nullptr) w = expf(__ldg(p.sinks + g * p.G + ((r0 + r) & (p.G - 1))) - lse) * dlt;
+              if (p.sinks != nullptr) w = expf(sk[i] - lse) * dlt;
             }
             if (!BF16) md = fmaxf(md, fabsf(dlt));
           }

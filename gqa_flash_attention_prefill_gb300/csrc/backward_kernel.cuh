@@ -28,11 +28,11 @@
 // one warp gets the products issued (60-120 clocks each beside busy warps, 26 in
 // 1500 clocks of a CTA's 1950).  4096 tokens of 64 / 8 heads of 64, bf16: 442 us of
 // the call's 464, 1089 TFLOP/s of the seven products, tensor path 70% active, issue
-// slots 55%; 3598 ragged f16 tokens of 32 / 8 heads of 128: 138 of 158 us.
+// slots 55%; 3598 ragged f16 tokens of 32 / 8 heads of 128: 137 of 157 us.
 //
 // Tile and CTAs.  d = 64: tiles of 64 columns and two CTAs an SM, which overlap each
 // other's waits (one CTA with tiles of 128: 512 us, with two S tiles and two
-// product warps 460 but 107 us instead of 96 with a window of 128, where a
+// product warps 460 but 107 us instead of 95 with a window of 128, where a
 // unit is three tiles long).  d = 128: tiles of 128, which the products read
 // at full rate.  d = 256: 64, so that a tile of each operand fits.
 #pragma once
