@@ -618,6 +618,13 @@ int run_backward(const void* q, const void* k, const void* v, const int32_t* cu,
   p.N = N;
   p.reach = window > 0 && window < (1 << 30) ? window : 1 << 30;
   p.ctas = pl.ctas;
+  // Two terms where the tiles are some two a CTA at most: every query tile by every
+  // key tile of the call (or its window's), at their costs.  There a tile's time is
+  // latency (37 and 5 tokens of d = 256: 20.6 us, one term 19.5); 4096 tokens would take 590 us
+  // instead of 463, and their error stays at 1.41 times the results' own rounding with one.
+  const double keys = p.reach < total_kv ? p.reach + 128. : total_kv, rows = p.reach < total_q ? p.reach + 128. : total_q;
+  const double cost = pl.max_qtiles * (keys / N + 2.) * 3. + pl.max_ktiles * (rows * G / N + 2.) * 4.;
+  p.two = cost * Hkv <= 8. * pl.ctas;
   p.scale = scale;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.timeout_ns = wait_limit_ns();

@@ -81,6 +81,7 @@ struct BwdParams {
   int d, N;             // N: rows of a streamed tile
   int reach;            // the window, or 2^30: more than any length
   int ctas;
+  int two;              // P and dS in two 16-bit terms
   float scale, scale_log2;
   unsigned long long timeout_ns;
 };

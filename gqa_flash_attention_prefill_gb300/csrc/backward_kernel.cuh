@@ -16,7 +16,12 @@
 //
 // P and dS are rounded to the inputs' type because the tensor cores take no other
 // left operand beside a 16-bit right one: half a step of each, as the forward
-// kernels round P.  Everything else is fp32.
+// kernels round P.  Everything else is fp32.  Over many rows that makes a result's
+// error 1.41 times its own rounding; over a few it may be one p's alone, up to
+// twice.  So a small call (BwdParams::two), which leaves the GPU mostly idle, holds P
+// and dS as sums of two 16-bit terms, the second in the columns that the fp32 ones
+// leave free: 150 calls of a few tokens to some hundred were up to 1.94 times as far
+// from 64 bits as a form that rounds its results alone, and are up to 1.44 times.
 //
 // CTA: 8 or 16 softmax warps (each warpgroup takes a share of the columns), a
 // loading warp, a warp that issues the products.  Persistent: units are taken from a
@@ -111,7 +116,7 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-template <int KIND, int D, bool BF16>
+template <int KIND, int D, bool BF16, bool TWO>
 __device__ __forceinline__ bool bwd_tile(const BwdTile& t, float sl2, float mul, uint32_t bar_s,
                                          uint32_t par_s, uint32_t bar_p, uint32_t bar_t,
                                          uint32_t par_t, uint32_t bar_d,
@@ -153,6 +158,12 @@ __device__ __forceinline__ bool bwd_tile(const BwdTile& t, float sl2, float mul,
 #pragma unroll
     for (int c = 0; c < CW; c += 2) pk[c / 2] = pack2<BF16>(x[c], x[c + 1]);
     tmem_store<CW / 2>(t.t_s, pk);
+    if constexpr (TWO) {
+#pragma unroll
+      for (int c = 0; c < CW; c += 2)
+        pk[c / 2] = pack2<BF16>(x[c] - unpack_lo<BF16>(pk[c / 2]), x[c + 1] - unpack_hi<BF16>(pk[c / 2]));
+      tmem_store<CW / 2>(t.t_s + CW / 2, pk);
+    }
     tmem_wait_st();
   }
   warp_arrive(bar_p);  // S is read (and P written)
@@ -184,8 +195,14 @@ __device__ __forceinline__ bool bwd_tile(const BwdTile& t, float sl2, float mul,
     unf2(fmul2(b, f2(x[c + 2], x[c + 3])), d2, d3);
     dk[c / 2] = pack2<BF16>(d0, d1);
     dk[c / 2 + 1] = pack2<BF16>(d2, d3);
+    if constexpr (TWO) {  // what the first term leaves, over T's values
+      y[c / 2] = pack2<BF16>(d0 - unpack_lo<BF16>(dk[c / 2]), d1 - unpack_hi<BF16>(dk[c / 2]));
+      y[c / 2 + 1] = pack2<BF16>(d2 - unpack_lo<BF16>(dk[c / 2 + 1]), d3 - unpack_hi<BF16>(dk[c / 2 + 1]));
+    }
   }
   tmem_store<CW / 2>(t.t_t, dk);
+  if constexpr (TWO)
+    tmem_store<CW / 2>(t.t_t + CW / 2, *reinterpret_cast<uint32_t(*)[CW / 2]>(y));
   tmem_wait_st();
   warp_arrive(bar_d);
   return true;
@@ -247,7 +264,7 @@ __device__ __forceinline__ void bwd_store(uint32_t t_acc, int cols, int col0, fl
   }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool TWO>
 __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
     backward_kernel(const __grid_constant__ BwdParams p) {
   using K = Bwd<D, BF16>;
@@ -437,6 +454,12 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
         for (int kk = 0; kk < N / 16; ++kk)
           mma_ts(acc, src + (kk / (CW / 16)) * CW + (kk % (CW / 16)) * 8,
                  b + (uint64_t)(kk * 128), kIdescO, (first && kk == 0) ? 0u : 1u);
+        if constexpr (TWO) {
+#pragma unroll
+          for (int kk = 0; kk < N / 16; ++kk)
+            mma_ts(acc, src + (kk / (CW / 16)) * CW + (kk % (CW / 16)) * 8 + CW / 2,
+                   b + (uint64_t)(kk * 128), kIdescO, 1u);
+        }
       };
       if constexpr (NS > 1) {
         ok = issue_s(it);
@@ -549,16 +572,16 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
         const uint32_t bs = bar(B::kSFull), ps = it & 1u, bp = bar(B::kPFull + (it & 1u)),
                        bt = bar(B::kTFull), bd = bar(B::kDFull);
         if (qa) {
-          ok = bwd_tile<kBwdQ, D, BF16>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+          ok = bwd_tile<kBwdQ, D, BF16, TWO>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
         } else {
           // The statistics came with B (this thread has to see their barrier).
           if (!(ok = wait(B::kBFull + s, (it / NS) & 1u))) break;
           if constexpr (D < 256)
-            ok = bwd_tile<kBwdKV, D, BF16>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+            ok = bwd_tile<kBwdKV, D, BF16, TWO>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
           else if (kind == kBwdK)
-            ok = bwd_tile<kBwdK, D, BF16>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+            ok = bwd_tile<kBwdK, D, BF16, TWO>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
           else
-            ok = bwd_tile<kBwdV, D, BF16>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+            ok = bwd_tile<kBwdV, D, BF16, TWO>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
         }
         if (!ok) break;
         if (kind != kBwdV) ++td;
@@ -610,9 +633,9 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
 
 namespace {
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool TWO>
 cudaError_t launch_backward(const BwdParams& p, cudaStream_t st) {
-  auto kern = backward_kernel<D, BF16>;
+  auto kern = backward_kernel<D, BF16, TWO>;
   static SmemAttr attr{};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

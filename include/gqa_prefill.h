@@ -397,9 +397,9 @@ GQA_API int gqa_cache_attention_workspace(int num_seqs, int total_q, int max_seq
  * anything.  16-bit tensors are 16-byte aligned.  Results share no memory with
  * one another or with an argument (GQA_ERR_INVALID).  Hq / Hkv is a power of
  * two up to 128; d is 64, 128 or 256.  Sums are fp32; p and ds are rounded once
- * to the inputs' type for their products (in f16 they are scaled by powers of
- * two first, so that small ones keep their bits).  The result is the same run
- * to run.  Four kernels are enqueued on `stream`.  Metadata, waits and return
+ * to the inputs' type for their products, or held in two such terms where a
+ * call is small (in f16 they are scaled by powers of two first, so that small
+ * ones keep their bits).  The result is the same run to run.  Four kernels are enqueued on `stream`.  Metadata, waits and return
  * codes as gqa_flash_prefill; a missing or small workspace is GQA_ERR_INVALID.
  */
 GQA_API int gqa_prefill_backward(const void* q, const void* k, const void* v,

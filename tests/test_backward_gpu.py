@@ -238,3 +238,19 @@ def test_offsets_past_32_bits(pkg):  # noqa: F811
     assert pkg.get_device_status() == 0
     R.check([got[0][long:], got[1][long:], got[2][long:]], want[:3], bounds[:3])
     assert bool(torch.stack([x.isfinite().all() for x in got]).all())
+
+
+@pytest.mark.parametrize("pre,new,hq,hkv,d,dtype,window", [([0], [2], 2, 2, 128, "bf16", 0), ([34, 2], [3, 8], 2, 1, 256, "bf16", 128),
+                                                           ([89], [2], 4, 4, 64, "f16", 0), ([0, 2966], [102, 14], 2, 1, 64, "bf16", 0),
+                                                           ([0], [83], 1, 1, 64, "f16", 0), ([5112, 0], [36, 3], 4, 4, 64, "bf16", 128),
+                                                           ([0, 0], [3, 2], 8, 2, 64, "f16", 128), ([0], [27], 2, 2, 256, "f16", 0)])
+def test_small_calls_lose_nothing_to_p_and_ds(pkg, pre, new, hq, hkv, d, dtype, window):  # noqa: F811
+    """Over a few rows an error is not averaged away, so P and dS are held in two terms: off by 2^-17 (bf16) at most.  With
+    that, fp32 sums of d products ((d + 3) f of some 5 times the score) and the exponential a result is off by 2^-14 of
+    its norm, beside its own rounding."""
+    b = batch(pre, new, hq, hkv, d, dtype, window=window, sink="head")
+    out, lse, dout, got = run(pkg, b)
+    want, _ = R.gradients(b, out, lse, dout)
+    for x, y in zip(got[:3], want[:3]):
+        own = (y.to(b.q.dtype).double() - y).norm()
+        assert float((x.double() - y).norm()) <= float(own) + 2.0 ** -14 * float(y.norm())
