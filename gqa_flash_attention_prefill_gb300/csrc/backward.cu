@@ -23,6 +23,13 @@ constexpr int kPlanBins = 64;
 // unit is not cut.
 constexpr int kShares = 1;
 constexpr int kMinTiles = 8;
+// Pairs up to which a sequence's P and dS are held in two terms: 724 tokens of one query head, 256 of
+// eight.  Error against 64 bits over that of results that are rounded alone, 1300 sequences of 1 to 700
+// tokens, the worst of dq, dk and dv: with two terms 1.00 (1.06 where a result cancels), with one 1.43, up
+// to 1.5 where pairs are few and twice over a handful; above the limit 1.49 at most, with scores of 8
+// times the spread (a p or two a row) too.  Price: 2000 sequences of 30 tokens, 64 / 8 heads of 64, 964 -> 1048
+// us; 100 of 300 tokens, above the limit, would take 669 instead of 576.
+constexpr long long kTwoPairs = 1 << 19;
 
 // Relative cost of a streamed tile: its products.
 __device__ __forceinline__ int tile_cost(int kind) {
@@ -37,6 +44,12 @@ __device__ __forceinline__ int find_seq(const int32_t* first, int n, int x) {
     if (first[mid] <= x) lo = mid; else hi = mid;
   }
   return lo;
+}
+
+// Whether a sequence's P and dS are held in two 16-bit terms: where it has few pairs (of a
+// KV head's query rows and the keys that one sees), whatever stands beside it in the call.
+__device__ __forceinline__ bool two_terms(const BwdParams& p, int P, int E) {
+  return (long long)E * p.G * min(P + E, p.reach) <= kTwoPairs;
 }
 
 // Unit x of the list before cutting: first the query tiles, then the key tiles
@@ -225,11 +238,11 @@ __device__ __forceinline__ void bwd_plan(const BwdParams& p) {
   __syncthreads();
   for (int x = tid; x < total; x += threads) {
     BwdUnit u = plan_unit(p, x, nq, nk);
-    const int n = u.n, off = u.b_off, parts = parts_of(u.kind, n);
+    const int kind = u.kind, n = u.n, off = u.b_off, parts = parts_of(kind, n);
     int slot = -1;
     if (parts > 1) {
       slot = atomicAdd(&s_slots, parts);
-      const BwdJoin j = {u.kind, u.a_base, u.a_off, u.a_valid, slot, parts, u.seq, 0};
+      const BwdJoin j = {kind, u.a_base, u.a_off, u.a_valid, slot, parts, u.seq, 0};
       p.joins[atomicAdd(&s_joins, 1)] = j;
     }
     for (int i = 0; i < parts; ++i) {
@@ -237,7 +250,8 @@ __device__ __forceinline__ void bwd_plan(const BwdParams& p) {
       u.n = t1 - t0;
       u.b_off = off + t0 * p.N;
       u.slot = parts > 1 ? slot + i : -1;
-      p.units[atomicAdd(&s_bins[bin_of(u.kind, u.n)], 1)] = u;
+      u.kind = kind + (two_terms(p, u.P, u.E) ? kBwdTwo : 0);
+      p.units[atomicAdd(&s_bins[bin_of(kind, u.n)], 1)] = u;
     }
   }
 }
@@ -618,13 +632,6 @@ int run_backward(const void* q, const void* k, const void* v, const int32_t* cu,
   p.N = N;
   p.reach = window > 0 && window < (1 << 30) ? window : 1 << 30;
   p.ctas = pl.ctas;
-  // Two terms where the tiles are some two a CTA at most: every query tile by every
-  // key tile of the call (or its window's), at their costs.  There a tile's time is
-  // latency (37 and 5 tokens of d = 256: 20.6 us, one term 19.5); 4096 tokens would take 590 us
-  // instead of 463, and their error stays at 1.41 times the results' own rounding with one.
-  const double keys = p.reach < total_kv ? p.reach + 128. : total_kv, rows = p.reach < total_q ? p.reach + 128. : total_q;
-  const double cost = pl.max_qtiles * (keys / N + 2.) * 3. + pl.max_ktiles * (rows * G / N + 2.) * 4.;
-  p.two = cost * Hkv <= 8. * pl.ctas;
   p.scale = scale;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.timeout_ns = wait_limit_ns();

@@ -23,6 +23,7 @@ namespace gqa {
 // keys still and queries streamed for dk and dv.  At d = 256 the tensor memory
 // holds one accumulator, so dk and dv are units of their own.
 enum BwdKind { kBwdQ = 0, kBwdKV = 1, kBwdK = 2, kBwdV = 3 };
+constexpr int kBwdTwo = 4;  // added to the kind in a record: P and dS in two 16-bit terms
 
 struct BwdUnit {      // one record of the plan, the same for every KV head
   int kind, n;        // n: tiles streamed (0: the rows get zeros)
@@ -81,7 +82,6 @@ struct BwdParams {
   int d, N;             // N: rows of a streamed tile
   int reach;            // the window, or 2^30: more than any length
   int ctas;
-  int two;              // P and dS in two 16-bit terms
   float scale, scale_log2;
   unsigned long long timeout_ns;
 };

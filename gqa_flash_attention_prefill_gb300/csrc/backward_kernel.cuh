@@ -16,12 +16,13 @@
 //
 // P and dS are rounded to the inputs' type because the tensor cores take no other
 // left operand beside a 16-bit right one: half a step of each, as the forward
-// kernels round P.  Everything else is fp32.  Over many rows that makes a result's
-// error 1.41 times its own rounding; over a few it may be one p's alone, up to
-// twice.  So a small call (BwdParams::two), which leaves the GPU mostly idle, holds P
-// and dS as sums of two 16-bit terms, the second in the columns that the fp32 ones
-// leave free: 150 calls of a few tokens to some hundred were up to 1.94 times as far
-// from 64 bits as a form that rounds its results alone, and are up to 1.44 times.
+// kernels round P.  Everything else is fp32.  Over many pairs that makes a result's
+// error some 1.43 times its own rounding; over a few it may be one p's alone, up to
+// twice.  So the units of a sequence with few pairs (two_terms in backward.cu) hold P and
+// dS as sums of two 16-bit terms, the second in the columns that the fp32 ones
+// leave free.  Both kinds of unit are in one kernel, so that a sequence's bits do not
+// depend on its company; the loops with the two terms beside them cost the others up to
+// 1.3% (4096 tokens 462 -> 464 us, 3598 ragged ones 157 -> 158).
 //
 // CTA: 8 or 16 softmax warps (each warpgroup takes a share of the columns), a
 // loading warp, a warp that issues the products.  Persistent: units are taken from a
@@ -61,6 +62,13 @@ constexpr uint32_t bwd_smem(int D) {
          bwd_stages(D) * (2u * bwd_b_bytes(D) + bwd_stat_bytes(D)) + 64u * 8u + 16u +
          kBwdRecs * 64u;
 }
+
+// A truth value that picks a form of a generic lambda.
+template <bool V>
+struct Const {
+  static constexpr bool value = V;
+  __device__ constexpr operator bool() const { return V; }
+};
 
 struct BwdBar {
   static constexpr int kRecFull = 0, kRecEmpty = 4, kAFull = 8, kAEmpty = 9, kBFull = 10,
@@ -264,7 +272,7 @@ __device__ __forceinline__ void bwd_store(uint32_t t_acc, int cols, int col0, fl
   }
 }
 
-template <int D, bool BF16, bool TWO>
+template <int D, bool BF16>
 __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
     backward_kernel(const __grid_constant__ BwdParams p) {
   using K = Bwd<D, BF16>;
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
       if (lane == 0) mbar_arrive(bar(B::kRecFull + rs));
       if (end) break;
       auto field = [&](int i) { return __shfl_sync(0xffffffffu, word, i); };
-      const int kind = field(0), n = field(1), a_base = field(2), a_off = field(3),
+      const int kind = field(0) & 3, n = field(1), a_base = field(2), a_off = field(3),
                 b_base = field(5), b_off = field(6), b_len = field(7), stat = field(11);
       if (n == 0) continue;
       const bool qa = kind == kBwdQ;
@@ -428,10 +436,10 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
     for (uint32_t un = 0; ok; ++un) {
       const uint32_t rs = un % kBwdRecs;
       if (!(ok = wait(B::kRecFull + rs, (un / kBwdRecs) & 1u))) break;
-      const int kind = recs[rs * 16], n = recs[rs * 16 + 1];
+      const int word = recs[rs * 16], kind = word & 3, n = recs[rs * 16 + 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B::kRecEmpty + rs));
-      if (kind < 0) break;
+      if (word < 0) break;
       if (n == 0) continue;
       const bool has_t = kind != kBwdV, has_p = kind == kBwdKV || kind == kBwdV;
       if (!(ok = wait(B::kAFull, uc & 1u))) break;
@@ -449,12 +457,12 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
       };
       // acc (+)= (the 16-bit tile at `src`) B: each warpgroup's columns stand at
       // the start of its fp32 ones.
-      auto issue_acc = [&](uint32_t acc, uint32_t src, uint64_t b, bool first) {
+      auto issue_acc = [&](auto two, uint32_t acc, uint32_t src, uint64_t b, bool first) {
 #pragma unroll
         for (int kk = 0; kk < N / 16; ++kk)
           mma_ts(acc, src + (kk / (CW / 16)) * CW + (kk % (CW / 16)) * 8,
                  b + (uint64_t)(kk * 128), kIdescO, (first && kk == 0) ? 0u : 1u);
-        if constexpr (TWO) {
+        if (two) {
 #pragma unroll
           for (int kk = 0; kk < N / 16; ++kk)
             mma_ts(acc, src + (kk / (CW / 16)) * CW + (kk % (CW / 16)) * 8 + CW / 2,
@@ -465,39 +473,50 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
         ok = issue_s(it);
         if (!ok) break;
       }
-      for (int j = 0; j < n; ++j, ++it) {
-        const uint32_t s = it % NS;
-        if constexpr (NS == 1) {
-          ok = issue_s(it);
-          if (!ok) break;
-        }
-        const uint64_t dB = dB0 + s * 2u * (K::kBBytes >> 4), dBt = dBt0 + s * 2u * (K::kBBytes >> 4);
-        if (has_t) {
-          const uint64_t b2 = dB + (K::kBBytes >> 4);
+      auto tiles = [&](auto two) {
+        for (int j = 0; j < n; ++j, ++it) {
+          const uint32_t s = it % NS;
+          if constexpr (NS == 1) {
+            ok = issue_s(it);
+            if (!ok) break;
+          }
+          const uint64_t dB = dB0 + s * 2u * (K::kBBytes >> 4), dBt = dBt0 + s * 2u * (K::kBBytes >> 4);
+          if (has_t) {
+            const uint64_t b2 = dB + (K::kBBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tmem + K::kColT, dA2 + kstep(kk, K::kAChunk), b2 + kstep(kk, K::kBChunk), kIdescS,
-                   kk > 0 ? 1u : 0u);
-          mma_commit(bar(B::kTFull));
-        }
-        if (j == n - 1) mma_commit(bar(B::kAEmpty));
-        if (!(ok = wait(B::kPFull + (it & 1u), (it >> 1) & 1u))) break;
-        if (j == 0 && uc > 0 && !(ok = wait(B::kAccFree, (uc - 1u) & 1u))) break;
-        tc_fence_after();
-        if (has_p)
-          issue_acc(tmem + K::kColAcc0, tmem, dBt + (K::kBBytes >> 4), j == 0);
-        if constexpr (NS > 1) {
-          if (j + 1 < n) ok = issue_s(it + 1);
-          if (!ok) break;
-        }
-        if (has_t) {
-          if (!(ok = wait(B::kDFull, td & 1u))) break;
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ss(tmem + K::kColT, dA2 + kstep(kk, K::kAChunk), b2 + kstep(kk, K::kBChunk), kIdescS,
+                     kk > 0 ? 1u : 0u);
+            mma_commit(bar(B::kTFull));
+          }
+          if (j == n - 1) mma_commit(bar(B::kAEmpty));
+          if (!(ok = wait(B::kPFull + (it & 1u), (it >> 1) & 1u))) break;
+          if (j == 0 && uc > 0 && !(ok = wait(B::kAccFree, (uc - 1u) & 1u))) break;
           tc_fence_after();
-          issue_acc(tmem + K::kColAcc1, tmem + K::kColT, dBt, j == 0);
-          ++td;
+          if (has_p)
+            issue_acc(two, tmem + K::kColAcc0, tmem, dBt + (K::kBBytes >> 4), j == 0);
+          if constexpr (NS > 1) {
+            if (j + 1 < n) ok = issue_s(it + 1);
+            if (!ok) break;
+          }
+          if (has_t) {
+            if (!(ok = wait(B::kDFull, td & 1u))) break;
+            tc_fence_after();
+            issue_acc(two, tmem + K::kColAcc1, tmem + K::kColT, dBt, j == 0);
+            ++td;
+          }
+          mma_commit(bar(B::kBEmpty + s));
         }
-        mma_commit(bar(B::kBEmpty + s));
-      }
+      };
+      // A branch a tile, or two forms of the loop: 157.7 or 161.4 us for 3598 ragged tokens
+      // of d = 128, 469 or 464 for 4096 of d = 64.
+      const bool two = (word & kBwdTwo) != 0;
+      if constexpr (D == 128)
+        tiles(two);
+      else if (two)
+        tiles(Const<true>{});
+      else
+        tiles(Const<false>{});
       if (!ok) break;
       mma_commit(bar(B::kAccDone));
       ++uc;
@@ -528,7 +547,7 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
       const int32_t* rec = recs + rs * 16;
       next = rec[0];
       if (next < 0) return true;
-      if (next == kBwdQ) {
+      if ((next & 3) == kBwdQ) {
         const size_t at = (size_t)rec[13] * p.stat_rows + rec[11] + rec[3] + r;
         next_nlse = __ldcg(p.nlse + at);
         next_nd = __ldcg(p.nd + at);
@@ -540,7 +559,8 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
     for (uint32_t un = 0; ok && next >= 0; ++un) {
       const uint32_t rs = un % kBwdRecs;
       const int32_t* rec = recs + rs * 16;
-      const int kind = next, n = rec[1];
+      const int kind = next & 3, n = rec[1];
+      const bool two_terms = (next & kBwdTwo) != 0;
       const bool qa = kind == kBwdQ;
       BwdTile t;
       t.row_nlse = next_nlse;
@@ -560,32 +580,39 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
         lo0 -= part * CW;
         hi0 -= part * CW;
       }
-      for (int j = 0; j < n; ++j, ++it) {
-        const uint32_t s = it % NS;
-        const int off = b_off + j * N;
-        t.t_s = t_lane + part * CW;
-        t.t_t = t_lane + K::kColT + part * CW;
-        t.stats = sStat + s * K::kStat + (uint32_t)part * CW * 4u;
-        t.lo = lo0 - off;
-        t.hi = hi0 - off;
-        t.masked = lo_max > off || hi_min < off + N - 1;
-        const uint32_t bs = bar(B::kSFull), ps = it & 1u, bp = bar(B::kPFull + (it & 1u)),
-                       bt = bar(B::kTFull), bd = bar(B::kDFull);
-        if (qa) {
-          ok = bwd_tile<kBwdQ, D, BF16, TWO>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
-        } else {
-          // The statistics came with B (this thread has to see their barrier).
-          if (!(ok = wait(B::kBFull + s, (it / NS) & 1u))) break;
-          if constexpr (D < 256)
-            ok = bwd_tile<kBwdKV, D, BF16, TWO>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
-          else if (kind == kBwdK)
-            ok = bwd_tile<kBwdK, D, BF16, TWO>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
-          else
-            ok = bwd_tile<kBwdV, D, BF16, TWO>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+      auto tiles = [&](auto two) {
+        constexpr bool TWO = decltype(two)::value;
+        for (int j = 0; j < n; ++j, ++it) {
+          const uint32_t s = it % NS;
+          const int off = b_off + j * N;
+          t.t_s = t_lane + part * CW;
+          t.t_t = t_lane + K::kColT + part * CW;
+          t.stats = sStat + s * K::kStat + (uint32_t)part * CW * 4u;
+          t.lo = lo0 - off;
+          t.hi = hi0 - off;
+          t.masked = lo_max > off || hi_min < off + N - 1;
+          const uint32_t bs = bar(B::kSFull), ps = it & 1u, bp = bar(B::kPFull + (it & 1u)),
+                         bt = bar(B::kTFull), bd = bar(B::kDFull);
+          if (qa) {
+            ok = bwd_tile<kBwdQ, D, BF16, TWO>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+          } else {
+            // The statistics came with B (this thread has to see their barrier).
+            if (!(ok = wait(B::kBFull + s, (it / NS) & 1u))) break;
+            if constexpr (D < 256)
+              ok = bwd_tile<kBwdKV, D, BF16, TWO>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+            else if (kind == kBwdK)
+              ok = bwd_tile<kBwdK, D, BF16, TWO>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+            else
+              ok = bwd_tile<kBwdV, D, BF16, TWO>(t, sl2, mul, bs, ps, bp, bt, td & 1u, bd, abort_flag, p);
+          }
+          if (!ok) break;
+          if (kind != kBwdV) ++td;
         }
-        if (!ok) break;
-        if (kind != kBwdV) ++td;
-      }
+      };
+      if (two_terms)
+        tiles(Const<true>{});
+      else
+        tiles(Const<false>{});
       if (!ok || !(ok = fetch(un + 1u))) break;
       // Half of the warpgroups take dv and half dk of a unit with both, else each
       // an equal share of the columns of its one result.
@@ -633,9 +660,9 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
 
 namespace {
 
-template <int D, bool BF16, bool TWO>
+template <int D, bool BF16>
 cudaError_t launch_backward(const BwdParams& p, cudaStream_t st) {
-  auto kern = backward_kernel<D, BF16, TWO>;
+  auto kern = backward_kernel<D, BF16>;
   static SmemAttr attr{};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

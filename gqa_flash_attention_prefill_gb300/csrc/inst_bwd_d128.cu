@@ -4,8 +4,7 @@
 namespace gqa {
 
 cudaError_t launch_bwd_d128(const BwdParams& p, bool bf16, cudaStream_t st) {
-  if (p.two) return bf16 ? launch_backward<128, true, true>(p, st) : launch_backward<128, false, true>(p, st);
-  return bf16 ? launch_backward<128, true, false>(p, st) : launch_backward<128, false, false>(p, st);
+  return bf16 ? launch_backward<128, true>(p, st) : launch_backward<128, false>(p, st);
 }
 
 }  // namespace gqa

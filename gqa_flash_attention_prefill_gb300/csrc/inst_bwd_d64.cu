@@ -4,8 +4,7 @@
 namespace gqa {
 
 cudaError_t launch_bwd_d64(const BwdParams& p, bool bf16, cudaStream_t st) {
-  if (p.two) return bf16 ? launch_backward<64, true, true>(p, st) : launch_backward<64, false, true>(p, st);
-  return bf16 ? launch_backward<64, true, false>(p, st) : launch_backward<64, false, false>(p, st);
+  return bf16 ? launch_backward<64, true>(p, st) : launch_backward<64, false>(p, st);
 }
 
 }  // namespace gqa

@@ -397,10 +397,13 @@ GQA_API int gqa_cache_attention_workspace(int num_seqs, int total_q, int max_seq
  * anything.  16-bit tensors are 16-byte aligned.  Results share no memory with
  * one another or with an argument (GQA_ERR_INVALID).  Hq / Hkv is a power of
  * two up to 128; d is 64, 128 or 256.  Sums are fp32; p and ds are rounded once
- * to the inputs' type for their products, or held in two such terms where a
- * call is small (in f16 they are scaled by powers of two first, so that small
- * ones keep their bits).  The result is the same run to run.  Four kernels are enqueued on `stream`.  Metadata, waits and return
- * codes as gqa_flash_prefill; a missing or small workspace is GQA_ERR_INVALID.
+ * to the inputs' type for their products, or held in two such terms for a sequence
+ * of at most 2^19 pairs (new tokens times Hq / Hkv times the keys that one can see;
+ * its own lengths and the window decide alone).  In f16 they are scaled by powers
+ * of two first, so that small ones keep their bits.  The result is the same run to
+ * run, and rows outside every sequence do not enter it.  Four kernels are enqueued
+ * on `stream`.  Metadata, waits and return codes as gqa_flash_prefill; a missing or
+ * small workspace is GQA_ERR_INVALID.
  */
 GQA_API int gqa_prefill_backward(const void* q, const void* k, const void* v,
                                  const int32_t* cu_seqlens_q, const int32_t* prefix_lens,
