@@ -55,6 +55,7 @@ struct NormParams {
   uint8_t* scales;
   float* rstd;
   float* part;  // [CTAs of the gradient][n]
+  uint32_t* failed;  // [CTAs of the gradient]: a wait ran out, there is no part (NULL: no waits)
   float* dweight;
   long long x_stride, h_stride, out_stride;
   uint32_t rows;  // rows x heads
@@ -424,7 +425,10 @@ template <bool BF16, bool F32, int V, int T>
 __global__ void __launch_bounds__(T) norm_backward_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(8) uint64_t bars[kMaxStages];
-  __shared__ uint32_t abort_word;
+  // A wait of row k that runs out sets abort_words[k & 1].  After the row's barrier
+  // every thread reads the same there: the next wait to set it is row k + 2's,
+  // behind a barrier that this thread has to pass first.
+  __shared__ uint32_t abort_words[2];
   __shared__ float s[2][64];
   const int TS = blockDim.x, lane = threadIdx.x, nv = p.n / 8;
   constexpr uint32_t es = F32 ? 4u : 2u;
@@ -432,7 +436,7 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const __grid_constant_
   const uint32_t sbar = smem_u32(bars), sring = smem_u32(ring);
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) mbar_init(sbar + 8 * i, 1u);
-    abort_word = 0u;
+    abort_words[0] = abort_words[1] = 0u;
     fence_barrier_init();
   }
   __syncthreads();
@@ -461,9 +465,9 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const __grid_constant_
   for (unsigned long long at_row = blockIdx.x; at_row < p.rows; at_row += gridDim.x, ++k) {
     const uint32_t row = (uint32_t)at_row;
     const float rstd = __ldg(p.rstd_in + row);
-    // A wait that runs out raises the status; the sums below are then of
-    // whatever the stage holds, and the rows still end.
-    (void)wait_bounded(sbar + 8 * st, par, &abort_word, p.status, p.timeout_ns);
+    // A wait that runs out raises the status, and ends the CTA for all its threads at
+    // the row's barrier: nothing of the row is stored, and no copy issued after it.
+    (void)wait_bounded(sbar + 8 * st, par, abort_words + (k & 1), p.status, p.timeout_ns);
     const uint8_t* at = ring + st * stage;
     float sum = 0.f, none = 0.f;
 #pragma unroll
@@ -474,6 +478,17 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const __grid_constant_
                         values<F32, BF16>(load_raw<F32>(at + off_h, 8 * c)), w[v], rstd, acc[v]);
     }
     row_reduce<true, false>(sum, none, 32, s[k & 1]);
+    if (abort_words[k & 1] != 0u) {
+      if (threadIdx.x == 0) {  // let the copies in flight land: row k's and those ahead of it
+        const uint32_t stages = (uint32_t)p.stages, ahead = k > 0 && stages > 1 ? stages - 1 : stages;
+        for (uint32_t j = k; j < k + ahead && blockIdx.x + (unsigned long long)j * gridDim.x < p.rows; ++j)
+          wait_drain(sbar + 8 * (j % stages), (j / stages) & 1u, p.timeout_ns);
+        if (p.part != nullptr) p.failed[blockIdx.x] = 1u;
+      }
+      if (p.part != nullptr)
+        for (int c = lane; c < p.n; c += TS) p.part[(size_t)blockIdx.x * p.n + c] = NAN;
+      return;
+    }
     // Every thread is past the row before: its stage is free.
     if (threadIdx.x == 0 && k > 0 && p.stages > 1)
       fill(k - 1 + p.stages, (st == 0 ? p.stages : st) - 1);
@@ -498,10 +513,8 @@ __global__ void __launch_bounds__(T) norm_backward_kernel(const __grid_constant_
       par ^= 1u;
     }
   }
-  if (abort_word != 0u && threadIdx.x == 0)  // let the copies in flight land
-    for (unsigned long long j = k > (uint32_t)p.stages ? k - p.stages : 0; j < k; ++j)
-        wait_drain(sbar + 8 * (uint32_t)(j % p.stages), (uint32_t)(j / p.stages) & 1u, p.timeout_ns);
   if (p.part == nullptr) return;
+  if (threadIdx.x == 0) p.failed[blockIdx.x] = 0u;
   float* part = p.part + (size_t)blockIdx.x * p.n;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -619,7 +632,12 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__
   a = s[lane][y];  // column y of the block, share `lane`
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  if (lane == 0 && blockIdx.x * 32 + y < p.n) p.dweight[blockIdx.x * 32 + y] = a;
+  if (lane == 0 && blockIdx.x * 32 + y < p.n) {
+    if (a != a && p.failed != nullptr)  // a CTA whose wait ran out leaves NaN, and its word
+      for (int b = 0; b < p.parts; ++b)
+        if (__ldcg(p.failed + b) != 0u) return;
+    p.dweight[blockIdx.x * 32 + y] = a;
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -798,12 +816,14 @@ int run_norm(const void* x, long long x_stride, const void* residual, void* resi
   return e == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
-size_t backward_bytes(const NormShape& s, int n) {
+// CTAs that the workspace has room for: a part of n floats each, and behind the parts a word each.
+size_t backward_ctas(const NormShape& s) {
   int sms = 152;
   unsigned int* status = nullptr;
   if (call_device(&sms, &status) != GQA_OK) sms = 152;
-  return 4u * (size_t)sms * backward_per_sm(s) * n;
+  return (size_t)sms * backward_per_sm(s);
 }
+size_t backward_bytes(const NormShape& s, int n) { return 4u * backward_ctas(s) * ((size_t)n + 1); }
 
 int run_norm_backward(const void* dy, long long dy_stride, const void* h, long long h_stride,
                       int stream_type, const float* rstd, const void* weight, int weight_type,
@@ -863,6 +883,7 @@ int run_norm_backward(const void* dy, long long dy_stride, const void* h, long l
   p.out = dx;
   p.dresidual = dresidual;
   p.part = static_cast<float*>(workspace);
+  if (p.part != nullptr && s.team == 0) p.failed = reinterpret_cast<uint32_t*>(p.part + backward_ctas(s) * n);
   p.dweight = dweight;
   p.x_stride = dy_stride;
   p.h_stride = h_stride;

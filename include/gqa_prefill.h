@@ -475,7 +475,8 @@ GQA_API int gqa_rms_norm(const void* x, long long x_stride, const void* residual
  *
  * dx and dresidual may be dy, h or dh themselves (same base, stride and type).
  * The result is the same run to run.  Otherwise as gqa_rms_norm; no result at
- * all is GQA_ERR_INVALID.
+ * all is GQA_ERR_INVALID.  Should a bounded wait run out, dweight is left as it
+ * was, and so are some rows of dx and dresidual.
  */
 GQA_API int gqa_rms_norm_backward(const void* dy, long long dy_stride, const void* h,
                                   long long h_stride, int stream_type, const float* rstd,
