@@ -407,14 +407,13 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
       }
       if (!ok) break;
     }
-    // Let every copy issued land before the CTA can exit.
-    if (*abort_flag) {
-      if (ua > 0) wait_drain(bar(B::kAFull), (ua - 1u) & 1u, p.timeout_ns);
-      if (lands > 0) wait_drain(bar(B::kLand), (lands - 1u) & 1u, p.timeout_ns);
-      for (uint32_t b = 0; b < NS; ++b)
-        if (it > b)
-          wait_drain(bar(B::kBFull + (it - 1u - b) % NS), ((it - 1u - b) / NS) & 1u, p.timeout_ns);
-    }
+    // Let every copy issued land before the CTA can exit: another warp may give up
+    // after this one has issued its last.
+    if (ua > 0) wait_drain(bar(B::kAFull), (ua - 1u) & 1u, p.timeout_ns);
+    if (lands > 0) wait_drain(bar(B::kLand), (lands - 1u) & 1u, p.timeout_ns);
+    for (uint32_t b = 0; b < NS; ++b)
+      if (it > b)
+        wait_drain(bar(B::kBFull + (it - 1u - b) % NS), ((it - 1u - b) / NS) & 1u, p.timeout_ns);
     __syncwarp();
   }
 
