@@ -214,9 +214,10 @@ __device__ __forceinline__ void bwd_plan(const BwdParams& p) {
       }
     }
     __syncthreads();
-    if (s_slots <= p.max_slots && s_joins <= p.max_joins) break;
+    const bool fits = s_slots <= p.max_slots && s_joins <= p.max_joins;
+    __syncthreads();  // all have read the counts, which are set anew below or in the next pass
+    if (fits) break;
     cap *= 2;
-    __syncthreads();
   }
   if (tid < 32) {  // the bins' first places: two bins a lane
     static_assert(kPlanBins == 64, "two bins a lane");
