@@ -23,6 +23,7 @@ constexpr int kPlanBins = 64;
 // unit is not cut.
 constexpr int kShares = 1;
 constexpr int kMinTiles = 8;
+constexpr int kMinCost = 4 * kMinTiles;  // of a tile at the most expensive
 // Pairs up to which a sequence's P and dS are held in two terms: 724 tokens of one query head, 256 of
 // eight.  Error against 64 bits over that of results that are rounded alone, 1300 sequences of 1 to 700
 // tokens, the worst of dq, dk and dv: with two terms 1.00 (1.06 where a result cancels), with one 1.43, up
@@ -32,7 +33,7 @@ constexpr int kMinTiles = 8;
 constexpr long long kTwoPairs = 1 << 19;
 
 // Relative cost of a streamed tile: its products.
-__device__ __forceinline__ int tile_cost(int kind) {
+__host__ __device__ __forceinline__ int tile_cost(int kind) {
   return kind == kBwdKV ? 4 : kind == kBwdV ? 2 : 3;
 }
 
@@ -191,7 +192,7 @@ __device__ __forceinline__ void bwd_plan(const BwdParams& p) {
   // The cost above which a unit is cut.  At most 2 sum / cap parts come of it;
   // should they not fit the workspace, the cap is doubled.
   long long cap = ((long long)s_total * p.Hkv + (long long)p.ctas * kShares - 1) / ((long long)p.ctas * kShares);
-  if (cap < 4 * kMinTiles) cap = 4 * kMinTiles;
+  if (cap < kMinCost) cap = kMinCost;
   auto parts_of = [&](int kind, int n) {
     const long long k = ((long long)n * tile_cost(kind) + cap - 1) / cap;
     return (int)(k < 1 ? 1 : k < n ? k : n);
@@ -480,7 +481,14 @@ int bwd_layout(int num_seqs, int total_q, int total_kv, int Hq, int Hkv, int d, 
   pl->max_qtiles = (int)qt;
   pl->max_ktiles = (int)kt;
   pl->stat_rows = qt * 128;
-  pl->max_slots = 2 * sms * kShares / Hkv + 1;
+  // Parts of cut units: what the CTAs' shares can make of them, and no more than the
+  // shapes can (a call of a few tokens cuts nothing, and needs no room for parts).
+  const int N = bwd_n(d);
+  auto parts = [&](int kind, long long rows_b) { return ((rows_b + N - 1) / N * tile_cost(kind) + kMinCost - 1) / kMinCost; };
+  const long long pq = parts(kBwdQ, total_kv), pk = parts(d == 256 ? kBwdK : kBwdKV, rows);
+  const long long by_shape = (pq > 1 ? qt * pq : 0) + (pk > 1 ? (d == 256 ? 2 : 1) * kt * pk : 0);
+  const long long by_share = 2 * sms * kShares / Hkv + 1;
+  pl->max_slots = (int)(by_shape < by_share ? by_shape : by_share);
   pl->max_joins = pl->max_slots / 2 + 1;
   pl->max_units = (int)(qt + (d == 256 ? 2 : 1) * kt) + pl->max_slots;
   size_t at = 0;
