@@ -162,8 +162,8 @@ __global__ void __launch_bounds__(kPlanThreads) bwd_scan_kernel(const __grid_con
     p.hdr[kBwdQTiles] = nq;
     p.hdr[kBwdKTiles] = nk;
   }
-  if (p.most != nullptr)
-    for (long long i = tid; i < 4ll * p.num_seqs * p.Hkv; i += kPlanThreads) p.most[i] = 0u;
+  if (p.most_v != nullptr)
+    for (long long i = tid; i < (long long)p.num_seqs * p.Hkv; i += kPlanThreads) p.most_v[i] = 0u;
 }
 
 // The list of units, by one CTA: their costs are summed, costly ones are cut, and
@@ -264,7 +264,7 @@ __device__ __forceinline__ void bwd_plan(const BwdParams& p) {
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ BwdParams p) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, ROUNDS = 16 / RPW;  // 16 rows a warp
-  __shared__ float s_nl[128], s_nd[128], s_w[128];
+  __shared__ float s_nl[128], s_nd[128], s_w[128], s_o2[128];
   __shared__ unsigned int s_most[2];
   grid_dep_launch_dependents();
   grid_dep_wait();
@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ B
             }
             if (!BF16) md = fmaxf(md, fabsf(dlt));
           }
+          if (!BF16) s_o2[r] = sq;
           s_nl[r] = nl;
           s_nd[r] = nd;
           s_w[r] = w;
@@ -356,16 +357,14 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const __grid_constant__ B
     }
     __syncthreads();
     if (!BF16 && tid == 0) {
-      unsigned int* most = p.most + ((size_t)b * p.Hkv + g) * 4;
-      if (keys) {
-        atomicMax(most + 2, s_most[0]);
-      } else {
-        atomicMax(most, s_most[0]);
-        atomicMax(most + 1, s_most[1]);
-      }
+      if (keys)
+        atomicMax(p.most_v + (size_t)b * p.Hkv + g, s_most[0]);
+      else
+        p.tile_most[(size_t)g * p.max_qtiles + tile] = make_uint2(s_most[0], s_most[1]);
     }
     if (!keys) {
       const size_t at = (size_t)g * p.stat_rows + (size_t)tile * 128;
+      if (!BF16 && tid < 128) p.row_o2[at + tid] = s_o2[tid];
       if (tid < 128) p.nlse[at + tid] = s_nl[tid];
       else p.nd[at + tid - 128] = s_nd[tid - 128];
       if (p.sinks != nullptr) {
@@ -458,7 +457,7 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ B
 struct BwdPlan {
   int ctas, max_qtiles, max_ktiles, max_units, max_slots, max_joins;
   long long stat_rows;
-  size_t units, joins, qt, kt, nlse, nd, sink, most, part, bytes;
+  size_t units, joins, qt, kt, nlse, nd, sink, o2, most, most_v, part, bytes;
 };
 
 int bwd_layout(int num_seqs, int total_q, int total_kv, int Hq, int Hkv, int d, int dtype, BwdPlan* pl) {
@@ -505,7 +504,10 @@ int bwd_layout(int num_seqs, int total_q, int total_kv, int Hq, int Hkv, int d, 
   pl->nlse = take(4u * (size_t)Hkv * pl->stat_rows);
   pl->nd = take(4u * (size_t)Hkv * pl->stat_rows);
   pl->sink = take(4u * (size_t)Hq * pl->max_qtiles);
-  pl->most = take(dtype == GQA_F16 ? 16u * (size_t)num_seqs * Hkv : 0u);
+  const size_t f16 = dtype == GQA_F16 ? 1u : 0u;
+  pl->o2 = take(f16 * 4u * (size_t)Hkv * pl->stat_rows);
+  pl->most = take(f16 * 8u * (size_t)Hkv * pl->max_qtiles);
+  pl->most_v = take(f16 * 4u * (size_t)num_seqs * Hkv);
   pl->part = take(4u * 128u * (size_t)d * bwd_accs(d) * Hkv * pl->max_slots);
   pl->bytes = at;
   return GQA_OK;
@@ -623,7 +625,11 @@ int run_backward(const void* q, const void* k, const void* v, const int32_t* cu,
   p.nlse = reinterpret_cast<float*>(ws + pl.nlse);
   p.nd = reinterpret_cast<float*>(ws + pl.nd);
   p.sink_part = reinterpret_cast<float*>(ws + pl.sink);
-  p.most = dtype == GQA_F16 ? reinterpret_cast<unsigned int*>(ws + pl.most) : nullptr;
+  if (dtype == GQA_F16) {
+    p.row_o2 = reinterpret_cast<float*>(ws + pl.o2);
+    p.tile_most = reinterpret_cast<uint2*>(ws + pl.most);
+    p.most_v = reinterpret_cast<unsigned int*>(ws + pl.most_v);
+  }
   p.part = reinterpret_cast<float*>(ws + pl.part);
   p.stat_rows = pl.stat_rows;
   p.max_qtiles = pl.max_qtiles;

@@ -72,7 +72,9 @@ struct BwdParams {
   float* nlse;        // [Hkv][stat_rows] -lse log2(e) (+ 15 in f16); -inf: no such row
   float* nd;          // [Hkv][stat_rows] -D
   float* sink_part;   // [Hq][max_qtiles]
-  unsigned int* most; // f16: [B][Hkv][4] largest |dout|^2, |D|, |v|^2 (bits of floats)
+  float* row_o2;      // f16: [Hkv][stat_rows] |dout|^2
+  uint2* tile_most;   // f16: [Hkv][max_qtiles] largest |dout|^2 and |D| of a query tile (bits of floats)
+  unsigned int* most_v; // f16: [B][Hkv] largest |v|^2 of the sequence
   float* part;        // [slot][Hkv][accumulators][d/4][128][4]
   unsigned int* status;
   long long stat_rows;
@@ -113,10 +115,9 @@ __device__ __forceinline__ void bwd_bounds(bool queries, int a, int P, int E, in
 }
 
 // dS = P (dP - D) is held in f16 times 2^k, with k from a bound of |dP - D| that
-// leaves a factor of two to the largest f16: |dP_ij| <= |dout_i| |v_j|.
-__device__ __forceinline__ int bwd_exponent(const unsigned int* most) {
-  const float o2 = __uint_as_float(most[0]), dm = __uint_as_float(most[1]),
-              v2 = __uint_as_float(most[2]);
+// leaves a factor of two to the largest f16: |dP_ij| <= |dout_i| |v_j|.  A dq unit has a
+// k for each query row, a dk unit one for the query rows that it streams.
+__device__ __forceinline__ int bwd_exponent(float o2, float dm, float v2) {
   const float bound = sqrtf(o2) * sqrtf(v2) + dm;
   if (!(bound > 0.f) || !(bound < 3e38f)) return 0;  // all zeros, or not finite
   int e;

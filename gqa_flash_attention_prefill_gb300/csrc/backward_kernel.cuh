@@ -538,20 +538,34 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
     uint32_t it = 0, td = 0, uc = 0;
     // The next unit's record, and what of global memory it needs: on its way while
     // this unit's results are stored.
-    int next = -1, next_k = 0;
-    float next_nlse = 0.f, next_nd = 0.f;
+    int next = -1;
+    float next_nlse = 0.f, next_nd = 0.f, next_o2 = 0.f, next_v2 = 0.f;
     auto fetch = [&](uint32_t un) -> bool {
       const uint32_t rs = un % kBwdRecs;
       if (!wait(B::kRecFull + rs, (un / kBwdRecs) & 1u)) return false;
       const int32_t* rec = recs + rs * 16;
       next = rec[0];
       if (next < 0) return true;
-      if ((next & 3) == kBwdQ) {
+      const int kind = next & 3;
+      if (kind == kBwdQ) {
         const size_t at = (size_t)rec[13] * p.stat_rows + rec[11] + rec[3] + r;
         next_nlse = __ldcg(p.nlse + at);
         next_nd = __ldcg(p.nd + at);
+        if constexpr (!BF16) next_o2 = __ldcg(p.row_o2 + at);
+      } else if (!BF16 && kind != kBwdV) {
+        // The largest of the query tiles that the unit streams.
+        const int t0 = rec[6] >> 7, t1 = (min(rec[6] + rec[1] * N, rec[7]) + 127) >> 7;
+        const uint2* most = p.tile_most + (size_t)rec[13] * p.max_qtiles + (rec[11] >> 7);
+        uint32_t o2 = 0u, dm = 0u;
+        for (int i = t0 + lane; i < t1; i += 32) {
+          const uint2 m = __ldcg(most + i);
+          o2 = max(o2, m.x);
+          dm = max(dm, m.y);
+        }
+        next_o2 = __uint_as_float(__reduce_max_sync(0xffffffffu, o2));
+        next_nd = __uint_as_float(__reduce_max_sync(0xffffffffu, dm));
       }
-      if constexpr (!BF16) next_k = bwd_exponent(p.most + ((size_t)rec[12] * p.Hkv + rec[13]) * 4);
+      if (!BF16 && kind != kBwdV) next_v2 = __uint_as_float(__ldcg(p.most_v + (size_t)rec[12] * p.Hkv + rec[13]));
       return true;
     };
     bool ok = fetch(0);
@@ -566,8 +580,9 @@ __global__ void __launch_bounds__(bwd_threads(D), bwd_per_sm(D))
       t.row_nd = next_nd;
       float mul = 1.f, undo = 1.f;  // of dS, and of the results it enters
       if constexpr (!BF16) {
-        mul = ldexpf(1.f, next_k - (int)kBwdBias);
-        undo = ldexpf(1.f, -next_k);
+        const int k = bwd_exponent(next_o2, fabsf(next_nd), next_v2);
+        mul = ldexpf(1.f, k - (int)kBwdBias);
+        undo = ldexpf(1.f, -k);
       }
       const int a_off = rec[3], b_off = rec[6];
       // Columns the row keeps, counted from B's first row: key or packed row

@@ -400,7 +400,8 @@ GQA_API int gqa_cache_attention_workspace(int num_seqs, int total_q, int max_seq
  * to the inputs' type for their products, or held in two such terms for a sequence
  * of at most 2^19 pairs (new tokens times Hq / Hkv times the keys that one can see;
  * its own lengths and the window decide alone).  In f16 they are scaled by powers
- * of two first, so that small ones keep their bits.  The result is the same run to
+ * of two first, so that small ones keep their bits: ds by one for each query row
+ * for dq, and by one for the rows that 128 keys see together for dk.  The result is the same run to
  * run, and rows outside every sequence do not enter it.  Four kernels are enqueued
  * on `stream`.  Metadata, waits and return codes as gqa_flash_prefill; a missing or
  * small workspace is GQA_ERR_INVALID.
