@@ -632,12 +632,14 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__
   a = s[lane][y];  // column y of the block, share `lane`
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  if (lane == 0 && blockIdx.x * 32 + y < p.n) {
-    if (a != a && p.failed != nullptr)  // a CTA whose wait ran out leaves NaN, and its word
-      for (int b = 0; b < p.parts; ++b)
-        if (__ldcg(p.failed + b) != 0u) return;
-    p.dweight[blockIdx.x * 32 + y] = a;
+  if (p.failed != nullptr && __any_sync(0xffffffffu, a != a)) {
+    // The values' own NaN, or a share that is missing: a CTA whose wait ran out leaves
+    // NaN, and its word.
+    uint32_t failed = 0u;
+    for (int b = lane; b < p.parts; b += 32) failed |= __ldcg(p.failed + b);
+    if (__any_sync(0xffffffffu, failed != 0u)) return;
   }
+  if (lane == 0 && blockIdx.x * 32 + y < p.n) p.dweight[blockIdx.x * 32 + y] = a;
 }
 
 // ------------------------------------------------------------------ host

@@ -111,3 +111,24 @@ def test_gradient_of_heads(pkg, heads, n):  # noqa: F811
     wide = lambda t: torch.cat([t[:, :1], t, t[:, :1]], 1)[:, 1:heads + 1]  # noqa: E731
     dy, h = (wide(randn(130, heads, n, seed=s, dtype=torch.bfloat16)) for s in (1, 2))
     gradient(pkg, dy, h, randn(n, seed=4), 0.0, None, ("dx", "dweight"))
+
+
+@pytest.mark.parametrize("rows,n", [(700, 1024), (400, 4096), (60, 16384), (700, 256)])
+def test_values_that_are_not_finite(pkg, rows, n):  # noqa: F811
+    """A NaN or an infinity of dy is written where it belongs: its row of dx, its column of dweight, and nowhere else."""
+    dy, h, w = randn(rows, n, seed=1, dtype=torch.bfloat16), randn(rows, n, seed=2, dtype=torch.bfloat16), randn(n, seed=3)
+    rstd = (h.float().square().mean(-1) + EPS).rsqrt()
+    want = pkg.rms_norm_backward(dy, h, w, rstd)
+    dy[5, 9], dy[rows - 2, n - 3] = float("nan"), float("inf")
+    h[rows - 2, n - 3] = 1.0  # not zero: an infinity times zero is NaN
+    ws = nan(pkg.rms_norm_backward_workspace(rows, 1, n, "bf16") // 4, dtype=torch.float32)
+    dx, dw = torch.full_like(dy, 7.0), torch.full((n,), 7.0, device="cuda")
+    pkg.gqa_rms_norm_backward(dy, h, w, rstd, dx, dweight=dw, workspace=ws)
+    torch.cuda.synchronize()
+    assert pkg.get_device_status() == 0
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    rest[5] = rest[rows - 2] = False
+    assert torch.equal(dx[rest], want[0][rest]) and not bool(dx[~rest].isfinite().any())
+    col = torch.ones(n, dtype=torch.bool, device="cuda")
+    col[9] = col[n - 3] = False
+    assert bool(dw[9].isnan()) and bool(dw[n - 3].isinf()) and torch.equal(dw[col], want[2][col])
