@@ -22,7 +22,7 @@
 // dS as sums of two 16-bit terms, the second in the columns that the fp32 ones
 // leave free.  Both kinds of unit are in one kernel, so that a sequence's bits do not
 // depend on its company; the loops with the two terms beside them cost the others up to
-// 1.3% (4096 tokens 462 -> 464 us, 3598 ragged ones 157 -> 158).
+// 1% (4096 tokens 462 -> 463 us, 3598 ragged ones 157 -> 158).
 //
 // CTA: 8 or 16 softmax warps (each warpgroup takes a share of the columns), a
 // loading warp, a warp that issues the products.  Persistent: units are taken from a
@@ -33,8 +33,12 @@
 // all of its bandwidth), its softmax for 460-490, and they overlap as far as
 // one warp gets the products issued (60-120 clocks each beside busy warps, 26 in
 // 1500 clocks of a CTA's 1950).  4096 tokens of 64 / 8 heads of 64, bf16: 442 us of
-// the call's 464, 1089 TFLOP/s of the seven products, tensor path 70% active, issue
-// slots 55%; 3598 ragged f16 tokens of 32 / 8 heads of 128: 137 of 157 us.
+// the call's 463, 1089 TFLOP/s of the seven products, tensor path 70% active, issue
+// slots 55%; 3598 ragged f16 tokens of 32 / 8 heads of 128: 139 of 159 us, tensor path
+// 59%.  2048 tokens of 16 / 4 heads of 256, bf16: 217 of 235 us, one stage, so that a
+// tile's load, S, T and second products follow one another.  Registers: 96 a thread (two
+// CTAs of ten warps, or one of 18, an SM), with 4 to 7 words spilled at d = 64 and 128: 0.06%
+// and 0.4% of the instructions executed.
 //
 // Tile and CTAs.  d = 64: tiles of 64 columns and two CTAs an SM, which overlap each
 // other's waits (one CTA with tiles of 128: 512 us, with two S tiles and two
